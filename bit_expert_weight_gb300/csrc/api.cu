@@ -69,6 +69,12 @@ static int device_cc_minor()
     return g_minor[cur_device()];
 }
 
+bool device_supported()
+{
+    // The library is compiled for sm_103a only.
+    return device_cc_major() == 10 && device_cc_minor() == 3;
+}
+
 int *device_status_word()
 {
     ensure_device_info();
@@ -92,12 +98,6 @@ namespace {
 
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool device_supported()
-{
-    // The library is compiled for sm_103a only.
-    return device_cc_major() == 10 && device_cc_minor() == 3;
-}
 
 smoe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SMOE_OK : SMOE_ERR_CUDA; }
 

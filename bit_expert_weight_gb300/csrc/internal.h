@@ -18,6 +18,8 @@ size_t moe_workspace_zero_bytes(const smoe_layer_desc *layer, int64_t num_tokens
 int device_sm_count();
 // Compute capability major of the current device (cached per device).
 int device_cc_major();
+// Whether the current device is the one the library is compiled for (sm_103a).
+bool device_supported();
 // Pointer to the device status word of the current device.
 int *device_status_word();
 
@@ -190,6 +192,12 @@ cudaError_t launch_tc_logits(const uint16_t *x, const uint16_t *router_w, int64_
 // stage_mask: 1 sort + gather, 2 gate/up GEMM, 4 down GEMM + combine.
 cudaError_t launch_grouped(const GroupedArgs &a, const void *x, int x_bf16, float *y, int stage_mask,
                            cudaStream_t stream);
+
+// ------------------------------------------- rotation, paged cache, attention
+
+cudaError_t launch_rope(const smoe_rope_args &a, cudaStream_t stream);
+cudaError_t launch_kv_append(const smoe_kv_append_args &a, cudaStream_t stream);
+cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, cudaStream_t stream);
 
 int layer_grid_ctas_max();
 cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream);

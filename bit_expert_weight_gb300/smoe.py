@@ -37,7 +37,13 @@ EXPORTED = [
     "smoe_repacked_bytes_mixed", "smoe_repack_mixed", "smoe_unpack_mixed",
     "smoe_moe_workspace_bytes_mixed", "smoe_moe_forward_mixed", "smoe_moe_forward_stage_mixed",
     "smoe_debug_set_waits", "smoe_moe_path_dtype",
+    "smoe_rope_table", "smoe_rope", "smoe_kv_append", "smoe_attention",
 ]
+
+# Bytes of smoe_attention's workspace (SMOE_ATTENTION_WORKSPACE_BYTES) and
+# the kinds of frequency tables (SMOE_ROPE_* in include/smoe.h).
+ATTENTION_WORKSPACE_BYTES = 64 << 20
+ROPE_KINDS = {"plain": 0, "linear": 1, "parts": 2, "bands": 3}
 
 # Execution paths (SMOE_PATH_* in include/smoe.h).
 PATH_AUTO, PATH_STREAM, PATH_GROUPED = 0, 1, 2
@@ -97,6 +103,62 @@ class LayerDesc(ctypes.Structure):
         ("expert_tiles", ctypes.c_void_p), ("shared_tiles", ctypes.c_void_p),
         ("shared_ffn_dim", ctypes.c_int32), ("shared_gate_w", ctypes.c_void_p),
     ]
+
+
+class RopeScaling(ctypes.Structure):
+    """smoe_rope_scaling (include/smoe.h)."""
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("fast", ctypes.c_double),
+                ("slow", ctypes.c_double)]
+
+
+class RopeArgs(ctypes.Structure):
+    """smoe_rope_args (include/smoe.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("x_row_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("num_rows", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("rot_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("norm_w", ctypes.c_void_p)]
+
+
+# smoe_kv_cache and smoe_kv_batch, the first members of the two structs below
+_CACHE_BATCH = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("k_page_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("_pad", ctypes.c_int32),
+                ("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
+                ("num_seqs", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """smoe_kv_append_args (include/smoe.h)."""
+    _fields_ = _CACHE_BATCH + [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("qo_row_stride", ctypes.c_int64), ("qo_head_stride", ctypes.c_int64),
+        ("num_heads", ctypes.c_int32), ("dtype", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("rot_scale", ctypes.c_float), ("eps", ctypes.c_float),
+        ("positions", ctypes.c_void_p), ("table", ctypes.c_void_p), ("q_norm", ctypes.c_void_p),
+        ("k_norm", ctypes.c_void_p)]
+
+
+class AttentionArgs(ctypes.Structure):
+    """smoe_attention_args (include/smoe.h)."""
+    _fields_ = _CACHE_BATCH + [
+        ("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("num_heads", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -182,6 +244,14 @@ def load(path: str | None = None):
     L.smoe_moe_forward_stage_mixed.restype = I
     L.smoe_get_device_status.argtypes = [P]
     L.smoe_get_device_status.restype = I
+    L.smoe_rope_table.argtypes = [I32, ctypes.c_double, ctypes.POINTER(RopeScaling), P, P]
+    L.smoe_rope_table.restype = I
+    L.smoe_rope.argtypes = [ctypes.POINTER(RopeArgs), P]
+    L.smoe_rope.restype = I
+    L.smoe_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), P]
+    L.smoe_kv_append.restype = I
+    L.smoe_attention.argtypes = [ctypes.POINTER(AttentionArgs), P, S, P]
+    L.smoe_attention.restype = I
     L.smoe_debug_set_waits.argtypes = [ctypes.c_longlong, I]
     L.smoe_debug_set_waits.restype = None
     _lib = L
@@ -500,6 +570,168 @@ def vault_repack_layer(meta: bytes, vault_dev: torch.Tensor, layer: int, num_exp
                                           num_experts, _ptr(tiles), n, _stream(stream)),
            "smoe_vault_repack_layer")
     return tiles
+
+
+# ------------------------------------ rotation, paged cache, attention
+
+_DTYPES = {torch.float32: SMOE_F32, torch.bfloat16: SMOE_BF16}
+
+
+def _heads(name, t):
+    """A [rows, heads, head_dim] fp32 or bf16 CUDA view with contiguous channels:
+    (pointer, row stride, head stride, smoe_dtype)."""
+    if t.dim() != 3 or t.stride(2) != 1 or not t.is_cuda:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] CUDA tensor with contiguous "
+                         "channels")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be fp32 or bf16")
+    return t.data_ptr(), t.stride(0), t.stride(1), dt
+
+
+def _device_array(name, t, dtype, numel=None):
+    """Pointer of a contiguous CUDA tensor of `dtype` with at least `numel` elements
+    (None: no tensor, a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{name} must have {numel} elements")
+    return t.data_ptr()
+
+
+def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows):
+    """The members of smoe_kv_cache and smoe_kv_batch."""
+    P, Hkv, page, D = k_pages.shape
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.bfloat16 or not t.is_cuda:
+            raise ValueError(f"{name} must be a bf16 CUDA tensor")
+        if t.stride()[1:] != (page * D, D, 1):
+            raise ValueError(f"{name}: the last three dimensions must be contiguous")
+    B = kv_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] < B:
+        raise ValueError("page_table must be [sequences, pages]")
+    return (k_pages.data_ptr(), v_pages.data_ptr(), P, k_pages.stride(0), v_pages.stride(0), page,
+            Hkv, D, 0, _device_array("row_start", row_start, torch.int32, B + 1),
+            _device_array("kv_len", kv_len, torch.int32),
+            _device_array("page_table", page_table, torch.int32), rows, B, page_table.shape[1])
+
+
+def rope_table(rot_dim: int, theta: float, kind="plain", factor=1.0, original_len=4096.0,
+               fast=None, slow=1.0, device="cuda"):
+    """smoe_rope_table: (table, rot_scale) -- the frequency table as an int64 tensor on
+    `device` and the factor on cosine and sine.  kind: "plain", "linear", "parts" (fast 32,
+    slow 1 by default) or "bands" (fast 4, slow 1)."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}")
+    if fast is None:
+        fast = 4.0 if kind == "bands" else 32.0
+    sc = RopeScaling(ROPE_KINDS[kind], factor, original_len, fast, slow)
+    out = (ctypes.c_int64 * max(rot_dim // 2, 1))()
+    scale = ctypes.c_float()
+    _check(load().smoe_rope_table(rot_dim, theta, ctypes.byref(sc), out, ctypes.byref(scale)),
+           "smoe_rope_table")
+    return torch.tensor(list(out), dtype=torch.int64).to(device), scale.value
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, rot_scale=1.0, out=None,
+         interleaved=False, norm_w=None, eps=1e-6, stream=None):
+    """smoe_rope: x [rows, heads, head_dim] (fp32 or bf16) rotated at `positions` (int32
+    [rows]), after a norm of each head where norm_w (bf16 [head_dim]) is given.  The first
+    2 * table.numel() channels rotate.  out: a tensor of x's shape and dtype (x itself
+    rotates in place)."""
+    T, H, D = x.shape
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and dtype")
+    xp, xr, xh, dt = _heads("x", x)
+    op, orow, oh, _ = _heads("out", out)
+    a = RopeArgs(xp, op, xr, xh, orow, oh, T, H, D, dt, 2 * table.numel(), interleaved, rot_scale,
+                 eps, _device_array("positions", positions, torch.int32, T),
+                 _device_array("table", table, torch.int64),
+                 _device_array("norm_w", norm_w, torch.bfloat16, D))
+    _check(load().smoe_rope(ctypes.byref(a), _stream(stream)), "smoe_rope")
+    return out
+
+
+def kv_append(q, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              row_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, table=None,
+              rot_scale=1.0, q_out=None, positions=None, interleaved=False, q_norm=None,
+              k_norm=None, eps=1e-6, stream=None):
+    """smoe_kv_append: store the rows' keys (normed, rotated) and values in the paged cache
+    and return the queries (normed, rotated) in bf16; q None: only k and v, returns None.
+    q [rows, heads, head_dim], k and v [rows, kv heads, head_dim], all fp32 or all bf16;
+    pages bf16 [pages, kv heads, page size, head_dim]; row_start int32 [sequences + 1], kv_len
+    int32 [sequences] (the new rows included), page_table int32 [sequences, pages].  table
+    None: no rotation."""
+    T, Hkv, D = k.shape
+    kp, kr, kh, dt = _heads("k", k)
+    vp, vr, vh, vdt = _heads("v", v)
+    if v.shape != k.shape or (Hkv, D) != (k_pages.shape[1], k_pages.shape[3]):
+        raise ValueError("k and v must be [rows, kv heads, head_dim] of the pages")
+    qp = op = None
+    qr = qh = orow = oh = H = 0
+    qdt = dt
+    if q is not None:
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q must have k's rows and head_dim")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16:
+            raise ValueError("q_out must be bf16 of q's shape")
+        H = q.shape[1]
+        qp, qr, qh, qdt = _heads("q", q)
+        op, orow, oh, _ = _heads("q_out", q_out)
+    if not dt == vdt == qdt:
+        raise TypeError("q, k and v must have one dtype")
+    a = KvAppendArgs(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, kp, vp,
+                     op, qr, qh, kr, kh, vr, vh, orow, oh, H, dt,
+                     0 if table is None else 2 * table.numel(), interleaved, rot_scale, eps,
+                     _device_array("positions", positions, torch.int32, T),
+                     _device_array("table", table, torch.int64),
+                     _device_array("q_norm", q_norm, torch.bfloat16, D),
+                     _device_array("k_norm", k_norm, torch.bfloat16, D))
+    _check(load().smoe_kv_append(ctypes.byref(a), _stream(stream)), "smoe_kv_append")
+    return q_out if q is not None else None
+
+
+def attention_workspace(device="cuda", stream=None):
+    """A zeroed workspace for `attention`, the same for every shape."""
+    ws = torch.empty(ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+    _check(load().smoe_moe_workspace_init(_ptr(ws), ws.numel(), _stream(stream)),
+           "workspace_init")
+    return ws
+
+
+def attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              row_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+              max_rows: int, ws: torch.Tensor, scale=None, window=0, out=None,
+              out_dtype=torch.bfloat16, stream=None):
+    """smoe_attention: the rows' attention over the paged cache (which holds their own keys
+    and values).  q bf16 [rows, heads, head_dim]; max_rows: no sequence has more rows;
+    window 0: every key up to the row's own; scale default head_dim ** -0.5.  Returns out
+    [rows, heads, head_dim] in out_dtype (bf16 or fp32)."""
+    T, H, D = q.shape
+    qp, qr, qh, qdt = _heads("q", q)
+    if qdt != SMOE_BF16:
+        raise TypeError("q must be bf16")
+    if D != k_pages.shape[3]:
+        raise ValueError("q and the pages must have one head_dim")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=out_dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    op, orow, oh, odt = _heads("out", out)
+    a = AttentionArgs(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, op,
+                      qr, qh, orow, oh, H, odt, max_rows, window,
+                      D ** -0.5 if scale is None else scale)
+    _check(load().smoe_attention(ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream(stream)),
+           "smoe_attention")
+    return out
 
 
 def device_status(stream=None) -> int:

@@ -23,7 +23,9 @@
  *   "CMF v2 -- Format Specification", 5 -- routing masks (expert bitfields,
  *     LSB-first): smoe_router_opts.expert_mask.
  *   ".smoe Binary Format", Expert Table Entry / Tensor Descriptor / Arch
- *     Block "SARC" -- the vault reader (smoe_vault_*).
+ *     Block "SARC" -- the vault reader (smoe_vault_*), and the constants of
+ *     the attention half of a layer (smoe_rope, smoe_kv_append,
+ *     smoe_attention).
  *
  * Conventions (all entry points):
  *   - Every pointer argument is DEVICE memory owned by the caller unless the
@@ -493,6 +495,188 @@ smoe_status smoe_moe_forward_stage(const smoe_layer_desc *layer, const void *x,
 smoe_status smoe_moe_forward_noalloc(const smoe_layer_desc *layer, const void *x,
                                      smoe_dtype x_dtype, int64_t num_tokens, float *y,
                                      int32_t *ids_out, float *w_out, void *cuda_stream);
+
+/* -------------------------------------- rotation, paged cache, attention */
+
+/* What a decoder layer needs beside its expert layer, between the
+ * projections (plain matrix products, the caller's): the position rotation
+ * of its heads, the write of new keys and values into a paged cache, and the
+ * attention of the new rows over that cache.  The arch block of a vault
+ * carries the sizes and constants (num_heads, num_kv_heads, head_dim,
+ * rope_theta, rms_norm_eps, the has_qk_norm flag).  Everything here is
+ * inference only: there are no gradients.
+ *
+ * Heads.  x, q, k and v are [rows, heads, head_dim] views: element (r, h, c)
+ * lies at data + r * row_stride + h * head_stride + c (strides in elements),
+ * so a slice of one projection's output needs no copy.  Pointers are 16-byte
+ * aligned and strides are multiples of 8 elements.
+ *
+ * Rotation.  Pair i (0 <= i < rot_dim / 2) of a head at position p turns by
+ * t = p * f_i:
+ *   a' = rot_scale * (a cos t - b sin t),  b' = rot_scale * (b cos t + a sin t)
+ * with (a, b) = channels (i, i + rot_dim / 2), or (2i, 2i + 1) where
+ * `interleaved` is set; channels from rot_dim on pass through.  The
+ * frequencies come as a table of int64, f_i / (2 pi) in units of 2^-64 turns
+ * per position: the low 64 bits of p * table[i] are the angle as a fraction
+ * of a turn, exactly reduced, so that far positions (and negative ones)
+ * rotate as precisely as near ones without 64-bit floating point.  With a
+ * norm weight w (bf16 [head_dim]) a head is first normed over all its
+ * channels: x * rsqrt(mean(x^2) + eps) * w.  All of it is computed in fp32
+ * and rounded once to the output's type.
+ *
+ * Paged cache.  k_pages and v_pages are bf16 [num_pages, num_kv_heads,
+ * page_size, head_dim]; the last three dimensions are contiguous, pages lie
+ * k_page_stride and v_page_stride elements apart (so keys and values may
+ * share one buffer).  page_size is 16, 32, 64, 128 or 256.
+ *
+ * Batch.  Sequence b owns rows row_start[b] .. row_start[b + 1] - 1 (none is
+ * fine) and has kv_len[b] keys, the new rows' own included: its row number j
+ * of n is key i = kv_len[b] - n + j.  Key i lies in page
+ * page_table[b * table_stride + i / page_size] at slot i % page_size.  Rows
+ * from row_start[num_seqs] on belong to no sequence: they give and
+ * get nothing (a captured graph may be replayed with a smaller batch).  All
+ * of these arrays are DEVICE int32, read when the kernel runs. */
+#define SMOE_MAX_HEAD_DIM 256
+#define SMOE_MAX_SEQS 2048
+
+typedef enum {
+    SMOE_ROPE_PLAIN = 0,  /* f_i = theta^(-2 i / rot_dim)                     */
+    SMOE_ROPE_LINEAR = 1, /* every f_i divided by factor                      */
+    SMOE_ROPE_PARTS = 2,  /* by turns: pairs that turn more than `fast` times
+                             in original_len positions are kept, those below
+                             `slow` turns divided by factor, a linear ramp
+                             over the pair index between (its ends rounded
+                             outwards); rot_scale = 0.1 ln(factor) + 1        */
+    SMOE_ROPE_BANDS = 3   /* by wavelength 2 pi / f_i: shorter than
+                             original_len / fast kept, longer than
+                             original_len / slow divided by factor, between
+                             them blended linearly in original_len / wavelength */
+} smoe_rope_kind;
+
+typedef struct {
+    int32_t kind;         /* smoe_rope_kind                                   */
+    double factor;        /* >= 1                                             */
+    double original_len;  /* PARTS, BANDS: > 0                                */
+    double fast, slow;    /* PARTS, BANDS: fast > slow > 0                    */
+} smoe_rope_scaling;
+
+/* The rotation's frequency table.  HOST function, no GPU used.
+ *   rot_dim    even, 2 .. SMOE_MAX_HEAD_DIM
+ *   theta      > 1
+ *   scaling    nullable (plain frequencies)
+ *   table      HOST out int64 [rot_dim / 2]; copy it to the device
+ *   rot_scale  HOST out: the factor on cosine and sine
+ * Errors: SMOE_ERR_INVALID_ARG. */
+smoe_status smoe_rope_table(int32_t rot_dim, double theta, const smoe_rope_scaling *scaling,
+                            int64_t *table, float *rot_scale);
+
+typedef struct {
+    const void *x;             /* [num_rows, num_heads, head_dim]             */
+    void *out;                 /* same shape and dtype; may be x itself (then
+                                  with x's strides), else no overlap          */
+    int64_t x_row_stride, x_head_stride, out_row_stride, out_head_stride;
+    int64_t num_rows;
+    int32_t num_heads, head_dim; /* head_dim a multiple of 8, <= 256          */
+    int32_t dtype;             /* smoe_dtype of x and out                     */
+    int32_t rot_dim;           /* a multiple of 8, 8 .. head_dim              */
+    int32_t interleaved;       /* pairs (2i, 2i + 1) instead of halves        */
+    float rot_scale;           /* finite                                      */
+    float eps;                 /* of the norm; >= 0, finite                   */
+    const int32_t *positions;  /* [num_rows], any int32                       */
+    const int64_t *table;      /* [rot_dim / 2]                               */
+    const void *norm_w;        /* nullable bf16 [head_dim], 16-byte aligned   */
+} smoe_rope_args;
+
+/* Rotate (and norm, with a weight) heads.  Errors: SMOE_ERR_INVALID_ARG,
+ * SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
+smoe_status smoe_rope(const smoe_rope_args *args, void *cuda_stream);
+
+typedef struct {
+    void *k_pages, *v_pages;   /* 16-byte aligned                             */
+    int64_t num_pages, k_page_stride, v_page_stride;
+    int32_t page_size, num_kv_heads, head_dim;  /* head_dim 64 or 128         */
+} smoe_kv_cache;
+
+typedef struct {
+    const int32_t *row_start;  /* [num_seqs + 1]                              */
+    const int32_t *kv_len;     /* [num_seqs]                                  */
+    const int32_t *page_table; /* [num_seqs, table_stride]                    */
+    int64_t num_rows;          /* rows of q, k, v and the outputs             */
+    int32_t num_seqs;          /* 0 .. SMOE_MAX_SEQS                          */
+    int32_t table_stride;      /* pages of a table row; kv_len is at most
+                                  table_stride * page_size                    */
+} smoe_kv_batch;
+
+typedef struct {
+    smoe_kv_cache cache;
+    smoe_kv_batch batch;
+    const void *q, *k, *v;     /* q nullable: only k and v then               */
+    void *q_out;               /* bf16 [num_rows, num_heads, head_dim]; may be
+                                  q itself where that is bf16                 */
+    int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride,
+        v_head_stride, qo_row_stride, qo_head_stride;
+    int32_t num_heads;         /* of q                                        */
+    int32_t dtype;             /* smoe_dtype of q, k and v                    */
+    int32_t rot_dim;           /* 0: no rotation (table may then be NULL)     */
+    int32_t interleaved;
+    float rot_scale, eps;
+    const int32_t *positions;  /* nullable [num_rows]; default: the row's key
+                                  index                                       */
+    const int64_t *table;
+    const void *q_norm, *k_norm; /* nullable bf16 [head_dim]                  */
+} smoe_kv_append_args;
+
+/* Append the new rows to the cache: each row's k, normed and rotated, and
+ * its v, rounded to bf16, go to the slots of the row's key; q, normed and
+ * rotated, goes to q_out.  One launch.  The slots of one call must be
+ * distinct (no two sequences write one page).  A row whose key index is
+ * negative (a chunk longer than kv_len) is not stored.  A page id outside
+ * the pool, a key past the page table and a row_start out of order store
+ * nothing and are recorded: SMOE_ERR_DEVICE_FAULT from
+ * smoe_get_device_status.  Errors: SMOE_ERR_INVALID_ARG,
+ * SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
+smoe_status smoe_kv_append(const smoe_kv_append_args *args, void *cuda_stream);
+
+/* Bytes of the attention's workspace: the same for every shape.  256-byte
+ * aligned, zeroed once (smoe_moe_workspace_init does it) and again after a
+ * call that returned an error or recorded a fault; calls that can overlap on
+ * the device need a workspace each. */
+#define SMOE_ATTENTION_WORKSPACE_BYTES (64u << 20)
+
+typedef struct {
+    smoe_kv_cache cache;
+    smoe_kv_batch batch;
+    const void *q;             /* bf16 [num_rows, num_heads, head_dim]        */
+    void *out;                 /* same shape, bf16 or fp32 (out_dtype)        */
+    int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+    int32_t num_heads;         /* a multiple of num_kv_heads, at most 128
+                                  times as many: query head h reads kv head
+                                  h / (num_heads / num_kv_heads)              */
+    int32_t out_dtype;         /* smoe_dtype                                  */
+    int32_t max_rows;          /* no sequence of the batch has more rows; the
+                                  kernel is chosen by it                      */
+    int32_t window;            /* 0: a row sees every key up to its own; else
+                                  the last `window` of them                   */
+    float scale;               /* of q . k; finite, > 0                       */
+} smoe_attention_args;
+
+/* Attention of the new rows over the cache (which holds their own keys and
+ * values already): row with key index i sees the keys j <= i, j > i - window
+ * where window > 0, and
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q . k_j) - max).
+ * A row that sees no key (kv_len 0, or a chunk longer than kv_len) gets
+ * zeros.  Keys past kv_len are never used, whatever their slots hold; keys
+ * and values below it must be finite.  Scores, maxima, sums and outputs are
+ * accumulated in fp32.  Work is split along the keys so that every SM has
+ * the same share; the parts are joined in a fixed order, so the same batch
+ * gives the same bits on every call.
+ * A page id outside the pool, a length past the page table, rows out of
+ * order and a sequence of more than max_rows rows are recorded
+ * (SMOE_ERR_DEVICE_FAULT); that sequence's output is then unspecified.
+ * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_WORKSPACE, SMOE_ERR_UNSUPPORTED
+ * (device), SMOE_ERR_CUDA. */
+smoe_status smoe_attention(const smoe_attention_args *args, void *workspace,
+                           size_t workspace_bytes, void *cuda_stream);
 
 /* Testing only: make the layer kernel's bounded waits short and, if
  * stall_routing is nonzero, make its routing step wait for logits that no
