@@ -112,7 +112,7 @@ __device__ __forceinline__ void seen(const smoe_attention_args &a, const Seq &s,
 // time, and their sums are joined at the end.
 template <int D>
 __global__ void __launch_bounds__(32 * kDecWarps, 1)
-    attend_rows_kernel(const smoe_attention_args a, int *status)
+    attend_tiles_kernel(const smoe_attention_args a, int *status)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_m[kDecWarps][kDecRows], s_l[kDecWarps][kDecRows];
@@ -314,28 +314,564 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     }
 }
 
+// ------------------------------------------------- few rows (decode steps)
+
+// Sequences of at most kDecRows packed rows: bound by reading the keys and
+// values.  The work of a launch is one line of steps: for every sequence and
+// kv head (an item) kItemSteps for its own cost (its queries, its output),
+// then its keys in steps of kDecKeys.  Every warp of the grid is a worker
+// with an equal share [w q, (w + 1) q) of that line, whatever the lengths,
+// and copies its keys into a ring of its own that runs ahead over item
+// borders; no warp waits for another one in the loop.  An item cut by shares
+// is computed in parts.  Parts of one CTA are joined in shared memory, once,
+// at its end; what still is a part then goes to the workspace, and the CTA
+// that arrives last joins the item's parts, in CTA order.
+constexpr int kItemSteps = 3;
+constexpr int kMaxCtas = 256;
+constexpr size_t kPartsAt = 4096;  // workspace: arrival counters, then the parts
+
+static_assert(kMaxCtas * sizeof(unsigned) <= kPartsAt, "counters");
+
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Key steps of one item of s (0: no rows).  A row that sees nothing still
+// takes a step: it writes its zeros.
+__device__ __forceinline__ int item_steps(const smoe_attention_args &a, const Seq &s)
+{
+    if (s.rows == 0)
+        return 0;
+    int lo, hi, x, y;
+    seen(a, s, 0, lo, x);
+    seen(a, s, s.rows - 1, y, hi);
+    const int n = hi > lo ? (hi + kDecKeys - 1) / kDecKeys - lo / kDecKeys : 0;
+    return n > 1 ? n : 1;
+}
+
+// Where a worker's share begins.
+struct Share {
+    int64_t q;       // steps per worker
+    int64_t total;   // steps of the launch
+    int64_t before;  // steps before the sequence that holds its first
+    int b;           // that sequence
+};
+
+// Steps per worker: an equal share, but no item in so many parts that the
+// joining costs more than the sharing saves.  A CTA reads a part in about
+// 1/8 of the time that it takes for 8 steps, so n steps are read and joined
+// fastest by about sqrt(n) CTAs.
+__device__ __forceinline__ int64_t steps_per_worker(int64_t total, int longest)
+{
+    const int64_t q = ceil_div(total, (int64_t)gridDim.x * kDecWarps);
+    const int64_t least = static_cast<int64_t>(sqrtf(static_cast<float>(longest)) * 0.125f);
+    return q > least ? q : (least > 1 ? least : 1);
+}
+
+// The shares of the CTA's warps.  Thread t looks at the sequences
+// [t per, (t + 1) per), SMOE_MAX_SEQS in all at most.
+__device__ __forceinline__ Share find_share(const smoe_attention_args &a, int *status)
+{
+    constexpr int kThreads = 32 * kDecWarps, kPer = SMOE_MAX_SEQS / kThreads;
+    static_assert(kPer * kThreads == SMOE_MAX_SEQS, "sequences per thread");
+    __shared__ int64_t s_sum[kDecWarps];
+    __shared__ int s_max[kDecWarps];
+    __shared__ Share s_share[kDecWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = a.batch.num_seqs, per = (n + kThreads - 1) / kThreads;
+    int u[kPer];  // steps of an item, its own cost included
+    int64_t sum = 0;
+    int mx = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = tid * per + i;
+        const int k = i < per && b < n ? item_steps(a, seq_at(a, b, status)) : 0;
+        u[i] = k > 0 ? k + kItemSteps : 0;
+        sum += u[i];
+        mx = k > mx ? k : mx;
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        incl += lane >= o ? v : 0;
+        const int m = __shfl_xor_sync(0xffffffffu, mx, o);
+        mx = m > mx ? m : mx;
+    }
+    if (lane == 31)
+        s_sum[warp] = incl;
+    if (lane == 0)
+        s_max[warp] = mx;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+        before += w < warp ? s_sum[w] : 0;
+        total += s_sum[w];
+        mx = s_max[w] > mx ? s_max[w] : mx;
+    }
+    const int Hkv = a.cache.num_kv_heads;
+    Share sh;
+    sh.total = total * Hkv;
+    sh.q = steps_per_worker(sh.total, mx);
+    int64_t at = (before + incl - sum) * Hkv;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int64_t next = at + (int64_t)u[i] * Hkv;
+        for (int w = 0; w < kDecWarps; ++w) {
+            const int64_t w0 = ((int64_t)blockIdx.x * kDecWarps + w) * sh.q;
+            if (w0 >= at && w0 < next) {
+                sh.b = tid * per + i;
+                sh.before = at;
+                s_share[w] = sh;
+            }
+        }
+        at = next;
+    }
+    __syncthreads();
+    if (((int64_t)blockIdx.x * kDecWarps + warp) * sh.q < sh.total)
+        return s_share[warp];
+    sh.b = n;  // nothing left for this worker
+    sh.before = sh.total;
+    return sh;
+}
+
+// A place on the line of steps, at an item.
+struct Cursor {
+    Seq s, next;        // its sequence, and the one after it (loaded early)
+    int b, h, steps;    // key steps of the item
+    int64_t at;         // its first step on the line
+    int k_lo, k_hi;     // keys seen by any of its rows
+};
+
+__device__ __forceinline__ void cursor_keys(const smoe_attention_args &a, Cursor &c)
+{
+    int x, y;
+    c.steps = item_steps(a, c.s);
+    c.k_lo = c.k_hi = 0;
+    if (c.s.rows > 0) {
+        seen(a, c.s, 0, c.k_lo, x);
+        seen(a, c.s, c.s.rows - 1, y, c.k_hi);
+    }
+}
+
+__device__ __forceinline__ Seq seq_or_none(const smoe_attention_args &a, int b, int *status)
+{
+    Seq s;
+    s.row0 = 0;
+    s.rows = s.len = 0;
+    return b < a.batch.num_seqs ? seq_at(a, b, status) : s;
+}
+
+__device__ __forceinline__ Cursor cursor_at(const smoe_attention_args &a, const Share &sh,
+                                            int64_t w0, int *status)
+{
+    Cursor c;
+    c.b = sh.b;
+    c.s = seq_or_none(a, c.b, status);
+    c.next = seq_or_none(a, c.b + 1, status);
+    cursor_keys(a, c);
+    const int len = c.steps + kItemSteps;
+    c.h = c.steps ? static_cast<int>((w0 - sh.before) / len) : 0;
+    c.at = sh.before + (int64_t)c.h * len;
+    return c;
+}
+
+// To the next item; past the last one its sequence has no rows.
+__device__ __forceinline__ void cursor_next(const smoe_attention_args &a, Cursor &c, int *status)
+{
+    c.at += c.steps + kItemSteps;
+    if (++c.h < a.cache.num_kv_heads)
+        return;
+    c.h = 0;
+    do {
+        ++c.b;
+        c.s = c.next;
+        c.next = seq_or_none(a, c.b + 1, status);
+    } while (c.s.rows == 0 && c.b < a.batch.num_seqs);
+    cursor_keys(a, c);
+}
+
+// Key steps [s0, s1) of the cursor's item that lie in the share [w0, w1).
+__device__ __forceinline__ void steps_in(const Cursor &c, int64_t w0, int64_t w1, int &s0, int &s1)
+{
+    const int64_t k = c.at + kItemSteps;
+    s0 = w0 > k ? static_cast<int>(w0 - k) : 0;
+    s1 = w1 - k < c.steps ? static_cast<int>(w1 - k) : c.steps;
+}
+
+// A part that a warp leaves for its CTA to join.
+struct PartInfo {
+    const float *at;   // outputs [rows][D], maxima [rows], sums [rows]
+    int64_t row0;
+    int nrows, h;      // packed rows (0: no part)
+    int64_t first, last;  // the workers that share the item
+};
+
+__host__ __device__ constexpr int dec_part_floats(int D) { return kDecRows * (D + 2); }
+
+// Joins two parts' (maximum, sum, pair of outputs).
+__device__ __forceinline__ void join_part(float &m, float &l, float2 &v, float pm, float pl, float2 y)
+{
+    const float mn = fmaxf(m, pm);
+    const float fo = mn == -INFINITY ? 0.f : ex2(m - mn), fn = mn == -INFINITY ? 0.f : ex2(pm - mn);
+    v.x = v.x * fo + y.x * fn;
+    v.y = v.y * fo + y.y * fn;
+    l = l * fo + pl * fn;
+    m = mn;
+}
+
+__device__ __forceinline__ void write_out(const smoe_attention_args &a, int G, int64_t row0, int h, int r,
+                                          int c, float2 v, float l)
+{
+    const float inv = l > 0.f ? 1.0f / l : 0.f;  // a row that sees no key: zeros
+    const int64_t at = (row0 + r / G) * a.out_row_stride + (int64_t)(h * G + r % G) * a.out_head_stride + c;
+    if (a.out_dtype == SMOE_F32)
+        *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(v.x * inv, v.y * inv);
+    else
+        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at) = pack_bf16x2(v.x * inv, v.y * inv);
+}
+
 template <int D>
-cudaError_t launch_rows(const smoe_attention_args &a, cudaStream_t stream)
+__global__ void __launch_bounds__(32 * kDecWarps, 1)
+    attend_rows_kernel(const smoe_attention_args a, uint8_t *workspace, int *status)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PartInfo s_part[kDecWarps][2];  // 0: of an item begun earlier, 1: begun here
+    __shared__ int s_last;
+    constexpr int KB = D / 16;  // k blocks of Q K^T, pairs of column blocks of P V
+    constexpr int kThreads = 32 * kDecWarps;
+    static_assert(dec_part_floats(D) * 4 <= kDecStages * dec_step_bytes(D), "a part fits a ring");
+    static_assert(kPartsAt + (size_t)kMaxCtas * (kDecWarps + 2) * dec_part_floats(D) * 4 <=
+                      SMOE_ATTENTION_WORKSPACE_BYTES,
+                  "workspace");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.num_heads / a.cache.num_kv_heads, page = a.cache.page_size;
+    const int g = lane >> 2, c2 = 2 * (lane & 3);
+    const float sc = a.scale * 1.44269504088896341f;
+
+    const Share sh = find_share(a, status);
+    const int64_t me = (int64_t)blockIdx.x * kDecWarps + warp;
+    if ((int64_t)blockIdx.x * kDecWarps * sh.q >= sh.total)
+        return;  // nothing for the whole CTA
+    if (lane == 0)
+        s_part[warp][0].nrows = s_part[warp][1].nrows = 0;
+    const int64_t w0 = me * sh.q, w1 = w0 + sh.q;
+    Cursor cc = cursor_at(a, sh, w0, status), ld = cc;
+    const uint32_t ring = smem_u32(smem) + warp * kDecStages * dec_step_bytes(D);
+    unsigned *arrived = reinterpret_cast<unsigned *>(workspace);
+    float *worker_parts = reinterpret_cast<float *>(workspace + kPartsAt);  // one per worker
+    float *cta_parts = worker_parts + (int64_t)kMaxCtas * kDecWarps * dec_part_floats(D);  // two per CTA
+
+    // The loading end of the ring: the next step to copy, its page id already
+    // on the way.
+    int ls, ls1, filled = 0, pg = 0;
+    steps_in(ld, w0, w1, ls, ls1);
+    auto seek = [&]() {  // to a step that exists, or past the share
+        while (ld.s.rows > 0 && ls >= ls1) {
+            if (ld.at + ld.steps + kItemSteps >= w1) {
+                ld.s.rows = 0;
+                break;
+            }
+            cursor_next(a, ld, status);
+            steps_in(ld, w0, w1, ls, ls1);
+        }
+        const int k0 = (ld.k_lo / kDecKeys + ls) * kDecKeys;
+        pg = ld.s.rows > 0 && k0 < ld.k_hi
+                 ? a.batch.page_table[(int64_t)ld.b * a.batch.table_stride + k0 / page]
+                 : 0;
+    };
+    seek();
+    auto issue = [&]() {
+        if (ld.s.rows > 0) {
+            const int k0 = (ld.k_lo / kDecKeys + ls) * kDecKeys;
+            if (k0 < ld.k_hi) {
+                const bool there = pg >= 0 && pg < a.cache.num_pages;
+                if (!there && lane == 0)
+                    set_status(status, kStatusBadArg);
+                const int64_t at = ((int64_t)ld.h * page + k0 % page) * D;
+                const uint16_t *ks = static_cast<const uint16_t *>(a.cache.k_pages) +
+                                     (there ? pg * a.cache.k_page_stride + at : 0);
+                const uint16_t *vs = static_cast<const uint16_t *>(a.cache.v_pages) +
+                                     (there ? pg * a.cache.v_page_stride + at : 0);
+                const uint32_t dk = ring + filled * dec_step_bytes(D), dv = dk + kDecKeys * D * 2;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const int e = i * 32 + lane, r = e / (D / 8), c = e % (D / 8);
+                    // slots of keys that no row sees are not read: zeros
+                    const bool v = there && k0 + r >= ld.k_lo && k0 + r < ld.k_hi;
+                    cp_async16(dk + chunk_at<D>(r, c), ks + (v ? r * D + c * 8 : 0), v);
+                    cp_async16(dv + chunk_at<D>(r, c), vs + (v ? r * D + c * 8 : 0), v);
+                }
+            }
+            filled = filled + 1 == kDecStages ? 0 : filled + 1;
+            ++ls;
+            seek();
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kDecStages - 1; ++st)
+        issue();
+
+    int used = 0;  // the ring's reading end
+    for (; cc.s.rows > 0 && cc.at < w1; cursor_next(a, cc, status)) {
+        int s0, s1;
+        steps_in(cc, w0, w1, s0, s1);
+        if (s0 >= s1)
+            continue;
+        // ---- one item, or the part of it that lies in the share
+        const int nrows = cc.s.rows * G;  // packed rows, kDecRows at most
+        int lo[2], hi[2], t_lo, t_hi, x;  // [t_lo, t_hi) is seen by every row
+        seen(a, cc.s, cc.s.rows - 1, t_lo, x);
+        seen(a, cc.s, 0, x, t_hi);
+        uint32_t q[KB][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int m = g + 8 * r;
+            const bool on = m < nrows;
+            lo[r] = hi[r] = 0;
+            if (on)
+                seen(a, cc.s, m / G, lo[r], hi[r]);
+            const uint16_t *src = static_cast<const uint16_t *>(a.q) +
+                                  (cc.s.row0 + m / G) * a.q_row_stride +
+                                  (int64_t)(cc.h * G + m % G) * a.q_head_stride;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                q[kb][r] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * kb + c2) : 0u;
+                q[kb][2 + r] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * kb + 8 + c2) : 0u;
+            }
+        }
+        float o[2 * KB][4];
+#pragma unroll
+        for (int n = 0; n < 2 * KB; ++n)
+            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        int k0 = (cc.k_lo / kDecKeys + s0) * kDecKeys;
+
+        for (int st = s0; st < s1; ++st, k0 += kDecKeys) {
+            issue();
+            cp_async_wait<kDecStages - 1>();
+            __syncwarp();
+            const uint32_t dk = ring + used * dec_step_bytes(D), dv = dk + kDecKeys * D * 2;
+            used = used + 1 == kDecStages ? 0 : used + 1;
+            if (k0 >= cc.k_hi)
+                continue;  // no row sees a key: nothing was copied
+            float p[2][4] = {};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                uint32_t b[4];
+                ldm4(b, dk + chunk_at<D>((lane & 7) + ((lane >> 4) << 3), 2 * kb + ((lane >> 3) & 1)));
+                mma_bf16(p[0], q[kb], b[0], b[1]);
+                mma_bf16(p[1], q[kb], b[2], b[3]);
+            }
+            if (k0 < t_lo || k0 + kDecKeys > t_hi) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = k0 + 8 * n + c2 + (e & 1), r = e >> 1;
+                        if (key < lo[r] || key >= hi[r])
+                            p[n][e] = -INFINITY;
+                    }
+            }
+            float f[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float v = fmaxf(fmaxf(p[0][2 * r], p[0][2 * r + 1]),
+                                fmaxf(p[1][2 * r], p[1][2 * r + 1]));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                const float mn = fmaxf(mx[r], v * sc);
+                const float mu = mn == -INFINITY ? 0.f : mn;  // a row that has seen nothing yet
+                f[r] = ex2(mx[r] - mu);
+                mx[r] = mn;
+                float t = 0.f;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &y = p[n][2 * r + e];
+                        y = ex2(fmaf(y, sc, -mu));
+                        t += y;
+                    }
+                sum[r] = sum[r] * f[r] + t;
+            }
+            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < 2 * KB; ++n) {
+                    o[n][0] *= f[0];
+                    o[n][1] *= f[0];
+                    o[n][2] *= f[1];
+                    o[n][3] *= f[1];
+                }
+            }
+            // P as bf16 hi + lo: the loop waits for memory, not for the second
+            // product, and the output keeps fp32 accuracy
+            uint32_t hi4[4], lo4[4];
+            split_bf16x2(p[0][0], p[0][1], hi4[0], lo4[0]);
+            split_bf16x2(p[0][2], p[0][3], hi4[1], lo4[1]);
+            split_bf16x2(p[1][0], p[1][1], hi4[2], lo4[2]);
+            split_bf16x2(p[1][2], p[1][3], hi4[3], lo4[3]);
+#pragma unroll
+            for (int n = 0; n < KB; ++n) {
+                uint32_t b[4];
+                ldm4t(b, dv + chunk_at<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
+                mma_bf16(o[2 * n], hi4, b[0], b[1]);
+                mma_bf16(o[2 * n], lo4, b[0], b[1]);
+                mma_bf16(o[2 * n + 1], hi4, b[2], b[3]);
+                mma_bf16(o[2 * n + 1], lo4, b[2], b[3]);
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+        }
+        if (s0 == 0 && s1 == cc.steps) {
+            // the whole item
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (g + 8 * r < nrows)
+#pragma unroll
+                    for (int n = 0; n < 2 * KB; ++n)
+                        write_out(a, G, cc.s.row0, cc.h, g + 8 * r, 8 * n + c2,
+                                  make_float2(o[n][2 * r], o[n][2 * r + 1]), sum[r]);
+        } else {
+            // a part: into the warp's ring where no later item has keys in the
+            // share (every copy has been used then), else into the workspace,
+            // while the ring works on
+            const int which = s0 == 0 ? 1 : 0;
+            const int64_t after = cc.at + cc.steps + kItemSteps;
+            const bool idle = after + kItemSteps >= w1 || after >= sh.total;
+            float *part = idle ? reinterpret_cast<float *>(smem + warp * kDecStages * dec_step_bytes(D))
+                               : worker_parts + me * dec_part_floats(D);
+            if (lane == 0) {
+                PartInfo &pi = s_part[warp][which];
+                pi.at = part;
+                pi.row0 = cc.s.row0;
+                pi.nrows = nrows;
+                pi.h = cc.h;
+                pi.first = (cc.at + kItemSteps) / sh.q;
+                pi.last = (cc.at + kItemSteps + cc.steps - 1) / sh.q;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int n = 0; n < 2 * KB; ++n)
+                    *reinterpret_cast<float2 *>(part + (g + 8 * r) * D + 8 * n + c2) =
+                        make_float2(o[n][2 * r], o[n][2 * r + 1]);
+                if ((lane & 3) == 0) {
+                    part[kDecRows * D + g + 8 * r] = mx[r];
+                    part[kDecRows * (D + 1) + g + 8 * r] = sum[r];
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // ---- join the CTA's parts: of the item begun before it, then of the items
+    // begun by each warp
+    const int64_t b0 = (int64_t)blockIdx.x * kDecWarps;
+    for (int j = -1; j < kDecWarps; ++j) {
+        const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
+        if (pi.nrows == 0)
+            continue;
+        const int wa = j < 0 ? 0 : j;
+        const int wb = pi.last - b0 < kDecWarps ? static_cast<int>(pi.last - b0) : kDecWarps - 1;
+        const int c_first = static_cast<int>(pi.first / kDecWarps), c_last = static_cast<int>(pi.last / kDecWarps);
+        const bool whole = c_first == c_last;
+        float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D);
+        for (int e = tid; e < pi.nrows * (D / 2); e += kThreads) {
+            const int r = e / (D / 2), c = 2 * (e % (D / 2));
+            float m = -INFINITY, l = 0.f;
+            float2 v = make_float2(0.f, 0.f);
+            for (int w = wa; w <= wb; ++w) {
+                const float *p = s_part[w][w == j ? 1 : 0].at;
+                join_part(m, l, v, p[kDecRows * D + r], p[kDecRows * (D + 1) + r],
+                          *reinterpret_cast<const float2 *>(p + r * D + c));
+            }
+            if (whole) {
+                write_out(a, G, pi.row0, pi.h, r, c, v, l);
+            } else {
+                __stcg(reinterpret_cast<float2 *>(out + r * D + c), v);
+                if (c == 0) {
+                    __stcg(out + kDecRows * D + r, m);
+                    __stcg(out + kDecRows * (D + 1) + r, l);
+                }
+            }
+        }
+        if (whole)
+            continue;
+        // the item goes over CTAs: the last to arrive joins their parts
+        __threadfence();
+        __syncthreads();
+        if (tid == 0)
+            s_last = atomicAdd(arrived + c_first, 1u) == static_cast<unsigned>(c_last - c_first);
+        __syncthreads();
+        if (!s_last)
+            continue;
+        __threadfence();
+        for (int e = tid; e < pi.nrows * (D / 2); e += kThreads) {
+            const int r = e / (D / 2), c = 2 * (e % (D / 2));
+            float m = -INFINITY, l = 0.f;
+            float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int k = c_first; k <= c_last; ++k) {
+                const float *p = cta_parts + (2 * (int64_t)k + (k == c_first ? 1 : 0)) * dec_part_floats(D);
+                join_part(m, l, v, __ldcg(p + kDecRows * D + r), __ldcg(p + kDecRows * (D + 1) + r),
+                          __ldcg(reinterpret_cast<const float2 *>(p + r * D + c)));
+            }
+            write_out(a, G, pi.row0, pi.h, r, c, v, l);
+        }
+        if (tid == 0)
+            arrived[c_first] = 0;  // for the next launch
+    }
+}
+
+template <int D>
+cudaError_t launch_rows(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream)
+{
+    constexpr int smem = dec_smem_bytes(D);
+    cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    const int sms = device_sm_count();
+    attend_rows_kernel<D><<<sms < kMaxCtas ? sms : kMaxCtas, 32 * kDecWarps, smem, stream>>>(
+        a, workspace, device_status_word());
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_tiles(const smoe_attention_args &a, cudaStream_t stream)
 {
     const int G = a.num_heads / a.cache.num_kv_heads;
     const int64_t tiles = ((int64_t)a.max_rows * G + kDecRows - 1) / kDecRows;
-    cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<D>,
+    cudaError_t e = cudaFuncSetAttribute(attend_tiles_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          dec_smem_bytes(D));
     if (e != cudaSuccess)
         return e;
     const dim3 grid(static_cast<unsigned>(tiles), a.cache.num_kv_heads, a.batch.num_seqs);
-    attend_rows_kernel<D><<<grid, 32 * kDecWarps, dec_smem_bytes(D), stream>>>(
+    attend_tiles_kernel<D><<<grid, 32 * kDecWarps, dec_smem_bytes(D), stream>>>(
         a, device_status_word());
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream)
+{
+    const int G = a.num_heads / a.cache.num_kv_heads;
+    return (int64_t)a.max_rows * G <= kDecRows ? launch_rows<D>(a, workspace, stream)
+                                               : launch_tiles<D>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, cudaStream_t stream)
 {
-    (void)workspace;
-    return a.cache.head_dim == 64 ? launch_rows<64>(a, stream) : launch_rows<128>(a, stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    return a.cache.head_dim == 64 ? launch<64>(a, ws, stream) : launch<128>(a, ws, stream);
 }
 
 }  // namespace smoe
