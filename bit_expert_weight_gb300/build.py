@@ -25,7 +25,7 @@ NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "
 
 LIBS = {
     "libsmoe.so": ["api.cu", "quant.cu", "repack.cu", "router.cu", "layer.cu", "grouped.cu", "noalloc.cu",
-                   "vault.cu", "decoder_api.cu", "rotary.cu", "attention.cu"],
+                   "vault.cu", "decoder_api.cu", "rotary.cu", "attention.cu", "attention_chunk.cu"],
     "libsmoe_synth.so": ["synth.cu"],
 }
 

@@ -1,0 +1,66 @@
+// attention.cuh -- what the attention kernels share: the sequences of a batch,
+// the keys that a row sees, and the layout of the workspace.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace smoe {
+
+// Workspace: one arrival counter per CTA (zero between launches), then the
+// parts of items that several CTAs share.
+constexpr size_t kPartsAt = 4096;
+constexpr int kMaxCounters = static_cast<int>(kPartsAt / sizeof(unsigned));
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A sequence of the batch as the kernels use it; an impossible one is
+// recorded and gets what is left of it in range.
+struct Seq {
+    int64_t row0;  // first row
+    int rows;      // new rows
+    int len;       // keys
+};
+
+__device__ __forceinline__ Seq seq_at(const smoe_attention_args &a, int b, int *status)
+{
+    Seq s;
+    const int r0 = a.batch.row_start[b], r1 = a.batch.row_start[b + 1];
+    s.row0 = r0;
+    s.rows = r1 - r0;
+    s.len = a.batch.kv_len[b];
+    bool bad = r0 < 0 || r1 < r0 || r1 > a.batch.num_rows || s.rows > a.max_rows || s.len < 0 ||
+               s.len > (int64_t)a.batch.table_stride * a.cache.page_size;
+    if (bad) {
+        set_status(status, kStatusBadArg);
+        s.row0 = 0;
+        s.rows = s.len = 0;
+    }
+    return s;
+}
+
+// Keys seen by new row `token` of s: [lo, hi).
+__device__ __forceinline__ void seen(const smoe_attention_args &a, const Seq &s, int token, int &lo,
+                                     int &hi)
+{
+    const int64_t i = (int64_t)s.len - s.rows + token;
+    hi = i + 1 > 0 ? static_cast<int>(i + 1) : 0;
+    lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+}
+
+__device__ __forceinline__ Seq seq_or_none(const smoe_attention_args &a, int b, int *status)
+{
+    Seq s;
+    s.row0 = 0;
+    s.rows = s.len = 0;
+    return b < a.batch.num_seqs ? seq_at(a, b, status) : s;
+}
+
+}  // namespace smoe

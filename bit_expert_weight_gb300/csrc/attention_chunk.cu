@@ -1,0 +1,922 @@
+// attention_chunk.cu -- attention of chunks of new rows over a paged cache on
+// the fifth-generation tensor cores (the mathematics: attention.cu).
+//
+// An item is one tile of 256 packed rows (row m of it: new row (m0 + m) / G,
+// head (m0 + m) % G of the kv head), as two halves A and B of 128, over the
+// keys that its rows see, 128 keys (a unit) at a time.  Per unit and half:
+//   S = Q K^T            tcgen05.mma, Q and K in shared memory, S in tensor
+//                        memory (128 lanes = rows, 128 columns = keys)
+//   P = exp2(S - m)      one thread per row: S from tensor memory to
+//                        registers, P as bf16 back over the S columns
+//   O += P V             tcgen05.mma, P from tensor memory, V in shared memory
+// The tensor cores work on one half while the threads of the other half
+// compute its exponentials.  m is the row's maximum when it was last raised:
+// it follows the true maximum only once that is more than 2^8 above it, so
+// that O is rescaled rarely; P is at most 2^8, its sum is kept in fp32 and the
+// final division by that sum makes the choice of m drop out.  P is rounded to
+// bf16 for the tensor cores (2^-9 of each p), the sum is not.
+//
+// Roles of the 12 warps of a CTA, one CTA per SM:
+//   warps 0..3  half A, warps 4..7 half B: queries into shared memory,
+//               softmax, rescaling, output
+//   warp 8      issues the MMAs
+//   warp 9      loads K and V by TMA, page by page, into a ring of 4 stages of
+//               128 keys (K and V alternating), 128-byte swizzle
+//   warps 10, 11  none
+// Work split: as in attention.cu, the items form a line of units, cut into
+// equal shares, one per CTA; parts of an item are joined by the last of its
+// CTAs to arrive.  Every wait is bounded; one that runs out is recorded as
+// SMOE_ERR_TIMEOUT and ends the CTA's work.
+#include <cuda.h>
+#include <math.h>
+
+#include "attention.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace smoe {
+
+namespace {
+
+constexpr int kHalf = 128;              // rows of a half (MMA M)
+constexpr int kTileRows2 = 2 * kHalf;   // packed rows of an item
+constexpr int kKeys = 128;              // keys of a unit (MMA N of Q K^T, K of P V)
+constexpr int kStages = 4;
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+// Three warpgroups: two of softmax warps, and one of the MMA and loading warps
+// and two idle ones, which hands registers over: 2 x 128 x 216 + 128 x 72 are
+// the 384 x 168 that the CTA is launched with.
+constexpr int kThreads = 384;
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
+static_assert(256 * kSoftRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
+constexpr int kItemUnits = 1;           // an item's own cost, in units
+constexpr int kMaxCtas = 240;
+constexpr float kRaise = 8.0f;          // log2 of how far the maximum may run ahead of m
+
+__host__ __device__ constexpr int q_half_bytes(int D) { return kHalf * D * 2; }
+__host__ __device__ constexpr int stage_bytes(int D) { return kKeys * D * 2; }
+__host__ __device__ constexpr int smem_bytes(int D)
+{
+    return 2 * q_half_bytes(D) + kStages * stage_bytes(D) + 1024;  // slack for the alignment
+}
+// A part: outputs [D][rows], then the rows' m, then their sums.
+__host__ __device__ constexpr int part_floats(int D) { return (D + 2) * kTileRows2; }
+static_assert(kPartsAt + (size_t)2 * kMaxCtas * part_floats(128) * 4 <= SMOE_ATTENTION_WORKSPACE_BYTES,
+              "workspace");
+static_assert(kMaxCtas <= kMaxCounters, "counters");
+
+// Tensor memory columns: S (and P over it) and O of each half.
+__device__ __forceinline__ constexpr uint32_t col_s(int half) { return half * kKeys; }
+template <int D>
+__device__ __forceinline__ constexpr uint32_t col_o(int half)
+{
+    return 2 * kKeys + half * D;
+}
+
+struct Smem {
+    uint64_t kv_full[kStages];   // loader: 1 arrival + bytes
+    uint64_t kv_empty[kStages];  // 1 MMA commit
+    uint64_t q_full[2];          // 4 warps
+    uint64_t s_full[2];          // 1 MMA commit
+    uint64_t p_full[2][2];       // 4 warps: keys 0..63, 64..127
+    uint64_t o_full[2];          // 1 MMA commit
+    uint64_t joined;             // 8 warps
+    uint64_t drain;              // final MMA commit
+    uint32_t tmem_base;
+    uint32_t last_fill[kStages]; // 1 + last use filled, per stage (drain after a failure)
+    int fail, last;
+    // the work split
+    int64_t scan[kThreads / 32];
+    int scan_max[kThreads / 32];
+    int64_t q, total, before;    // units per CTA, in all, before the CTA's first item's tile
+    int b, t;                    // that tile
+    int tiles[SMOE_MAX_SEQS + 1];  // tiles of the sequences before each
+};
+
+// ------------------------------------------------------------ PTX helpers
+
+// Shared-memory matrix descriptor: operand with its M or N dimension
+// contiguous (64 elements = 128 bytes, 128-byte swizzle), 8 rows of K per
+// 1024-byte atom; the next 64 elements of M or N lie `lead` bytes on.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr, uint32_t lead)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(lead >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// Instruction descriptors of kind::f16, bf16 in, fp32 out, M = 128: Q K^T
+// (both K-major, N = keys) and P V (V with N = channels contiguous).
+constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kHalf >> 4) << 24);
+constexpr uint32_t kIdescQK = kIdescBase | ((uint32_t)(kKeys >> 3) << 17);
+template <int D>
+__device__ __forceinline__ constexpr uint32_t idesc_pv()
+{
+    return kIdescBase | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+#define SMOE_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+                      "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define SMOE_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), \
+                      "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+#define SMOE_U8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), \
+                      "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+
+// 32 lanes x 32 consecutive columns of tensor memory into r[0..31].
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : SMOE_R8(r, 0), SMOE_R8(r, 8), SMOE_R8(r, 16), SMOE_R8(r, 24)
+                 : "r"(addr));
+}
+// No use of r[0..31] moves above this point.
+__device__ __forceinline__ void pin32(uint32_t *r)
+{
+    asm volatile("" : SMOE_U8(r, 0), SMOE_U8(r, 8));
+    asm volatile("" : SMOE_U8(r, 16), SMOE_U8(r, 24));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SMOE_W8(r, 0),
+                 SMOE_W8(r, 8), SMOE_W8(r, 16), SMOE_W8(r, 24), "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SMOE_W8(r, 0),
+                 SMOE_W8(r, 8), "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Bounded wait that records a timeout in the CTA's fail flag.
+__device__ __forceinline__ bool wait_for(Smem &sm, uint64_t *bar, unsigned parity, int *status)
+{
+    if (mbar_test_wait(bar, parity))
+        return true;
+    if (*reinterpret_cast<volatile int *>(&sm.fail))
+        return false;
+    if (mbar_wait_bounded(bar, parity))
+        return true;
+    set_status(status, kStatusTimeout);
+    *reinterpret_cast<volatile int *>(&sm.fail) = 1;
+    return false;
+}
+
+// ------------------------------------------------------------ work split
+
+// A tile of a sequence's packed rows, and a place on the line of units.
+struct Tile {
+    Seq s, next;        // its sequence, and the one after it (loaded early)
+    int b, t, h;
+    int m0, rows;       // first packed row, packed rows (256 at most; 0: no tile)
+    int units;
+    int64_t at;         // its first unit on the line
+    int k_lo, k_hi;     // keys seen by any of its rows; unit 0 begins at kbase
+    int t_lo, t_hi;     // keys seen by every row
+    int kbase;
+};
+
+__device__ __forceinline__ void tile_keys(const smoe_attention_args &a, int G, Tile &c)
+{
+    c.m0 = c.t * kTileRows2;
+    const int left = c.s.rows * G - c.m0;
+    c.rows = left < kTileRows2 ? (left > 0 ? left : 0) : kTileRows2;
+    c.k_lo = c.k_hi = c.t_lo = c.t_hi = 0;
+    if (c.rows > 0) {
+        seen(a, c.s, c.m0 / G, c.k_lo, c.t_hi);
+        seen(a, c.s, (c.m0 + c.rows - 1) / G, c.t_lo, c.k_hi);
+    }
+    c.kbase = c.k_lo / kKeys * kKeys;
+    const int n = (c.k_hi - c.kbase + kKeys - 1) / kKeys;
+    // rows that see nothing still take a unit: they get their zeros
+    c.units = c.rows == 0 ? 0 : (n > 1 ? n : 1);
+}
+
+// To the next item; past the last one it has no rows.
+__device__ __forceinline__ void tile_next(const smoe_attention_args &a, int G, Tile &c, int *status)
+{
+    c.at += c.units + kItemUnits;
+    if (++c.h < a.cache.num_kv_heads)
+        return;
+    c.h = 0;
+    ++c.t;
+    tile_keys(a, G, c);
+    while (c.rows == 0 && c.b < a.batch.num_seqs) {
+        ++c.b;
+        c.s = c.next;
+        c.next = seq_or_none(a, c.b + 1, status);
+        c.t = 0;
+        tile_keys(a, G, c);
+    }
+}
+
+// Units [u0, u1) of the item that lie in the share [w0, w1).
+__device__ __forceinline__ void units_in(const Tile &c, int64_t w0, int64_t w1, int &u0, int &u1)
+{
+    const int64_t k = c.at + kItemUnits;
+    u0 = w0 > k ? static_cast<int>(w0 - k) : 0;
+    u1 = w1 - k < c.units ? static_cast<int>(w1 - k) : c.units;
+}
+
+__device__ __forceinline__ int tiles_of(const Seq &s, int G) { return (s.rows * G + kTileRows2 - 1) / kTileRows2; }
+
+// Exclusive sum of v over the CTA's threads; total and maximum of all.
+__device__ __forceinline__ int64_t scan_all(Smem &sm, int64_t v, int &mx, int64_t &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        incl += lane >= o ? x : 0;
+        const int m = __shfl_xor_sync(0xffffffffu, mx, o);
+        mx = m > mx ? m : mx;
+    }
+    __syncthreads();
+    if (lane == 31)
+        sm.scan[warp] = incl;
+    if (lane == 0)
+        sm.scan_max[warp] = mx;
+    __syncthreads();
+    int64_t before = incl - v;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? sm.scan[w] : 0;
+        total += sm.scan[w];
+        mx = sm.scan_max[w] > mx ? sm.scan_max[w] : mx;
+    }
+    return before;
+}
+
+// The CTA's share, into shared memory: q, total, and the tile at its start.
+__device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, Smem &sm, int *status)
+{
+    const int tid = threadIdx.x, n = a.batch.num_seqs, Hkv = a.cache.num_kv_heads;
+    // tiles before each sequence
+    const int per = (n + kThreads - 1) / kThreads;
+    int64_t sum = 0, total;
+    int mx = 0;
+    for (int b = tid * per; b < n && b < (tid + 1) * per; ++b)
+        sum += tiles_of(seq_at(a, b, status), G);
+    int64_t before = scan_all(sm, sum, mx, total);
+    for (int b = tid * per; b < n && b < (tid + 1) * per; ++b) {
+        sm.tiles[b] = static_cast<int>(before);
+        before += tiles_of(seq_at(a, b, status), G);
+    }
+    const int all = static_cast<int>(total);
+    if (tid == 0)
+        sm.tiles[n] = all;
+    __syncthreads();
+    // units of the tiles [i0, i1) of this thread
+    const int pt = (all + kThreads - 1) / kThreads;
+    const int i0 = tid * pt < all ? tid * pt : all, i1 = i0 + pt < all ? i0 + pt : all;
+    Tile c;
+    int b0 = 0, hi = n - 1;
+    while (b0 < hi) {  // last sequence with tiles[b] <= i0
+        const int mid = (b0 + hi + 1) >> 1;
+        if (sm.tiles[mid] <= i0)
+            b0 = mid;
+        else
+            hi = mid - 1;
+    }
+    sum = 0;
+    for (int i = i0, b = b0; i < i1; ++i) {
+        if (i == i0 || i >= sm.tiles[b + 1]) {
+            while (i >= sm.tiles[b + 1])
+                ++b;
+            c.s = seq_at(a, b, status);
+        }
+        c.t = i - sm.tiles[b];
+        tile_keys(a, G, c);
+        sum += c.units + kItemUnits;
+        mx = c.units > mx ? c.units : mx;
+    }
+    before = scan_all(sm, sum, mx, total) * Hkv;
+    total *= Hkv;
+    // Equal shares, but no item in so many parts that the joining costs more
+    // than the sharing saves: reading a part takes about as long as a unit.
+    int64_t q = ceil_div(total, gridDim.x);
+    const int64_t least = static_cast<int64_t>(sqrtf(static_cast<float>(mx)));
+    q = q > least ? q : least;
+    const int64_t w0 = q * blockIdx.x;
+    if (tid == 0) {
+        sm.q = q;
+        sm.total = total;
+    }
+    if (w0 >= before && w0 < before + sum * Hkv) {
+        for (int i = i0, b = b0; i < i1; ++i) {
+            if (i == i0 || i >= sm.tiles[b + 1]) {
+                while (i >= sm.tiles[b + 1])
+                    ++b;
+                c.s = seq_at(a, b, status);
+            }
+            c.t = i - sm.tiles[b];
+            tile_keys(a, G, c);
+            const int64_t next = before + (int64_t)(c.units + kItemUnits) * Hkv;
+            if (w0 >= before && w0 < next) {
+                sm.b = b;
+                sm.t = c.t;
+                sm.before = before;
+            }
+            before = next;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, const Smem &sm, int64_t w0,
+                                           int *status)
+{
+    Tile c;
+    c.b = sm.b;
+    c.t = sm.t;
+    c.s = seq_or_none(a, c.b, status);
+    c.next = seq_or_none(a, c.b + 1, status);
+    tile_keys(a, G, c);
+    const int len = c.units + kItemUnits;
+    c.h = static_cast<int>((w0 - sm.before) / len);
+    c.at = sm.before + (int64_t)c.h * len;
+    return c;
+}
+
+// ------------------------------------------------------------ roles
+
+struct Maps {
+    CUtensorMap k, v;  // (channels, slots, kv heads, pages), boxes of 64 x box_rows x 1 x 1
+};
+
+// Keys and values of every unit, K and V in turn (warp 9).  A lane copies one
+// 64-channel half of one page's share of the unit.  Slots past the keys that
+// the item sees are not copied page by page; what remains of their pages is
+// cleared before the product with V.
+template <int D>
+__device__ void loader(const smoe_attention_args &a, int G, const Maps *maps, Smem &sm, uint8_t *ring,
+                       int64_t w0, int64_t w1, int *status)
+{
+    const int lane = threadIdx.x & 31, page = a.cache.page_size;
+    const int box = page < kKeys ? page : kKeys, boxes = kKeys / box;
+    const int i = lane / (D / 64), half = lane % (D / 64);
+    uint32_t it = 0;
+    for (Tile c = first_tile(a, G, sm, w0, status); c.rows > 0 && c.at < w1; tile_next(a, G, c, status)) {
+        int u0, u1;
+        units_in(c, w0, w1, u0, u1);
+        for (int u = u0; u < u1; ++u) {
+            const int k0 = c.kbase + u * kKeys + i * box;
+            bool on = i < boxes && k0 < c.k_hi && k0 + box > c.k_lo;
+            int pg = 0;
+            if (on) {
+                pg = a.batch.page_table[(int64_t)c.b * a.batch.table_stride + k0 / page];
+                if (pg < 0 || pg >= a.cache.num_pages) {
+                    set_status(status, kStatusBadArg);
+                    on = false;
+                }
+            }
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, on)) * box * 128u;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++it) {
+                const int s = it % kStages;
+                if (!__all_sync(0xffffffffu,
+                                wait_for(sm, &sm.kv_empty[s], ((it / kStages) & 1u) ^ 1u, status)))
+                    return;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm.kv_full[s], bytes);
+                    sm.last_fill[s] = it + 1;
+                }
+                __syncwarp();
+                if (on)
+                    tma_load_4d(ring + s * stage_bytes(D) + half * (kKeys * 128) + i * box * 128,
+                                kv == 0 ? &maps->k : &maps->v, 64 * half, k0 % page, c.h, pg,
+                                &sm.kv_full[s]);
+            }
+        }
+    }
+}
+
+// Zero the rows of a V stage whose keys the item does not see: their slots
+// may hold anything, and 0 x NaN is NaN.
+template <int D>
+__device__ __forceinline__ void clear_unseen(uint8_t *stage, int key0, int lo, int hi)
+{
+    const int lane = threadIdx.x & 31;
+    for (int r = 0; r < kKeys; ++r) {
+        if (key0 + r >= lo && key0 + r < hi)
+            continue;
+        if (lane < D / 8)
+            *reinterpret_cast<uint4 *>(stage + (lane / 8) * (kKeys * 128) + r * 128 + (lane % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
+// The MMAs (warp 8; lane 0 issues).
+template <int D>
+__device__ void mma_issuer(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, uint8_t *ring,
+                           int64_t w0, int64_t w1, int *status)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t tb = sm.tmem_base;
+    const uint64_t qd = sw128_desc(smem_u32(sq)), kd = sw128_desc(smem_u32(ring));
+    const uint64_t vd = sw128_desc_mn(smem_u32(ring), kKeys * 128);
+    uint32_t it = 0;                // ring uses
+    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // items and units of each half
+    auto ok = [&](uint64_t *bar, unsigned parity) {
+        return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
+    };
+    // S of a half from the K stage s
+    auto qk = [&](int half, int s) {
+        if (lane == 0) {
+            const uint64_t ad = qd + (uint64_t)(half * (q_half_bytes(D) >> 4));
+            const uint64_t bd = kd + (uint64_t)(s * (stage_bytes(D) >> 4));
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                // 16 channels: 32 bytes inside a 64-channel half, which is 16 KB
+                const uint64_t off = (uint64_t)((k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2);
+                mma_ss(tb + col_s(half), ad + off, bd + off, kIdescQK, k > 0);
+            }
+            umma_commit(&sm.s_full[half]);
+        }
+        __syncwarp();
+    };
+    for (Tile c = first_tile(a, G, sm, w0, status); c.rows > 0 && c.at < w1; tile_next(a, G, c, status)) {
+        int u0, u1;
+        units_in(c, w0, w1, u0, u1);
+        if (u0 >= u1)
+            continue;
+        const int halves = c.rows > kHalf ? 2 : 1;
+        // the first K, both halves
+        int s = it % kStages;
+        if (!ok(&sm.kv_full[s], (it / kStages) & 1u))
+            return;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half >= halves)
+                break;
+            if (!ok(&sm.q_full[half], qn[half]++ & 1u))
+                return;
+            tc_fence_after();
+            qk(half, s);
+        }
+        if (lane == 0)
+            umma_commit(&sm.kv_empty[s]);
+        ++it;
+        for (int u = u0; u < u1; ++u) {
+            const bool last = u + 1 == u1;
+            const int sv = it % kStages, sk = (it + 1) % kStages;
+            if (!ok(&sm.kv_full[sv], (it / kStages) & 1u))
+                return;
+            const int key0 = c.kbase + u * kKeys;
+            if (key0 < c.k_lo || key0 + kKeys > c.k_hi)
+                clear_unseen<D>(ring + sv * stage_bytes(D), key0, c.k_lo, c.k_hi);
+            if (!last && !ok(&sm.kv_full[sk], ((it + 1) / kStages) & 1u))
+                return;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (half >= halves)
+                    break;
+#pragma unroll
+                for (int ph = 0; ph < 2; ++ph) {
+                    if (!ok(&sm.p_full[half][ph], pn[half] & 1u))
+                        return;
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 4 * ph; k < 4 * ph + 4; ++k)  // 16 keys each
+                            mma_ts(tb + col_o<D>(half), tb + col_s(half) + 8 * k,
+                                   vd + (uint64_t)(sv * (stage_bytes(D) >> 4) + k * (16 * 128 >> 4)),
+                                   idesc_pv<D>(), u > u0 || k > 0);
+                    }
+                }
+                ++pn[half];
+                if (half == halves - 1 && lane == 0)
+                    umma_commit(&sm.kv_empty[sv]);
+                if (!last)
+                    qk(half, sk);
+                else if (lane == 0)
+                    umma_commit(&sm.o_full[half]);
+                __syncwarp();
+            }
+            if (!last && lane == 0)
+                umma_commit(&sm.kv_empty[sk]);
+            it += last ? 1 : 2;
+        }
+    }
+}
+
+// Queries, softmax and output of half `half` (warps 4 half .. 4 half + 3).
+template <int D>
+__device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, float *parts,
+                        unsigned *arrived, int half, int64_t w0, int64_t w1, int *status)
+{
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const int r = 32 * quarter + lane;  // row of the half, lane of tensor memory
+    const uint32_t tl = sm.tmem_base + (static_cast<uint32_t>(32 * quarter) << 16);
+    const float sc = a.scale * 1.44269504088896341f;
+    uint32_t items = 0, sn = 0, jn = 0;  // items and units of this half, joins
+    auto ok = [&](uint64_t *bar, unsigned parity) {
+        return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
+    };
+    for (Tile c = first_tile(a, G, sm, w0, status); c.rows > 0 && c.at < w1; tile_next(a, G, c, status)) {
+        int u0, u1;
+        units_in(c, w0, w1, u0, u1);
+        if (u0 >= u1)
+            continue;
+        const int m = kHalf * half + r;         // row of the item
+        const bool on = m < c.rows;
+        const bool active = c.rows > kHalf * half;  // the half has rows
+        const int64_t token = c.s.row0 + (c.m0 + m) / G;
+        const int head = c.h * G + (c.m0 + m) % G;
+        int lo = 0, hi = 0;
+        if (on)
+            seen(a, c.s, (c.m0 + m) / G, lo, hi);
+        float mr = -INFINITY, sum = 0.f;
+        if (active) {
+            // queries, swizzled; the last S of the item before is done, and
+            // with it every read of the old queries
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
+                                                               token * a.q_row_stride +
+                                                               (int64_t)head * a.q_head_stride);
+            uint8_t *dst = sq + half * q_half_bytes(D) + r * 128;
+            uint4 v[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                v[i] = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<uint4 *>(dst + (i / 8) * (kHalf * 128) + (((i % 8) ^ (r & 7)) << 4)) = v[i];
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.q_full[half]);
+            for (int u = u0; u < u1; ++u, ++sn) {
+                if (!ok(&sm.s_full[half], sn & 1u))
+                    return;
+                tc_fence_after();
+                uint32_t s[kKeys];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld32(tl + col_s(half) + 32 * i, s + 32 * i);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pin32(s + 32 * i);
+                const int key0 = c.kbase + u * kKeys;
+                if (key0 < c.t_lo || key0 + kKeys > c.t_hi) {
+                    const int first = lo - key0, end = hi - key0;
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+                        if (i < first || i >= end)
+                            s[i] = 0xff800000u;  // -infinity
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+                for (int i = 4; i < kKeys; ++i)
+                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                const bool raise = top > mr + kRaise;
+                if (__any_sync(0xffffffffu, raise)) {
+                    // to the maximum; other rows of the warp keep theirs, so
+                    // that a row's result does not depend on its neighbours
+                    const float mn = raise ? top : mr;
+                    const float f = raise ? ex2(mr - mn) : 1.f;
+                    mr = mn;
+                    sum *= f;
+                    if (u > u0) {
+#pragma unroll
+                        for (int i = 0; i < D; i += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tl + col_o<D>(half) + i, o);
+                            tmem_wait_ld();
+                            pin32(o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st32(tl + col_o<D>(half) + i, o);
+                        }
+                    }
+                }
+                const float mu = mr == -INFINITY ? 0.f : mr;  // a row that has seen nothing yet
+                const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
+                uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+                for (int ph = 0; ph < 2; ++ph) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = 64 * ph + 32 * q + 2 * i;
+                            float x, y;
+                            unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, mu2), x, y);
+                            x = ex2(x);
+                            y = ex2(y);
+                            acc[i & 1] = add2(acc[i & 1], pair(x, y));
+                            p[i] = pack_bf16x2(x, y);
+                        }
+                        tmem_st16(tl + col_s(half) + 32 * ph + 16 * q, p);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.p_full[half][ph]);
+                }
+                float x, y;
+                unpair(add2(acc[0], acc[1]), x, y);
+                sum += x + y;
+            }
+            if (!ok(&sm.o_full[half], items++ & 1u))
+                return;
+            tc_fence_after();
+        }
+        const int64_t k = c.at + kItemUnits;
+        const int c_first = static_cast<int>(k / sm.q), c_last = static_cast<int>((k + c.units - 1) / sm.q);
+        const bool whole = c_first == c_last;
+        auto write_out = [&](int col, const float *v, float inv) {  // 16 columns
+            const int64_t at = token * a.out_row_stride + (int64_t)head * a.out_head_stride + col;
+            if (a.out_dtype == SMOE_F32) {
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
+                                         v[4 * i + 3] * inv);
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv),
+                                        pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                        pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                                        pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+            }
+        };
+        float *part = parts + (2 * (int64_t)blockIdx.x + (static_cast<int>(blockIdx.x) == c_first ? 1 : 0)) *
+                                  part_floats(D);
+        if (active) {
+            const float inv = sum > 0.f ? 1.0f / sum : 0.f;  // a row that sees no key: zeros
+            for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tmem_ld16(tl + col_o<D>(half) + i, o);
+                tmem_wait_ld();
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    asm volatile("" : "+r"(o[j]));
+                    v[j] = __uint_as_float(o[j]);
+                }
+                if (whole) {
+                    if (on)
+                        write_out(i, v, inv);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        __stcg(part + (i + j) * kTileRows2 + m, v[j]);
+                }
+            }
+            if (!whole) {
+                __stcg(part + D * kTileRows2 + m, mr);
+                __stcg(part + (D + 1) * kTileRows2 + m, sum);
+            }
+            // the output is read before the next item's P lets P V overwrite it
+            tc_fence_before();
+        }
+        if (whole)
+            continue;
+        // ---- the last of the item's CTAs to arrive joins its parts
+        __threadfence();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sm.joined);
+        if (!ok(&sm.joined, jn & 1u))
+            return;
+        ++jn;
+        if (threadIdx.x == 0)
+            sm.last = atomicAdd(arrived + c_first, 1u) == static_cast<unsigned>(c_last - c_first);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sm.joined);
+        if (!ok(&sm.joined, jn & 1u))
+            return;
+        ++jn;
+        if (*reinterpret_cast<volatile int *>(&sm.last)) {
+            __threadfence();
+            if (active && on) {
+                float mj = -INFINITY, lj = 0.f;
+                for (int j = c_first; j <= c_last; ++j) {
+                    const float *p = parts + (2 * (int64_t)j + (j == c_first ? 1 : 0)) * part_floats(D);
+                    const float pm = __ldcg(p + D * kTileRows2 + m), pl = __ldcg(p + (D + 1) * kTileRows2 + m);
+                    const float mn = fmaxf(mj, pm);
+                    if (mn != -INFINITY)
+                        lj = lj * ex2(mj - mn) + pl * ex2(pm - mn);
+                    mj = mn;
+                }
+                const float inv = lj > 0.f ? 1.0f / lj : 0.f;
+                for (int i = 0; i < D; i += 16) {
+                    float v[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        v[e] = 0.f;
+                    for (int j = c_first; j <= c_last; ++j) {
+                        const float *p = parts + (2 * (int64_t)j + (j == c_first ? 1 : 0)) * part_floats(D);
+                        const float f = mj == -INFINITY ? 0.f : ex2(__ldcg(p + D * kTileRows2 + m) - mj);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            v[e] = fmaf(__ldcg(p + (i + e) * kTileRows2 + m), f, v[e]);
+                    }
+                    write_out(i, v, inv);
+                }
+            }
+            if (threadIdx.x == 0)
+                arrived[c_first] = 0;  // for the next launch
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_chunk_kernel(const smoe_attention_args a, const __grid_constant__ Maps maps, uint8_t *workspace,
+                        int *status)
+{
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Smem sm;
+    uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sq = base, *ring = base + 2 * q_half_bytes(D);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.num_heads / a.cache.num_kv_heads;
+    if (tid == 0) {
+        sm.fail = 0;
+        sm.b = a.batch.num_seqs;
+        sm.t = 0;
+        sm.before = 0;
+        for (int i = 0; i < kStages; ++i) {
+            sm.last_fill[i] = 0;
+            mbar_init(&sm.kv_full[i], 1);
+            mbar_init(&sm.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i][0], 4);
+            mbar_init(&sm.p_full[i][1], 4);
+            mbar_init(&sm.o_full[i], 1);
+        }
+        mbar_init(&sm.joined, kSoftWarps);
+        mbar_init(&sm.drain, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    find_share(a, G, sm, status);
+    const int64_t w0 = sm.q * blockIdx.x;
+    if (w0 >= sm.total)
+        return;  // nothing for this CTA
+    const int64_t w1 = w0 + sm.q;
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sm.tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        softmax<D>(a, G, sm, sq, reinterpret_cast<float *>(workspace + kPartsAt),
+                   reinterpret_cast<unsigned *>(workspace), warp >> 2, w0, w1, status);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kLoadWarp) {
+            loader<D>(a, G, &maps, sm, ring, w0, w1, status);
+        } else if (warp == kMmaWarp) {
+            mma_issuer<D>(a, G, sm, sq, ring, w0, w1, status);
+            __syncwarp();
+            if (lane == 0) {
+                // every MMA issued so far has completed once this commit lands
+                umma_commit(&sm.drain);
+                if (!mbar_wait_bounded(&sm.drain, 0)) {
+                    set_status(status, kStatusTimeout);
+                    *reinterpret_cast<volatile int *>(&sm.fail) = 1;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    // After a failure copies may be left unwaited: the loader waits (bounded)
+    // for the last fill of every stage, so that none is in flight at the end.
+    if (*reinterpret_cast<volatile int *>(&sm.fail) && warp == kLoadWarp && lane < kStages) {
+        const uint32_t last = sm.last_fill[lane];
+        if (last > 0 && !mbar_wait_bounded(&sm.kv_full[lane], ((last - 1) / kStages) & 1u))
+            set_status(status, kStatusTimeout);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem_base), "r"(512)
+                     : "memory");
+    }
+}
+
+// ------------------------------------------------------------ host side
+
+// Tensor map of one of the cache's halves: (channels, slots, kv heads, pages),
+// read in boxes of 64 channels x box_rows slots.
+bool page_map(CUtensorMap *m, const void *pages, const smoe_kv_cache &c, int64_t page_stride, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.num_kv_heads), static_cast<cuuint64_t>(c.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.head_dim) * 2,
+                                   static_cast<cuuint64_t>(c.page_size) * c.head_dim * 2,
+                                   static_cast<cuuint64_t>(page_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pages), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream)
+{
+    Maps maps;
+    const int box = a.cache.page_size < kKeys ? a.cache.page_size : kKeys;
+    if (!page_map(&maps.k, a.cache.k_pages, a.cache, a.cache.k_page_stride, box) ||
+        !page_map(&maps.v, a.cache.v_pages, a.cache, a.cache.v_page_stride, box))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attend_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         smem_bytes(D));
+    if (e != cudaSuccess)
+        return e;
+    const int sms = device_sm_count();
+    attend_chunk_kernel<D><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, smem_bytes(D), stream>>>(
+        a, maps, workspace, device_status_word());
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream)
+{
+    return a.cache.head_dim == 64 ? launch<64>(a, workspace, stream) : launch<128>(a, workspace, stream);
+}
+
+}  // namespace smoe

@@ -198,6 +198,8 @@ cudaError_t launch_grouped(const GroupedArgs &a, const void *x, int x_bf16, floa
 cudaError_t launch_rope(const smoe_rope_args &a, cudaStream_t stream);
 cudaError_t launch_kv_append(const smoe_kv_append_args &a, cudaStream_t stream);
 cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, cudaStream_t stream);
+// chunks of rows, on the tensor cores (attention_chunk.cu)
+cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream);
 
 int layer_grid_ctas_max();
 cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream);
