@@ -46,13 +46,18 @@ __device__ __forceinline__ Seq seq_at(const smoe_attention_args &a, int b, int *
     return s;
 }
 
-// Keys seen by new row `token` of s: [lo, hi).
+// Keys seen by a row with key index i (negative: none): [lo, hi).
+__device__ __forceinline__ void seen_from(const smoe_attention_args &a, int i, int &lo, int &hi)
+{
+    hi = i >= 0 ? i + 1 : 0;
+    lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+}
+
+// Keys seen by new row `token` of s.
 __device__ __forceinline__ void seen(const smoe_attention_args &a, const Seq &s, int token, int &lo,
                                      int &hi)
 {
-    const int64_t i = (int64_t)s.len - s.rows + token;
-    hi = i + 1 > 0 ? static_cast<int>(i + 1) : 0;
-    lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+    seen_from(a, s.len - s.rows + token, lo, hi);
 }
 
 __device__ __forceinline__ Seq seq_or_none(const smoe_attention_args &a, int b, int *status)

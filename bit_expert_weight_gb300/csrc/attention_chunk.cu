@@ -17,12 +17,14 @@
 // bf16 for the tensor cores (2^-9 of each p), the sum is not.
 //
 // Roles of the 12 warps of a CTA, one CTA per SM:
-//   warps 0..3  half A, warps 4..7 half B: queries into shared memory,
-//               softmax, rescaling, output
+//   warps 0..3  half A, warps 4..7 half B: softmax, rescaling, output
 //   warp 8      issues the MMAs
 //   warp 9      loads K and V by TMA, page by page, into a ring of 4 stages of
 //               128 keys (K and V alternating), 128-byte swizzle
-//   warps 10, 11  none
+//   warp 10     walks the line of items and hands them to the other warps
+//               through a ring of records in shared memory
+//   warp 11     loads the queries, as soon as the products with the ones
+//               before are done
 // Work split: as in attention.cu, the items form a line of units, cut into
 // equal shares, one per CTA; parts of an item are joined by the last of its
 // CTAs to arrive.  Every wait is bounded; one that runs out is recorded as
@@ -45,13 +47,10 @@ constexpr int kKeys = 128;              // keys of a unit (MMA N of Q K^T, K of 
 constexpr int kStages = 4;
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-// Three warpgroups: two of softmax warps, and one of the MMA and loading warps
-// and two idle ones, which hands registers over: 2 x 128 x 216 + 128 x 72 are
-// the 384 x 168 that the CTA is launched with.
+constexpr int kItemWarp = 10, kQueryWarp = 11;
+constexpr int kItemSlots = 4;
 constexpr int kThreads = 384;
-constexpr int kSoftRegs = 216, kOtherRegs = 72;
-static_assert(256 * kSoftRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
-constexpr int kItemUnits = 1;           // an item's own cost, in units
+constexpr int kItemUnits = 2;           // an item's own cost, in units
 constexpr int kMaxCtas = 240;
 constexpr float kRaise = 8.0f;          // log2 of how far the maximum may run ahead of m
 
@@ -75,10 +74,26 @@ __device__ __forceinline__ constexpr uint32_t col_o(int half)
     return 2 * kKeys + half * D;
 }
 
+// One item, or the part of it in the CTA's share, as the item warp hands it
+// on.  rows 0: there are no more.
+struct Item {
+    int64_t row0;           // the sequence's first row
+    int b, h, m0, rows;     // sequence, kv head, first packed row, packed rows
+    int i0;                 // key index of the sequence's first new row
+    int u0, u1, kbase;      // units; unit u begins at key kbase + 128 u
+    int k_lo, k_hi;         // keys seen by any of the rows
+    int t_lo, t_hi;         // keys seen by every row
+    int c_first, c_last;    // the CTAs that share the item
+};
+
 struct Smem {
+    uint64_t item_full[kItemSlots];   // item warp
+    uint64_t item_empty[kItemSlots];  // the 8 softmax warps, MMA warp, both loading warps
+    Item item[kItemSlots];
     uint64_t kv_full[kStages];   // loader: 1 arrival + bytes
     uint64_t kv_empty[kStages];  // 1 MMA commit
-    uint64_t q_full[2];          // 4 warps
+    uint64_t q_full[2];          // query warp
+    uint64_t q_empty[2];         // 1 MMA commit
     uint64_t s_full[2];          // 1 MMA commit
     uint64_t p_full[2][2];       // 4 warps: keys 0..63, 64..127
     uint64_t o_full[2];          // 1 MMA commit
@@ -157,14 +172,6 @@ __device__ __forceinline__ void pin32(uint32_t *r)
 {
     asm volatile("" : SMOE_U8(r, 0), SMOE_U8(r, 8));
     asm volatile("" : SMOE_U8(r, 16), SMOE_U8(r, 24));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SMOE_W8(r, 0),
-                 SMOE_W8(r, 8), SMOE_W8(r, 16), SMOE_W8(r, 24), "r"(addr)
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
 {
@@ -392,6 +399,64 @@ __device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, 
 
 // ------------------------------------------------------------ roles
 
+// The items of the CTA's share, in order (warp 10).
+__device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64_t w0, int64_t w1, int *status)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t n = 0;
+    for (Tile c = first_tile(a, G, sm, w0, status);; tile_next(a, G, c, status)) {
+        const bool end = c.rows == 0 || c.at >= w1;
+        int u0 = 0, u1 = 0;
+        if (!end) {
+            units_in(c, w0, w1, u0, u1);
+            if (u0 >= u1)
+                continue;
+        }
+        const int slot = n % kItemSlots;
+        if (!__all_sync(0xffffffffu, wait_for(sm, &sm.item_empty[slot], ((n / kItemSlots) & 1u) ^ 1u, status)))
+            return;
+        if (lane == 0) {
+            Item &t = sm.item[slot];
+            const int64_t k = c.at + kItemUnits;
+            t.row0 = c.s.row0;
+            t.b = c.b;
+            t.h = c.h;
+            t.m0 = c.m0;
+            t.rows = end ? 0 : c.rows;
+            t.i0 = c.s.len - c.s.rows;
+            t.u0 = u0;
+            t.u1 = u1;
+            t.kbase = c.kbase;
+            t.k_lo = c.k_lo;
+            t.k_hi = c.k_hi;
+            t.t_lo = c.t_lo;
+            t.t_hi = c.t_hi;
+            t.c_first = static_cast<int>(k / sm.q);
+            t.c_last = static_cast<int>((k + c.units - 1) / sm.q);
+            mbar_arrive(&sm.item_full[slot]);
+        }
+        __syncwarp();
+        ++n;
+        if (end)
+            return;
+    }
+}
+
+// The next item of a role (n counts them).  False: there are no more, or a
+// wait ran out.
+__device__ __forceinline__ bool next_item(Smem &sm, uint32_t &n, Item &t, int *status)
+{
+    const int slot = n % kItemSlots;
+    if (!__all_sync(0xffffffffu, wait_for(sm, &sm.item_full[slot], (n / kItemSlots) & 1u, status)))
+        return false;
+    t = sm.item[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(&sm.item_empty[slot]);
+    ++n;
+    return t.rows > 0;
+}
+
 struct Maps {
     CUtensorMap k, v;  // (channels, slots, kv heads, pages), boxes of 64 x box_rows x 1 x 1
 };
@@ -401,17 +466,15 @@ struct Maps {
 // the item sees are not copied page by page; what remains of their pages is
 // cleared before the product with V.
 template <int D>
-__device__ void loader(const smoe_attention_args &a, int G, const Maps *maps, Smem &sm, uint8_t *ring,
-                       int64_t w0, int64_t w1, int *status)
+__device__ void loader(const smoe_attention_args &a, const Maps *maps, Smem &sm, uint8_t *ring, int *status)
 {
     const int lane = threadIdx.x & 31, page = a.cache.page_size;
     const int box = page < kKeys ? page : kKeys, boxes = kKeys / box;
     const int i = lane / (D / 64), half = lane % (D / 64);
-    uint32_t it = 0;
-    for (Tile c = first_tile(a, G, sm, w0, status); c.rows > 0 && c.at < w1; tile_next(a, G, c, status)) {
-        int u0, u1;
-        units_in(c, w0, w1, u0, u1);
-        for (int u = u0; u < u1; ++u) {
+    uint32_t it = 0, n = 0;
+    Item c;
+    while (next_item(sm, n, c, status)) {
+        for (int u = c.u0; u < c.u1; ++u) {
             const int k0 = c.kbase + u * kKeys + i * box;
             bool on = i < boxes && k0 < c.k_hi && k0 + box > c.k_lo;
             int pg = 0;
@@ -443,6 +506,50 @@ __device__ void loader(const smoe_attention_args &a, int G, const Maps *maps, Sm
     }
 }
 
+// The queries of every item (warp 11): row r of a half as it is packed, into
+// the swizzled layout the MMA reads; rows past the item's are zeros.
+template <int D>
+__device__ void query_loader(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, int *status)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes per row, rows per round
+    uint32_t n = 0, qn[2] = {0, 0};
+    Item c;
+    while (next_item(sm, n, c, status)) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (c.rows <= kHalf * half)
+                break;
+            if (!__all_sync(0xffffffffu, wait_for(sm, &sm.q_empty[half], (qn[half]++ & 1u) ^ 1u, status)))
+                return;
+            const uint32_t dst = smem_u32(sq + half * q_half_bytes(D));
+            for (int r0 = 0; r0 < kHalf; r0 += 32) {
+                const int m = kHalf * half + r0 + lane;
+                const int pm = c.m0 + m;
+                const int64_t at = m < c.rows ? (c.row0 + pm / G) * a.q_row_stride +
+                                                    (int64_t)(c.h * G + pm % G) * a.q_head_stride
+                                              : -1;
+#pragma unroll 4
+                for (int k = 0; k < 32 / kRows; ++k) {
+                    const int row = k * kRows + lane / kLanes, ch = lane % kLanes, r = r0 + row;
+                    const int64_t from = __shfl_sync(0xffffffffu, at, row);
+                    const uint16_t *src = static_cast<const uint16_t *>(a.q) + (from >= 0 ? from + 8 * ch : 0);
+                    const int bytes = from >= 0 ? 16 : 0;  // the rest is filled with zeros
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     dst + (ch / 8) * (kHalf * 128) + r * 128 + (((ch % 8) ^ (r & 7)) << 4)),
+                                 "l"(src), "r"(bytes)
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.q_full[half]);
+        }
+    }
+}
+
 // Zero the rows of a V stage whose keys the item does not see: their slots
 // may hold anything, and 0 x NaN is NaN.
 template <int D>
@@ -462,20 +569,19 @@ __device__ __forceinline__ void clear_unseen(uint8_t *stage, int key0, int lo, i
 
 // The MMAs (warp 8; lane 0 issues).
 template <int D>
-__device__ void mma_issuer(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, uint8_t *ring,
-                           int64_t w0, int64_t w1, int *status)
+__device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int *status)
 {
     const int lane = threadIdx.x & 31;
     const uint32_t tb = sm.tmem_base;
     const uint64_t qd = sw128_desc(smem_u32(sq)), kd = sw128_desc(smem_u32(ring));
     const uint64_t vd = sw128_desc_mn(smem_u32(ring), kKeys * 128);
-    uint32_t it = 0;                // ring uses
+    uint32_t it = 0, n = 0;                   // ring uses, items
     uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // items and units of each half
     auto ok = [&](uint64_t *bar, unsigned parity) {
         return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
     };
     // S of a half from the K stage s
-    auto qk = [&](int half, int s) {
+    auto qk = [&](int half, int s, bool last) {
         if (lane == 0) {
             const uint64_t ad = qd + (uint64_t)(half * (q_half_bytes(D) >> 4));
             const uint64_t bd = kd + (uint64_t)(s * (stage_bytes(D) >> 4));
@@ -486,14 +592,14 @@ __device__ void mma_issuer(const smoe_attention_args &a, int G, Smem &sm, uint8_
                 mma_ss(tb + col_s(half), ad + off, bd + off, kIdescQK, k > 0);
             }
             umma_commit(&sm.s_full[half]);
+            if (last)  // of the item
+                umma_commit(&sm.q_empty[half]);
         }
         __syncwarp();
     };
-    for (Tile c = first_tile(a, G, sm, w0, status); c.rows > 0 && c.at < w1; tile_next(a, G, c, status)) {
-        int u0, u1;
-        units_in(c, w0, w1, u0, u1);
-        if (u0 >= u1)
-            continue;
+    Item c;
+    while (next_item(sm, n, c, status)) {
+        const int u0 = c.u0, u1 = c.u1;
         const int halves = c.rows > kHalf ? 2 : 1;
         // the first K, both halves
         int s = it % kStages;
@@ -506,7 +612,7 @@ __device__ void mma_issuer(const smoe_attention_args &a, int G, Smem &sm, uint8_
             if (!ok(&sm.q_full[half], qn[half]++ & 1u))
                 return;
             tc_fence_after();
-            qk(half, s);
+            qk(half, s, u0 + 1 == u1);
         }
         if (lane == 0)
             umma_commit(&sm.kv_empty[s]);
@@ -542,7 +648,7 @@ __device__ void mma_issuer(const smoe_attention_args &a, int G, Smem &sm, uint8_
                 if (half == halves - 1 && lane == 0)
                     umma_commit(&sm.kv_empty[sv]);
                 if (!last)
-                    qk(half, sk);
+                    qk(half, sk, u + 2 == u1);
                 else if (lane == 0)
                     umma_commit(&sm.o_full[half]);
                 __syncwarp();
@@ -554,10 +660,10 @@ __device__ void mma_issuer(const smoe_attention_args &a, int G, Smem &sm, uint8_
     }
 }
 
-// Queries, softmax and output of half `half` (warps 4 half .. 4 half + 3).
+// Softmax and output of half `half` (warps 4 half .. 4 half + 3).
 template <int D>
-__device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, float *parts,
-                        unsigned *arrived, int half, int64_t w0, int64_t w1, int *status)
+__device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *parts, unsigned *arrived,
+                        int half, int *status)
 {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int r = 32 * quarter + lane;  // row of the half, lane of tensor memory
@@ -567,65 +673,58 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, uint8_t *
     auto ok = [&](uint64_t *bar, unsigned parity) {
         return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
     };
-    for (Tile c = first_tile(a, G, sm, w0, status); c.rows > 0 && c.at < w1; tile_next(a, G, c, status)) {
-        int u0, u1;
-        units_in(c, w0, w1, u0, u1);
-        if (u0 >= u1)
-            continue;
+    uint32_t n = 0;
+    Item c;
+    while (next_item(sm, n, c, status)) {
+        const int u0 = c.u0, u1 = c.u1;
         const int m = kHalf * half + r;         // row of the item
         const bool on = m < c.rows;
         const bool active = c.rows > kHalf * half;  // the half has rows
-        const int64_t token = c.s.row0 + (c.m0 + m) / G;
+        const int64_t token = c.row0 + (c.m0 + m) / G;
         const int head = c.h * G + (c.m0 + m) % G;
         int lo = 0, hi = 0;
         if (on)
-            seen(a, c.s, (c.m0 + m) / G, lo, hi);
+            seen_from(a, c.i0 + (c.m0 + m) / G, lo, hi);
         float mr = -INFINITY, sum = 0.f;
         if (active) {
-            // queries, swizzled; the last S of the item before is done, and
-            // with it every read of the old queries
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
-                                                               token * a.q_row_stride +
-                                                               (int64_t)head * a.q_head_stride);
-            uint8_t *dst = sq + half * q_half_bytes(D) + r * 128;
-            uint4 v[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                v[i] = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<uint4 *>(dst + (i / 8) * (kHalf * 128) + (((i % 8) ^ (r & 7)) << 4)) = v[i];
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.q_full[half]);
             for (int u = u0; u < u1; ++u, ++sn) {
                 if (!ok(&sm.s_full[half], sn & 1u))
                     return;
                 tc_fence_after();
-                uint32_t s[kKeys];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tmem_ld32(tl + col_s(half) + 32 * i, s + 32 * i);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pin32(s + 32 * i);
+                // S in four chunks of 32 keys.  The maximum first; the last
+                // two chunks are then read a second time rather than kept in
+                // registers.  P of chunk i goes over S of chunk i / 2, which
+                // has been read for good by then.
+                const uint32_t ts = tl + col_s(half);
                 const int key0 = c.kbase + u * kKeys;
-                if (key0 < c.t_lo || key0 + kKeys > c.t_hi) {
-                    const int first = lo - key0, end = hi - key0;
+                const bool edge = key0 < c.t_lo || key0 + kKeys > c.t_hi;
+                const int first = lo - key0, end = hi - key0;
+                uint32_t s[2][32];
+                auto mask = [&](uint32_t *v, int at) {
+                    if (edge)
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-                        if (i < first || i >= end)
-                            s[i] = 0xff800000u;  // -infinity
+                        for (int e = 0; e < 32; ++e)
+                            if (at + e < first || at + e >= end)
+                                v[e] = 0xff800000u;  // -infinity
+                };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto most = [&](const uint32_t *v) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+                };
+#pragma unroll
+                for (int h = 1; h >= 0; --h) {
+                    tmem_ld32(ts + 64 * h, s[0]);
+                    tmem_ld32(ts + 64 * h + 32, s[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        pin32(s[k]);
+                        mask(s[k], 64 * h + 32 * k);
+                        most(s[k]);
+                    }
                 }
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-                for (int i = 4; i < kKeys; ++i)
-                    mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                 const bool raise = top > mr + kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
@@ -636,16 +735,16 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, uint8_t *
                     mr = mn;
                     sum *= f;
                     if (u > u0) {
-#pragma unroll
-                        for (int i = 0; i < D; i += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tl + col_o<D>(half) + i, o);
+                        for (int k = 0; k < D; k += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tl + col_o<D>(half) + k, o);
                             tmem_wait_ld();
-                            pin32(o);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st32(tl + col_o<D>(half) + i, o);
+                            for (int e = 0; e < 16; ++e) {
+                                asm volatile("" : "+r"(o[e]));
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            }
+                            tmem_st16(tl + col_o<D>(half) + k, o);
                         }
                     }
                 }
@@ -653,27 +752,34 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, uint8_t *
                 const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
                 uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-                for (int ph = 0; ph < 2; ++ph) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int e = 64 * ph + 32 * q + 2 * i;
-                            float x, y;
-                            unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, mu2), x, y);
-                            x = ex2(x);
-                            y = ex2(y);
-                            acc[i & 1] = add2(acc[i & 1], pair(x, y));
-                            p[i] = pack_bf16x2(x, y);
-                        }
-                        tmem_st16(tl + col_s(half) + 32 * ph + 16 * q, p);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t *v = s[k & 1];
+                    if (k >= 2) {
+                        if (k == 2)
+                            tmem_wait_ld();
+                        pin32(v);
+                        mask(v, 32 * k);
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&sm.p_full[half][ph]);
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x, y;
+                        unpair(fma2(pair(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, mu2), x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        acc[e & 1] = add2(acc[e & 1], pair(x, y));
+                        p[e] = pack_bf16x2(x, y);
+                    }
+                    tmem_st16(ts + 16 * k, p);
+                    if (k < 2)
+                        tmem_ld32(ts + 64 + 32 * k, v);  // chunk k + 2
+                    if (k & 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&sm.p_full[half][k >> 1]);
+                    }
                 }
                 float x, y;
                 unpair(add2(acc[0], acc[1]), x, y);
@@ -683,8 +789,7 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, uint8_t *
                 return;
             tc_fence_after();
         }
-        const int64_t k = c.at + kItemUnits;
-        const int c_first = static_cast<int>(k / sm.q), c_last = static_cast<int>((k + c.units - 1) / sm.q);
+        const int c_first = c.c_first, c_last = c.c_last;
         const bool whole = c_first == c_last;
         auto write_out = [&](int col, const float *v, float inv) {  // 16 columns
             const int64_t at = token * a.out_row_stride + (int64_t)head * a.out_head_stride + col;
@@ -807,8 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.kv_full[i], 1);
             mbar_init(&sm.kv_empty[i], 1);
         }
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(&sm.item_full[i], 1);
+            mbar_init(&sm.item_empty[i], kSoftWarps + 3);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i][0], 4);
             mbar_init(&sm.p_full[i][1], 4);
@@ -836,23 +946,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
 
     if (warp < kSoftWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        softmax<D>(a, G, sm, sq, reinterpret_cast<float *>(workspace + kPartsAt),
-                   reinterpret_cast<unsigned *>(workspace), warp >> 2, w0, w1, status);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kLoadWarp) {
-            loader<D>(a, G, &maps, sm, ring, w0, w1, status);
-        } else if (warp == kMmaWarp) {
-            mma_issuer<D>(a, G, sm, sq, ring, w0, w1, status);
-            __syncwarp();
-            if (lane == 0) {
-                // every MMA issued so far has completed once this commit lands
-                umma_commit(&sm.drain);
-                if (!mbar_wait_bounded(&sm.drain, 0)) {
-                    set_status(status, kStatusTimeout);
-                    *reinterpret_cast<volatile int *>(&sm.fail) = 1;
-                }
+        softmax<D>(a, G, sm, reinterpret_cast<float *>(workspace + kPartsAt),
+                   reinterpret_cast<unsigned *>(workspace), warp >> 2, status);
+    } else if (warp == kLoadWarp) {
+        loader<D>(a, &maps, sm, ring, status);
+    } else if (warp == kQueryWarp) {
+        query_loader<D>(a, G, sm, sq, status);
+    } else if (warp == kItemWarp) {
+        item_walker(a, G, sm, w0, w1, status);
+    } else if (warp == kMmaWarp) {
+        mma_issuer<D>(sm, sq, ring, status);
+        __syncwarp();
+        if (lane == 0) {
+            // every MMA issued so far has completed once this commit lands
+            umma_commit(&sm.drain);
+            if (!mbar_wait_bounded(&sm.drain, 0)) {
+                set_status(status, kStatusTimeout);
+                *reinterpret_cast<volatile int *>(&sm.fail) = 1;
             }
         }
     }
