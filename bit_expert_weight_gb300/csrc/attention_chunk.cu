@@ -18,18 +18,21 @@
 //
 // Roles of the 12 warps of a CTA, one CTA per SM:
 //   warps 0..3  half A, warps 4..7 half B: softmax, rescaling, output
-//   warp 8      issues the MMAs
-//   warp 9      loads K and V by TMA, page by page, into a ring of 4 stages of
-//               128 keys (K and V alternating), 128-byte swizzle
-//   warp 10     walks the line of items and hands them to the other warps
-//               through a ring of records in shared memory
-//   warp 11     loads the queries, as soon as the products with the ones
-//               before are done
+//   warps 8, 9  issue the MMAs of half A and half B.  One thread takes about
+//               50 cycles to issue an MMA that runs for 64, and about 100 for
+//               each wait and commit: one warp for both halves kept the tensor
+//               cores waiting
+//   warp 10     loads K and V by TMA, page by page, into rings of 3 and 2
+//               units, 128-byte swizzle
+//   warp 11     walks the line of items, hands them to the other warps through
+//               a ring of records in shared memory, and loads the queries as
+//               soon as the products with the ones before are done
 // Work split: as in attention.cu, the items form a line of units, cut into
 // equal shares, one per CTA; parts of an item are joined by the last of its
 // CTAs to arrive.  Every wait is bounded; one that runs out is recorded as
 // SMOE_ERR_TIMEOUT and ends the CTA's work.
 #include <cuda.h>
+#include <limits.h>
 #include <math.h>
 
 #include "attention.cuh"
@@ -44,10 +47,10 @@ namespace {
 constexpr int kHalf = 128;              // rows of a half (MMA M)
 constexpr int kTileRows2 = 2 * kHalf;   // packed rows of an item
 constexpr int kKeys = 128;              // keys of a unit (MMA N of Q K^T, K of P V)
-constexpr int kStages = 4;
+constexpr int kKStages = 3, kVStages = 2;  // units of K and of V in shared memory
+constexpr int kFree = 4;                   // releases told apart
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kItemWarp = 10, kQueryWarp = 11;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11;
 constexpr int kItemSlots = 4;
 constexpr int kThreads = 384;
 constexpr int kItemUnits = 2;           // an item's own cost, in units
@@ -58,12 +61,13 @@ __host__ __device__ constexpr int q_half_bytes(int D) { return kHalf * D * 2; }
 __host__ __device__ constexpr int stage_bytes(int D) { return kKeys * D * 2; }
 __host__ __device__ constexpr int smem_bytes(int D)
 {
-    return 2 * q_half_bytes(D) + kStages * stage_bytes(D) + 1024;  // slack for the alignment
+    return 2 * q_half_bytes(D) + (kKStages + kVStages) * stage_bytes(D) + 1024;  // slack for the alignment
 }
 // A part: outputs [D][rows], then the rows' m, then their sums.
 __host__ __device__ constexpr int part_floats(int D) { return (D + 2) * kTileRows2; }
 static_assert(kPartsAt + (size_t)2 * kMaxCtas * part_floats(128) * 4 <= SMOE_ATTENTION_WORKSPACE_BYTES,
               "workspace");
+static_assert((SMOE_MAX_SEQS + 1) * sizeof(int) <= (kKStages + kVStages) * stage_bytes(64), "sequence table");
 static_assert(kMaxCtas <= kMaxCounters, "counters");
 
 // Tensor memory columns: S (and P over it) and O of each half.
@@ -88,26 +92,28 @@ struct Item {
 
 struct Smem {
     uint64_t item_full[kItemSlots];   // item warp
-    uint64_t item_empty[kItemSlots];  // the 8 softmax warps, MMA warp, both loading warps
+    uint64_t item_empty[kItemSlots];  // 8 softmax warps, 2 MMA warps, loading warp
     Item item[kItemSlots];
-    uint64_t kv_full[kStages];   // loader: 1 arrival + bytes
-    uint64_t kv_empty[kStages];  // 1 MMA commit
-    uint64_t q_full[2];          // query warp
+    uint64_t k_full[kKStages];   // loader: 1 arrival + bytes
+    uint64_t v_full[kVStages];   // loader: 1 arrival + bytes
+    uint64_t v_raw;              // loader, for its own use: a V that it clears in part
+    uint64_t unit_done[kFree];   // both MMA warps: the products of a unit
+    uint64_t q_full[2];          // item warp
     uint64_t q_empty[2];         // 1 MMA commit
     uint64_t s_full[2];          // 1 MMA commit
     uint64_t p_full[2][2];       // 4 warps: keys 0..63, 64..127
     uint64_t o_full[2];          // 1 MMA commit
+    uint64_t turn[2][4];         // the other half's warp on the same lanes
     uint64_t joined;             // 8 warps
-    uint64_t drain;              // final MMA commit
+    uint64_t drain;              // final commits of both MMA warps
     uint32_t tmem_base;
-    uint32_t last_fill[kStages]; // 1 + last use filled, per stage (drain after a failure)
+    uint32_t units_filled[2], raw_filled;  // K, V, v_raw (drain after a failure)
     int fail, last;
     // the work split
     int64_t scan[kThreads / 32];
     int scan_max[kThreads / 32];
     int64_t q, total, before;    // units per CTA, in all, before the CTA's first item's tile
     int b, t;                    // that tile
-    int tiles[SMOE_MAX_SEQS + 1];  // tiles of the sequences before each
 };
 
 // ------------------------------------------------------------ PTX helpers
@@ -206,10 +212,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Bounded wait that records a timeout in the CTA's fail flag.
 __device__ __forceinline__ bool wait_for(Smem &sm, uint64_t *bar, unsigned parity, int *status)
 {
-    if (mbar_test_wait(bar, parity))
+    if (mbar_try_wait(bar, parity))
         return true;
     if (*reinterpret_cast<volatile int *>(&sm.fail))
         return false;
@@ -307,7 +320,9 @@ __device__ __forceinline__ int64_t scan_all(Smem &sm, int64_t v, int &mx, int64_
 }
 
 // The CTA's share, into shared memory: q, total, and the tile at its start.
-__device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, Smem &sm, int *status)
+// `tiles`: room for a number per sequence and one more.
+__device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, Smem &sm, int *tiles,
+                                           int *status)
 {
     const int tid = threadIdx.x, n = a.batch.num_seqs, Hkv = a.cache.num_kv_heads;
     // tiles before each sequence
@@ -318,12 +333,12 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
         sum += tiles_of(seq_at(a, b, status), G);
     int64_t before = scan_all(sm, sum, mx, total);
     for (int b = tid * per; b < n && b < (tid + 1) * per; ++b) {
-        sm.tiles[b] = static_cast<int>(before);
+        tiles[b] = static_cast<int>(before);
         before += tiles_of(seq_at(a, b, status), G);
     }
     const int all = static_cast<int>(total);
     if (tid == 0)
-        sm.tiles[n] = all;
+        tiles[n] = all;
     __syncthreads();
     // units of the tiles [i0, i1) of this thread
     const int pt = (all + kThreads - 1) / kThreads;
@@ -332,19 +347,19 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
     int b0 = 0, hi = n - 1;
     while (b0 < hi) {  // last sequence with tiles[b] <= i0
         const int mid = (b0 + hi + 1) >> 1;
-        if (sm.tiles[mid] <= i0)
+        if (tiles[mid] <= i0)
             b0 = mid;
         else
             hi = mid - 1;
     }
     sum = 0;
     for (int i = i0, b = b0; i < i1; ++i) {
-        if (i == i0 || i >= sm.tiles[b + 1]) {
-            while (i >= sm.tiles[b + 1])
+        if (i == i0 || i >= tiles[b + 1]) {
+            while (i >= tiles[b + 1])
                 ++b;
             c.s = seq_at(a, b, status);
         }
-        c.t = i - sm.tiles[b];
+        c.t = i - tiles[b];
         tile_keys(a, G, c);
         sum += c.units + kItemUnits;
         mx = c.units > mx ? c.units : mx;
@@ -363,12 +378,12 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
     }
     if (w0 >= before && w0 < before + sum * Hkv) {
         for (int i = i0, b = b0; i < i1; ++i) {
-            if (i == i0 || i >= sm.tiles[b + 1]) {
-                while (i >= sm.tiles[b + 1])
+            if (i == i0 || i >= tiles[b + 1]) {
+                while (i >= tiles[b + 1])
                     ++b;
                 c.s = seq_at(a, b, status);
             }
-            c.t = i - sm.tiles[b];
+            c.t = i - tiles[b];
             tile_keys(a, G, c);
             const int64_t next = before + (int64_t)(c.units + kItemUnits) * Hkv;
             if (w0 >= before && w0 < next) {
@@ -399,11 +414,42 @@ __device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, 
 
 // ------------------------------------------------------------ roles
 
-// The items of the CTA's share, in order (warp 10).
-__device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64_t w0, int64_t w1, int *status)
+// The queries of one half of an item: row r as it is packed, into the
+// swizzled layout that the MMA reads; rows past the item's are zeros.
+template <int D>
+__device__ __forceinline__ void load_queries(const smoe_attention_args &a, int G, const Tile &c, int half,
+                                             uint8_t *sq)
 {
     const int lane = threadIdx.x & 31;
-    uint32_t n = 0;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes per row, rows per round
+    const uint32_t dst = smem_u32(sq + half * q_half_bytes(D));
+    for (int r0 = 0; r0 < kHalf; r0 += 32) {
+        const int m = kHalf * half + r0 + lane;
+        const int pm = c.m0 + m;
+        const int64_t at = m < c.rows ? (c.s.row0 + pm / G) * a.q_row_stride +
+                                            (int64_t)(c.h * G + pm % G) * a.q_head_stride
+                                      : -1;
+#pragma unroll 4
+        for (int k = 0; k < 32 / kRows; ++k) {
+            const int row = k * kRows + lane / kLanes, ch = lane % kLanes, r = r0 + row;
+            const int64_t from = __shfl_sync(0xffffffffu, at, row);
+            const uint16_t *src = static_cast<const uint16_t *>(a.q) + (from >= 0 ? from + 8 * ch : 0);
+            const int bytes = from >= 0 ? 16 : 0;  // the rest is filled with zeros
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             dst + (ch / 8) * (kHalf * 128) + r * 128 + (((ch % 8) ^ (r & 7)) << 4)),
+                         "l"(src), "r"(bytes)
+                         : "memory");
+        }
+    }
+}
+
+// The items of the CTA's share, in order, and their queries (warp 11).
+template <int D>
+__device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, int64_t w0, int64_t w1,
+                            int *status)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t n = 0, qn[2] = {0, 0};
     for (Tile c = first_tile(a, G, sm, w0, status);; tile_next(a, G, c, status)) {
         const bool end = c.rows == 0 || c.at >= w1;
         int u0 = 0, u1 = 0;
@@ -439,6 +485,19 @@ __device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64
         ++n;
         if (end)
             return;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (c.rows <= kHalf * half)
+                break;
+            if (!__all_sync(0xffffffffu, wait_for(sm, &sm.q_empty[half], (qn[half]++ & 1u) ^ 1u, status)))
+                return;
+            load_queries<D>(a, G, c, half, sq);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.q_full[half]);
+        }
     }
 }
 
@@ -461,201 +520,163 @@ struct Maps {
     CUtensorMap k, v;  // (channels, slots, kv heads, pages), boxes of 64 x box_rows x 1 x 1
 };
 
-// Keys and values of every unit, K and V in turn (warp 9).  A lane copies one
-// 64-channel half of one page's share of the unit.  Slots past the keys that
-// the item sees are not copied page by page; what remains of their pages is
-// cleared before the product with V.
-template <int D>
-__device__ void loader(const smoe_attention_args &a, const Maps *maps, Smem &sm, uint8_t *ring, int *status)
-{
-    const int lane = threadIdx.x & 31, page = a.cache.page_size;
-    const int box = page < kKeys ? page : kKeys, boxes = kKeys / box;
-    const int i = lane / (D / 64), half = lane % (D / 64);
-    uint32_t it = 0, n = 0;
-    Item c;
-    while (next_item(sm, n, c, status)) {
-        for (int u = c.u0; u < c.u1; ++u) {
-            const int k0 = c.kbase + u * kKeys + i * box;
-            bool on = i < boxes && k0 < c.k_hi && k0 + box > c.k_lo;
-            int pg = 0;
-            if (on) {
-                pg = a.batch.page_table[(int64_t)c.b * a.batch.table_stride + k0 / page];
-                if (pg < 0 || pg >= a.cache.num_pages) {
-                    set_status(status, kStatusBadArg);
-                    on = false;
-                }
-            }
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, on)) * box * 128u;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++it) {
-                const int s = it % kStages;
-                if (!__all_sync(0xffffffffu,
-                                wait_for(sm, &sm.kv_empty[s], ((it / kStages) & 1u) ^ 1u, status)))
-                    return;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm.kv_full[s], bytes);
-                    sm.last_fill[s] = it + 1;
-                }
-                __syncwarp();
-                if (on)
-                    tma_load_4d(ring + s * stage_bytes(D) + half * (kKeys * 128) + i * box * 128,
-                                kv == 0 ? &maps->k : &maps->v, 64 * half, k0 % page, c.h, pg,
-                                &sm.kv_full[s]);
-            }
-        }
-    }
-}
-
-// The queries of every item (warp 11): row r of a half as it is packed, into
-// the swizzled layout the MMA reads; rows past the item's are zeros.
-template <int D>
-__device__ void query_loader(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, int *status)
-{
-    const int lane = threadIdx.x & 31;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes per row, rows per round
-    uint32_t n = 0, qn[2] = {0, 0};
-    Item c;
-    while (next_item(sm, n, c, status)) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (c.rows <= kHalf * half)
-                break;
-            if (!__all_sync(0xffffffffu, wait_for(sm, &sm.q_empty[half], (qn[half]++ & 1u) ^ 1u, status)))
-                return;
-            const uint32_t dst = smem_u32(sq + half * q_half_bytes(D));
-            for (int r0 = 0; r0 < kHalf; r0 += 32) {
-                const int m = kHalf * half + r0 + lane;
-                const int pm = c.m0 + m;
-                const int64_t at = m < c.rows ? (c.row0 + pm / G) * a.q_row_stride +
-                                                    (int64_t)(c.h * G + pm % G) * a.q_head_stride
-                                              : -1;
-#pragma unroll 4
-                for (int k = 0; k < 32 / kRows; ++k) {
-                    const int row = k * kRows + lane / kLanes, ch = lane % kLanes, r = r0 + row;
-                    const int64_t from = __shfl_sync(0xffffffffu, at, row);
-                    const uint16_t *src = static_cast<const uint16_t *>(a.q) + (from >= 0 ? from + 8 * ch : 0);
-                    const int bytes = from >= 0 ? 16 : 0;  // the rest is filled with zeros
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                     dst + (ch / 8) * (kHalf * 128) + r * 128 + (((ch % 8) ^ (r & 7)) << 4)),
-                                 "l"(src), "r"(bytes)
-                                 : "memory");
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.q_full[half]);
-        }
-    }
-}
-
 // Zero the rows of a V stage whose keys the item does not see: their slots
 // may hold anything, and 0 x NaN is NaN.
 template <int D>
 __device__ __forceinline__ void clear_unseen(uint8_t *stage, int key0, int lo, int hi)
 {
     const int lane = threadIdx.x & 31;
-    for (int r = 0; r < kKeys; ++r) {
-        if (key0 + r >= lo && key0 + r < hi)
+    const int below = lo > key0 ? lo - key0 : 0, left = hi - key0 > 0 ? hi - key0 : 0;  // rows [below, left) stay
+    constexpr int kLanes = D / 8;
+    for (int i = lane / kLanes; i < kKeys; i += 32 / kLanes) {
+        if (i >= below && i < left)
             continue;
-        if (lane < D / 8)
-            *reinterpret_cast<uint4 *>(stage + (lane / 8) * (kKeys * 128) + r * 128 + (lane % 8) * 16) =
-                make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(stage + (lane % kLanes / 8) * (kKeys * 128) + i * 128 + (lane % 8) * 16) =
+            make_uint4(0, 0, 0, 0);
     }
     fence_async_smem();
     __syncwarp();
 }
 
-// The MMAs (warp 8; lane 0 issues).
+// Keys and values of every unit (warp 10): K, then V, of one unit after the
+// other.  A lane copies one 64-channel half of one page's share of the unit.
+// Pages without a key that the item sees are not read; the rest of V's first
+// and last page is cleared before the MMA warps get it.
 template <int D>
-__device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int *status)
+__device__ void loader(const smoe_attention_args &a, const Maps *maps, Smem &sm, uint8_t *ring, int *status)
 {
-    const int lane = threadIdx.x & 31;
-    const uint32_t tb = sm.tmem_base;
-    const uint64_t qd = sw128_desc(smem_u32(sq)), kd = sw128_desc(smem_u32(ring));
-    const uint64_t vd = sw128_desc_mn(smem_u32(ring), kKeys * 128);
-    uint32_t it = 0, n = 0;                   // ring uses, items
-    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // items and units of each half
+    const int lane = threadIdx.x & 31, page = a.cache.page_size;
+    const int box = page < kKeys ? page : kKeys, boxes = kKeys / box;
+    const int i = lane / (D / 64), half = lane % (D / 64);
+    const int at = half * (kKeys * 128) + i * box * 128;  // of the lane's box in a stage
+    uint32_t g = 0, n = 0, raw = 0;                       // units, items, cleared V
     auto ok = [&](uint64_t *bar, unsigned parity) {
         return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
     };
-    // S of a half from the K stage s
-    auto qk = [&](int half, int s, bool last) {
-        if (lane == 0) {
-            const uint64_t ad = qd + (uint64_t)(half * (q_half_bytes(D) >> 4));
-            const uint64_t bd = kd + (uint64_t)(s * (stage_bytes(D) >> 4));
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                // 16 channels: 32 bytes inside a 64-channel half, which is 16 KB
-                const uint64_t off = (uint64_t)((k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2);
-                mma_ss(tb + col_s(half), ad + off, bd + off, kIdescQK, k > 0);
-            }
-            umma_commit(&sm.s_full[half]);
-            if (last)  // of the item
-                umma_commit(&sm.q_empty[half]);
-        }
-        __syncwarp();
-    };
     Item c;
     while (next_item(sm, n, c, status)) {
-        const int u0 = c.u0, u1 = c.u1;
-        const int halves = c.rows > kHalf ? 2 : 1;
-        // the first K, both halves
-        int s = it % kStages;
-        if (!ok(&sm.kv_full[s], (it / kStages) & 1u))
-            return;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half >= halves)
-                break;
-            if (!ok(&sm.q_full[half], qn[half]++ & 1u))
+        auto wanted = [&](int k0) { return i < boxes && k0 < c.k_hi && k0 + box > c.k_lo; };
+        // the page of a unit, looked up one unit ahead
+        auto page_of = [&](int u) {
+            const int k0 = c.kbase + u * kKeys + i * box;
+            return u < c.u1 && wanted(k0) ? a.batch.page_table[(int64_t)c.b * a.batch.table_stride + k0 / page]
+                                          : INT_MIN;
+        };
+        int next = page_of(c.u0);
+        for (int u = c.u0; u < c.u1; ++u, ++g) {
+            const int key0 = c.kbase + u * kKeys, k0 = key0 + i * box;
+            const int pg = next;
+            next = page_of(u + 1);
+            const bool on = pg >= 0 && pg < a.cache.num_pages;
+            if (!on && wanted(k0))
+                set_status(status, kStatusBadArg);
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, on)) * box * 128u;
+            // K takes the place of unit g - 3, V that of unit g - 2
+            if (g >= kKStages && !ok(&sm.unit_done[(g - kKStages) % kFree], ((g - kKStages) / kFree) & 1u))
                 return;
-            tc_fence_after();
-            qk(half, s, u0 + 1 == u1);
-        }
-        if (lane == 0)
-            umma_commit(&sm.kv_empty[s]);
-        ++it;
-        for (int u = u0; u < u1; ++u) {
-            const bool last = u + 1 == u1;
-            const int sv = it % kStages, sk = (it + 1) % kStages;
-            if (!ok(&sm.kv_full[sv], (it / kStages) & 1u))
+            uint64_t *full = &sm.k_full[g % kKStages];
+            if (lane == 0) {
+                sm.units_filled[0] = g + 1;
+                mbar_arrive_expect_tx(full, bytes);
+            }
+            __syncwarp();
+            if (on)
+                tma_load_4d(ring + (g % kKStages) * stage_bytes(D) + at, &maps->k, 64 * half, k0 % page, c.h, pg,
+                            full);
+            if (g >= kVStages && !ok(&sm.unit_done[(g - kVStages) % kFree], ((g - kVStages) / kFree) & 1u))
                 return;
-            const int key0 = c.kbase + u * kKeys;
-            if (key0 < c.k_lo || key0 + kKeys > c.k_hi)
-                clear_unseen<D>(ring + sv * stage_bytes(D), key0, c.k_lo, c.k_hi);
-            if (!last && !ok(&sm.kv_full[sk], ((it + 1) / kStages) & 1u))
-                return;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (half >= halves)
-                    break;
-#pragma unroll
-                for (int ph = 0; ph < 2; ++ph) {
-                    if (!ok(&sm.p_full[half][ph], pn[half] & 1u))
-                        return;
-                    tc_fence_after();
-                    if (lane == 0) {
-#pragma unroll
-                        for (int k = 4 * ph; k < 4 * ph + 4; ++k)  // 16 keys each
-                            mma_ts(tb + col_o<D>(half), tb + col_s(half) + 8 * k,
-                                   vd + (uint64_t)(sv * (stage_bytes(D) >> 4) + k * (16 * 128 >> 4)),
-                                   idesc_pv<D>(), u > u0 || k > 0);
-                    }
+            uint8_t *stage = ring + (kKStages + g % kVStages) * stage_bytes(D);
+            const bool edge = key0 < c.k_lo || key0 + kKeys > c.k_hi;
+            full = edge ? &sm.v_raw : &sm.v_full[g % kVStages];
+            if (lane == 0) {
+                if (edge)
+                    sm.raw_filled = raw + 1;
+                else
+                    sm.units_filled[1] = g + 1;
+                mbar_arrive_expect_tx(full, bytes);
+            }
+            __syncwarp();
+            if (on)
+                tma_load_4d(stage + at, &maps->v, 64 * half, k0 % page, c.h, pg, full);
+            if (edge) {
+                if (!ok(&sm.v_raw, raw++ & 1u))
+                    return;
+                clear_unseen<D>(stage, key0, c.k_lo, c.k_hi);
+                if (lane == 0) {
+                    sm.units_filled[1] = g + 1;
+                    mbar_arrive(&sm.v_full[g % kVStages]);
                 }
-                ++pn[half];
-                if (half == halves - 1 && lane == 0)
-                    umma_commit(&sm.kv_empty[sv]);
-                if (!last)
-                    qk(half, sk, u + 2 == u1);
-                else if (lane == 0)
-                    umma_commit(&sm.o_full[half]);
                 __syncwarp();
             }
-            if (!last && lane == 0)
-                umma_commit(&sm.kv_empty[sk]);
-            it += last ? 1 : 2;
+        }
+    }
+}
+
+// The MMAs of one half (one lane of warps 8 and 9).
+template <int D>
+__device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *status)
+{
+    const uint32_t ts = sm.tmem_base + col_s(half), to = sm.tmem_base + col_o<D>(half);
+    const uint64_t qd = sw128_desc(smem_u32(sq) + half * q_half_bytes(D)), kd = sw128_desc(smem_u32(ring));
+    const uint64_t vd = sw128_desc_mn(smem_u32(ring) + kKStages * stage_bytes(D), kKeys * 128);
+    constexpr uint64_t kStep = stage_bytes(D) >> 4;
+    uint32_t g = 0, n = 0;    // units, items
+    uint32_t qn = 0, pn = 0;  // items and units of this half
+    auto ok = [&](uint64_t *bar, unsigned parity) { return wait_for(sm, bar, parity, status); };
+    // S of unit x
+    auto qk = [&](uint32_t x) {
+        const uint64_t bd = kd + (x % kKStages) * kStep;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            // 16 channels: 32 bytes inside a 64-channel half, which is 16 KB
+            const uint64_t off = (uint64_t)((k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2);
+            mma_ss(ts, qd + off, bd + off, kIdescQK, k > 0);
+        }
+        umma_commit(&sm.s_full[half]);
+    };
+    for (;; ++n) {
+        const int slot = n % kItemSlots;
+        if (!ok(&sm.item_full[slot], (n / kItemSlots) & 1u))
+            return;
+        const int rows = sm.item[slot].rows, units = sm.item[slot].u1 - sm.item[slot].u0;
+        mbar_arrive(&sm.item_empty[slot]);
+        if (rows == 0)
+            return;
+        if (rows <= kHalf * half) {
+            // no rows in this half: nothing to wait for but the unit itself
+            for (int i = 0; i < units; ++i, ++g) {
+                if (!ok(&sm.v_full[g % kVStages], (g / kVStages) & 1u))
+                    return;
+                mbar_arrive(&sm.unit_done[g % kFree]);
+            }
+            continue;
+        }
+        if (!ok(&sm.q_full[half], qn++ & 1u) || !ok(&sm.k_full[g % kKStages], (g / kKStages) & 1u))
+            return;
+        tc_fence_after();
+        qk(g);
+        for (int u = 0; u < units; ++u, ++g, ++pn) {
+            const bool last = u + 1 == units;
+            if (last)  // the item's last S is on its way: its queries are free after it
+                umma_commit(&sm.q_empty[half]);
+            if (!ok(&sm.v_full[g % kVStages], (g / kVStages) & 1u) ||
+                (!last && !ok(&sm.k_full[(g + 1) % kKStages], ((g + 1) / kKStages) & 1u)))
+                return;
+            const uint64_t bd = vd + (g % kVStages) * kStep;
+#pragma unroll
+            for (int ph = 0; ph < 2; ++ph) {
+                if (!ok(&sm.p_full[half][ph], pn & 1u))
+                    return;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 4 * ph; k < 4 * ph + 4; ++k)  // 16 keys each
+                    mma_ts(to, ts + 8 * k, bd + (uint64_t)(k * (16 * 128 >> 4)), idesc_pv<D>(), u > 0 || k > 0);
+            }
+            if (last)
+                umma_commit(&sm.o_full[half]);
+            else  // over P, which the products above read first: MMAs of one thread run in order
+                qk(g + 1);
+            umma_commit(&sm.unit_done[g % kFree]);
         }
     }
 }
@@ -673,10 +694,11 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
     auto ok = [&](uint64_t *bar, unsigned parity) {
         return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
     };
-    uint32_t n = 0;
+    uint32_t n = 0, tn = 0;  // items, turns
     Item c;
     while (next_item(sm, n, c, status)) {
         const int u0 = c.u0, u1 = c.u1;
+        const bool both = c.rows > kHalf;
         const int m = kHalf * half + r;         // row of the item
         const bool on = m < c.rows;
         const bool active = c.rows > kHalf * half;  // the half has rows
@@ -691,39 +713,40 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
                 if (!ok(&sm.s_full[half], sn & 1u))
                     return;
                 tc_fence_after();
-                // S in four chunks of 32 keys.  The maximum first; the last
-                // two chunks are then read a second time rather than kept in
-                // registers.  P of chunk i goes over S of chunk i / 2, which
-                // has been read for good by then.
+                // S in two parts of 64 keys.  The maximum first, from the
+                // second part to the first; the second is then read again
+                // rather than kept in registers.  P goes over the S of the
+                // first part, which has been read for good by then.  The loops
+                // stay loops: the code of all roles has to fit the instruction
+                // cache.
                 const uint32_t ts = tl + col_s(half);
                 const int key0 = c.kbase + u * kKeys;
                 const bool edge = key0 < c.t_lo || key0 + kKeys > c.t_hi;
-                const int first = lo - key0, end = hi - key0;
-                uint32_t s[2][32];
-                auto mask = [&](uint32_t *v, int at) {
-                    if (edge)
+                uint32_t s[64];
+                auto load = [&](int part) {
+                    tmem_ld32(ts + 64 * part, s);
+                    tmem_ld32(ts + 64 * part + 32, s + 32);
+                };
+                auto loaded = [&](int part) {
+                    tmem_wait_ld();
+                    pin32(s);
+                    pin32(s + 32);
+                    if (edge) {
+                        const int first = lo - key0 - 64 * part, end = hi - key0 - 64 * part;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (at + e < first || at + e >= end)
-                                v[e] = 0xff800000u;  // -infinity
+                        for (int e = 0; e < 64; ++e)
+                            if (e < first || e >= end)
+                                s[e] = 0xff800000u;  // -infinity
+                    }
                 };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto most = [&](const uint32_t *v) {
+#pragma unroll 1
+                for (int part = 1; part >= 0; --part) {
+                    load(part);
+                    loaded(part);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
-                };
-#pragma unroll
-                for (int h = 1; h >= 0; --h) {
-                    tmem_ld32(ts + 64 * h, s[0]);
-                    tmem_ld32(ts + 64 * h + 32, s[1]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        pin32(s[k]);
-                        mask(s[k], 64 * h + 32 * k);
-                        most(s[k]);
-                    }
+                    for (int e = 0; e < 64; e += 2)
+                        mx[e / 2 & 3] = max3(mx[e / 2 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                 const bool raise = top > mr + kRaise;
@@ -749,37 +772,40 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
                     }
                 }
                 const float mu = mr == -INFINITY ? 0.f : mr;  // a row that has seen nothing yet
+                // The halves take turns, so that one computes exponentials
+                // while the tensor cores work for the other
+                if (both && !ok(&sm.turn[half][quarter], (tn & 1u) ^ (half == 0 ? 1u : 0u)))
+                    return;
                 const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
                 uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    if (part)
+                        loaded(1);
+                    uint32_t p[32];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t *v = s[k & 1];
-                    if (k >= 2) {
-                        if (k == 2)
-                            tmem_wait_ld();
-                        pin32(v);
-                        mask(v, 32 * k);
-                    }
-                    uint32_t p[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 32; ++e) {
                         float x, y;
-                        unpair(fma2(pair(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc2, mu2), x, y);
+                        unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, mu2), x, y);
                         x = ex2(x);
                         y = ex2(y);
                         acc[e & 1] = add2(acc[e & 1], pair(x, y));
                         p[e] = pack_bf16x2(x, y);
+                        if ((e & 15) == 15)
+                            tmem_st16(ts + 32 * part + (e & 16), p + (e & 16));
                     }
-                    tmem_st16(ts + 16 * k, p);
-                    if (k < 2)
-                        tmem_ld32(ts + 64 + 32 * k, v);  // chunk k + 2
-                    if (k & 1) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&sm.p_full[half][k >> 1]);
-                    }
+                    if (part == 0)
+                        load(1);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sm.p_full[half][part]);
+                }
+                if (both) {
+                    if (lane == 0)
+                        mbar_arrive(&sm.turn[half ^ 1][quarter]);
+                    ++tn;
                 }
                 float x, y;
                 unpair(add2(acc[0], acc[1]), x, y);
@@ -907,11 +933,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.b = a.batch.num_seqs;
         sm.t = 0;
         sm.before = 0;
-        for (int i = 0; i < kStages; ++i) {
-            sm.last_fill[i] = 0;
-            mbar_init(&sm.kv_full[i], 1);
-            mbar_init(&sm.kv_empty[i], 1);
-        }
+        sm.units_filled[0] = sm.units_filled[1] = sm.raw_filled = 0;
+        for (int i = 0; i < kKStages; ++i)
+            mbar_init(&sm.k_full[i], 1);
+        for (int i = 0; i < kVStages; ++i)
+            mbar_init(&sm.v_full[i], 1);
+        mbar_init(&sm.v_raw, 1);
+        for (int i = 0; i < kFree; ++i)
+            mbar_init(&sm.unit_done[i], 2);
         for (int i = 0; i < kItemSlots; ++i) {
             mbar_init(&sm.item_full[i], 1);
             mbar_init(&sm.item_empty[i], kSoftWarps + 3);
@@ -923,13 +952,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.p_full[i][0], 4);
             mbar_init(&sm.p_full[i][1], 4);
             mbar_init(&sm.o_full[i], 1);
+            for (int j = 0; j < 4; ++j)
+                mbar_init(&sm.turn[i][j], 1);
         }
         mbar_init(&sm.joined, kSoftWarps);
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.drain, 2);
         fence_mbar_init();
     }
     __syncthreads();
-    find_share(a, G, sm, status);
+    // (the ring is not in use yet)
+    find_share(a, G, sm, reinterpret_cast<int *>(ring), status);
     const int64_t w0 = sm.q * blockIdx.x;
     if (w0 >= sm.total)
         return;  // nothing for this CTA
@@ -950,14 +982,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                    reinterpret_cast<unsigned *>(workspace), warp >> 2, status);
     } else if (warp == kLoadWarp) {
         loader<D>(a, &maps, sm, ring, status);
-    } else if (warp == kQueryWarp) {
-        query_loader<D>(a, G, sm, sq, status);
     } else if (warp == kItemWarp) {
-        item_walker(a, G, sm, w0, w1, status);
-    } else if (warp == kMmaWarp) {
-        mma_issuer<D>(sm, sq, ring, status);
-        __syncwarp();
+        item_walker<D>(a, G, sm, sq, w0, w1, status);
+    } else {
         if (lane == 0) {
+            mma_issuer<D>(sm, sq, ring, warp - kMmaWarp, status);
             // every MMA issued so far has completed once this commit lands
             umma_commit(&sm.drain);
             if (!mbar_wait_bounded(&sm.drain, 0)) {
@@ -969,9 +998,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     // After a failure copies may be left unwaited: the loader waits (bounded)
     // for the last fill of every stage, so that none is in flight at the end.
-    if (*reinterpret_cast<volatile int *>(&sm.fail) && warp == kLoadWarp && lane < kStages) {
-        const uint32_t last = sm.last_fill[lane];
-        if (last > 0 && !mbar_wait_bounded(&sm.kv_full[lane], ((last - 1) / kStages) & 1u))
+    if (*reinterpret_cast<volatile int *>(&sm.fail) && warp == kLoadWarp && lane == 0) {
+        bool done = true;
+        for (uint32_t i = 0; i < kKStages && i < sm.units_filled[0]; ++i) {
+            const uint32_t g = sm.units_filled[0] - 1 - i;
+            done = mbar_wait_bounded(&sm.k_full[g % kKStages], (g / kKStages) & 1u) && done;
+        }
+        for (uint32_t i = 0; i < kVStages && i < sm.units_filled[1]; ++i) {
+            const uint32_t g = sm.units_filled[1] - 1 - i;
+            done = mbar_wait_bounded(&sm.v_full[g % kVStages], (g / kVStages) & 1u) && done;
+        }
+        if (sm.raw_filled)
+            done = mbar_wait_bounded(&sm.v_raw, (sm.raw_filled - 1) & 1u) && done;
+        if (!done)
             set_status(status, kStatusTimeout);
     }
     tc_fence_before();
