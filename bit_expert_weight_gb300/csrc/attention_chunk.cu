@@ -3,30 +3,40 @@
 //
 // An item is one tile of 256 packed rows (row m of it: new row (m0 + m) / G,
 // head (m0 + m) % G of the kv head), as two halves A and B of 128, over the
-// keys that its rows see, 128 keys (a unit) at a time.  Per unit and half:
+// keys that its rows see, loaded 128 keys (a unit) at a time.  Per half and
+// 64 keys (a step):
 //   S = Q K^T            tcgen05.mma, Q and K in shared memory, S in tensor
-//                        memory (128 lanes = rows, 128 columns = keys)
+//                        memory (128 lanes = rows, 64 columns = keys)
 //   P = exp2(S - m)      one thread per row: S from tensor memory to
 //                        registers, P as bf16 back over the S columns
 //   O += P V             tcgen05.mma, P from tensor memory, V in shared memory
-// The tensor cores work on one half while the threads of the other half
-// compute its exponentials.  m is the row's maximum when it was last raised:
-// it follows the true maximum only once that is more than 2^8 above it, so
-// that O is rescaled rarely; P is at most 2^8, its sum is kept in fp32 and the
-// final division by that sum makes the choice of m drop out.  P is rounded to
-// bf16 for the tensor cores (2^-9 of each p), the sum is not.
+// S has two buffers of 64 columns per half: the next step's S is computed
+// while the threads work on this one's exponentials, so that they never wait
+// for the tensor cores but at an item's start.  (With one buffer of 128
+// columns a unit took 3,550 cycles: the exponentials and the products took
+// turns.)  m is the row's maximum when it was last raised: it follows the true
+// maximum only once that is more than 2^8 above it, so that O is rescaled
+// rarely; P is at most 2^8, its sum is kept in fp32 and the final division by
+// that sum makes the choice of m drop out.  P is rounded to bf16 for the
+// tensor cores (2^-9 of each p), the sum is not.
 //
-// Roles of the 12 warps of a CTA, one CTA per SM:
+// Bounds, per unit: 2,048 cycles of shared memory for N = 64 products of Q
+// and K (64 KB of Q and 32 KB of K per half, 128 bytes a cycle) less what the
+// products with V (1,024 cycles of tensor cores, 16 KB of V per half) overlap;
+// 1,024 cycles of exponentials.
+//
+// Roles of the 16 warps of a CTA, one CTA per SM:
 //   warps 0..3  half A, warps 4..7 half B: softmax, rescaling, output
 //   warps 8, 9  issue the MMAs of half A and half B.  One thread takes about
-//               50 cycles to issue an MMA that runs for 64, and about 100 for
-//               each wait and commit: one warp for both halves kept the tensor
-//               cores waiting
+//               50 cycles to issue an MMA that runs for 32 to 64, and about 100
+//               for each wait and commit: one warp for both halves kept the
+//               tensor cores waiting
 //   warp 10     loads K and V by TMA, page by page, into rings of 3 and 2
 //               units, 128-byte swizzle
-//   warp 11     walks the line of items, hands them to the other warps through
-//               a ring of records in shared memory, and loads the queries as
-//               soon as the products with the ones before are done
+//   warp 11     walks the line of items and hands them to the other warps
+//               through a ring of records in shared memory
+//   warps 12..15  load the queries, as soon as the products with the ones
+//               before are done
 // Work split: as in attention.cu, the items form a line of units, cut into
 // equal shares, one per CTA; parts of an item are joined by the last of its
 // CTAs to arrive.  Every wait is bounded; one that runs out is recorded as
@@ -46,14 +56,15 @@ namespace {
 
 constexpr int kHalf = 128;              // rows of a half (MMA M)
 constexpr int kTileRows2 = 2 * kHalf;   // packed rows of an item
-constexpr int kKeys = 128;              // keys of a unit (MMA N of Q K^T, K of P V)
+constexpr int kKeys = 128;              // keys of a unit
+constexpr int kStep = 64;               // keys of a step (MMA N of Q K^T, K of P V)
 constexpr int kKStages = 3, kVStages = 2;  // units of K and of V in shared memory
 constexpr int kFree = 4;                   // releases told apart
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11, kQueryWarp = 12;
 constexpr int kItemSlots = 4;
-constexpr int kThreads = 384;
-constexpr int kItemUnits = 2;           // an item's own cost, in units
+constexpr int kThreads = 512;
+constexpr int kItemUnits = 4;           // an item's own cost, in units
 constexpr int kMaxCtas = 240;
 constexpr float kRaise = 8.0f;          // log2 of how far the maximum may run ahead of m
 
@@ -92,18 +103,16 @@ struct Item {
 
 struct Smem {
     uint64_t item_full[kItemSlots];   // item warp
-    uint64_t item_empty[kItemSlots];  // 8 softmax warps, 2 MMA warps, loading warp
+    uint64_t item_empty[kItemSlots];  // all warps but the item warp
     Item item[kItemSlots];
     uint64_t k_full[kKStages];   // loader: 1 arrival + bytes
     uint64_t v_full[kVStages];   // loader: 1 arrival + bytes
     uint64_t v_raw;              // loader, for its own use: a V that it clears in part
     uint64_t unit_done[kFree];   // both MMA warps: the products of a unit
-    uint64_t q_full[2];          // item warp
+    uint64_t q_full[2];          // 2 query warps; the half's 4 warps: no wait of theirs on s_done is open
     uint64_t q_empty[2];         // 1 MMA commit
-    uint64_t s_full[2];          // 1 MMA commit
-    uint64_t p_full[2][2];       // 4 warps: keys 0..63, 64..127
-    uint64_t o_full[2];          // 1 MMA commit
-    uint64_t turn[2][4];         // the other half's warp on the same lanes
+    uint64_t s_done[2][2];       // [half][buffer] 1 MMA commit: S, after the P V before it
+    uint64_t p_full[2][2];       // [half][buffer] 4 warps
     uint64_t joined;             // 8 warps
     uint64_t drain;              // final commits of both MMA warps
     uint32_t tmem_base;
@@ -135,7 +144,7 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr, uint32_t lead)
 // Instruction descriptors of kind::f16, bf16 in, fp32 out, M = 128: Q K^T
 // (both K-major, N = keys) and P V (V with N = channels contiguous).
 constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kHalf >> 4) << 24);
-constexpr uint32_t kIdescQK = kIdescBase | ((uint32_t)(kKeys >> 3) << 17);
+constexpr uint32_t kIdescQK = kIdescBase | ((uint32_t)(kStep >> 3) << 17);
 template <int D>
 __device__ __forceinline__ constexpr uint32_t idesc_pv()
 {
@@ -414,42 +423,11 @@ __device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, 
 
 // ------------------------------------------------------------ roles
 
-// The queries of one half of an item: row r as it is packed, into the
-// swizzled layout that the MMA reads; rows past the item's are zeros.
-template <int D>
-__device__ __forceinline__ void load_queries(const smoe_attention_args &a, int G, const Tile &c, int half,
-                                             uint8_t *sq)
+// The items of the CTA's share, in order (warp 11).
+__device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64_t w0, int64_t w1, int *status)
 {
     const int lane = threadIdx.x & 31;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes per row, rows per round
-    const uint32_t dst = smem_u32(sq + half * q_half_bytes(D));
-    for (int r0 = 0; r0 < kHalf; r0 += 32) {
-        const int m = kHalf * half + r0 + lane;
-        const int pm = c.m0 + m;
-        const int64_t at = m < c.rows ? (c.s.row0 + pm / G) * a.q_row_stride +
-                                            (int64_t)(c.h * G + pm % G) * a.q_head_stride
-                                      : -1;
-#pragma unroll 4
-        for (int k = 0; k < 32 / kRows; ++k) {
-            const int row = k * kRows + lane / kLanes, ch = lane % kLanes, r = r0 + row;
-            const int64_t from = __shfl_sync(0xffffffffu, at, row);
-            const uint16_t *src = static_cast<const uint16_t *>(a.q) + (from >= 0 ? from + 8 * ch : 0);
-            const int bytes = from >= 0 ? 16 : 0;  // the rest is filled with zeros
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             dst + (ch / 8) * (kHalf * 128) + r * 128 + (((ch % 8) ^ (r & 7)) << 4)),
-                         "l"(src), "r"(bytes)
-                         : "memory");
-        }
-    }
-}
-
-// The items of the CTA's share, in order, and their queries (warp 11).
-template <int D>
-__device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, int64_t w0, int64_t w1,
-                            int *status)
-{
-    const int lane = threadIdx.x & 31;
-    uint32_t n = 0, qn[2] = {0, 0};
+    uint32_t n = 0;
     for (Tile c = first_tile(a, G, sm, w0, status);; tile_next(a, G, c, status)) {
         const bool end = c.rows == 0 || c.at >= w1;
         int u0 = 0, u1 = 0;
@@ -485,19 +463,6 @@ __device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, uint8
         ++n;
         if (end)
             return;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (c.rows <= kHalf * half)
-                break;
-            if (!__all_sync(0xffffffffu, wait_for(sm, &sm.q_empty[half], (qn[half]++ & 1u) ^ 1u, status)))
-                return;
-            load_queries<D>(a, G, c, half, sq);
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.q_full[half]);
-        }
     }
 }
 
@@ -514,6 +479,53 @@ __device__ __forceinline__ bool next_item(Smem &sm, uint32_t &n, Item &t, int *s
         mbar_arrive(&sm.item_empty[slot]);
     ++n;
     return t.rows > 0;
+}
+
+// The queries of half of every item's half `half` (warps 12..15): row r as it
+// is packed, into the swizzled layout that the MMA reads; rows past the
+// item's are zeros.
+template <int D>
+__device__ void query_loader(const smoe_attention_args &a, int G, Smem &sm, uint8_t *sq, int half, int part,
+                             int *status)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes per row, rows per round
+    const uint32_t dst = smem_u32(sq + half * q_half_bytes(D));
+    uint32_t n = 0, qn = 0;
+    Item c;
+    while (next_item(sm, n, c, status)) {
+        if (c.rows <= kHalf * half)
+            continue;
+        int64_t at[kHalf / 2 / 32];  // of the rows 32 i + lane of this part
+#pragma unroll
+        for (int i = 0; i < kHalf / 2 / 32; ++i) {
+            const int m = kHalf * half + kHalf / 2 * part + 32 * i + lane;
+            const int pm = c.m0 + m;
+            at[i] = m < c.rows ? (c.row0 + pm / G) * a.q_row_stride + (int64_t)(c.h * G + pm % G) * a.q_head_stride
+                               : -1;
+        }
+        if (!__all_sync(0xffffffffu, wait_for(sm, &sm.q_empty[half], (qn++ & 1u) ^ 1u, status)))
+            return;
+#pragma unroll
+        for (int i = 0; i < kHalf / 2 / 32; ++i) {
+#pragma unroll 4
+            for (int k = 0; k < 32 / kRows; ++k) {
+                const int row = k * kRows + lane / kLanes, ch = lane % kLanes, r = kHalf / 2 * part + 32 * i + row;
+                const int64_t from = __shfl_sync(0xffffffffu, at[i], row);
+                const uint16_t *src = static_cast<const uint16_t *>(a.q) + (from >= 0 ? from + 8 * ch : 0);
+                const int bytes = from >= 0 ? 16 : 0;  // the rest is filled with zeros
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 dst + (ch / 8) * (kHalf * 128) + r * 128 + (((ch % 8) ^ (r & 7)) << 4)),
+                             "l"(src), "r"(bytes)
+                             : "memory");
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sm.q_full[half]);
+    }
 }
 
 struct Maps {
@@ -619,20 +631,19 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
     const uint32_t ts = sm.tmem_base + col_s(half), to = sm.tmem_base + col_o<D>(half);
     const uint64_t qd = sw128_desc(smem_u32(sq) + half * q_half_bytes(D)), kd = sw128_desc(smem_u32(ring));
     const uint64_t vd = sw128_desc_mn(smem_u32(ring) + kKStages * stage_bytes(D), kKeys * 128);
-    constexpr uint64_t kStep = stage_bytes(D) >> 4;
+    constexpr uint64_t kStage = stage_bytes(D) >> 4;
     uint32_t g = 0, n = 0;    // units, items
     uint32_t qn = 0, pn = 0;  // items and units of this half
     auto ok = [&](uint64_t *bar, unsigned parity) { return wait_for(sm, bar, parity, status); };
-    // S of unit x
+    // S of step x of the CTA, into its buffer
     auto qk = [&](uint32_t x) {
-        const uint64_t bd = kd + (x % kKStages) * kStep;
+        const uint64_t bd = kd + (x / 2 % kKStages) * kStage + (x & 1) * (kStep * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
             // 16 channels: 32 bytes inside a 64-channel half, which is 16 KB
             const uint64_t off = (uint64_t)((k / 4) * (kHalf * 128 >> 4) + (k % 4) * 2);
-            mma_ss(ts, qd + off, bd + off, kIdescQK, k > 0);
+            mma_ss(ts + (x & 1) * kStep, qd + off, bd + off, kIdescQK, k > 0);
         }
-        umma_commit(&sm.s_full[half]);
     };
     for (;; ++n) {
         const int slot = n % kItemSlots;
@@ -654,28 +665,34 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
         if (!ok(&sm.q_full[half], qn++ & 1u) || !ok(&sm.k_full[g % kKStages], (g / kKStages) & 1u))
             return;
         tc_fence_after();
-        qk(g);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            qk(2 * g + b);
+            umma_commit(&sm.s_done[half][b]);
+        }
         for (int u = 0; u < units; ++u, ++g, ++pn) {
             const bool last = u + 1 == units;
-            if (last)  // the item's last S is on its way: its queries are free after it
+            if (last)  // the item's last S are on their way: its queries are free after them
                 umma_commit(&sm.q_empty[half]);
             if (!ok(&sm.v_full[g % kVStages], (g / kVStages) & 1u) ||
                 (!last && !ok(&sm.k_full[(g + 1) % kKStages], ((g + 1) / kKStages) & 1u)))
                 return;
-            const uint64_t bd = vd + (g % kVStages) * kStep;
+            const uint64_t bd = vd + (g % kVStages) * kStage;
 #pragma unroll
-            for (int ph = 0; ph < 2; ++ph) {
-                if (!ok(&sm.p_full[half][ph], pn & 1u))
+            for (int b = 0; b < 2; ++b) {
+                if (!ok(&sm.p_full[half][b], pn & 1u))
                     return;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 4 * ph; k < 4 * ph + 4; ++k)  // 16 keys each
-                    mma_ts(to, ts + 8 * k, bd + (uint64_t)(k * (16 * 128 >> 4)), idesc_pv<D>(), u > 0 || k > 0);
+                for (int k = 0; k < kStep / 16; ++k)  // 16 keys each
+                    mma_ts(to, ts + b * kStep + 8 * k, bd + (uint64_t)((b * kStep + 16 * k) * 128 >> 4),
+                           idesc_pv<D>(), u > 0 || b > 0 || k > 0);
+                // the S after next over P, which the products above read first:
+                // MMAs of one thread run in order
+                if (!last)
+                    qk(2 * (g + 1) + b);
+                umma_commit(&sm.s_done[half][b]);
             }
-            if (last)
-                umma_commit(&sm.o_full[half]);
-            else  // over P, which the products above read first: MMAs of one thread run in order
-                qk(g + 1);
             umma_commit(&sm.unit_done[g % kFree]);
         }
     }
@@ -690,15 +707,16 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
     const int r = 32 * quarter + lane;  // row of the half, lane of tensor memory
     const uint32_t tl = sm.tmem_base + (static_cast<uint32_t>(32 * quarter) << 16);
     const float sc = a.scale * 1.44269504088896341f;
-    uint32_t items = 0, sn = 0, jn = 0;  // items and units of this half, joins
+    uint32_t sn = 0, jn = 0;  // commits of each s_done of this half, joins
     auto ok = [&](uint64_t *bar, unsigned parity) {
         return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
     };
-    uint32_t n = 0, tn = 0;  // items, turns
+    uint32_t n = 0;  // items
+    if (lane == 0)
+        mbar_arrive(&sm.q_full[half]);
     Item c;
     while (next_item(sm, n, c, status)) {
         const int u0 = c.u0, u1 = c.u1;
-        const bool both = c.rows > kHalf;
         const int m = kHalf * half + r;         // row of the item
         const bool on = m < c.rows;
         const bool active = c.rows > kHalf * half;  // the half has rows
@@ -709,45 +727,31 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
             seen_from(a, c.i0 + (c.m0 + m) / G, lo, hi);
         float mr = -INFINITY, sum = 0.f;
         if (active) {
-            for (int u = u0; u < u1; ++u, ++sn) {
-                if (!ok(&sm.s_full[half], sn & 1u))
+            const int steps = 2 * (u1 - u0);
+#pragma unroll 1
+            for (int v = 0; v < steps; ++v) {
+                if (!ok(&sm.s_done[half][v & 1], (sn + v / 2) & 1u))
                     return;
                 tc_fence_after();
-                // S in two parts of 64 keys.  The maximum first, from the
-                // second part to the first; the second is then read again
-                // rather than kept in registers.  P goes over the S of the
-                // first part, which has been read for good by then.  The loops
-                // stay loops: the code of all roles has to fit the instruction
-                // cache.
-                const uint32_t ts = tl + col_s(half);
-                const int key0 = c.kbase + u * kKeys;
-                const bool edge = key0 < c.t_lo || key0 + kKeys > c.t_hi;
-                uint32_t s[64];
-                auto load = [&](int part) {
-                    tmem_ld32(ts + 64 * part, s);
-                    tmem_ld32(ts + 64 * part + 32, s + 32);
-                };
-                auto loaded = [&](int part) {
-                    tmem_wait_ld();
-                    pin32(s);
-                    pin32(s + 32);
-                    if (edge) {
-                        const int first = lo - key0 - 64 * part, end = hi - key0 - 64 * part;
+                const uint32_t ts = tl + col_s(half) + (v & 1) * kStep;
+                const int key0 = c.kbase + u0 * kKeys + v * kStep;
+                uint32_t s[kStep];
+                tmem_ld32(ts, s);
+                tmem_ld32(ts + 32, s + 32);
+                tmem_wait_ld();
+                pin32(s);
+                pin32(s + 32);
+                if (key0 < c.t_lo || key0 + kStep > c.t_hi) {
+                    const int first = lo - key0, end = hi - key0;
 #pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (e < first || e >= end)
-                                s[e] = 0xff800000u;  // -infinity
-                    }
-                };
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                for (int part = 1; part >= 0; --part) {
-                    load(part);
-                    loaded(part);
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2)
-                        mx[e / 2 & 3] = max3(mx[e / 2 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    for (int e = 0; e < kStep; ++e)
+                        if (e < first || e >= end)
+                            s[e] = 0xff800000u;  // -infinity
                 }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < kStep; e += 2)
+                    mx[e / 2 & 3] = max3(mx[e / 2 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                 const bool raise = top > mr + kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
@@ -757,7 +761,12 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
                     const float f = raise ? ex2(mr - mn) : 1.f;
                     mr = mn;
                     sum *= f;
-                    if (u > u0) {
+                    if (v > 0) {
+                        // O is at rest once the step before has been added
+                        if (!ok(&sm.s_done[half][(v - 1) & 1], (sn + (v - 1) / 2 + 1) & 1u))
+                            return;
+                        tc_fence_after();
+#pragma unroll 1
                         for (int k = 0; k < D; k += 16) {
                             uint32_t o[16];
                             tmem_ld16(tl + col_o<D>(half) + k, o);
@@ -772,48 +781,38 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
                     }
                 }
                 const float mu = mr == -INFINITY ? 0.f : mr;  // a row that has seen nothing yet
-                // The halves take turns, so that one computes exponentials
-                // while the tensor cores work for the other
-                if (both && !ok(&sm.turn[half][quarter], (tn & 1u) ^ (half == 0 ? 1u : 0u)))
-                    return;
                 const uint64_t sc2 = pair(sc, sc), mu2 = pair(-mu, -mu);
                 uint64_t acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll 1
-                for (int part = 0; part < 2; ++part) {
-                    if (part)
-                        loaded(1);
-                    uint32_t p[32];
+                uint32_t p[kStep / 2];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float x, y;
-                        unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, mu2), x, y);
-                        x = ex2(x);
-                        y = ex2(y);
-                        acc[e & 1] = add2(acc[e & 1], pair(x, y));
-                        p[e] = pack_bf16x2(x, y);
-                        if ((e & 15) == 15)
-                            tmem_st16(ts + 32 * part + (e & 16), p + (e & 16));
-                    }
-                    if (part == 0)
-                        load(1);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&sm.p_full[half][part]);
+                for (int e = 0; e < kStep / 2; ++e) {
+                    float x, y;
+                    unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, mu2), x, y);
+                    x = ex2(x);
+                    y = ex2(y);
+                    acc[e & 1] = add2(acc[e & 1], pair(x, y));
+                    p[e] = pack_bf16x2(x, y);
+                    if ((e & 15) == 15)
+                        tmem_st16(ts + (e & 16), p + (e & 16));
                 }
-                if (both) {
-                    if (lane == 0)
-                        mbar_arrive(&sm.turn[half ^ 1][quarter]);
-                    ++tn;
-                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.p_full[half][v & 1]);
                 float x, y;
                 unpair(add2(acc[0], acc[1]), x, y);
                 sum += x + y;
             }
-            if (!ok(&sm.o_full[half], items++ & 1u))
+            // every step is in O
+            sn += u1 - u0;
+            if (!ok(&sm.s_done[half][0], sn & 1u) || !ok(&sm.s_done[half][1], sn & 1u))
                 return;
+            ++sn;
             tc_fence_after();
+            // only now may the next item's S complete another phase of s_done
+            if (lane == 0)
+                mbar_arrive(&sm.q_full[half]);
         }
         const int c_first = c.c_first, c_last = c.c_last;
         const bool whole = c_first == c_last;
@@ -839,23 +838,21 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
                                   part_floats(D);
         if (active) {
             const float inv = sum > 0.f ? 1.0f / sum : 0.f;  // a row that sees no key: zeros
-            for (int i = 0; i < D; i += 16) {
-                uint32_t o[16];
-                tmem_ld16(tl + col_o<D>(half) + i, o);
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+                uint32_t o[32];
+                tmem_ld32(tl + col_o<D>(half) + i, o);
                 tmem_wait_ld();
-                float v[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    asm volatile("" : "+r"(o[j]));
-                    v[j] = __uint_as_float(o[j]);
-                }
+                pin32(o);
                 if (whole) {
-                    if (on)
-                        write_out(i, v, inv);
+                    if (on) {
+                        write_out(i, reinterpret_cast<const float *>(o), inv);
+                        write_out(i + 16, reinterpret_cast<const float *>(o + 16), inv);
+                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        __stcg(part + (i + j) * kTileRows2 + m, v[j]);
+                    for (int j = 0; j < 32; ++j)
+                        __stcg(part + (i + j) * kTileRows2 + m, __uint_as_float(o[j]));
                 }
             }
             if (!whole) {
@@ -943,17 +940,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.unit_done[i], 2);
         for (int i = 0; i < kItemSlots; ++i) {
             mbar_init(&sm.item_full[i], 1);
-            mbar_init(&sm.item_empty[i], kSoftWarps + 3);
+            mbar_init(&sm.item_empty[i], kThreads / 32 - 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_full[i], 2 + kSoftWarps / 2);
             mbar_init(&sm.q_empty[i], 1);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i][0], 4);
-            mbar_init(&sm.p_full[i][1], 4);
-            mbar_init(&sm.o_full[i], 1);
-            for (int j = 0; j < 4; ++j)
-                mbar_init(&sm.turn[i][j], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&sm.s_done[i][j], 1);
+                mbar_init(&sm.p_full[i][j], 4);
+            }
         }
         mbar_init(&sm.joined, kSoftWarps);
         mbar_init(&sm.drain, 2);
@@ -983,7 +978,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLoadWarp) {
         loader<D>(a, &maps, sm, ring, status);
     } else if (warp == kItemWarp) {
-        item_walker<D>(a, G, sm, sq, w0, w1, status);
+        item_walker(a, G, sm, w0, w1, status);
+    } else if (warp >= kQueryWarp) {
+        query_loader<D>(a, G, sm, sq, (warp - kQueryWarp) / 2, (warp - kQueryWarp) % 2, status);
     } else {
         if (lane == 0) {
             mma_issuer<D>(sm, sq, ring, warp - kMmaWarp, status);
