@@ -75,6 +75,24 @@ bool device_supported()
     return device_cc_major() == 10 && device_cc_minor() == 3;
 }
 
+const DeviceFacts &device_facts()
+{
+    static DeviceFacts facts[kMaxDevices];
+    static std::atomic<bool> known[kMaxDevices];
+    const int dev = cur_device();
+    if (!known[dev].load(std::memory_order_acquire)) {
+        ensure_device_info();
+        std::lock_guard<std::mutex> lk(g_mu);
+        facts[dev].sms = g_sms[dev];
+        facts[dev].supported = g_major[dev] == 10 && g_minor[dev] == 3;
+        facts[dev].status = g_status_ptr[dev];
+        facts[dev].index = dev;
+        // nothing is kept of a device that could not be asked
+        known[dev].store(g_major[dev] != 0, std::memory_order_release);
+    }
+    return facts[dev];
+}
+
 int *device_status_word()
 {
     ensure_device_info();

@@ -570,28 +570,28 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
 }
 
 template <int D>
-cudaError_t launch_rows(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream)
+cudaError_t launch_rows(const smoe_attention_args &a, uint8_t *workspace, const DeviceFacts &dev,
+                        cudaStream_t stream)
 {
-    constexpr int smem = dec_smem_bytes(D);
-    cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<bool> allowed[kMaxDeviceIndex];
+    const cudaError_t e = allow_smem(attend_rows_kernel<D>, dec_smem_bytes(D), dev, allowed);
     if (e != cudaSuccess)
         return e;
-    const int sms = device_sm_count();
-    attend_rows_kernel<D><<<sms < kMaxCtas ? sms : kMaxCtas, 32 * kDecWarps, smem, stream>>>(
-        a, workspace, device_status_word());
+    attend_rows_kernel<D><<<dev.sms < kMaxCtas ? dev.sms : kMaxCtas, 32 * kDecWarps, dec_smem_bytes(D), stream>>>(
+        a, workspace, dev.status);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, cudaStream_t stream)
+cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, const DeviceFacts &dev,
+                             cudaStream_t stream)
 {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int G = a.num_heads / a.cache.num_kv_heads;
     if ((int64_t)a.max_rows * G > kDecRows)
-        return launch_attention_chunk(a, ws, stream);
-    return a.cache.head_dim == 64 ? launch_rows<64>(a, ws, stream) : launch_rows<128>(a, ws, stream);
+        return launch_attention_chunk(a, ws, dev, stream);
+    return a.cache.head_dim == 64 ? launch_rows<64>(a, ws, dev, stream) : launch_rows<128>(a, ws, dev, stream);
 }
 
 }  // namespace smoe

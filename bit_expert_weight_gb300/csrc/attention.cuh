@@ -2,6 +2,8 @@
 // the keys that a row sees, and the layout of the workspace.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -11,6 +13,18 @@ namespace smoe {
 // parts of items that several CTAs share.
 constexpr size_t kPartsAt = 4096;
 constexpr int kMaxCounters = static_cast<int>(kPartsAt / sizeof(unsigned));
+
+// Allow a kernel its dynamic shared memory, once per device.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, const DeviceFacts &dev, std::atomic<bool> *done)
+{
+    if (done[dev.index].load(std::memory_order_acquire))
+        return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done[dev.index].store(true, std::memory_order_release);
+    return e;
+}
 
 __device__ __forceinline__ float ex2(float x)
 {

@@ -1041,28 +1041,28 @@ bool page_map(CUtensorMap *m, const void *pages, const smoe_kv_cache &c, int64_t
 }
 
 template <int D>
-cudaError_t launch(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream)
+cudaError_t launch(const smoe_attention_args &a, uint8_t *workspace, const DeviceFacts &dev, cudaStream_t stream)
 {
+    static std::atomic<bool> allowed[kMaxDeviceIndex];
     Maps maps;
     const int box = a.cache.page_size < kKeys ? a.cache.page_size : kKeys;
     if (!page_map(&maps.k, a.cache.k_pages, a.cache, a.cache.k_page_stride, box) ||
         !page_map(&maps.v, a.cache.v_pages, a.cache, a.cache.v_page_stride, box))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attend_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes(D));
+    const cudaError_t e = allow_smem(attend_chunk_kernel<D>, smem_bytes(D), dev, allowed);
     if (e != cudaSuccess)
         return e;
-    const int sms = device_sm_count();
-    attend_chunk_kernel<D><<<sms < kMaxCtas ? sms : kMaxCtas, kThreads, smem_bytes(D), stream>>>(
-        a, maps, workspace, device_status_word());
+    attend_chunk_kernel<D><<<dev.sms < kMaxCtas ? dev.sms : kMaxCtas, kThreads, smem_bytes(D), stream>>>(
+        a, maps, workspace, dev.status);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream)
+cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *workspace, const DeviceFacts &dev,
+                                   cudaStream_t stream)
 {
-    return a.cache.head_dim == 64 ? launch<64>(a, workspace, stream) : launch<128>(a, workspace, stream);
+    return a.cache.head_dim == 64 ? launch<64>(a, workspace, dev, stream) : launch<128>(a, workspace, dev, stream);
 }
 
 }  // namespace smoe

@@ -120,7 +120,7 @@ smoe_status smoe_rope(const smoe_rope_args *a, void *cuda_stream)
     if (a->out == a->x &&
         (a->x_row_stride != a->out_row_stride || a->x_head_stride != a->out_head_stride))
         return SMOE_ERR_INVALID_ARG;
-    if (!device_supported())
+    if (!device_facts().supported)
         return SMOE_ERR_UNSUPPORTED;
     return cuda_status(launch_rope(*a, static_cast<cudaStream_t>(cuda_stream)));
 }
@@ -148,9 +148,10 @@ smoe_status smoe_kv_append(const smoe_kv_append_args *a, void *cuda_stream)
     if (!(isfinite(a->eps) && a->eps >= 0.0f) || (a->q_norm && !aligned16(a->q_norm)) ||
         (a->k_norm && !aligned16(a->k_norm)))
         return SMOE_ERR_INVALID_ARG;
-    if (!device_supported())
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
         return SMOE_ERR_UNSUPPORTED;
-    return cuda_status(launch_kv_append(*a, static_cast<cudaStream_t>(cuda_stream)));
+    return cuda_status(launch_kv_append(*a, dev, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 smoe_status smoe_attention(const smoe_attention_args *a, void *workspace, size_t workspace_bytes,
@@ -171,9 +172,10 @@ smoe_status smoe_attention(const smoe_attention_args *a, void *workspace, size_t
         return SMOE_ERR_INVALID_ARG;
     if (workspace_bytes < SMOE_ATTENTION_WORKSPACE_BYTES)
         return SMOE_ERR_WORKSPACE;
-    if (!device_supported())
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
         return SMOE_ERR_UNSUPPORTED;
-    return cuda_status(launch_attention(*a, workspace, static_cast<cudaStream_t>(cuda_stream)));
+    return cuda_status(launch_attention(*a, workspace, dev, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 }  // extern "C"

@@ -20,6 +20,15 @@ int device_sm_count();
 int device_cc_major();
 // Whether the current device is the one the library is compiled for (sm_103a).
 bool device_supported();
+// The same facts of the current device in one look (cached per device).
+struct DeviceFacts {
+    int sms;         // streaming multiprocessors
+    bool supported;  // the device the library is compiled for
+    int *status;     // device status word
+    int index;       // < kMaxDeviceIndex
+};
+constexpr int kMaxDeviceIndex = 64;
+const DeviceFacts &device_facts();
 // Pointer to the device status word of the current device.
 int *device_status_word();
 
@@ -196,10 +205,12 @@ cudaError_t launch_grouped(const GroupedArgs &a, const void *x, int x_bf16, floa
 // ------------------------------------------- rotation, paged cache, attention
 
 cudaError_t launch_rope(const smoe_rope_args &a, cudaStream_t stream);
-cudaError_t launch_kv_append(const smoe_kv_append_args &a, cudaStream_t stream);
-cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, cudaStream_t stream);
+cudaError_t launch_kv_append(const smoe_kv_append_args &a, const DeviceFacts &dev, cudaStream_t stream);
+cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, const DeviceFacts &dev,
+                             cudaStream_t stream);
 // chunks of rows, on the tensor cores (attention_chunk.cu)
-cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *workspace, cudaStream_t stream);
+cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *workspace, const DeviceFacts &dev,
+                                   cudaStream_t stream);
 
 int layer_grid_ctas_max();
 cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream);

@@ -295,7 +295,7 @@ cudaError_t launch_rope(const smoe_rope_args &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-cudaError_t launch_kv_append(const smoe_kv_append_args &a, cudaStream_t stream)
+cudaError_t launch_kv_append(const smoe_kv_append_args &a, const DeviceFacts &dev, cudaStream_t stream)
 {
     const int per = heads_per_warp(a.cache.head_dim);
     const int heads = (a.q ? a.num_heads : 0) + 2 * a.cache.num_kv_heads;
@@ -304,8 +304,7 @@ cudaError_t launch_kv_append(const smoe_kv_append_args &a, cudaStream_t stream)
     if (blocks > 0x7fffffff)
         return cudaErrorInvalidConfiguration;
     auto k = a.dtype == SMOE_F32 ? kv_append_kernel<true> : kv_append_kernel<false>;
-    k<<<static_cast<unsigned>(blocks), 32 * kRotWarps, 0, stream>>>(a, chunks,
-                                                                    device_status_word());
+    k<<<static_cast<unsigned>(blocks), 32 * kRotWarps, 0, stream>>>(a, chunks, dev.status);
     return cudaGetLastError();
 }
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -246,11 +247,11 @@ def load(path: str | None = None):
     L.smoe_get_device_status.restype = I
     L.smoe_rope_table.argtypes = [I32, ctypes.c_double, ctypes.POINTER(RopeScaling), P, P]
     L.smoe_rope_table.restype = I
-    L.smoe_rope.argtypes = [ctypes.POINTER(RopeArgs), P]
+    L.smoe_rope.argtypes = [P, P]
     L.smoe_rope.restype = I
-    L.smoe_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), P]
+    L.smoe_kv_append.argtypes = [P, P]
     L.smoe_kv_append.restype = I
-    L.smoe_attention.argtypes = [ctypes.POINTER(AttentionArgs), P, S, P]
+    L.smoe_attention.argtypes = [P, P, S, P]
     L.smoe_attention.restype = I
     L.smoe_debug_set_waits.argtypes = [ctypes.c_longlong, I]
     L.smoe_debug_set_waits.restype = None
@@ -574,50 +575,74 @@ def vault_repack_layer(meta: bytes, vault_dev: torch.Tensor, layer: int, num_exp
 
 # ------------------------------------ rotation, paged cache, attention
 
+# These calls are short (one launch of a few microseconds), so their arguments
+# are packed as the C struct's bytes: a ctypes.Structure takes three times as
+# long to fill.
+_CODES = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+
+
+def _packer(cls):
+    s = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_rope, _pack_append, _pack_attention = map(_packer, (RopeArgs, KvAppendArgs, AttentionArgs))
 _DTYPES = {torch.float32: SMOE_F32, torch.bfloat16: SMOE_BF16}
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _handle(stream, t):
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _heads(name, t):
     """A [rows, heads, head_dim] fp32 or bf16 CUDA view with contiguous channels:
     (pointer, row stride, head stride, smoe_dtype)."""
-    if t.dim() != 3 or t.stride(2) != 1 or not t.is_cuda:
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1 or not t.is_cuda:
         raise ValueError(f"{name} must be a [rows, heads, head_dim] CUDA tensor with contiguous "
                          "channels")
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be fp32 or bf16")
-    return t.data_ptr(), t.stride(0), t.stride(1), dt
+    return t.data_ptr(), st[0], st[1], dt
 
 
-def _device_array(name, t, dtype, numel=None):
+def _device_array(name, t, dtype, numel):
     """Pointer of a contiguous CUDA tensor of `dtype` with at least `numel` elements
     (None: no tensor, a null pointer)."""
     if t is None:
-        return None
+        return 0
     if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
-    if numel is not None and t.numel() < numel:
+    if t.numel() < numel:
         raise ValueError(f"{name} must have {numel} elements")
     return t.data_ptr()
 
 
 def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows):
     """The members of smoe_kv_cache and smoe_kv_batch."""
-    P, Hkv, page, D = k_pages.shape
-    if v_pages.shape != k_pages.shape:
+    P, Hkv, page, D = shape = k_pages.shape
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must have one shape")
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != torch.bfloat16 or not t.is_cuda:
-            raise ValueError(f"{name} must be a bf16 CUDA tensor")
-        if t.stride()[1:] != (page * D, D, 1):
-            raise ValueError(f"{name}: the last three dimensions must be contiguous")
+    if not (k_pages.dtype == v_pages.dtype == torch.bfloat16 and k_pages.is_cuda and
+            v_pages.is_cuda):
+        raise ValueError("k_pages and v_pages must be bf16 CUDA tensors")
+    if not ks[1:] == vs[1:] == (page * D, D, 1):
+        raise ValueError("k_pages, v_pages: the last three dimensions must be contiguous")
     B = kv_len.numel()
-    if page_table.dim() != 2 or page_table.shape[0] < B:
+    tb, pages = page_table.shape
+    if tb < B:
         raise ValueError("page_table must be [sequences, pages]")
-    return (k_pages.data_ptr(), v_pages.data_ptr(), P, k_pages.stride(0), v_pages.stride(0), page,
-            Hkv, D, 0, _device_array("row_start", row_start, torch.int32, B + 1),
-            _device_array("kv_len", kv_len, torch.int32),
-            _device_array("page_table", page_table, torch.int32), rows, B, page_table.shape[1])
+    i32 = torch.int32
+    return (k_pages.data_ptr(), v_pages.data_ptr(), P, ks[0], vs[0], page, Hkv, D, 0,
+            _device_array("row_start", row_start, i32, B + 1),
+            _device_array("kv_len", kv_len, i32, B),
+            _device_array("page_table", page_table, i32, 0), rows, B, pages)
 
 
 def rope_table(rot_dim: int, theta: float, kind="plain", factor=1.0, original_len=4096.0,
@@ -650,11 +675,11 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, rot_scal
         raise ValueError("out must have x's shape and dtype")
     xp, xr, xh, dt = _heads("x", x)
     op, orow, oh, _ = _heads("out", out)
-    a = RopeArgs(xp, op, xr, xh, orow, oh, T, H, D, dt, 2 * table.numel(), interleaved, rot_scale,
-                 eps, _device_array("positions", positions, torch.int32, T),
-                 _device_array("table", table, torch.int64),
-                 _device_array("norm_w", norm_w, torch.bfloat16, D))
-    _check(load().smoe_rope(ctypes.byref(a), _stream(stream)), "smoe_rope")
+    a = _pack_rope(xp, op, xr, xh, orow, oh, T, H, D, dt, 2 * table.numel(), interleaved,
+                   rot_scale, eps, _device_array("positions", positions, torch.int32, T),
+                   _device_array("table", table, torch.int64, 0),
+                   _device_array("norm_w", norm_w, torch.bfloat16, D))
+    _check(load().smoe_rope(a, _handle(stream, x)), "smoe_rope")
     return out
 
 
@@ -673,8 +698,7 @@ def kv_append(q, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     vp, vr, vh, vdt = _heads("v", v)
     if v.shape != k.shape or (Hkv, D) != (k_pages.shape[1], k_pages.shape[3]):
         raise ValueError("k and v must be [rows, kv heads, head_dim] of the pages")
-    qp = op = None
-    qr = qh = orow = oh = H = 0
+    qp = op = qr = qh = orow = oh = H = 0
     qdt = dt
     if q is not None:
         if q.shape[0] != T or q.shape[2] != D:
@@ -688,14 +712,14 @@ def kv_append(q, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         op, orow, oh, _ = _heads("q_out", q_out)
     if not dt == vdt == qdt:
         raise TypeError("q, k and v must have one dtype")
-    a = KvAppendArgs(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, kp, vp,
+    a = _pack_append(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, kp, vp,
                      op, qr, qh, kr, kh, vr, vh, orow, oh, H, dt,
                      0 if table is None else 2 * table.numel(), interleaved, rot_scale, eps,
                      _device_array("positions", positions, torch.int32, T),
-                     _device_array("table", table, torch.int64),
+                     _device_array("table", table, torch.int64, 0),
                      _device_array("q_norm", q_norm, torch.bfloat16, D),
                      _device_array("k_norm", k_norm, torch.bfloat16, D))
-    _check(load().smoe_kv_append(ctypes.byref(a), _stream(stream)), "smoe_kv_append")
+    _check(load().smoe_kv_append(a, _handle(stream, k)), "smoe_kv_append")
     return q_out if q is not None else None
 
 
@@ -726,10 +750,10 @@ def attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     op, orow, oh, odt = _heads("out", out)
-    a = AttentionArgs(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, op,
-                      qr, qh, orow, oh, H, odt, max_rows, window,
-                      D ** -0.5 if scale is None else scale)
-    _check(load().smoe_attention(ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream(stream)),
+    a = _pack_attention(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, op,
+                        qr, qh, orow, oh, H, odt, max_rows, window,
+                        D ** -0.5 if scale is None else scale)
+    _check(load().smoe_attention(a, ws.data_ptr(), ws.nbytes, _handle(stream, q)),
            "smoe_attention")
     return out
 
