@@ -28,7 +28,7 @@ constexpr int kDecStages = 3;  // steps in flight per warp
 __host__ __device__ constexpr int dec_step_bytes(int D) { return 2 * kDecKeys * D * 2; }
 __host__ __device__ constexpr int dec_smem_bytes(int D)
 {
-    return kDecWarps * kDecStages * dec_step_bytes(D);
+    return kDecWarps * kDecStages * dec_step_bytes(D) + (SMOE_MAX_SEQS + 1) * 16;  // rings, sequences
 }
 
 // 16-byte chunk c of row r of a tile of 2 D bytes per row: the low three
@@ -83,64 +83,78 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr)
 constexpr int kItemSteps = 3;
 constexpr int kMaxCtas = 256;
 
-// Key steps of one item of s (0: no rows).  A row that sees nothing still
-// takes a step: it writes its zeros.
-__device__ __forceinline__ int item_steps(const smoe_attention_args &a, const Seq &s)
+// A sequence of the batch in shared memory, with the place of its first item
+// on the line of steps.
+struct RowSeq {
+    int row0, rows, len;
+    uint32_t at;
+};
+
+// Key steps of one item (0: no rows).  A row that sees nothing still takes a
+// step: it writes its zeros.
+__device__ __forceinline__ int item_steps(const smoe_attention_args &a, int rows, int len)
 {
-    if (s.rows == 0)
+    if (rows == 0)
         return 0;
     int lo, hi, x, y;
-    seen(a, s, 0, lo, x);
-    seen(a, s, s.rows - 1, y, hi);
+    seen_from(a, len - rows, lo, x);
+    seen_from(a, len - 1, y, hi);
     const int n = hi > lo ? (hi + kDecKeys - 1) / kDecKeys - lo / kDecKeys : 0;
     return n > 1 ? n : 1;
 }
 
-// Where a worker's share begins.
+// How the line of steps is shared.
 struct Share {
-    int64_t q;       // steps per worker
-    int64_t total;   // steps of the launch
-    int64_t before;  // steps before the sequence that holds its first
-    int b;           // that sequence
+    uint32_t q, total;  // steps per worker, in all
 };
 
 // Steps per worker: an equal share, but no item in so many parts that the
 // joining costs more than the sharing saves.  A CTA reads a part in about
 // 1/8 of the time that it takes for 8 steps, so n steps are read and joined
 // fastest by about sqrt(n) CTAs.
-__device__ __forceinline__ int64_t steps_per_worker(int64_t total, int longest)
+__device__ __forceinline__ uint32_t steps_per_worker(uint32_t total, int longest)
 {
-    const int64_t q = ceil_div(total, (int64_t)gridDim.x * kDecWarps);
-    const int64_t least = static_cast<int64_t>(sqrtf(static_cast<float>(longest)) * 0.125f);
+    const uint32_t workers = gridDim.x * kDecWarps;
+    const uint32_t q = total / workers + (total % workers != 0);
+    const uint32_t least = static_cast<uint32_t>(sqrtf(static_cast<float>(longest)) * 0.125f);
     return q > least ? q : (least > 1 ? least : 1);
 }
 
-// The shares of the CTA's warps.  Thread t looks at the sequences
-// [t per, (t + 1) per), SMOE_MAX_SEQS in all at most.
-__device__ __forceinline__ Share find_share(const smoe_attention_args &a, int *status)
+// The batch into shared memory (n + 1 entries), and the shares.  Each thread
+// takes `per` sequences in a row.  The line has fewer than 2^32 steps; a batch
+// beyond that is recorded and not worked on.
+__device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs, int *status)
 {
-    constexpr int kThreads = 32 * kDecWarps, kPer = SMOE_MAX_SEQS / kThreads;
-    static_assert(kPer * kThreads == SMOE_MAX_SEQS, "sequences per thread");
-    __shared__ int64_t s_sum[kDecWarps];
+    __shared__ uint32_t s_sum[kDecWarps];
     __shared__ int s_max[kDecWarps];
-    __shared__ Share s_share[kDecWarps];
+    __shared__ int s_over;
+    constexpr int kThreads = 32 * kDecWarps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = a.batch.num_seqs, per = (n + kThreads - 1) / kThreads;
-    int u[kPer];  // steps of an item, its own cost included
-    int64_t sum = 0;
+    const int n = a.batch.num_seqs, per = (n + kThreads - 1) / kThreads, Hkv = a.cache.num_kv_heads;
+    if (tid == 0)
+        s_over = 0;
+    uint32_t sum = 0;
     int mx = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    float all = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
-        const int k = i < per && b < n ? item_steps(a, seq_at(a, b, status)) : 0;
-        u[i] = k > 0 ? k + kItemSteps : 0;
-        sum += u[i];
+        if (b >= n)
+            break;
+        const Seq s = seq_at(a, b, status);
+        const int k = item_steps(a, s.rows, s.len);
+        seqs[b].row0 = static_cast<int>(s.row0);
+        seqs[b].rows = s.rows;
+        seqs[b].len = s.len;
+        seqs[b].at = k > 0 ? k + kItemSteps : 0;
+        sum += seqs[b].at;
+        all += static_cast<float>(seqs[b].at) * static_cast<float>(Hkv);
         mx = k > mx ? k : mx;
     }
-    int64_t incl = sum;
+    uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
         incl += lane >= o ? v : 0;
         const int m = __shfl_xor_sync(0xffffffffu, mx, o);
         mx = m > mx ? m : mx;
@@ -150,125 +164,161 @@ __device__ __forceinline__ Share find_share(const smoe_attention_args &a, int *s
     if (lane == 0)
         s_max[warp] = mx;
     __syncthreads();
-    int64_t total = 0, before = 0;
+    if (all > 1.0e6f * 16.0f)  // a thread's own part: 256 of them stay below 2^32
+        s_over = 1;
+    uint32_t total = 0, before = incl - sum;
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
         before += w < warp ? s_sum[w] : 0;
         total += s_sum[w];
         mx = s_max[w] > mx ? s_max[w] : mx;
     }
-    const int Hkv = a.cache.num_kv_heads;
-    Share sh;
-    sh.total = total * Hkv;
-    sh.q = steps_per_worker(sh.total, mx);
-    int64_t at = (before + incl - sum) * Hkv;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t next = at + (int64_t)u[i] * Hkv;
-        for (int w = 0; w < kDecWarps; ++w) {
-            const int64_t w0 = ((int64_t)blockIdx.x * kDecWarps + w) * sh.q;
-            if (w0 >= at && w0 < next) {
-                sh.b = tid * per + i;
-                sh.before = at;
-                s_share[w] = sh;
-            }
-        }
-        at = next;
+    before *= Hkv;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b >= n)
+            break;
+        const uint32_t k = seqs[b].at * Hkv;
+        seqs[b].at = before;
+        before += k;
+    }
+    if (tid == 0) {
+        seqs[n].row0 = seqs[n].rows = seqs[n].len = 0;
+        seqs[n].at = total * Hkv;
     }
     __syncthreads();
-    if (((int64_t)blockIdx.x * kDecWarps + warp) * sh.q < sh.total)
-        return s_share[warp];
-    sh.b = n;  // nothing left for this worker
-    sh.before = sh.total;
+    Share sh;
+    sh.total = total * Hkv;
+    if (s_over) {
+        set_status(status, kStatusBadArg);
+        sh.total = 0;
+    }
+    sh.q = steps_per_worker(sh.total, mx);
     return sh;
 }
 
 // A place on the line of steps, at an item.
 struct Cursor {
-    Seq s, next;        // its sequence, and the one after it (loaded early)
-    int b, h, steps;    // key steps of the item
-    int64_t at;         // its first step on the line
-    int k_lo, k_hi;     // keys seen by any of its rows
+    int row0, rows, len;  // its sequence (rows 0: past the last)
+    int b, h, steps;      // key steps of the item
+    uint32_t at;          // its first step on the line
+    int k_lo, k_hi;       // keys seen by any of its rows
 };
 
-__device__ __forceinline__ void cursor_keys(const smoe_attention_args &a, Cursor &c)
+__device__ __forceinline__ void cursor_seq(const smoe_attention_args &a, const RowSeq *seqs, Cursor &c)
 {
+    c.row0 = seqs[c.b].row0;
+    c.rows = seqs[c.b].rows;
+    c.len = seqs[c.b].len;
+    c.steps = item_steps(a, c.rows, c.len);
     int x, y;
-    c.steps = item_steps(a, c.s);
-    c.k_lo = c.k_hi = 0;
-    if (c.s.rows > 0) {
-        seen(a, c.s, 0, c.k_lo, x);
-        seen(a, c.s, c.s.rows - 1, y, c.k_hi);
-    }
+    seen_from(a, c.len - c.rows, c.k_lo, x);
+    seen_from(a, c.len - 1, y, c.k_hi);
 }
 
-__device__ __forceinline__ Cursor cursor_at(const smoe_attention_args &a, const Share &sh,
-                                            int64_t w0, int *status)
+__device__ __forceinline__ Cursor cursor_at(const smoe_attention_args &a, const RowSeq *seqs, uint32_t w0)
 {
     Cursor c;
-    c.b = sh.b;
-    c.s = seq_or_none(a, c.b, status);
-    c.next = seq_or_none(a, c.b + 1, status);
-    cursor_keys(a, c);
-    const int len = c.steps + kItemSteps;
-    c.h = c.steps ? static_cast<int>((w0 - sh.before) / len) : 0;
-    c.at = sh.before + (int64_t)c.h * len;
+    int lo = 0, hi = a.batch.num_seqs;  // the last sequence that begins at or before w0
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seqs[mid].at <= w0)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    c.b = lo;
+    cursor_seq(a, seqs, c);
+    const uint32_t len = c.steps + kItemSteps;
+    c.h = c.rows ? (w0 - seqs[lo].at) / len : 0;
+    c.at = seqs[lo].at + c.h * len;
     return c;
 }
 
-// To the next item; past the last one its sequence has no rows.
-__device__ __forceinline__ void cursor_next(const smoe_attention_args &a, Cursor &c, int *status)
+// To the next item.
+__device__ __forceinline__ void cursor_next(const smoe_attention_args &a, const RowSeq *seqs, Cursor &c)
 {
     c.at += c.steps + kItemSteps;
     if (++c.h < a.cache.num_kv_heads)
         return;
     c.h = 0;
-    do {
+    do
         ++c.b;
-        c.s = c.next;
-        c.next = seq_or_none(a, c.b + 1, status);
-    } while (c.s.rows == 0 && c.b < a.batch.num_seqs);
-    cursor_keys(a, c);
+    while (seqs[c.b].rows == 0 && c.b < a.batch.num_seqs);
+    cursor_seq(a, seqs, c);
 }
 
 // Key steps [s0, s1) of the cursor's item that lie in the share [w0, w1).
-__device__ __forceinline__ void steps_in(const Cursor &c, int64_t w0, int64_t w1, int &s0, int &s1)
+__device__ __forceinline__ void steps_in(const Cursor &c, uint32_t w0, uint32_t w1, int &s0, int &s1)
 {
-    const int64_t k = c.at + kItemSteps;
+    const uint32_t k = c.at + kItemSteps;
     s0 = w0 > k ? static_cast<int>(w0 - k) : 0;
-    s1 = w1 - k < c.steps ? static_cast<int>(w1 - k) : c.steps;
+    s1 = w1 <= k ? 0 : (w1 - k < static_cast<uint32_t>(c.steps) ? static_cast<int>(w1 - k) : c.steps);
 }
 
 // A part that a warp leaves for its CTA to join.
 struct PartInfo {
-    const float *at;   // outputs [rows][D], maxima [rows], sums [rows]
-    int64_t row0;
-    int nrows, h;      // packed rows (0: no part)
-    int64_t first, last;  // the workers that share the item
+    const float *at;       // outputs [rows][D], maxima [rows], sums [rows]
+    int row0;
+    int nrows, h;          // packed rows (0: no part)
+    uint32_t first, last;  // the workers that share the item
 };
 
 __host__ __device__ constexpr int dec_part_floats(int D) { return kDecRows * (D + 2); }
 
-// Joins two parts' (maximum, sum, pair of outputs).
-__device__ __forceinline__ void join_part(float &m, float &l, float2 &v, float pm, float pl, float2 y)
-{
-    const float mn = fmaxf(m, pm);
-    const float fo = mn == -INFINITY ? 0.f : ex2(m - mn), fn = mn == -INFINITY ? 0.f : ex2(pm - mn);
-    v.x = v.x * fo + y.x * fn;
-    v.y = v.y * fo + y.y * fn;
-    l = l * fo + pl * fn;
-    m = mn;
-}
-
-__device__ __forceinline__ void write_out(const smoe_attention_args &a, int G, int64_t row0, int h, int r,
-                                          int c, float2 v, float l)
+// N consecutive outputs of a row, divided by the row's sum.
+template <int N>
+__device__ __forceinline__ void write_out(const smoe_attention_args &a, int G, int row0, int h, int r, int c,
+                                          const float (&v)[N], float l)
 {
     const float inv = l > 0.f ? 1.0f / l : 0.f;  // a row that sees no key: zeros
-    const int64_t at = (row0 + r / G) * a.out_row_stride + (int64_t)(h * G + r % G) * a.out_head_stride + c;
-    if (a.out_dtype == SMOE_F32)
-        *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(v.x * inv, v.y * inv);
-    else
-        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at) = pack_bf16x2(v.x * inv, v.y * inv);
+    const int64_t at = (row0 + static_cast<int64_t>(r / G)) * a.out_row_stride +
+                       (int64_t)(h * G + r % G) * a.out_head_stride + c;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        if (a.out_dtype == SMOE_F32)
+            *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at + i) =
+                make_float2(v[i] * inv, v[i + 1] * inv);
+        else
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at + i) =
+                pack_bf16x2(v[i] * inv, v[i + 1] * inv);
+    }
+}
+
+// Joins row r of n parts (part(k): where part k lies) in the order k = 0, 1,
+// ...: one warp, a lane holds D / 32 consecutive outputs.  CG: the parts come
+// from other SMs, so they are read past the L1 cache.
+template <int D, bool CG, class Part>
+__device__ __forceinline__ void join_row(Part part, int n, int r, int lane, float &m, float &l,
+                                         float (&v)[D / 32])
+{
+    auto ld = [](const float *p) { return CG ? __ldcg(p) : *p; };
+    m = -INFINITY;
+    for (int k = lane; k < n; k += 32)
+        m = fmaxf(m, ld(part(k) + kDecRows * D + r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        v[i] = 0.f;
+    if (m == -INFINITY)
+        return;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+        const float *p = part(k);
+        const float f = ex2(ld(p + kDecRows * D + r) - m);
+        l += ld(p + kDecRows * (D + 1) + r) * f;
+        const float2 *src = reinterpret_cast<const float2 *>(p + r * D + lane * (D / 32));
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const float2 y = CG ? __ldcg(src + i) : src[i];
+            v[2 * i] = fmaf(y.x, f, v[2 * i]);
+            v[2 * i + 1] = fmaf(y.y, f, v[2 * i + 1]);
+        }
+    }
 }
 
 template <int D>
@@ -279,7 +329,6 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     __shared__ PartInfo s_part[kDecWarps][2];  // 0: of an item begun earlier, 1: begun here
     __shared__ int s_last;
     constexpr int KB = D / 16;  // k blocks of Q K^T, pairs of column blocks of P V
-    constexpr int kThreads = 32 * kDecWarps;
     static_assert(dec_part_floats(D) * 4 <= kDecStages * dec_step_bytes(D), "a part fits a ring");
     static_assert(kPartsAt + (size_t)kMaxCtas * (kDecWarps + 2) * dec_part_floats(D) * 4 <=
                       SMOE_ATTENTION_WORKSPACE_BYTES,
@@ -289,14 +338,17 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     const int g = lane >> 2, c2 = 2 * (lane & 3);
     const float sc = a.scale * 1.44269504088896341f;
 
-    const Share sh = find_share(a, status);
-    const int64_t me = (int64_t)blockIdx.x * kDecWarps + warp;
-    if ((int64_t)blockIdx.x * kDecWarps * sh.q >= sh.total)
+    RowSeq *seqs = reinterpret_cast<RowSeq *>(smem + kDecWarps * kDecStages * dec_step_bytes(D));
+    const Share sh = plan(a, seqs, status);
+    const uint32_t me = blockIdx.x * kDecWarps + warp;
+    if ((uint64_t)blockIdx.x * kDecWarps * sh.q >= sh.total)
         return;  // nothing for the whole CTA
     if (lane == 0)
         s_part[warp][0].nrows = s_part[warp][1].nrows = 0;
-    const int64_t w0 = me * sh.q, w1 = w0 + sh.q;
-    Cursor cc = cursor_at(a, sh, w0, status), ld = cc;
+    // shares end at the line's end
+    const uint32_t w0 = (uint64_t)me * sh.q < sh.total ? me * sh.q : sh.total;
+    const uint32_t w1 = sh.total - w0 > sh.q ? w0 + sh.q : sh.total;
+    Cursor cc = cursor_at(a, seqs, w0), ld = cc;
     const uint32_t ring = smem_u32(smem) + warp * kDecStages * dec_step_bytes(D);
     unsigned *arrived = reinterpret_cast<unsigned *>(workspace);
     float *worker_parts = reinterpret_cast<float *>(workspace + kPartsAt);  // one per worker
@@ -307,22 +359,22 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     int ls, ls1, filled = 0, pg = 0;
     steps_in(ld, w0, w1, ls, ls1);
     auto seek = [&]() {  // to a step that exists, or past the share
-        while (ld.s.rows > 0 && ls >= ls1) {
+        while (ld.rows > 0 && ls >= ls1) {
             if (ld.at + ld.steps + kItemSteps >= w1) {
-                ld.s.rows = 0;
+                ld.rows = 0;
                 break;
             }
-            cursor_next(a, ld, status);
+            cursor_next(a, seqs, ld);
             steps_in(ld, w0, w1, ls, ls1);
         }
         const int k0 = (ld.k_lo / kDecKeys + ls) * kDecKeys;
-        pg = ld.s.rows > 0 && k0 < ld.k_hi
+        pg = ld.rows > 0 && k0 < ld.k_hi
                  ? a.batch.page_table[(int64_t)ld.b * a.batch.table_stride + k0 / page]
                  : 0;
     };
     seek();
     auto issue = [&]() {
-        if (ld.s.rows > 0) {
+        if (ld.rows > 0) {
             const int k0 = (ld.k_lo / kDecKeys + ls) * kDecKeys;
             if (k0 < ld.k_hi) {
                 const bool there = pg >= 0 && pg < a.cache.num_pages;
@@ -354,16 +406,16 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         issue();
 
     int used = 0;  // the ring's reading end
-    for (; cc.s.rows > 0 && cc.at < w1; cursor_next(a, cc, status)) {
+    for (; cc.rows > 0 && cc.at < w1; cursor_next(a, seqs, cc)) {
         int s0, s1;
         steps_in(cc, w0, w1, s0, s1);
         if (s0 >= s1)
             continue;
         // ---- one item, or the part of it that lies in the share
-        const int nrows = cc.s.rows * G;  // packed rows, kDecRows at most
+        const int nrows = cc.rows * G;  // packed rows, kDecRows at most
         int lo[2], hi[2], t_lo, t_hi, x;  // [t_lo, t_hi) is seen by every row
-        seen(a, cc.s, cc.s.rows - 1, t_lo, x);
-        seen(a, cc.s, 0, x, t_hi);
+        seen_from(a, cc.len - 1, t_lo, x);
+        seen_from(a, cc.len - cc.rows, x, t_hi);
         uint32_t q[KB][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -371,9 +423,9 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
             const bool on = m < nrows;
             lo[r] = hi[r] = 0;
             if (on)
-                seen(a, cc.s, m / G, lo[r], hi[r]);
+                seen_from(a, cc.len - cc.rows + m / G, lo[r], hi[r]);
             const uint16_t *src = static_cast<const uint16_t *>(a.q) +
-                                  (cc.s.row0 + m / G) * a.q_row_stride +
+                                  (cc.row0 + static_cast<int64_t>(m / G)) * a.q_row_stride +
                                   (int64_t)(cc.h * G + m % G) * a.q_head_stride;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
@@ -474,22 +526,23 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
             for (int r = 0; r < 2; ++r)
                 if (g + 8 * r < nrows)
 #pragma unroll
-                    for (int n = 0; n < 2 * KB; ++n)
-                        write_out(a, G, cc.s.row0, cc.h, g + 8 * r, 8 * n + c2,
-                                  make_float2(o[n][2 * r], o[n][2 * r + 1]), sum[r]);
+                    for (int n = 0; n < 2 * KB; ++n) {
+                        const float v[2] = {o[n][2 * r], o[n][2 * r + 1]};
+                        write_out<2>(a, G, cc.row0, cc.h, g + 8 * r, 8 * n + c2, v, sum[r]);
+                    }
         } else {
             // a part: into the warp's ring where no later item has keys in the
             // share (every copy has been used then), else into the workspace,
             // while the ring works on
             const int which = s0 == 0 ? 1 : 0;
-            const int64_t after = cc.at + cc.steps + kItemSteps;
-            const bool idle = after + kItemSteps >= w1 || after >= sh.total;
+            const uint32_t after = cc.at + cc.steps + kItemSteps;
+            const bool idle = after >= w1 || w1 - after <= kItemSteps;
             float *part = idle ? reinterpret_cast<float *>(smem + warp * kDecStages * dec_step_bytes(D))
-                               : worker_parts + me * dec_part_floats(D);
+                               : worker_parts + (int64_t)me * dec_part_floats(D);
             if (lane == 0) {
                 PartInfo &pi = s_part[warp][which];
                 pi.at = part;
-                pi.row0 = cc.s.row0;
+                pi.row0 = cc.row0;
                 pi.nrows = nrows;
                 pi.h = cc.h;
                 pi.first = (cc.at + kItemSteps) / sh.q;
@@ -511,8 +564,10 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     cp_async_wait<0>();
     __syncthreads();
     // ---- join the CTA's parts: of the item begun before it, then of the items
-    // begun by each warp
-    const int64_t b0 = (int64_t)blockIdx.x * kDecWarps;
+    // begun by each warp.  Warp w joins the rows w, w + 8.
+    const uint32_t b0 = blockIdx.x * kDecWarps;
+    constexpr int kPer = D / 32;  // outputs of a lane
+#pragma unroll 1
     for (int j = -1; j < kDecWarps; ++j) {
         const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
         if (pi.nrows == 0)
@@ -522,23 +577,20 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         const int c_first = static_cast<int>(pi.first / kDecWarps), c_last = static_cast<int>(pi.last / kDecWarps);
         const bool whole = c_first == c_last;
         float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D);
-        for (int e = tid; e < pi.nrows * (D / 2); e += kThreads) {
-            const int r = e / (D / 2), c = 2 * (e % (D / 2));
-            float m = -INFINITY, l = 0.f;
-            float2 v = make_float2(0.f, 0.f);
-            for (int w = wa; w <= wb; ++w) {
-                const float *p = s_part[w][w == j ? 1 : 0].at;
-                join_part(m, l, v, p[kDecRows * D + r], p[kDecRows * (D + 1) + r],
-                          *reinterpret_cast<const float2 *>(p + r * D + c));
-            }
+        float m, l, v[kPer];
+        for (int r = warp; r < pi.nrows; r += kDecWarps) {
+            join_row<D, false>([&](int k) { return s_part[wa + k][wa + k == j ? 1 : 0].at; }, wb - wa + 1, r, lane,
+                               m, l, v);
             if (whole) {
-                write_out(a, G, pi.row0, pi.h, r, c, v, l);
-            } else {
-                __stcg(reinterpret_cast<float2 *>(out + r * D + c), v);
-                if (c == 0) {
-                    __stcg(out + kDecRows * D + r, m);
-                    __stcg(out + kDecRows * (D + 1) + r, l);
-                }
+                write_out<kPer>(a, G, pi.row0, pi.h, r, lane * kPer, v, l);
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2)
+                __stcg(reinterpret_cast<float2 *>(out + r * D + lane * kPer + i), make_float2(v[i], v[i + 1]));
+            if (lane == 0) {
+                __stcg(out + kDecRows * D + r, m);
+                __stcg(out + kDecRows * (D + 1) + r, l);
             }
         }
         if (whole)
@@ -552,17 +604,13 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         if (!s_last)
             continue;
         __threadfence();
-        for (int e = tid; e < pi.nrows * (D / 2); e += kThreads) {
-            const int r = e / (D / 2), c = 2 * (e % (D / 2));
-            float m = -INFINITY, l = 0.f;
-            float2 v = make_float2(0.f, 0.f);
-#pragma unroll 4
-            for (int k = c_first; k <= c_last; ++k) {
-                const float *p = cta_parts + (2 * (int64_t)k + (k == c_first ? 1 : 0)) * dec_part_floats(D);
-                join_part(m, l, v, __ldcg(p + kDecRows * D + r), __ldcg(p + kDecRows * (D + 1) + r),
-                          __ldcg(reinterpret_cast<const float2 *>(p + r * D + c)));
-            }
-            write_out(a, G, pi.row0, pi.h, r, c, v, l);
+        for (int r = warp; r < pi.nrows; r += kDecWarps) {
+            join_row<D, true>(
+                [&](int k) {
+                    return cta_parts + (2 * (int64_t)(c_first + k) + (k == 0 ? 1 : 0)) * dec_part_floats(D);
+                },
+                c_last - c_first + 1, r, lane, m, l, v);
+            write_out<kPer>(a, G, pi.row0, pi.h, r, lane * kPer, v, l);
         }
         if (tid == 0)
             arrived[c_first] = 0;  // for the next launch
