@@ -106,7 +106,13 @@ __device__ __forceinline__ int item_steps(const smoe_attention_args &a, int rows
 // How the line of steps is shared.
 struct Share {
     uint32_t q, total;  // steps per worker, in all
+    uint32_t unit;      // an item's length is rounded up to a multiple of this
 };
+
+__device__ __forceinline__ uint32_t item_length(int steps, uint32_t unit)
+{
+    return (steps + kItemSteps + unit - 1) / unit * unit;
+}
 
 // Steps per worker: an equal share, but no item in so many parts that the
 // joining costs more than the sharing saves.  A CTA reads a part in about
@@ -125,7 +131,7 @@ __device__ __forceinline__ uint32_t steps_per_worker(uint32_t total, int longest
 // beyond that is recorded and not worked on.
 __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs, int *status)
 {
-    __shared__ uint32_t s_sum[kDecWarps];
+    __shared__ uint32_t s_sum[2][kDecWarps];
     __shared__ int s_max[kDecWarps];
     __shared__ int s_over;
     constexpr int kThreads = 32 * kDecWarps;
@@ -133,7 +139,10 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
     const int n = a.batch.num_seqs, per = (n + kThreads - 1) / kThreads, Hkv = a.cache.num_kv_heads;
     if (tid == 0)
         s_over = 0;
-    uint32_t sum = 0;
+    // Lengths as they are, and rounded up to the steps that a CTA takes at one
+    // per worker: where the grid has room for the latter, every CTA works on
+    // one item only and has one join.
+    uint32_t sum[2] = {0, 0};
     int mx = 0;
     float all = 0.f;
 #pragma unroll 1
@@ -146,55 +155,68 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
         seqs[b].row0 = static_cast<int>(s.row0);
         seqs[b].rows = s.rows;
         seqs[b].len = s.len;
-        seqs[b].at = k > 0 ? k + kItemSteps : 0;
-        sum += seqs[b].at;
-        all += static_cast<float>(seqs[b].at) * static_cast<float>(Hkv);
+        seqs[b].at = k;
+        if (k > 0) {
+            sum[0] += item_length(k, 1);
+            sum[1] += item_length(k, kDecWarps);
+            all += static_cast<float>(k + 2 * kDecWarps) * static_cast<float>(Hkv);
+        }
         mx = k > mx ? k : mx;
     }
-    uint32_t incl = sum;
+    uint32_t incl[2] = {sum[0], sum[1]};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        incl += lane >= o ? v : 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl[j], o);
+            incl[j] += lane >= o ? v : 0;
+        }
         const int m = __shfl_xor_sync(0xffffffffu, mx, o);
         mx = m > mx ? m : mx;
     }
-    if (lane == 31)
-        s_sum[warp] = incl;
+    if (lane == 31) {
+        s_sum[0][warp] = incl[0];
+        s_sum[1][warp] = incl[1];
+    }
     if (lane == 0)
         s_max[warp] = mx;
     __syncthreads();
-    if (all > 1.0e6f * 16.0f)  // a thread's own part: 256 of them stay below 2^32
+    if (all > 1.6e7f)  // of a thread: 256 of them stay below 2^32
         s_over = 1;
-    uint32_t total = 0, before = incl - sum;
+    uint32_t total[2] = {0, 0}, before[2] = {incl[0] - sum[0], incl[1] - sum[1]};
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
-        before += w < warp ? s_sum[w] : 0;
-        total += s_sum[w];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            before[j] += w < warp ? s_sum[j][w] : 0;
+            total[j] += s_sum[j][w];
+        }
         mx = s_max[w] > mx ? s_max[w] : mx;
     }
-    before *= Hkv;
+    Share sh;
+    sh.q = steps_per_worker(total[0] * Hkv, mx);
+    const bool room = sh.q == 1 && total[1] * Hkv <= gridDim.x * kDecWarps;
+    sh.unit = room ? kDecWarps : 1;
+    sh.total = total[room] * Hkv;
+    uint32_t at = before[room] * Hkv;
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= n)
             break;
-        const uint32_t k = seqs[b].at * Hkv;
-        seqs[b].at = before;
-        before += k;
+        const int k = seqs[b].at;
+        seqs[b].at = at;
+        at += k > 0 ? item_length(k, sh.unit) * Hkv : 0;
     }
     if (tid == 0) {
         seqs[n].row0 = seqs[n].rows = seqs[n].len = 0;
-        seqs[n].at = total * Hkv;
+        seqs[n].at = sh.total;
     }
     __syncthreads();
-    Share sh;
-    sh.total = total * Hkv;
     if (s_over) {
         set_status(status, kStatusBadArg);
         sh.total = 0;
     }
-    sh.q = steps_per_worker(sh.total, mx);
     return sh;
 }
 
@@ -202,22 +224,26 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
 struct Cursor {
     int row0, rows, len;  // its sequence (rows 0: past the last)
     int b, h, steps;      // key steps of the item
+    uint32_t len_line;    // its length on the line
     uint32_t at;          // its first step on the line
     int k_lo, k_hi;       // keys seen by any of its rows
 };
 
-__device__ __forceinline__ void cursor_seq(const smoe_attention_args &a, const RowSeq *seqs, Cursor &c)
+__device__ __forceinline__ void cursor_seq(const smoe_attention_args &a, const Share &sh, const RowSeq *seqs,
+                                           Cursor &c)
 {
     c.row0 = seqs[c.b].row0;
     c.rows = seqs[c.b].rows;
     c.len = seqs[c.b].len;
     c.steps = item_steps(a, c.rows, c.len);
+    c.len_line = item_length(c.steps, sh.unit);
     int x, y;
     seen_from(a, c.len - c.rows, c.k_lo, x);
     seen_from(a, c.len - 1, y, c.k_hi);
 }
 
-__device__ __forceinline__ Cursor cursor_at(const smoe_attention_args &a, const RowSeq *seqs, uint32_t w0)
+__device__ __forceinline__ Cursor cursor_at(const smoe_attention_args &a, const Share &sh, const RowSeq *seqs,
+                                            uint32_t w0)
 {
     Cursor c;
     int lo = 0, hi = a.batch.num_seqs;  // the last sequence that begins at or before w0
@@ -229,24 +255,24 @@ __device__ __forceinline__ Cursor cursor_at(const smoe_attention_args &a, const 
             hi = mid - 1;
     }
     c.b = lo;
-    cursor_seq(a, seqs, c);
-    const uint32_t len = c.steps + kItemSteps;
-    c.h = c.rows ? (w0 - seqs[lo].at) / len : 0;
-    c.at = seqs[lo].at + c.h * len;
+    cursor_seq(a, sh, seqs, c);
+    c.h = c.rows ? (w0 - seqs[lo].at) / c.len_line : 0;
+    c.at = seqs[lo].at + c.h * c.len_line;
     return c;
 }
 
 // To the next item.
-__device__ __forceinline__ void cursor_next(const smoe_attention_args &a, const RowSeq *seqs, Cursor &c)
+__device__ __forceinline__ void cursor_next(const smoe_attention_args &a, const Share &sh, const RowSeq *seqs,
+                                            Cursor &c)
 {
-    c.at += c.steps + kItemSteps;
+    c.at += c.len_line;
     if (++c.h < a.cache.num_kv_heads)
         return;
     c.h = 0;
     do
         ++c.b;
     while (seqs[c.b].rows == 0 && c.b < a.batch.num_seqs);
-    cursor_seq(a, seqs, c);
+    cursor_seq(a, sh, seqs, c);
 }
 
 // Key steps [s0, s1) of the cursor's item that lie in the share [w0, w1).
@@ -287,36 +313,62 @@ __device__ __forceinline__ void write_out(const smoe_attention_args &a, int G, i
 }
 
 // Joins row r of n parts (part(k): where part k lies) in the order k = 0, 1,
-// ...: one warp, a lane holds D / 32 consecutive outputs.  CG: the parts come
-// from other SMs, so they are read past the L1 cache.
+// ...: half a warp per row, a lane holds D / 16 consecutive outputs.  Parts
+// are taken eight at a time, all their loads in flight together: the join
+// waits for latency, not for bandwidth.  CG: the parts come from other SMs,
+// so they are read past the L1 cache.
 template <int D, bool CG, class Part>
 __device__ __forceinline__ void join_row(Part part, int n, int r, int lane, float &m, float &l,
-                                         float (&v)[D / 32])
+                                         float (&v)[D / 16])
 {
+    constexpr int kBatch = 8, kPer = D / 16;
     auto ld = [](const float *p) { return CG ? __ldcg(p) : *p; };
+    auto ld4 = [](const float *p) {
+        const float4 *q = reinterpret_cast<const float4 *>(p);
+        return CG ? __ldcg(q) : *q;
+    };
     m = -INFINITY;
-    for (int k = lane; k < n; k += 32)
-        m = fmaxf(m, ld(part(k) + kDecRows * D + r));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     l = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < kPer; ++i)
         v[i] = 0.f;
-    if (m == -INFINITY)
-        return;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-        const float *p = part(k);
-        const float f = ex2(ld(p + kDecRows * D + r) - m);
-        l += ld(p + kDecRows * (D + 1) + r) * f;
-        const float2 *src = reinterpret_cast<const float2 *>(p + r * D + lane * (D / 32));
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+        float pm[kBatch], pl[kBatch];
+        float4 y[kBatch][kPer / 4];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            const float2 y = CG ? __ldcg(src + i) : src[i];
-            v[2 * i] = fmaf(y.x, f, v[2 * i]);
-            v[2 * i + 1] = fmaf(y.y, f, v[2 * i + 1]);
+        for (int k = 0; k < kBatch; ++k) {
+            const bool on = k0 + k < n;
+            const float *p = part(on ? k0 + k : 0);
+            pm[k] = on ? ld(p + kDecRows * D + r) : -INFINITY;
+            pl[k] = on ? ld(p + kDecRows * (D + 1) + r) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer / 4; ++i)
+                y[k][i] = on ? ld4(p + r * D + lane * kPer + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            mn = fmaxf(mn, pm[k]);
+        if (mn == -INFINITY)
+            continue;  // nothing seen so far
+        const float fo = ex2(m - mn);
+        m = mn;
+        l *= fo;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            v[i] *= fo;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float f = ex2(pm[k] - mn);
+            l = fmaf(pl[k], f, l);
+#pragma unroll
+            for (int i = 0; i < kPer / 4; ++i) {
+                v[4 * i] = fmaf(y[k][i].x, f, v[4 * i]);
+                v[4 * i + 1] = fmaf(y[k][i].y, f, v[4 * i + 1]);
+                v[4 * i + 2] = fmaf(y[k][i].z, f, v[4 * i + 2]);
+                v[4 * i + 3] = fmaf(y[k][i].w, f, v[4 * i + 3]);
+            }
         }
     }
 }
@@ -327,7 +379,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PartInfo s_part[kDecWarps][2];  // 0: of an item begun earlier, 1: begun here
-    __shared__ int s_last;
+    __shared__ int s_final[kDecWarps + 1];     // this CTA joins the item's parts of all CTAs
     constexpr int KB = D / 16;  // k blocks of Q K^T, pairs of column blocks of P V
     static_assert(dec_part_floats(D) * 4 <= kDecStages * dec_step_bytes(D), "a part fits a ring");
     static_assert(kPartsAt + (size_t)kMaxCtas * (kDecWarps + 2) * dec_part_floats(D) * 4 <=
@@ -348,7 +400,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     // shares end at the line's end
     const uint32_t w0 = (uint64_t)me * sh.q < sh.total ? me * sh.q : sh.total;
     const uint32_t w1 = sh.total - w0 > sh.q ? w0 + sh.q : sh.total;
-    Cursor cc = cursor_at(a, seqs, w0), ld = cc;
+    Cursor cc = cursor_at(a, sh, seqs, w0), ld = cc;
     const uint32_t ring = smem_u32(smem) + warp * kDecStages * dec_step_bytes(D);
     unsigned *arrived = reinterpret_cast<unsigned *>(workspace);
     float *worker_parts = reinterpret_cast<float *>(workspace + kPartsAt);  // one per worker
@@ -360,11 +412,11 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     steps_in(ld, w0, w1, ls, ls1);
     auto seek = [&]() {  // to a step that exists, or past the share
         while (ld.rows > 0 && ls >= ls1) {
-            if (ld.at + ld.steps + kItemSteps >= w1) {
+            if (ld.at + ld.len_line >= w1) {
                 ld.rows = 0;
                 break;
             }
-            cursor_next(a, seqs, ld);
+            cursor_next(a, sh, seqs, ld);
             steps_in(ld, w0, w1, ls, ls1);
         }
         const int k0 = (ld.k_lo / kDecKeys + ls) * kDecKeys;
@@ -406,7 +458,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         issue();
 
     int used = 0;  // the ring's reading end
-    for (; cc.rows > 0 && cc.at < w1; cursor_next(a, seqs, cc)) {
+    for (; cc.rows > 0 && cc.at < w1; cursor_next(a, sh, seqs, cc)) {
         int s0, s1;
         steps_in(cc, w0, w1, s0, s1);
         if (s0 >= s1)
@@ -535,7 +587,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
             // share (every copy has been used then), else into the workspace,
             // while the ring works on
             const int which = s0 == 0 ? 1 : 0;
-            const uint32_t after = cc.at + cc.steps + kItemSteps;
+            const uint32_t after = cc.at + cc.len_line;
             const bool idle = after >= w1 || w1 - after <= kItemSteps;
             float *part = idle ? reinterpret_cast<float *>(smem + warp * kDecStages * dec_step_bytes(D))
                                : worker_parts + (int64_t)me * dec_part_floats(D);
@@ -564,53 +616,63 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     cp_async_wait<0>();
     __syncthreads();
     // ---- join the CTA's parts: of the item begun before it, then of the items
-    // begun by each warp.  Warp w joins the rows w, w + 8.
+    // begun by each warp.  Each half warp takes one row of one item at a time.
+    constexpr int kPer = D / 16;  // outputs of a lane
     const uint32_t b0 = blockIdx.x * kDecWarps;
-    constexpr int kPer = D / 32;  // outputs of a lane
+    const int hw = tid >> 4, l16 = lane & 15;
+    float m, l, v[kPer];
+    int base = 0;  // rows of the items so far
 #pragma unroll 1
     for (int j = -1; j < kDecWarps; ++j) {
         const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
-        if (pi.nrows == 0)
-            continue;
+        // rows go round over the half warps, whatever item they are of
+        const int r0 = (hw - base) & (2 * kDecWarps - 1);
+        base += pi.nrows;
         const int wa = j < 0 ? 0 : j;
         const int wb = pi.last - b0 < kDecWarps ? static_cast<int>(pi.last - b0) : kDecWarps - 1;
-        const int c_first = static_cast<int>(pi.first / kDecWarps), c_last = static_cast<int>(pi.last / kDecWarps);
-        const bool whole = c_first == c_last;
-        float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D);
-        float m, l, v[kPer];
-        for (int r = warp; r < pi.nrows; r += kDecWarps) {
-            join_row<D, false>([&](int k) { return s_part[wa + k][wa + k == j ? 1 : 0].at; }, wb - wa + 1, r, lane,
-                               m, l, v);
-            if (whole) {
-                write_out<kPer>(a, G, pi.row0, pi.h, r, lane * kPer, v, l);
+        for (int r = r0; r < pi.nrows; r += 2 * kDecWarps) {
+            join_row<D, false>([&](int k) { return s_part[wa + k][wa + k == j ? 1 : 0].at; }, wb - wa + 1, r, l16, m,
+                               l, v);
+            if (pi.first / kDecWarps == pi.last / kDecWarps) {
+                write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, v, l);
                 continue;
             }
+            // the item goes over CTAs
+            float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D);
 #pragma unroll
-            for (int i = 0; i < kPer; i += 2)
-                __stcg(reinterpret_cast<float2 *>(out + r * D + lane * kPer + i), make_float2(v[i], v[i + 1]));
-            if (lane == 0) {
+            for (int i = 0; i < kPer; i += 4)
+                __stcg(reinterpret_cast<float4 *>(out + r * D + l16 * kPer + i),
+                       make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+            if (l16 == 0) {
                 __stcg(out + kDecRows * D + r, m);
                 __stcg(out + kDecRows * (D + 1) + r, l);
             }
+            __threadfence();
         }
-        if (whole)
+    }
+    // ---- of the items that go over CTAs (the one begun before this CTA, the
+    // last one begun in it), the last CTA to arrive joins the parts
+    __syncthreads();
+    if (tid <= kDecWarps) {
+        const PartInfo &pi = s_part[tid ? tid - 1 : 0][tid ? 1 : 0];
+        const uint32_t c_first = pi.first / kDecWarps, c_last = pi.last / kDecWarps;
+        s_final[tid] = pi.nrows > 0 && c_first != c_last && atomicAdd(arrived + c_first, 1u) == c_last - c_first;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int j = -1; j < kDecWarps; ++j) {
+        if (!s_final[j + 1])
             continue;
-        // the item goes over CTAs: the last to arrive joins their parts
         __threadfence();
-        __syncthreads();
-        if (tid == 0)
-            s_last = atomicAdd(arrived + c_first, 1u) == static_cast<unsigned>(c_last - c_first);
-        __syncthreads();
-        if (!s_last)
-            continue;
-        __threadfence();
-        for (int r = warp; r < pi.nrows; r += kDecWarps) {
+        const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
+        const int c_first = static_cast<int>(pi.first / kDecWarps), c_last = static_cast<int>(pi.last / kDecWarps);
+        if (hw < pi.nrows) {
             join_row<D, true>(
                 [&](int k) {
                     return cta_parts + (2 * (int64_t)(c_first + k) + (k == 0 ? 1 : 0)) * dec_part_floats(D);
                 },
-                c_last - c_first + 1, r, lane, m, l, v);
-            write_out<kPer>(a, G, pi.row0, pi.h, r, lane * kPer, v, l);
+                c_last - c_first + 1, hw, l16, m, l, v);
+            write_out<kPer>(a, G, pi.row0, pi.h, hw, l16 * kPer, v, l);
         }
         if (tid == 0)
             arrived[c_first] = 0;  // for the next launch
