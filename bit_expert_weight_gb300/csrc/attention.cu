@@ -21,14 +21,20 @@ namespace smoe {
 namespace {
 
 constexpr int kDecWarps = 8;   // warps per CTA, each with keys of its own
-constexpr int kDecRows = 16;   // packed rows per tile (mma M)
+constexpr int kMmaRows = 16;   // packed rows of an mma tile (mma M)
 constexpr int kDecKeys = 16;   // keys per warp and step (mma K of P V); a page holds them
-constexpr int kDecStages = 3;  // steps in flight per warp
 
+// The kernel's instances by tiles per item, T: up to 16 packed rows, the
+// queries in registers and three steps in flight per warp; or up to 32, the
+// queries in shared memory and two steps in flight.
+__host__ __device__ constexpr int dec_rows(int T) { return T * kMmaRows; }
+__host__ __device__ constexpr int dec_stages(int T) { return T == 1 ? 3 : 2; }
 __host__ __device__ constexpr int dec_step_bytes(int D) { return 2 * kDecKeys * D * 2; }
-__host__ __device__ constexpr int dec_smem_bytes(int D)
+__host__ __device__ constexpr int dec_ring_bytes(int D, int T) { return dec_stages(T) * dec_step_bytes(D); }
+__host__ __device__ constexpr int dec_query_bytes(int D, int T) { return T == 1 ? 0 : dec_rows(T) * D * 2; }
+__host__ __device__ constexpr int dec_smem_bytes(int D, int T)
 {
-    return kDecWarps * kDecStages * dec_step_bytes(D) + (SMOE_MAX_SEQS + 1) * 16;  // rings, sequences
+    return kDecWarps * (dec_ring_bytes(D, T) + dec_query_bytes(D, T)) + (SMOE_MAX_SEQS + 1) * 16;
 }
 
 // 16-byte chunk c of row r of a tile of 2 D bytes per row: the low three
@@ -70,7 +76,7 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr)
 
 // ------------------------------------------------- few rows (decode steps)
 
-// Sequences of at most kDecRows packed rows: bound by reading the keys and
+// Sequences of at most 16 (or 32) packed rows: bound by reading the keys and
 // values.  The work of a launch is one line of steps: for every sequence and
 // kv head (an item) kItemSteps for its own cost (its queries, its output),
 // then its keys in steps of kDecKeys.  Every warp of the grid is a worker
@@ -197,8 +203,8 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
     sh.q = steps_per_worker(total[0] * Hkv, mx);
     const bool room = sh.q == 1 && total[1] * Hkv <= gridDim.x * kDecWarps;
     sh.unit = room ? kDecWarps : 1;
-    sh.total = total[room] * Hkv;
-    uint32_t at = before[room] * Hkv;
+    sh.total = (room ? total[1] : total[0]) * Hkv;
+    uint32_t at = (room ? before[1] : before[0]) * Hkv;
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
@@ -291,7 +297,7 @@ struct PartInfo {
     uint32_t first, last;  // the workers that share the item
 };
 
-__host__ __device__ constexpr int dec_part_floats(int D) { return kDecRows * (D + 2); }
+__host__ __device__ constexpr int dec_part_floats(int D, int T) { return dec_rows(T) * (D + 2); }
 
 // N consecutive outputs of a row, divided by the row's sum.
 template <int N>
@@ -317,7 +323,7 @@ __device__ __forceinline__ void write_out(const smoe_attention_args &a, int G, i
 // are taken eight at a time, all their loads in flight together: the join
 // waits for latency, not for bandwidth.  CG: the parts come from other SMs,
 // so they are read past the L1 cache.
-template <int D, bool CG, class Part>
+template <int D, int T, bool CG, class Part>
 __device__ __forceinline__ void join_row(Part part, int n, int r, int lane, float &m, float &l,
                                          float (&v)[D / 16])
 {
@@ -340,8 +346,8 @@ __device__ __forceinline__ void join_row(Part part, int n, int r, int lane, floa
         for (int k = 0; k < kBatch; ++k) {
             const bool on = k0 + k < n;
             const float *p = part(on ? k0 + k : 0);
-            pm[k] = on ? ld(p + kDecRows * D + r) : -INFINITY;
-            pl[k] = on ? ld(p + kDecRows * (D + 1) + r) : 0.f;
+            pm[k] = on ? ld(p + dec_rows(T) * D + r) : -INFINITY;
+            pl[k] = on ? ld(p + dec_rows(T) * (D + 1) + r) : 0.f;
 #pragma unroll
             for (int i = 0; i < kPer / 4; ++i)
                 y[k][i] = on ? ld4(p + r * D + lane * kPer + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -373,7 +379,7 @@ __device__ __forceinline__ void join_row(Part part, int n, int r, int lane, floa
     }
 }
 
-template <int D>
+template <int D, int T>
 __global__ void __launch_bounds__(32 * kDecWarps, 1)
     attend_rows_kernel(const smoe_attention_args a, uint8_t *workspace, int *status)
 {
@@ -381,8 +387,10 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     __shared__ PartInfo s_part[kDecWarps][2];  // 0: of an item begun earlier, 1: begun here
     __shared__ int s_final[kDecWarps + 1];     // this CTA joins the item's parts of all CTAs
     constexpr int KB = D / 16;  // k blocks of Q K^T, pairs of column blocks of P V
-    static_assert(dec_part_floats(D) * 4 <= kDecStages * dec_step_bytes(D), "a part fits a ring");
-    static_assert(kPartsAt + (size_t)kMaxCtas * (kDecWarps + 2) * dec_part_floats(D) * 4 <=
+    constexpr int kStages = dec_stages(T), kRows = dec_rows(T);
+    static_assert(dec_part_floats(D, T) * 4 <= dec_ring_bytes(D, T) + dec_query_bytes(D, T),
+                  "a part fits a ring and its queries");
+    static_assert(kPartsAt + (size_t)kMaxCtas * (kDecWarps + 2) * dec_part_floats(D, T) * 4 <=
                       SMOE_ATTENTION_WORKSPACE_BYTES,
                   "workspace");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     const int g = lane >> 2, c2 = 2 * (lane & 3);
     const float sc = a.scale * 1.44269504088896341f;
 
-    RowSeq *seqs = reinterpret_cast<RowSeq *>(smem + kDecWarps * kDecStages * dec_step_bytes(D));
+    RowSeq *seqs = reinterpret_cast<RowSeq *>(smem + kDecWarps * (dec_ring_bytes(D, T) + dec_query_bytes(D, T)));
     const Share sh = plan(a, seqs, status);
     const uint32_t me = blockIdx.x * kDecWarps + warp;
     if ((uint64_t)blockIdx.x * kDecWarps * sh.q >= sh.total)
@@ -401,10 +409,12 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     const uint32_t w0 = (uint64_t)me * sh.q < sh.total ? me * sh.q : sh.total;
     const uint32_t w1 = sh.total - w0 > sh.q ? w0 + sh.q : sh.total;
     Cursor cc = cursor_at(a, sh, seqs, w0), ld = cc;
-    const uint32_t ring = smem_u32(smem) + warp * kDecStages * dec_step_bytes(D);
+    // a warp's memory: its ring, then its queries (T > 1)
+    const uint32_t ring = smem_u32(smem) + warp * (dec_ring_bytes(D, T) + dec_query_bytes(D, T));
+    const uint32_t query = ring + dec_ring_bytes(D, T);
     unsigned *arrived = reinterpret_cast<unsigned *>(workspace);
     float *worker_parts = reinterpret_cast<float *>(workspace + kPartsAt);  // one per worker
-    float *cta_parts = worker_parts + (int64_t)kMaxCtas * kDecWarps * dec_part_floats(D);  // two per CTA
+    float *cta_parts = worker_parts + (int64_t)kMaxCtas * kDecWarps * dec_part_floats(D, T);  // two per CTA
 
     // The loading end of the ring: the next step to copy, its page id already
     // on the way.
@@ -447,14 +457,14 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
                     cp_async16(dv + chunk_at<D>(r, c), vs + (v ? r * D + c * 8 : 0), v);
                 }
             }
-            filled = filled + 1 == kDecStages ? 0 : filled + 1;
+            filled = filled + 1 == kStages ? 0 : filled + 1;
             ++ls;
             seek();
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int st = 0; st < kDecStages - 1; ++st)
+    for (int st = 0; st < kStages - 1; ++st)
         issue();
 
     int used = 0;  // the ring's reading end
@@ -464,124 +474,168 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         if (s0 >= s1)
             continue;
         // ---- one item, or the part of it that lies in the share
-        const int nrows = cc.rows * G;  // packed rows, kDecRows at most
-        int lo[2], hi[2], t_lo, t_hi, x;  // [t_lo, t_hi) is seen by every row
+        const int nrows = cc.rows * G;  // packed rows, kRows at most
+        int lo[T][2], hi[T][2], t_lo, t_hi, x;  // [t_lo, t_hi) is seen by every row
         seen_from(a, cc.len - 1, t_lo, x);
         seen_from(a, cc.len - cc.rows, x, t_hi);
-        uint32_t q[KB][4];
+        // row m of the item in q
+        auto query_at = [&](int m) {
+            return static_cast<const uint16_t *>(a.q) + (cc.row0 + static_cast<int64_t>(m / G)) * a.q_row_stride +
+                   (int64_t)(cc.h * G + m % G) * a.q_head_stride;
+        };
+        uint32_t q[T == 1 ? KB : 1][4];
+        if (T == 1) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int m = g + 8 * r;
-            const bool on = m < nrows;
-            lo[r] = hi[r] = 0;
-            if (on)
-                seen_from(a, cc.len - cc.rows + m / G, lo[r], hi[r]);
-            const uint16_t *src = static_cast<const uint16_t *>(a.q) +
-                                  (cc.row0 + static_cast<int64_t>(m / G)) * a.q_row_stride +
-                                  (int64_t)(cc.h * G + m % G) * a.q_head_stride;
+            for (int r = 0; r < 2; ++r) {
+                const int m = g + 8 * r;
+                const bool on = m < nrows;
+                const uint16_t *src = query_at(m);
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                q[kb][r] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * kb + c2) : 0u;
-                q[kb][2 + r] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * kb + 8 + c2) : 0u;
+                for (int kb = 0; kb < (T == 1 ? KB : 0); ++kb) {
+                    q[kb][r] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * kb + c2) : 0u;
+                    q[kb][2 + r] = on ? *reinterpret_cast<const uint32_t *>(src + 16 * kb + 8 + c2) : 0u;
+                }
             }
+        } else {
+            __syncwarp();  // the queries before are no longer read
+#pragma unroll 4
+            for (int e = lane; e < kRows * (D / 8); e += 32) {
+                const int m = e / (D / 8), c = e % (D / 8);
+                cp_async16(query + chunk_at<D>(m, c), m < nrows ? query_at(m) + c * 8 : a.q, m < nrows);
+            }
+            // (they come with the copies of the next step)
         }
-        float o[2 * KB][4];
+        float o[T][2 * KB][4], mx[T][2], sum[T][2];
 #pragma unroll
-        for (int n = 0; n < 2 * KB; ++n)
-            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        for (int t = 0; t < T; ++t) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int m = kMmaRows * t + g + 8 * r;
+                lo[t][r] = hi[t][r] = 0;
+                if (m < nrows)
+                    seen_from(a, cc.len - cc.rows + m / G, lo[t][r], hi[t][r]);
+                mx[t][r] = -INFINITY;
+                sum[t][r] = 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < 2 * KB; ++n)
+                o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+        }
         int k0 = (cc.k_lo / kDecKeys + s0) * kDecKeys;
 
         for (int st = s0; st < s1; ++st, k0 += kDecKeys) {
             issue();
-            cp_async_wait<kDecStages - 1>();
+            if (T > 1 && st == s0)
+                cp_async_wait<0>();  // the queries too
+            else
+                cp_async_wait<kStages - 1>();
             __syncwarp();
             const uint32_t dk = ring + used * dec_step_bytes(D), dv = dk + kDecKeys * D * 2;
-            used = used + 1 == kDecStages ? 0 : used + 1;
+            used = used + 1 == kStages ? 0 : used + 1;
             if (k0 >= cc.k_hi)
                 continue;  // no row sees a key: nothing was copied
-            float p[2][4] = {};
+            float p[T][2][4] = {};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 uint32_t b[4];
                 ldm4(b, dk + chunk_at<D>((lane & 7) + ((lane >> 4) << 3), 2 * kb + ((lane >> 3) & 1)));
-                mma_bf16(p[0], q[kb], b[0], b[1]);
-                mma_bf16(p[1], q[kb], b[2], b[3]);
-            }
-            if (k0 < t_lo || k0 + kDecKeys > t_hi) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = k0 + 8 * n + c2 + (e & 1), r = e >> 1;
-                        if (key < lo[r] || key >= hi[r])
-                            p[n][e] = -INFINITY;
-                    }
-            }
-            float f[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float v = fmaxf(fmaxf(p[0][2 * r], p[0][2 * r + 1]),
-                                fmaxf(p[1][2 * r], p[1][2 * r + 1]));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                const float mn = fmaxf(mx[r], v * sc);
-                const float mu = mn == -INFINITY ? 0.f : mn;  // a row that has seen nothing yet
-                f[r] = ex2(mx[r] - mu);
-                mx[r] = mn;
-                float t = 0.f;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &y = p[n][2 * r + e];
-                        y = ex2(fmaf(y, sc, -mu));
-                        t += y;
-                    }
-                sum[r] = sum[r] * f[r] + t;
-            }
-            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
-#pragma unroll
-                for (int n = 0; n < 2 * KB; ++n) {
-                    o[n][0] *= f[0];
-                    o[n][1] *= f[0];
-                    o[n][2] *= f[1];
-                    o[n][3] *= f[1];
+                for (int t = 0; t < T; ++t) {
+                    uint32_t qs[4];
+                    if (T > 1)
+                        ldm4(qs, query + chunk_at<D>(kMmaRows * t + (lane & 15), 2 * kb + (lane >> 4)));
+                    const uint32_t (&qf)[4] = T > 1 ? qs : q[T == 1 ? kb : 0];
+                    mma_bf16(p[t][0], qf, b[0], b[1]);
+                    mma_bf16(p[t][1], qf, b[2], b[3]);
                 }
             }
             // P as bf16 hi + lo: the loop waits for memory, not for the second
             // product, and the output keeps fp32 accuracy
-            uint32_t hi4[4], lo4[4];
-            split_bf16x2(p[0][0], p[0][1], hi4[0], lo4[0]);
-            split_bf16x2(p[0][2], p[0][3], hi4[1], lo4[1]);
-            split_bf16x2(p[1][0], p[1][1], hi4[2], lo4[2]);
-            split_bf16x2(p[1][2], p[1][3], hi4[3], lo4[3]);
+            uint32_t hi4[T][4], lo4[T][4];
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                if (k0 < t_lo || k0 + kDecKeys > t_hi) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = k0 + 8 * n + c2 + (e & 1), r = e >> 1;
+                            if (key < lo[t][r] || key >= hi[t][r])
+                                p[t][n][e] = -INFINITY;
+                        }
+                }
+                float f[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float v = fmaxf(fmaxf(p[t][0][2 * r], p[t][0][2 * r + 1]),
+                                    fmaxf(p[t][1][2 * r], p[t][1][2 * r + 1]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                    const float mn = fmaxf(mx[t][r], v * sc);
+                    const float mu = mn == -INFINITY ? 0.f : mn;  // a row that has seen nothing yet
+                    f[r] = ex2(mx[t][r] - mu);
+                    mx[t][r] = mn;
+                    float y = 0.f;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float &w = p[t][n][2 * r + e];
+                            w = ex2(fmaf(w, sc, -mu));
+                            y += w;
+                        }
+                    sum[t][r] = sum[t][r] * f[r] + y;
+                }
+                if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+                    for (int n = 0; n < 2 * KB; ++n) {
+                        o[t][n][0] *= f[0];
+                        o[t][n][1] *= f[0];
+                        o[t][n][2] *= f[1];
+                        o[t][n][3] *= f[1];
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        split_bf16x2(p[t][n][2 * r], p[t][n][2 * r + 1], hi4[t][2 * n + r], lo4[t][2 * n + r]);
+            }
 #pragma unroll
             for (int n = 0; n < KB; ++n) {
                 uint32_t b[4];
                 ldm4t(b, dv + chunk_at<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
-                mma_bf16(o[2 * n], hi4, b[0], b[1]);
-                mma_bf16(o[2 * n], lo4, b[0], b[1]);
-                mma_bf16(o[2 * n + 1], hi4, b[2], b[3]);
-                mma_bf16(o[2 * n + 1], lo4, b[2], b[3]);
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    mma_bf16(o[t][2 * n], hi4[t], b[0], b[1]);
+                    mma_bf16(o[t][2 * n], lo4[t], b[0], b[1]);
+                    mma_bf16(o[t][2 * n + 1], hi4[t], b[2], b[3]);
+                    mma_bf16(o[t][2 * n + 1], lo4[t], b[2], b[3]);
+                }
             }
             __syncwarp();
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-        }
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                sum[t][r] += __shfl_xor_sync(0xffffffffu, sum[t][r], 1);
+                sum[t][r] += __shfl_xor_sync(0xffffffffu, sum[t][r], 2);
+            }
         if (s0 == 0 && s1 == cc.steps) {
             // the whole item
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (g + 8 * r < nrows)
+            for (int t = 0; t < T; ++t)
 #pragma unroll
-                    for (int n = 0; n < 2 * KB; ++n) {
-                        const float v[2] = {o[n][2 * r], o[n][2 * r + 1]};
-                        write_out<2>(a, G, cc.row0, cc.h, g + 8 * r, 8 * n + c2, v, sum[r]);
-                    }
+                for (int r = 0; r < 2; ++r) {
+                    const int m = kMmaRows * t + g + 8 * r;
+                    if (m < nrows)
+#pragma unroll
+                        for (int n = 0; n < 2 * KB; ++n) {
+                            const float v[2] = {o[t][n][2 * r], o[t][n][2 * r + 1]};
+                            write_out<2>(a, G, cc.row0, cc.h, m, 8 * n + c2, v, sum[t][r]);
+                        }
+                }
         } else {
             // a part: into the warp's ring where no later item has keys in the
             // share (every copy has been used then), else into the workspace,
@@ -589,8 +643,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
             const int which = s0 == 0 ? 1 : 0;
             const uint32_t after = cc.at + cc.len_line;
             const bool idle = after >= w1 || w1 - after <= kItemSteps;
-            float *part = idle ? reinterpret_cast<float *>(smem + warp * kDecStages * dec_step_bytes(D))
-                               : worker_parts + (int64_t)me * dec_part_floats(D);
+            float *part = idle ? reinterpret_cast<float *>(smem + warp * (dec_ring_bytes(D, T) + dec_query_bytes(D, T)))
+                               : worker_parts + (int64_t)me * dec_part_floats(D, T);
             if (lane == 0) {
                 PartInfo &pi = s_part[warp][which];
                 pi.at = part;
@@ -601,16 +655,21 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
                 pi.last = (cc.at + kItemSteps + cc.steps - 1) / sh.q;
             }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int n = 0; n < 2 * KB; ++n)
-                    *reinterpret_cast<float2 *>(part + (g + 8 * r) * D + 8 * n + c2) =
-                        make_float2(o[n][2 * r], o[n][2 * r + 1]);
-                if ((lane & 3) == 0) {
-                    part[kDecRows * D + g + 8 * r] = mx[r];
-                    part[kDecRows * (D + 1) + g + 8 * r] = sum[r];
+                for (int r = 0; r < 2; ++r) {
+                    const int m = kMmaRows * t + g + 8 * r;
+                    if (m >= nrows)
+                        continue;
+#pragma unroll
+                    for (int n = 0; n < 2 * KB; ++n)
+                        *reinterpret_cast<float2 *>(part + m * D + 8 * n + c2) =
+                            make_float2(o[t][n][2 * r], o[t][n][2 * r + 1]);
+                    if ((lane & 3) == 0) {
+                        part[kRows * D + m] = mx[t][r];
+                        part[kRows * (D + 1) + m] = sum[t][r];
+                    }
                 }
-            }
         }
     }
     cp_async_wait<0>();
@@ -631,21 +690,21 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         const int wa = j < 0 ? 0 : j;
         const int wb = pi.last - b0 < kDecWarps ? static_cast<int>(pi.last - b0) : kDecWarps - 1;
         for (int r = r0; r < pi.nrows; r += 2 * kDecWarps) {
-            join_row<D, false>([&](int k) { return s_part[wa + k][wa + k == j ? 1 : 0].at; }, wb - wa + 1, r, l16, m,
+            join_row<D, T, false>([&](int k) { return s_part[wa + k][wa + k == j ? 1 : 0].at; }, wb - wa + 1, r, l16, m,
                                l, v);
             if (pi.first / kDecWarps == pi.last / kDecWarps) {
                 write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, v, l);
                 continue;
             }
             // the item goes over CTAs
-            float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D);
+            float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D, T);
 #pragma unroll
             for (int i = 0; i < kPer; i += 4)
                 __stcg(reinterpret_cast<float4 *>(out + r * D + l16 * kPer + i),
                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
             if (l16 == 0) {
-                __stcg(out + kDecRows * D + r, m);
-                __stcg(out + kDecRows * (D + 1) + r, l);
+                __stcg(out + kRows * D + r, m);
+                __stcg(out + kRows * (D + 1) + r, l);
             }
             __threadfence();
         }
@@ -666,28 +725,29 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         __threadfence();
         const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
         const int c_first = static_cast<int>(pi.first / kDecWarps), c_last = static_cast<int>(pi.last / kDecWarps);
-        if (hw < pi.nrows) {
-            join_row<D, true>(
+        for (int r = hw; r < pi.nrows; r += 2 * kDecWarps) {
+            join_row<D, T, true>(
                 [&](int k) {
-                    return cta_parts + (2 * (int64_t)(c_first + k) + (k == 0 ? 1 : 0)) * dec_part_floats(D);
+                    return cta_parts + (2 * (int64_t)(c_first + k) + (k == 0 ? 1 : 0)) * dec_part_floats(D, T);
                 },
-                c_last - c_first + 1, hw, l16, m, l, v);
-            write_out<kPer>(a, G, pi.row0, pi.h, hw, l16 * kPer, v, l);
+                c_last - c_first + 1, r, l16, m, l, v);
+            write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, v, l);
         }
         if (tid == 0)
             arrived[c_first] = 0;  // for the next launch
     }
 }
 
-template <int D>
+template <int D, int T>
 cudaError_t launch_rows(const smoe_attention_args &a, uint8_t *workspace, const DeviceFacts &dev,
                         cudaStream_t stream)
 {
     static std::atomic<bool> allowed[kMaxDeviceIndex];
-    const cudaError_t e = allow_smem(attend_rows_kernel<D>, dec_smem_bytes(D), dev, allowed);
+    constexpr int smem = dec_smem_bytes(D, T);
+    const cudaError_t e = allow_smem(attend_rows_kernel<D, T>, smem, dev, allowed);
     if (e != cudaSuccess)
         return e;
-    attend_rows_kernel<D><<<dev.sms < kMaxCtas ? dev.sms : kMaxCtas, 32 * kDecWarps, dec_smem_bytes(D), stream>>>(
+    attend_rows_kernel<D, T><<<dev.sms < kMaxCtas ? dev.sms : kMaxCtas, 32 * kDecWarps, smem, stream>>>(
         a, workspace, dev.status);
     return cudaGetLastError();
 }
@@ -698,10 +758,13 @@ cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, cons
                              cudaStream_t stream)
 {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int G = a.num_heads / a.cache.num_kv_heads;
-    if ((int64_t)a.max_rows * G > kDecRows)
-        return launch_attention_chunk(a, ws, dev, stream);
-    return a.cache.head_dim == 64 ? launch_rows<64>(a, ws, dev, stream) : launch_rows<128>(a, ws, dev, stream);
+    const int64_t rows = (int64_t)a.max_rows * (a.num_heads / a.cache.num_kv_heads);
+    const bool wide = a.cache.head_dim == 128;
+    if (rows <= dec_rows(1))
+        return wide ? launch_rows<128, 1>(a, ws, dev, stream) : launch_rows<64, 1>(a, ws, dev, stream);
+    if (rows <= dec_rows(2))
+        return wide ? launch_rows<128, 2>(a, ws, dev, stream) : launch_rows<64, 2>(a, ws, dev, stream);
+    return launch_attention_chunk(a, ws, dev, stream);
 }
 
 }  // namespace smoe

@@ -48,6 +48,9 @@ SINGLE = [
     ([1] * 4, [1, 2, 130, 1000], 8, 2, 128, 16, 1),
     ([2] * 3, [2, 40, 700], 16, 2, 128, 16, 0),
     ([3, 1, 0, 5], [1, 1, 0, 3], 6, 2, 64, 16, 0),            # chunks longer than kv_len
+    ([2] * 40, [(331 * i) % 1200 + 2 for i in range(40)], 32, 2, 128, 16, 0),
+    ([7, 7, 0, 1], [7, 3, 300, 4000], 8, 2, 64, 64, 64),
+    ([6, 2], [700, 5], 5, 1, 128, 32, 200),
 ]
 CHUNKS = [
     ([5] * 6, [5, 6, 130, 131, 997, 4000], 32, 8, 128, 32, 0),
