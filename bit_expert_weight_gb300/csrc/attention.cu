@@ -267,6 +267,16 @@ __device__ __forceinline__ Cursor cursor_at(const smoe_attention_args &a, const 
     return c;
 }
 
+// Where the border between two shares that nominally lies at x, in the
+// cursor's item, is drawn: at x, or at the nearer end of an item of at most
+// half a share, which is not worth being cut.
+__device__ __forceinline__ uint32_t border(const Share &sh, const Cursor &c, uint32_t x)
+{
+    if (x <= c.at || 2 * c.len_line > sh.q)
+        return x;
+    return 2 * (x - c.at) < c.len_line ? c.at : c.at + c.len_line;
+}
+
 // To the next item.
 __device__ __forceinline__ void cursor_next(const smoe_attention_args &a, const Share &sh, const RowSeq *seqs,
                                             Cursor &c)
@@ -318,65 +328,91 @@ __device__ __forceinline__ void write_out(const smoe_attention_args &a, int G, i
     }
 }
 
-// Joins row r of n parts (part(k): where part k lies) in the order k = 0, 1,
-// ...: half a warp per row, a lane holds D / 16 consecutive outputs.  Parts
-// are taken eight at a time, all their loads in flight together: the join
-// waits for latency, not for bandwidth.  CG: the parts come from other SMs,
-// so they are read past the L1 cache.
-template <int D, int T, bool CG, class Part>
-__device__ __forceinline__ void join_row(Part part, int n, int r, int lane, float &m, float &l,
-                                         float (&v)[D / 16])
-{
-    constexpr int kBatch = 8, kPer = D / 16;
-    auto ld = [](const float *p) { return CG ? __ldcg(p) : *p; };
-    auto ld4 = [](const float *p) {
-        const float4 *q = reinterpret_cast<const float4 *>(p);
-        return CG ? __ldcg(q) : *q;
-    };
-    m = -INFINITY;
-    l = 0.f;
+// A row's maximum, sum and the D / 16 consecutive outputs of a lane: half a
+// warp per row.
+template <int D>
+struct RowPart {
+    float m, l, v[D / 16];
+
+    __device__ __forceinline__ void clear()
+    {
+        m = -INFINITY;
+        l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        v[i] = 0.f;
+        for (int i = 0; i < D / 16; ++i)
+            v[i] = 0.f;
+    }
+    // Adds a part: its maximum, sum and outputs.
+    __device__ __forceinline__ void add(float pm, float pl, const float4 (&y)[D / 64])
+    {
+        const float mn = fmaxf(m, pm);
+        const float mu = mn == -INFINITY ? 0.f : mn;  // nothing seen so far
+        const float fo = ex2(m - mu), f = ex2(pm - mu);
+        m = mn;
+        l = fmaf(l, fo, pl * f);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            v[4 * i] = fmaf(v[4 * i], fo, y[i].x * f);
+            v[4 * i + 1] = fmaf(v[4 * i + 1], fo, y[i].y * f);
+            v[4 * i + 2] = fmaf(v[4 * i + 2], fo, y[i].z * f);
+            v[4 * i + 3] = fmaf(v[4 * i + 3], fo, y[i].w * f);
+        }
+    }
+};
+
+// The joins run once per launch, so most of their time is the fetching of
+// their code: the loop over a CTA's own parts stays a loop (8 parts unrolled
+// took 3,900 cycles, this 1,300), the one over other CTAs' parts, which waits
+// for the L2 cache, has the loads of four parts in flight.
+
+// Row r of the parts that warps wa .. wb of this CTA left (`tail`: warp wa's
+// is of an item begun in its share).
+template <int D, int T>
+__device__ __forceinline__ RowPart<D> join_near(const PartInfo (*parts)[2], int wa, int wb, bool tail, int r, int l16)
+{
+    RowPart<D> o;
+    o.clear();
+#pragma unroll 1
+    for (int w = wa; w <= wb; ++w) {
+        const float *p = parts[w][tail && w == wa ? 1 : 0].at;
+        float4 y[D / 64];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            y[i] = *reinterpret_cast<const float4 *>(p + r * D + l16 * (D / 16) + 4 * i);
+        o.add(p[dec_rows(T) * D + r], p[dec_rows(T) * (D + 1) + r], y);
+    }
+    return o;
+}
+
+// Row r of n parts of other CTAs: the first at `first`, part k at rest + k
+// step.  They are read past the L1 cache.
+template <int D, int T>
+__device__ __forceinline__ RowPart<D> join_far(const float *first, const float *rest, int64_t step, int n, int r,
+                                               int l16)
+{
+    constexpr int kBatch = 4;
+    RowPart<D> o;
+    o.clear();
 #pragma unroll 1
     for (int k0 = 0; k0 < n; k0 += kBatch) {
         float pm[kBatch], pl[kBatch];
-        float4 y[kBatch][kPer / 4];
+        float4 y[kBatch][D / 64];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const bool on = k0 + k < n;
-            const float *p = part(on ? k0 + k : 0);
-            pm[k] = on ? ld(p + dec_rows(T) * D + r) : -INFINITY;
-            pl[k] = on ? ld(p + dec_rows(T) * (D + 1) + r) : 0.f;
+            // past the end: the last part again, with no weight
+            const int at = k0 + k < n ? k0 + k : n - 1;
+            const float *p = at == 0 ? first : rest + at * step;
+            pm[k] = __ldcg(p + dec_rows(T) * D + r);
+            pl[k] = __ldcg(p + dec_rows(T) * (D + 1) + r);
 #pragma unroll
-            for (int i = 0; i < kPer / 4; ++i)
-                y[k][i] = on ? ld4(p + r * D + lane * kPer + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < D / 64; ++i)
+                y[k][i] = __ldcg(reinterpret_cast<const float4 *>(p + r * D + l16 * (D / 16) + 4 * i));
         }
-        float mn = m;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            mn = fmaxf(mn, pm[k]);
-        if (mn == -INFINITY)
-            continue;  // nothing seen so far
-        const float fo = ex2(m - mn);
-        m = mn;
-        l *= fo;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            v[i] *= fo;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const float f = ex2(pm[k] - mn);
-            l = fmaf(pl[k], f, l);
-#pragma unroll
-            for (int i = 0; i < kPer / 4; ++i) {
-                v[4 * i] = fmaf(y[k][i].x, f, v[4 * i]);
-                v[4 * i + 1] = fmaf(y[k][i].y, f, v[4 * i + 1]);
-                v[4 * i + 2] = fmaf(y[k][i].z, f, v[4 * i + 2]);
-                v[4 * i + 3] = fmaf(y[k][i].w, f, v[4 * i + 3]);
-            }
-        }
+            o.add(k0 + k < n ? pm[k] : -INFINITY, pl[k], y[k]);
     }
+    return o;
 }
 
 template <int D, int T>
@@ -405,10 +441,13 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         return;  // nothing for the whole CTA
     if (lane == 0)
         s_part[warp][0].nrows = s_part[warp][1].nrows = 0;
-    // shares end at the line's end
-    const uint32_t w0 = (uint64_t)me * sh.q < sh.total ? me * sh.q : sh.total;
-    const uint32_t w1 = sh.total - w0 > sh.q ? w0 + sh.q : sh.total;
-    Cursor cc = cursor_at(a, sh, seqs, w0), ld = cc;
+    // the share's borders, one per half warp; shares end at the line's end
+    const uint64_t nominal = (uint64_t)(me + (lane >> 4)) * sh.q;
+    Cursor cc = cursor_at(a, sh, seqs, nominal < sh.total ? static_cast<uint32_t>(nominal) : sh.total);
+    const uint32_t snapped = border(sh, cc, nominal < sh.total ? static_cast<uint32_t>(nominal) : sh.total);
+    const uint32_t w0 = __shfl_sync(0xffffffffu, snapped, 0), w1 = __shfl_sync(0xffffffffu, snapped, 16);
+    cc = cursor_at(a, sh, seqs, w0);
+    Cursor ld = cc;
     // a warp's memory: its ring, then its queries (T > 1)
     const uint32_t ring = smem_u32(smem) + warp * (dec_ring_bytes(D, T) + dec_query_bytes(D, T));
     const uint32_t query = ring + dec_ring_bytes(D, T);
@@ -463,11 +502,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         }
         cp_async_commit();
     };
-#pragma unroll
-    for (int st = 0; st < kStages - 1; ++st)
-        issue();
-
-    int used = 0;  // the ring's reading end
+    int used = 0, primed = 0;  // the ring's reading end, copies ahead of it
     for (; cc.rows > 0 && cc.at < w1; cursor_next(a, sh, seqs, cc)) {
         int s0, s1;
         steps_in(cc, w0, w1, s0, s1);
@@ -524,7 +559,11 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         int k0 = (cc.k_lo / kDecKeys + s0) * kDecKeys;
 
         for (int st = s0; st < s1; ++st, k0 += kDecKeys) {
-            issue();
+            // the first time as many as the ring holds
+            do
+                issue();
+            while (primed++ < kStages - 1);
+            primed = kStages;
             if (T > 1 && st == s0)
                 cp_async_wait<0>();  // the queries too
             else
@@ -679,7 +718,6 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     constexpr int kPer = D / 16;  // outputs of a lane
     const uint32_t b0 = blockIdx.x * kDecWarps;
     const int hw = tid >> 4, l16 = lane & 15;
-    float m, l, v[kPer];
     int base = 0;  // rows of the items so far
 #pragma unroll 1
     for (int j = -1; j < kDecWarps; ++j) {
@@ -690,10 +728,9 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         const int wa = j < 0 ? 0 : j;
         const int wb = pi.last - b0 < kDecWarps ? static_cast<int>(pi.last - b0) : kDecWarps - 1;
         for (int r = r0; r < pi.nrows; r += 2 * kDecWarps) {
-            join_row<D, T, false>([&](int k) { return s_part[wa + k][wa + k == j ? 1 : 0].at; }, wb - wa + 1, r, l16, m,
-                               l, v);
+            const RowPart<D> o = join_near<D, T>(s_part, wa, wb, j >= 0, r, l16);
             if (pi.first / kDecWarps == pi.last / kDecWarps) {
-                write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, v, l);
+                write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, o.v, o.l);
                 continue;
             }
             // the item goes over CTAs
@@ -701,14 +738,14 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
 #pragma unroll
             for (int i = 0; i < kPer; i += 4)
                 __stcg(reinterpret_cast<float4 *>(out + r * D + l16 * kPer + i),
-                       make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                       make_float4(o.v[i], o.v[i + 1], o.v[i + 2], o.v[i + 3]));
             if (l16 == 0) {
-                __stcg(out + kRows * D + r, m);
-                __stcg(out + kRows * (D + 1) + r, l);
+                __stcg(out + kRows * D + r, o.m);
+                __stcg(out + kRows * (D + 1) + r, o.l);
             }
-            __threadfence();
         }
     }
+    __threadfence();
     // ---- of the items that go over CTAs (the one begun before this CTA, the
     // last one begun in it), the last CTA to arrive joins the parts
     __syncthreads();
@@ -726,12 +763,11 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
         const int c_first = static_cast<int>(pi.first / kDecWarps), c_last = static_cast<int>(pi.last / kDecWarps);
         for (int r = hw; r < pi.nrows; r += 2 * kDecWarps) {
-            join_row<D, T, true>(
-                [&](int k) {
-                    return cta_parts + (2 * (int64_t)(c_first + k) + (k == 0 ? 1 : 0)) * dec_part_floats(D, T);
-                },
-                c_last - c_first + 1, r, l16, m, l, v);
-            write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, v, l);
+            // the first CTA's part, then those of the CTAs after it
+            const float *of = cta_parts + 2 * (int64_t)c_first * dec_part_floats(D, T);
+            const RowPart<D> o = join_far<D, T>(of + dec_part_floats(D, T), of, 2 * dec_part_floats(D, T),
+                                                c_last - c_first + 1, r, l16);
+            write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, o.v, o.l);
         }
         if (tid == 0)
             arrived[c_first] = 0;  // for the next launch
