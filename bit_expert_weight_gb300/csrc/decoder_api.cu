@@ -120,9 +120,10 @@ smoe_status smoe_rope(const smoe_rope_args *a, void *cuda_stream)
     if (a->out == a->x &&
         (a->x_row_stride != a->out_row_stride || a->x_head_stride != a->out_head_stride))
         return SMOE_ERR_INVALID_ARG;
-    if (!device_facts().supported)
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
         return SMOE_ERR_UNSUPPORTED;
-    return cuda_status(launch_rope(*a, static_cast<cudaStream_t>(cuda_stream)));
+    return cuda_status(launch_rope(*a, dev, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 smoe_status smoe_kv_append(const smoe_kv_append_args *a, void *cuda_stream)

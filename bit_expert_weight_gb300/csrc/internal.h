@@ -204,7 +204,7 @@ cudaError_t launch_grouped(const GroupedArgs &a, const void *x, int x_bf16, floa
 
 // ------------------------------------------- rotation, paged cache, attention
 
-cudaError_t launch_rope(const smoe_rope_args &a, cudaStream_t stream);
+cudaError_t launch_rope(const smoe_rope_args &a, const DeviceFacts &dev, cudaStream_t stream);
 cudaError_t launch_kv_append(const smoe_kv_append_args &a, const DeviceFacts &dev, cudaStream_t stream);
 cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, const DeviceFacts &dev,
                              cudaStream_t stream);
