@@ -74,11 +74,12 @@ __host__ __device__ constexpr int smem_bytes(int D)
 {
     return 2 * q_half_bytes(D) + (kKStages + kVStages) * stage_bytes(D) + 1024;  // slack for the alignment
 }
-// A part: outputs [D][rows], then the rows' m, then their sums.
+// A part: outputs [D][rows], so that a warp's lanes, a row each, write and read
+// whole sectors, then the rows' m, then their sums.
 __host__ __device__ constexpr int part_floats(int D) { return (D + 2) * kTileRows2; }
 static_assert(kPartsAt + (size_t)2 * kMaxCtas * part_floats(128) * 4 <= SMOE_ATTENTION_WORKSPACE_BYTES,
               "workspace");
-static_assert((SMOE_MAX_SEQS + 1) * sizeof(int) <= (kKStages + kVStages) * stage_bytes(64), "sequence table");
+static_assert((SMOE_MAX_SEQS + 1) * 16 <= (kKStages + kVStages) * stage_bytes(64), "sequence table");
 static_assert(kMaxCtas <= kMaxCounters, "counters");
 
 // Tensor memory columns: S (and P over it) and O of each half.
@@ -122,7 +123,9 @@ struct Smem {
     int64_t scan[kThreads / 32];
     int scan_max[kThreads / 32];
     int64_t q, total, before;    // units per CTA, in all, before the CTA's first item's tile
+    int unit;                    // an item's length is rounded up to a multiple of this
     int b, t;                    // that tile
+    Seq seq, next;               // its sequence, and the one after it
 };
 
 // ------------------------------------------------------------ PTX helpers
@@ -272,10 +275,16 @@ __device__ __forceinline__ void tile_keys(const smoe_attention_args &a, int G, T
     c.units = c.rows == 0 ? 0 : (n > 1 ? n : 1);
 }
 
-// To the next item; past the last one it has no rows.
-__device__ __forceinline__ void tile_next(const smoe_attention_args &a, int G, Tile &c, int *status)
+// An item's length on the line.
+__device__ __forceinline__ int item_length(const Tile &c, int unit)
 {
-    c.at += c.units + kItemUnits;
+    return (c.units + kItemUnits + unit - 1) / unit * unit;
+}
+
+// To the next item; past the last one it has no rows.
+__device__ __forceinline__ void tile_next(const smoe_attention_args &a, int G, int unit, Tile &c, int *status)
+{
+    c.at += item_length(c, unit);
     if (++c.h < a.cache.num_kv_heads)
         return;
     c.h = 0;
@@ -328,9 +337,23 @@ __device__ __forceinline__ int64_t scan_all(Smem &sm, int64_t v, int &mx, int64_
     return before;
 }
 
+// A sequence of the batch in shared memory, with the tiles before it.
+struct ChunkSeq {
+    int row0, rows, len, tiles;
+};
+
+__device__ __forceinline__ Seq seq_of(const ChunkSeq &c)
+{
+    Seq s;
+    s.row0 = c.row0;
+    s.rows = c.rows;
+    s.len = c.len;
+    return s;
+}
+
 // The CTA's share, into shared memory: q, total, and the tile at its start.
-// `tiles`: room for a number per sequence and one more.
-__device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, Smem &sm, int *tiles,
+// `seqs`: room for the batch and one more, in memory that is not in use yet.
+__device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, Smem &sm, ChunkSeq *seqs,
                                            int *status)
 {
     const int tid = threadIdx.x, n = a.batch.num_seqs, Hkv = a.cache.num_kv_heads;
@@ -338,84 +361,113 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
     const int per = (n + kThreads - 1) / kThreads;
     int64_t sum = 0, total;
     int mx = 0;
-    for (int b = tid * per; b < n && b < (tid + 1) * per; ++b)
-        sum += tiles_of(seq_at(a, b, status), G);
-    int64_t before = scan_all(sm, sum, mx, total);
+#pragma unroll 1
     for (int b = tid * per; b < n && b < (tid + 1) * per; ++b) {
-        tiles[b] = static_cast<int>(before);
-        before += tiles_of(seq_at(a, b, status), G);
+        const Seq s = seq_at(a, b, status);
+        seqs[b].row0 = static_cast<int>(s.row0);
+        seqs[b].rows = s.rows;
+        seqs[b].len = s.len;
+        sum += tiles_of(s, G);
+    }
+    int64_t before = scan_all(sm, sum, mx, total);
+#pragma unroll 1
+    for (int b = tid * per; b < n && b < (tid + 1) * per; ++b) {
+        seqs[b].tiles = static_cast<int>(before);
+        before += tiles_of(seq_of(seqs[b]), G);
     }
     const int all = static_cast<int>(total);
-    if (tid == 0)
-        tiles[n] = all;
+    if (tid == 0) {
+        seqs[n].row0 = seqs[n].rows = seqs[n].len = 0;
+        seqs[n].tiles = all;
+    }
     __syncthreads();
     // units of the tiles [i0, i1) of this thread
     const int pt = (all + kThreads - 1) / kThreads;
     const int i0 = tid * pt < all ? tid * pt : all, i1 = i0 + pt < all ? i0 + pt : all;
     Tile c;
     int b0 = 0, hi = n - 1;
-    while (b0 < hi) {  // last sequence with tiles[b] <= i0
+    while (b0 < hi) {  // last sequence with as many tiles before it
         const int mid = (b0 + hi + 1) >> 1;
-        if (tiles[mid] <= i0)
+        if (seqs[mid].tiles <= i0)
             b0 = mid;
         else
             hi = mid - 1;
     }
-    sum = 0;
-    for (int i = i0, b = b0; i < i1; ++i) {
-        if (i == i0 || i >= tiles[b + 1]) {
-            while (i >= tiles[b + 1])
-                ++b;
-            c.s = seq_at(a, b, status);
-        }
-        c.t = i - tiles[b];
+    auto tile_at = [&](int i, int &b) {
+        while (i >= seqs[b + 1].tiles)
+            ++b;
+        c.s = seq_of(seqs[b]);
+        c.t = i - seqs[b].tiles;
         tile_keys(a, G, c);
-        sum += c.units + kItemUnits;
-        mx = c.units > mx ? c.units : mx;
-    }
-    before = scan_all(sm, sum, mx, total) * Hkv;
-    total *= Hkv;
+    };
+    auto length = [&](int unit) {
+        int64_t l = 0;
+#pragma unroll 1
+        for (int i = i0, b = b0; i < i1; ++i) {
+            tile_at(i, b);
+            l += item_length(c, unit);
+            mx = c.units > mx ? c.units : mx;
+        }
+        return l;
+    };
+    sum = length(1);
+    before = scan_all(sm, sum, mx, total);
     // Equal shares, but no item in so many parts that the joining costs more
-    // than the sharing saves: reading a part takes about as long as a unit.
-    int64_t q = ceil_div(total, gridDim.x);
-    const int64_t least = static_cast<int64_t>(sqrtf(static_cast<float>(mx)));
+    // than the sharing saves: a cut costs about four units' time, and a part
+    // more one unit to read, so that up to ten units are best left together.
+    int64_t q = ceil_div(total * Hkv, gridDim.x);
+    const int64_t least = mx <= 10 ? mx + kItemUnits : static_cast<int64_t>(sqrtf(static_cast<float>(mx)));
     q = q > least ? q : least;
+    // Where the grid has room for it, every item begins a CTA's share, so that
+    // none is cut for the sake of its neighbours.
+    int unit = 1;
+    if (all * Hkv <= static_cast<int>(gridDim.x)) {
+        int64_t padded;
+        const int64_t own = length(static_cast<int>(q));
+        const int64_t at = scan_all(sm, own, mx, padded);
+        if (padded * Hkv <= q * gridDim.x) {
+            unit = static_cast<int>(q);
+            sum = own;
+            before = at;
+            total = padded;
+        }
+    }
+    before *= Hkv;
+    total *= Hkv;
     const int64_t w0 = q * blockIdx.x;
     if (tid == 0) {
         sm.q = q;
         sm.total = total;
+        sm.unit = unit;
     }
     if (w0 >= before && w0 < before + sum * Hkv) {
+#pragma unroll 1
         for (int i = i0, b = b0; i < i1; ++i) {
-            if (i == i0 || i >= tiles[b + 1]) {
-                while (i >= tiles[b + 1])
-                    ++b;
-                c.s = seq_at(a, b, status);
-            }
-            c.t = i - tiles[b];
-            tile_keys(a, G, c);
-            const int64_t next = before + (int64_t)(c.units + kItemUnits) * Hkv;
+            tile_at(i, b);
+            const int64_t next = before + (int64_t)item_length(c, unit) * Hkv;
             if (w0 >= before && w0 < next) {
                 sm.b = b;
                 sm.t = c.t;
                 sm.before = before;
+                sm.seq = c.s;
+                sm.next = seq_of(seqs[b + 1]);
             }
             before = next;
         }
     }
+    fence_async_smem();  // tensor copies will write where the batch lay
     __syncthreads();
 }
 
-__device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, const Smem &sm, int64_t w0,
-                                           int *status)
+__device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, const Smem &sm, int64_t w0)
 {
     Tile c;
     c.b = sm.b;
     c.t = sm.t;
-    c.s = seq_or_none(a, c.b, status);
-    c.next = seq_or_none(a, c.b + 1, status);
+    c.s = sm.seq;
+    c.next = sm.next;
     tile_keys(a, G, c);
-    const int len = c.units + kItemUnits;
+    const int len = item_length(c, sm.unit);
     c.h = static_cast<int>((w0 - sm.before) / len);
     c.at = sm.before + (int64_t)c.h * len;
     return c;
@@ -428,7 +480,7 @@ __device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64
 {
     const int lane = threadIdx.x & 31;
     uint32_t n = 0;
-    for (Tile c = first_tile(a, G, sm, w0, status);; tile_next(a, G, c, status)) {
+    for (Tile c = first_tile(a, G, sm, w0);; tile_next(a, G, sm.unit, c, status)) {
         const bool end = c.rows == 0 || c.at >= w1;
         int u0 = 0, u1 = 0;
         if (!end) {
@@ -849,13 +901,13 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
                         write_out(i, reinterpret_cast<const float *>(o), inv);
                         write_out(i + 16, reinterpret_cast<const float *>(o + 16), inv);
                     }
-                } else {
+                } else if (on) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         __stcg(part + (i + j) * kTileRows2 + m, __uint_as_float(o[j]));
                 }
             }
-            if (!whole) {
+            if (!whole && on) {
                 __stcg(part + D * kTileRows2 + m, mr);
                 __stcg(part + (D + 1) * kTileRows2 + m, sum);
             }
@@ -882,30 +934,40 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
         ++jn;
         if (*reinterpret_cast<volatile int *>(&sm.last)) {
             __threadfence();
-            if (active && on) {
+            // part j of the item
+            auto part_of = [&](int j) {
+                return parts + (2 * (int64_t)j + (j == c_first ? 1 : 0)) * part_floats(D);
+            };
+            // a lane per row: the row's maximum and sum over the parts, then its
+            // outputs, 32 of a part on their way together
+            if (on) {
                 float mj = -INFINITY, lj = 0.f;
-                for (int j = c_first; j <= c_last; ++j) {
-                    const float *p = parts + (2 * (int64_t)j + (j == c_first ? 1 : 0)) * part_floats(D);
-                    const float pm = __ldcg(p + D * kTileRows2 + m), pl = __ldcg(p + (D + 1) * kTileRows2 + m);
-                    const float mn = fmaxf(mj, pm);
-                    if (mn != -INFINITY)
-                        lj = lj * ex2(mj - mn) + pl * ex2(pm - mn);
-                    mj = mn;
-                }
+#pragma unroll 4
+                for (int j = c_first; j <= c_last; ++j)
+                    mj = fmaxf(mj, __ldcg(part_of(j) + D * kTileRows2 + m));
+                if (mj != -INFINITY)
+#pragma unroll 4
+                    for (int j = c_first; j <= c_last; ++j)
+                        lj += __ldcg(part_of(j) + (D + 1) * kTileRows2 + m) *
+                              ex2(__ldcg(part_of(j) + D * kTileRows2 + m) - mj);
                 const float inv = lj > 0.f ? 1.0f / lj : 0.f;
-                for (int i = 0; i < D; i += 16) {
-                    float v[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        v[e] = 0.f;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                    float v[32] = {};
+#pragma unroll 1
                     for (int j = c_first; j <= c_last; ++j) {
-                        const float *p = parts + (2 * (int64_t)j + (j == c_first ? 1 : 0)) * part_floats(D);
-                        const float f = mj == -INFINITY ? 0.f : ex2(__ldcg(p + D * kTileRows2 + m) - mj);
+                        const float *p = part_of(j) + i * kTileRows2 + m;
+                        float y[32];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            v[e] = fmaf(__ldcg(p + (i + e) * kTileRows2 + m), f, v[e]);
+                        for (int e = 0; e < 32; ++e)
+                            y[e] = __ldcg(p + e * kTileRows2);
+                        const float w = mj == -INFINITY ? 0.f : ex2(__ldcg(part_of(j) + D * kTileRows2 + m) - mj);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = fmaf(y[e], w, v[e]);
                     }
                     write_out(i, v, inv);
+                    write_out(i + 16, v + 16, inv);
                 }
             }
             if (threadIdx.x == 0)
@@ -954,13 +1016,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.drain, 2);
         fence_mbar_init();
     }
-    __syncthreads();
-    // (the ring is not in use yet)
-    find_share(a, G, sm, reinterpret_cast<int *>(ring), status);
-    const int64_t w0 = sm.q * blockIdx.x;
-    if (w0 >= sm.total)
-        return;  // nothing for this CTA
-    const int64_t w1 = w0 + sm.q;
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sm.tmem_base)),
@@ -971,8 +1026,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-
-    if (warp < kSoftWarps) {
+    // (the ring is not in use yet)
+    find_share(a, G, sm, reinterpret_cast<ChunkSeq *>(ring), status);
+    const int64_t w0 = sm.q * blockIdx.x;
+    const int64_t w1 = w0 + sm.q;
+    if (w0 >= sm.total) {
+        // nothing for this CTA
+    } else if (warp < kSoftWarps) {
         softmax<D>(a, G, sm, reinterpret_cast<float *>(workspace + kPartsAt),
                    reinterpret_cast<unsigned *>(workspace), warp >> 2, status);
     } else if (warp == kLoadWarp) {
