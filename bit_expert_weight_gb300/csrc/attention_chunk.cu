@@ -15,9 +15,9 @@
 // for the tensor cores but at an item's start.  (With one buffer of 128
 // columns a unit took 3,550 cycles: the exponentials and the products took
 // turns.)  m is the row's maximum when it was last raised: it follows the true
-// maximum only once that is more than 2^8 above it, so that O is rescaled
-// rarely; P is at most 2^8, its sum is kept in fp32 and the final division by
-// that sum makes the choice of m drop out.  P is rounded to bf16 for the
+// maximum only once that is more than 2^40 above it, so that O is hardly ever
+// rescaled; the final division by P's sum, kept in fp32, makes the choice of m
+// drop out.  P is rounded to bf16 for the
 // tensor cores (2^-9 of each p), the sum is not.
 //
 // Bounds, per unit: 2,048 cycles of shared memory for N = 64 products of Q
@@ -66,7 +66,9 @@ constexpr int kItemSlots = 4;
 constexpr int kThreads = 512;
 constexpr int kItemUnits = 4;           // an item's own cost, in units
 constexpr int kMaxCtas = 240;
-constexpr float kRaise = 8.0f;          // log2 of how far the maximum may run ahead of m
+// log2 of how far the maximum may run ahead of m.  P, its sum and O are floating
+// point, so a large P loses nothing; 2^40 leaves the sums room up to 2^127.
+constexpr float kRaise = 40.0f;
 
 __host__ __device__ constexpr int q_half_bytes(int D) { return kHalf * D * 2; }
 __host__ __device__ constexpr int stage_bytes(int D) { return kKeys * D * 2; }
