@@ -42,7 +42,6 @@
 // CTAs to arrive.  Every wait is bounded; one that runs out is recorded as
 // SMOE_ERR_TIMEOUT and ends the CTA's work.
 #include <cuda.h>
-#include <limits.h>
 #include <math.h>
 
 #include "attention.cuh"
@@ -108,8 +107,8 @@ struct Smem {
     uint64_t item_full[kItemSlots];   // item warp
     uint64_t item_empty[kItemSlots];  // all warps but the item warp
     Item item[kItemSlots];
-    uint64_t k_full[kKStages];   // loader: 1 arrival + bytes
-    uint64_t v_full[kVStages];   // loader: 1 arrival + bytes
+    uint64_t k_first;            // loader: the first unit's K (1 arrival + bytes, as below)
+    uint64_t kv_full[kVStages];  // loader: V of a unit and K of the next
     uint64_t v_raw;              // loader, for its own use: a V that it clears in part
     uint64_t unit_done[kFree];   // both MMA warps: the products of a unit
     uint64_t q_full[2];          // 2 query warps; the half's 4 warps: no wait of theirs on s_done is open
@@ -119,7 +118,7 @@ struct Smem {
     uint64_t joined;             // 8 warps
     uint64_t drain;              // final commits of both MMA warps
     uint32_t tmem_base;
-    uint32_t units_filled[2], raw_filled;  // K, V, v_raw (drain after a failure)
+    uint32_t k_filled, kv_filled, raw_filled;  // phases of k_first, kv_full, v_raw (drain after a failure)
     int fail, last;
     // the work split
     int64_t scan[kThreads / 32];
@@ -231,6 +230,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+// More bytes to come in the barrier's phase.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, unsigned bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
 }
 
 // Bounded wait that records a timeout in the CTA's fail flag.
@@ -604,10 +610,11 @@ __device__ __forceinline__ void clear_unseen(uint8_t *stage, int key0, int lo, i
     __syncwarp();
 }
 
-// Keys and values of every unit (warp 10): K, then V, of one unit after the
-// other.  A lane copies one 64-channel half of one page's share of the unit.
-// Pages without a key that the item sees are not read; the rest of V's first
-// and last page is cleared before the MMA warps get it.
+// Keys and values (warp 10): V of each unit together with K of the next one,
+// which take the places that one unit's products free.  A lane copies one
+// 64-channel half of one page's share of the unit.  Pages without a key that
+// the item sees are not read; the rest of V's first and last page is cleared
+// before the MMA warps get it.
 template <int D>
 __device__ void loader(const smoe_attention_args &a, const Maps *maps, Smem &sm, uint8_t *ring, int *status)
 {
@@ -615,66 +622,92 @@ __device__ void loader(const smoe_attention_args &a, const Maps *maps, Smem &sm,
     const int box = page < kKeys ? page : kKeys, boxes = kKeys / box;
     const int i = lane / (D / 64), half = lane % (D / 64);
     const int at = half * (kKeys * 128) + i * box * 128;  // of the lane's box in a stage
-    uint32_t g = 0, n = 0, raw = 0;                       // units, items, cleared V
+    uint32_t n = 0, raw = 0;                              // items, cleared V
     auto ok = [&](uint64_t *bar, unsigned parity) {
         return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
     };
-    Item c;
-    while (next_item(sm, n, c, status)) {
-        auto wanted = [&](int k0) { return i < boxes && k0 < c.k_hi && k0 + box > c.k_lo; };
-        // the page of a unit, looked up one unit ahead
-        auto page_of = [&](int u) {
-            const int k0 = c.kbase + u * kKeys + i * box;
-            return u < c.u1 && wanted(k0) ? a.batch.page_table[(int64_t)c.b * a.batch.table_stride + k0 / page]
-                                          : INT_MIN;
-        };
-        int next = page_of(c.u0);
-        for (int u = c.u0; u < c.u1; ++u, ++g) {
-            const int key0 = c.kbase + u * kKeys, k0 = key0 + i * box;
-            const int pg = next;
-            next = page_of(u + 1);
-            const bool on = pg >= 0 && pg < a.cache.num_pages;
-            if (!on && wanted(k0))
+    Item c = {};
+    // a unit's keys, and the lane's page of them (-1: none)
+    struct Unit {
+        int key0, lo, hi, head, page;
+        bool there;
+    };
+    auto unit_at = [&](int u) {
+        Unit x;
+        x.key0 = c.kbase + u * kKeys;
+        x.lo = c.k_lo;
+        x.hi = c.k_hi;
+        x.head = c.h;
+        x.there = true;
+        x.page = -1;
+        const int k0 = x.key0 + i * box;
+        if (i < boxes && k0 < c.k_hi && k0 + box > c.k_lo) {
+            x.page = a.batch.page_table[(int64_t)c.b * a.batch.table_stride + k0 / page];
+            if (x.page < 0 || x.page >= a.cache.num_pages) {
                 set_status(status, kStatusBadArg);
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, on)) * box * 128u;
-            // K takes the place of unit g - 3, V that of unit g - 2
-            if (g >= kKStages && !ok(&sm.unit_done[(g - kKStages) % kFree], ((g - kKStages) / kFree) & 1u))
-                return;
-            uint64_t *full = &sm.k_full[g % kKStages];
-            if (lane == 0) {
-                sm.units_filled[0] = g + 1;
-                mbar_arrive_expect_tx(full, bytes);
-            }
-            __syncwarp();
-            if (on)
-                tma_load_4d(ring + (g % kKStages) * stage_bytes(D) + at, &maps->k, 64 * half, k0 % page, c.h, pg,
-                            full);
-            if (g >= kVStages && !ok(&sm.unit_done[(g - kVStages) % kFree], ((g - kVStages) / kFree) & 1u))
-                return;
-            uint8_t *stage = ring + (kKStages + g % kVStages) * stage_bytes(D);
-            const bool edge = key0 < c.k_lo || key0 + kKeys > c.k_hi;
-            full = edge ? &sm.v_raw : &sm.v_full[g % kVStages];
-            if (lane == 0) {
-                if (edge)
-                    sm.raw_filled = raw + 1;
-                else
-                    sm.units_filled[1] = g + 1;
-                mbar_arrive_expect_tx(full, bytes);
-            }
-            __syncwarp();
-            if (on)
-                tma_load_4d(stage + at, &maps->v, 64 * half, k0 % page, c.h, pg, full);
-            if (edge) {
-                if (!ok(&sm.v_raw, raw++ & 1u))
-                    return;
-                clear_unseen<D>(stage, key0, c.k_lo, c.k_hi);
-                if (lane == 0) {
-                    sm.units_filled[1] = g + 1;
-                    mbar_arrive(&sm.v_full[g % kVStages]);
-                }
-                __syncwarp();
+                x.page = -1;
             }
         }
+        return x;
+    };
+    auto bytes_of = [&](const Unit &x) { return __popc(__ballot_sync(0xffffffffu, x.page >= 0)) * box * 128u; };
+    auto copy = [&](uint8_t *stage, const CUtensorMap *map, const Unit &x, uint64_t *full) {
+        if (x.page >= 0)
+            tma_load_4d(stage + at, map, 64 * half, (x.key0 + i * box) % page, x.head, x.page, full);
+    };
+    if (!next_item(sm, n, c, status))
+        return;
+    int u = c.u0;
+    Unit cur = unit_at(u);
+    const uint32_t first = bytes_of(cur);
+    if (lane == 0) {
+        sm.k_filled = 1;
+        mbar_arrive_expect_tx(&sm.k_first, first);
+    }
+    __syncwarp();
+    copy(ring, &maps->k, cur, &sm.k_first);
+    for (uint32_t g = 0;; ++g) {
+        Unit next = cur;
+        next.there = ++u < c.u1;
+        if (!next.there && next_item(sm, n, c, status)) {
+            u = c.u0;
+            next.there = true;
+        }
+        next.page = -1;
+        if (next.there)
+            next = unit_at(u);
+        if (g >= kVStages && !ok(&sm.unit_done[(g - kVStages) % kFree], ((g - kVStages) / kFree) & 1u))
+            return;
+        uint8_t *vs = ring + (kKStages + g % kVStages) * stage_bytes(D);
+        uint64_t *full = &sm.kv_full[g % kVStages];
+        const bool edge = cur.key0 < cur.lo || cur.key0 + kKeys > cur.hi;
+        const uint32_t vbytes = bytes_of(cur), kbytes = bytes_of(next);
+        if (lane == 0) {
+            sm.kv_filled = g + 1;
+            if (edge) {
+                sm.raw_filled = raw + 1;
+                mbar_arrive_expect_tx(&sm.v_raw, vbytes);
+                mbar_expect_tx(full, kbytes);
+            } else {
+                mbar_arrive_expect_tx(full, vbytes + kbytes);
+            }
+        }
+        __syncwarp();
+        copy(vs, &maps->v, cur, edge ? &sm.v_raw : full);
+        copy(ring + ((g + 1) % kKStages) * stage_bytes(D), &maps->k, next, full);
+        if (edge) {
+            const bool came = ok(&sm.v_raw, raw++ & 1u);
+            if (came)
+                clear_unseen<D>(vs, cur.key0, cur.lo, cur.hi);
+            if (lane == 0)
+                mbar_arrive(full);
+            __syncwarp();
+            if (!came)
+                return;
+        }
+        if (!next.there)
+            return;
+        cur = next;
     }
 }
 
@@ -710,13 +743,14 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
         if (rows <= kHalf * half) {
             // no rows in this half: nothing to wait for but the unit itself
             for (int i = 0; i < units; ++i, ++g) {
-                if (!ok(&sm.v_full[g % kVStages], (g / kVStages) & 1u))
+                if (!ok(&sm.kv_full[g % kVStages], (g / kVStages) & 1u))
                     return;
                 mbar_arrive(&sm.unit_done[g % kFree]);
             }
             continue;
         }
-        if (!ok(&sm.q_full[half], qn++ & 1u) || !ok(&sm.k_full[g % kKStages], (g / kKStages) & 1u))
+        // (K of a later item's first unit came with V of the unit before it)
+        if (!ok(&sm.q_full[half], qn++ & 1u) || (g == 0 && !ok(&sm.k_first, 0)))
             return;
         tc_fence_after();
 #pragma unroll
@@ -728,8 +762,7 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
             const bool last = u + 1 == units;
             if (last)  // the item's last S are on their way: its queries are free after them
                 umma_commit(&sm.q_empty[half]);
-            if (!ok(&sm.v_full[g % kVStages], (g / kVStages) & 1u) ||
-                (!last && !ok(&sm.k_full[(g + 1) % kKStages], ((g + 1) / kKStages) & 1u)))
+            if (!ok(&sm.kv_full[g % kVStages], (g / kVStages) & 1u))
                 return;
             const uint64_t bd = vd + (g % kVStages) * kStage;
 #pragma unroll
@@ -994,11 +1027,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.b = a.batch.num_seqs;
         sm.t = 0;
         sm.before = 0;
-        sm.units_filled[0] = sm.units_filled[1] = sm.raw_filled = 0;
-        for (int i = 0; i < kKStages; ++i)
-            mbar_init(&sm.k_full[i], 1);
+        sm.k_filled = sm.kv_filled = sm.raw_filled = 0;
+        mbar_init(&sm.k_first, 1);
         for (int i = 0; i < kVStages; ++i)
-            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.kv_full[i], 1);
         mbar_init(&sm.v_raw, 1);
         for (int i = 0; i < kFree; ++i)
             mbar_init(&sm.unit_done[i], 2);
@@ -1059,13 +1091,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // for the last fill of every stage, so that none is in flight at the end.
     if (*reinterpret_cast<volatile int *>(&sm.fail) && warp == kLoadWarp && lane == 0) {
         bool done = true;
-        for (uint32_t i = 0; i < kKStages && i < sm.units_filled[0]; ++i) {
-            const uint32_t g = sm.units_filled[0] - 1 - i;
-            done = mbar_wait_bounded(&sm.k_full[g % kKStages], (g / kKStages) & 1u) && done;
-        }
-        for (uint32_t i = 0; i < kVStages && i < sm.units_filled[1]; ++i) {
-            const uint32_t g = sm.units_filled[1] - 1 - i;
-            done = mbar_wait_bounded(&sm.v_full[g % kVStages], (g / kVStages) & 1u) && done;
+        if (sm.k_filled)
+            done = mbar_wait_bounded(&sm.k_first, 0);
+        for (uint32_t i = 0; i < kVStages && i < sm.kv_filled; ++i) {
+            const uint32_t g = sm.kv_filled - 1 - i;
+            done = mbar_wait_bounded(&sm.kv_full[g % kVStages], (g / kVStages) & 1u) && done;
         }
         if (sm.raw_filled)
             done = mbar_wait_bounded(&sm.v_raw, (sm.raw_filled - 1) & 1u) && done;
