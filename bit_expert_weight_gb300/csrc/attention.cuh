@@ -61,10 +61,14 @@ __device__ __forceinline__ Seq seq_at(const smoe_attention_args &a, int b, int *
 }
 
 // Keys seen by a row with key index i (negative: none): [lo, hi).
-__device__ __forceinline__ void seen_from(const smoe_attention_args &a, int i, int &lo, int &hi)
+__device__ __forceinline__ void seen_from(int window, int i, int &lo, int &hi)
 {
     hi = i >= 0 ? i + 1 : 0;
-    lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+    lo = window > 0 && hi > window ? hi - window : 0;
+}
+__device__ __forceinline__ void seen_from(const smoe_attention_args &a, int i, int &lo, int &hi)
+{
+    seen_from(a.window, i, lo, hi);
 }
 
 // Keys seen by new row `token` of s.

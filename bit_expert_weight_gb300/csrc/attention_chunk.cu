@@ -64,6 +64,9 @@ constexpr int kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11, kQueryWarp = 12;
 constexpr int kItemSlots = 4;
 constexpr int kThreads = 512;
 constexpr int kItemUnits = 4;           // an item's own cost, in units
+// Items of up to ten units are not cut: a cut costs about four units' time (a
+// part written and read, the join), and a part more one unit to read.
+constexpr int kWholeUnits = 10;
 constexpr int kMaxCtas = 240;
 // log2 of how far the maximum may run ahead of m.  P, its sum and O are floating
 // point, so a large P loses nothing; 2^40 leaves the sums room up to 2^127.
@@ -100,7 +103,7 @@ struct Item {
     int u0, u1, kbase;      // units; unit u begins at key kbase + 128 u
     int k_lo, k_hi;         // keys seen by any of the rows
     int t_lo, t_hi;         // keys seen by every row
-    int c_first, c_last;    // the CTAs that share the item
+    int c_first, c_last;    // the CTAs that share the item (equal: it is whole)
 };
 
 struct Smem {
@@ -121,9 +124,10 @@ struct Smem {
     uint32_t k_filled, kv_filled, raw_filled;  // phases of k_first, kv_full, v_raw (drain after a failure)
     int fail, last;
     // the work split
-    int64_t scan[kThreads / 32];
+    uint32_t scan[kThreads / 32];
     int scan_max[kThreads / 32];
     int64_t q, total, before;    // units per CTA, in all, before the CTA's first item's tile
+    int64_t border[2];           // the CTA's share
     int unit;                    // an item's length is rounded up to a multiple of this
     int b, t;                    // that tile
     Seq seq, next;               // its sequence, and the one after it
@@ -267,20 +271,38 @@ struct Tile {
     int kbase;
 };
 
+// The keys of tile t of a sequence.
+struct TileKeys {
+    int rows, units, k_lo, k_hi, t_lo, t_hi;
+};
+__device__ __forceinline__ TileKeys keys_of(int window, int G, int seq_rows, int len, int t)
+{
+    const int m0 = t * kTileRows2, left = seq_rows * G - m0;
+    TileKeys k;
+    k.rows = left < kTileRows2 ? (left > 0 ? left : 0) : kTileRows2;
+    k.k_lo = k.k_hi = k.t_lo = k.t_hi = 0;
+    if (k.rows > 0) {
+        const int i0 = len - seq_rows;  // key index of the first row
+        seen_from(window, i0 + m0 / G, k.k_lo, k.t_hi);
+        seen_from(window, i0 + (m0 + k.rows - 1) / G, k.t_lo, k.k_hi);
+    }
+    const int n = (k.k_hi - k.k_lo / kKeys * kKeys + kKeys - 1) / kKeys;
+    // rows that see nothing still take a unit: they get their zeros
+    k.units = k.rows == 0 ? 0 : (n > 1 ? n : 1);
+    return k;
+}
+
 __device__ __forceinline__ void tile_keys(const smoe_attention_args &a, int G, Tile &c)
 {
+    const TileKeys k = keys_of(a.window, G, c.s.rows, c.s.len, c.t);
     c.m0 = c.t * kTileRows2;
-    const int left = c.s.rows * G - c.m0;
-    c.rows = left < kTileRows2 ? (left > 0 ? left : 0) : kTileRows2;
-    c.k_lo = c.k_hi = c.t_lo = c.t_hi = 0;
-    if (c.rows > 0) {
-        seen(a, c.s, c.m0 / G, c.k_lo, c.t_hi);
-        seen(a, c.s, (c.m0 + c.rows - 1) / G, c.t_lo, c.k_hi);
-    }
-    c.kbase = c.k_lo / kKeys * kKeys;
-    const int n = (c.k_hi - c.kbase + kKeys - 1) / kKeys;
-    // rows that see nothing still take a unit: they get their zeros
-    c.units = c.rows == 0 ? 0 : (n > 1 ? n : 1);
+    c.rows = k.rows;
+    c.units = k.units;
+    c.k_lo = k.k_lo;
+    c.k_hi = k.k_hi;
+    c.t_lo = k.t_lo;
+    c.t_hi = k.t_hi;
+    c.kbase = k.k_lo / kKeys * kKeys;
 }
 
 // An item's length on the line.
@@ -317,32 +339,35 @@ __device__ __forceinline__ void units_in(const Tile &c, int64_t w0, int64_t w1, 
 
 __device__ __forceinline__ int tiles_of(const Seq &s, int G) { return (s.rows * G + kTileRows2 - 1) / kTileRows2; }
 
-// Exclusive sum of v over the CTA's threads; total and maximum of all.
-__device__ __forceinline__ int64_t scan_all(Smem &sm, int64_t v, int &mx, int64_t &total)
+// Sums over the CTA's threads: before the thread's own, and of all; and the
+// maximum of all.
+struct Scan {
+    uint32_t before, total;
+    int most;
+};
+__device__ __forceinline__ Scan scan_all(Smem &sm, uint32_t v, int mx)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = v;
+    uint32_t incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
         incl += lane >= o ? x : 0;
-        const int m = __shfl_xor_sync(0xffffffffu, mx, o);
-        mx = m > mx ? m : mx;
     }
+    mx = __reduce_max_sync(0xffffffffu, mx);
     __syncthreads();
-    if (lane == 31)
+    if (lane == 31) {
         sm.scan[warp] = incl;
-    if (lane == 0)
         sm.scan_max[warp] = mx;
-    __syncthreads();
-    int64_t before = incl - v;
-    total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        before += w < warp ? sm.scan[w] : 0;
-        total += sm.scan[w];
-        mx = sm.scan_max[w] > mx ? sm.scan_max[w] : mx;
     }
-    return before;
+    __syncthreads();
+    // the warps' sums, a lane per warp
+    const uint32_t w = lane < kThreads / 32 ? sm.scan[lane] : 0;
+    Scan s;
+    s.before = incl - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    s.total = __reduce_add_sync(0xffffffffu, w);
+    s.most = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? sm.scan_max[lane] : 0);
+    return s;
 }
 
 // A sequence of the batch in shared memory, with the tiles before it.
@@ -367,23 +392,24 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
     const int tid = threadIdx.x, n = a.batch.num_seqs, Hkv = a.cache.num_kv_heads;
     // tiles before each sequence
     const int per = (n + kThreads - 1) / kThreads;
-    int64_t sum = 0, total;
-    int mx = 0;
+    uint32_t sum = 0;
 #pragma unroll 1
     for (int b = tid * per; b < n && b < (tid + 1) * per; ++b) {
         const Seq s = seq_at(a, b, status);
         seqs[b].row0 = static_cast<int>(s.row0);
         seqs[b].rows = s.rows;
         seqs[b].len = s.len;
-        sum += tiles_of(s, G);
+        seqs[b].tiles = tiles_of(s, G);
+        sum += seqs[b].tiles;
     }
-    int64_t before = scan_all(sm, sum, mx, total);
+    Scan sc = scan_all(sm, sum, 0);
 #pragma unroll 1
     for (int b = tid * per; b < n && b < (tid + 1) * per; ++b) {
-        seqs[b].tiles = static_cast<int>(before);
-        before += tiles_of(seq_of(seqs[b]), G);
+        const int k = seqs[b].tiles;
+        seqs[b].tiles = static_cast<int>(sc.before);
+        sc.before += k;
     }
-    const int all = static_cast<int>(total);
+    const int all = static_cast<int>(sc.total);
     if (tid == 0) {
         seqs[n].row0 = seqs[n].rows = seqs[n].len = 0;
         seqs[n].tiles = all;
@@ -408,8 +434,11 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
         c.t = i - seqs[b].tiles;
         tile_keys(a, G, c);
     };
+    // the length of this thread's tiles on the line of one kv head (fewer than
+    // 2^32 units in all: 2^17 tiles of 2^15 units)
+    int mx = 0;
     auto length = [&](int unit) {
-        int64_t l = 0;
+        uint32_t l = 0;
 #pragma unroll 1
         for (int i = i0, b = b0; i < i1; ++i) {
             tile_at(i, b);
@@ -418,56 +447,78 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
         }
         return l;
     };
-    sum = length(1);
-    before = scan_all(sm, sum, mx, total);
-    // Equal shares, but no item in so many parts that the joining costs more
-    // than the sharing saves: a cut costs about four units' time, and a part
-    // more one unit to read, so that up to ten units are best left together.
-    int64_t q = ceil_div(total * Hkv, gridDim.x);
-    const int64_t least = mx <= 10 ? mx + kItemUnits : static_cast<int64_t>(sqrtf(static_cast<float>(mx)));
-    q = q > least ? q : least;
-    // Where the grid has room for it, every item begins a CTA's share, so that
-    // none is cut for the sake of its neighbours.
     int unit = 1;
-    if (all * Hkv <= static_cast<int>(gridDim.x)) {
-        int64_t padded;
-        const int64_t own = length(static_cast<int>(q));
-        const int64_t at = scan_all(sm, own, mx, padded);
-        if (padded * Hkv <= q * gridDim.x) {
+    int64_t q;
+    for (int pass = 0;; ++pass) {
+        const uint32_t l = length(unit);
+        const Scan s = scan_all(sm, l, mx);
+        if (pass == 0) {
+            // Equal shares, but no item in so many parts that the joining costs
+            // more than the sharing saves.
+            q = ceil_div((int64_t)s.total * Hkv, gridDim.x);
+            const int64_t least = s.most <= kWholeUnits ? s.most + kItemUnits
+                                               : static_cast<int64_t>(sqrtf(static_cast<float>(s.most)));
+            q = q > least ? q : least;
+            sum = l;
+            sc = s;
+            // Where the grid has room for it, every item begins a CTA's share,
+            // so that none is cut for the sake of its neighbours.
+            if (all * Hkv > static_cast<int>(gridDim.x))
+                break;
             unit = static_cast<int>(q);
-            sum = own;
-            before = at;
-            total = padded;
+        } else {
+            if ((int64_t)s.total * Hkv <= q * gridDim.x) {
+                sum = l;
+                sc = s;
+            } else {
+                unit = 1;
+            }
+            break;
         }
     }
-    before *= Hkv;
-    total *= Hkv;
-    const int64_t w0 = q * blockIdx.x;
+    const int64_t before = (int64_t)sc.before * Hkv, all_units = (int64_t)sc.total * Hkv;
     if (tid == 0) {
         sm.q = q;
-        sm.total = total;
+        sm.total = all_units;
         sm.unit = unit;
     }
-    if (w0 >= before && w0 < before + sum * Hkv) {
+    // The borders of the share: drawn at the nearer end of an item that is not
+    // worth being cut.
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const int64_t x = q * (blockIdx.x + side);
+        if (x >= all_units && tid == 0)
+            sm.border[side] = all_units;
+        if (x < before || x >= before + (int64_t)sum * Hkv)
+            continue;
+        int64_t at = before;
 #pragma unroll 1
         for (int i = i0, b = b0; i < i1; ++i) {
             tile_at(i, b);
-            const int64_t next = before + (int64_t)item_length(c, unit) * Hkv;
-            if (w0 >= before && w0 < next) {
-                sm.b = b;
-                sm.t = c.t;
-                sm.before = before;
-                sm.seq = c.s;
-                sm.next = seq_of(seqs[b + 1]);
+            const int len = item_length(c, unit);
+            const int64_t next = at + (int64_t)len * Hkv;
+            if (x < next) {
+                const int64_t item = at + (x - at) / len * len;
+                sm.border[side] = x == item || c.units > kWholeUnits ? x
+                                  : 2 * (x - item) < len             ? item
+                                                                     : item + len;
+                if (side == 0) {
+                    sm.b = b;
+                    sm.t = c.t;
+                    sm.before = at;
+                    sm.seq = c.s;
+                    sm.next = seq_of(seqs[b + 1]);
+                }
+                break;
             }
-            before = next;
+            at = next;
         }
     }
     fence_async_smem();  // tensor copies will write where the batch lay
     __syncthreads();
 }
 
-__device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, const Smem &sm, int64_t w0)
+__device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, const Smem &sm)
 {
     Tile c;
     c.b = sm.b;
@@ -476,7 +527,9 @@ __device__ __forceinline__ Tile first_tile(const smoe_attention_args &a, int G, 
     c.next = sm.next;
     tile_keys(a, G, c);
     const int len = item_length(c, sm.unit);
-    c.h = static_cast<int>((w0 - sm.before) / len);
+    // (a border drawn at an item's start lies in the item before it, or here)
+    const int64_t x = sm.q * blockIdx.x;
+    c.h = static_cast<int>((x - sm.before) / len);
     c.at = sm.before + (int64_t)c.h * len;
     return c;
 }
@@ -488,7 +541,7 @@ __device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64
 {
     const int lane = threadIdx.x & 31;
     uint32_t n = 0;
-    for (Tile c = first_tile(a, G, sm, w0);; tile_next(a, G, sm.unit, c, status)) {
+    for (Tile c = first_tile(a, G, sm);; tile_next(a, G, sm.unit, c, status)) {
         const bool end = c.rows == 0 || c.at >= w1;
         int u0 = 0, u1 = 0;
         if (!end) {
@@ -515,8 +568,9 @@ __device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64
             t.k_hi = c.k_hi;
             t.t_lo = c.t_lo;
             t.t_hi = c.t_hi;
-            t.c_first = static_cast<int>(k / sm.q);
-            t.c_last = static_cast<int>((k + c.units - 1) / sm.q);
+            const bool whole = u1 - u0 == c.units;
+            t.c_first = whole ? 0 : static_cast<int>(k / sm.q);
+            t.c_last = whole ? 0 : static_cast<int>((k + c.units - 1) / sm.q);
             mbar_arrive(&sm.item_full[slot]);
         }
         __syncwarp();
@@ -1062,9 +1116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     // (the ring is not in use yet)
     find_share(a, G, sm, reinterpret_cast<ChunkSeq *>(ring), status);
-    const int64_t w0 = sm.q * blockIdx.x;
-    const int64_t w1 = w0 + sm.q;
-    if (w0 >= sm.total) {
+    const int64_t w0 = sm.border[0], w1 = sm.border[1];
+    if (w0 >= w1) {
         // nothing for this CTA
     } else if (warp < kSoftWarps) {
         softmax<D>(a, G, sm, reinterpret_cast<float *>(workspace + kPartsAt),
