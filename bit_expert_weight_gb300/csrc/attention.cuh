@@ -35,6 +35,8 @@ __device__ __forceinline__ float ex2(float x)
 
 __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int kMaxLen = 0x7fffffff - 511;  // key indices and their roundings fit 31 bits
+
 // A sequence of the batch as the kernels use it; an impossible one is
 // recorded and gets what is left of it in range.
 struct Seq {
@@ -51,7 +53,7 @@ __device__ __forceinline__ Seq seq_at(const smoe_attention_args &a, int b, int *
     s.rows = r1 - r0;
     s.len = a.batch.kv_len[b];
     bool bad = r0 < 0 || r1 < r0 || r1 > a.batch.num_rows || s.rows > a.max_rows || s.len < 0 ||
-               s.len > (int64_t)a.batch.table_stride * a.cache.page_size;
+               s.len > kMaxLen || s.len > (int64_t)a.batch.table_stride * a.cache.page_size;
     if (bad) {
         set_status(status, kStatusBadArg);
         s.row0 = 0;

@@ -604,7 +604,7 @@ typedef struct {
     int64_t num_rows;          /* rows of q, k, v and the outputs             */
     int32_t num_seqs;          /* 0 .. SMOE_MAX_SEQS                          */
     int32_t table_stride;      /* pages of a table row; kv_len is at most
-                                  table_stride * page_size                    */
+                                  table_stride * page_size, and 2^31 - 512    */
 } smoe_kv_batch;
 
 typedef struct {
@@ -651,7 +651,8 @@ typedef struct {
     int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
     int32_t num_heads;         /* a multiple of num_kv_heads, at most 128
                                   times as many: query head h reads kv head
-                                  h / (num_heads / num_kv_heads)              */
+                                  h / (num_heads / num_kv_heads); num_rows *
+                                  num_heads < 2^31                            */
     int32_t out_dtype;         /* smoe_dtype                                  */
     int32_t max_rows;          /* no sequence of the batch has more rows; the
                                   kernel is chosen by it                      */

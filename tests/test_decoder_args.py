@@ -156,7 +156,7 @@ def attention_args(S, **kw):
 @pytest.mark.parametrize("kw", BAD_CACHE + [
     dict(q=None), dict(out=None), dict(q=PTR + 8), dict(out=PTR + 2), dict(out=PTR),
     dict(q_row_stride=2052), dict(out_head_stride=-8), dict(num_heads=0), dict(num_heads=18),
-    dict(num_heads=4 * 129), dict(out_dtype=2), dict(max_rows=0), dict(window=-1),
+    dict(num_heads=4 * 129), dict(num_rows=1 << 28), dict(out_dtype=2), dict(max_rows=0), dict(window=-1),
     dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
 ], ids=str)
 def test_attention_refuses(S, kw):

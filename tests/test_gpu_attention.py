@@ -92,6 +92,38 @@ def test_attention_fp32_out_views_and_scale(S, ws, case):
     assert bool((out[:, 0] == 9.0).all()) and bool((out[..., D:] == 9.0).all())
 
 
+@pytest.mark.parametrize("case", [
+    # more sequences than a CTA has threads, and as many as a batch may have
+    ([1] * 600, [(37 * i) % 130 for i in range(600)], 4, 2, 64, 16, 0),
+    ([1] * 2048, [(53 * i) % 90 + 1 for i in range(2048)], 8, 1, 128, 16, 0),
+    ([1] * 690 + [40] * 10, [(29 * i) % 200 + 40 for i in range(700)], 8, 2, 64, 32, 0),
+    ([2, 0, 20] * 682, [(31 * i) % 60 + 20 for i in range(2046)], 4, 1, 128, 16, 0),
+    # more tiles than a CTA has threads
+    ([4500, 1], [4500, 300], 32, 1, 64, 256, 0),
+    # few rows over many keys: items cut into many parts
+    ([20, 3], [60_001, 35_000], 16, 2, 128, 128, 0),
+    ([70], [50_000], 2, 1, 64, 64, 40_000),
+], ids=lambda c: f"{len(c[0])} sequences, rows {max(c[0])}, keys {max(c[1])}")
+def test_wide_batches(S, ws, case):
+    rows, kv, Hq, Hkv, D, page, window = case
+    p = Paged(rows, kv, Hq, Hkv, D, page, DEV, seed=len(rows))
+    out = run(S, ws, p, window=window)
+    assert S.device_status() == 0
+    p.check(out, True, window)
+    assert torch.equal(out, run(S, ws, p, window=window))
+
+
+@pytest.mark.parametrize("max_rows", [1, 3, 500])
+def test_idle_batch(S, ws, max_rows):
+    """No sequence has a row: nothing is written, and the workspace stays usable."""
+    p = Paged([0, 0, 0], [40, 0, 7], 8, 2, 128, 16, DEV)
+    q = torch.zeros(5, 8, 128, dtype=BF16, device=DEV)
+    out = torch.full_like(q, 3.0)
+    run(S, ws, p, q=q, out=out, max_rows=max_rows)
+    assert S.device_status() == 0 and bool((out == 3.0).all())
+    assert not bool(ws[:4096].any())
+
+
 def test_large_scores(S, ws):
     """Scores far apart, and growing along the keys: each new maximum rescales."""
     for rows, kv, D in (([1, 1], [900, 333], 128), ([150, 70], [900, 333], 128),
