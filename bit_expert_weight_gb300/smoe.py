@@ -611,6 +611,20 @@ def _heads(name, t):
     return t.data_ptr(), st[0], st[1], dt
 
 
+def _new_heads(x, dtype):
+    """A contiguous [rows, heads, head_dim] tensor of x's shape: (tensor, pointer, row stride,
+    head stride)."""
+    T, H, D = x.shape
+    # the quicker call, where it does not copy x's order of dimensions
+    if x.stride(1) != D:
+        out = torch.empty((T, H, D), dtype=dtype, device=x.device)
+    elif dtype is x.dtype:
+        out = torch.empty_like(x)
+    else:
+        out = torch.empty_like(x, dtype=dtype)
+    return out, out.data_ptr(), H * D, D
+
+
 def _device_array(name, t, dtype, numel):
     """Pointer of a contiguous CUDA tensor of `dtype` with at least `numel` elements
     (None: no tensor, a null pointer)."""
@@ -668,13 +682,14 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, rot_scal
     [rows]), after a norm of each head where norm_w (bf16 [head_dim]) is given.  The first
     2 * table.numel() channels rotate.  out: a tensor of x's shape and dtype (x itself
     rotates in place)."""
+    xp, xr, xh, dt = _heads("x", x)
     T, H, D = x.shape
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        out, op, orow, oh = _new_heads(x, x.dtype)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and dtype")
-    xp, xr, xh, dt = _heads("x", x)
-    op, orow, oh, _ = _heads("out", out)
+    else:
+        op, orow, oh, _ = _heads("out", out)
     a = _pack_rope(xp, op, xr, xh, orow, oh, T, H, D, dt, 2 * table.numel(), interleaved,
                    rot_scale, eps, _device_array("positions", positions, torch.int32, T),
                    _device_array("table", table, torch.int64, 0),
@@ -703,13 +718,14 @@ def kv_append(q, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     if q is not None:
         if q.shape[0] != T or q.shape[2] != D:
             raise ValueError("q must have k's rows and head_dim")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16:
-            raise ValueError("q_out must be bf16 of q's shape")
         H = q.shape[1]
         qp, qr, qh, qdt = _heads("q", q)
-        op, orow, oh, _ = _heads("q_out", q_out)
+        if q_out is None:
+            q_out, op, orow, oh = _new_heads(q, torch.bfloat16)
+        elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16:
+            raise ValueError("q_out must be bf16 of q's shape")
+        else:
+            op, orow, oh, _ = _heads("q_out", q_out)
     if not dt == vdt == qdt:
         raise TypeError("q, k and v must have one dtype")
     a = _pack_append(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, kp, vp,
@@ -746,10 +762,14 @@ def attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     if D != k_pages.shape[3]:
         raise ValueError("q and the pages must have one head_dim")
     if out is None:
-        out = torch.empty((T, H, D), dtype=out_dtype, device=q.device)
+        odt = _DTYPES.get(out_dtype)
+        if odt is None:
+            raise TypeError("out_dtype must be fp32 or bf16")
+        out, op, orow, oh = _new_heads(q, out_dtype)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    op, orow, oh, odt = _heads("out", out)
+    else:
+        op, orow, oh, odt = _heads("out", out)
     a = _pack_attention(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, op,
                         qr, qh, orow, oh, H, odt, max_rows, window,
                         D ** -0.5 if scale is None else scale)
