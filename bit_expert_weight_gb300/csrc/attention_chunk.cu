@@ -27,10 +27,8 @@
 //
 // Roles of the 16 warps of a CTA, one CTA per SM:
 //   warps 0..3  half A, warps 4..7 half B: softmax, rescaling, output
-//   warps 8, 9  issue the MMAs of half A and half B.  One thread takes about
-//               50 cycles to issue an MMA that runs for 32 to 64, and about 100
-//               for each wait and commit: one warp for both halves kept the
-//               tensor cores waiting
+//   warps 8, 9  issue the MMAs of half A and half B: with one warp for both,
+//               its waits for one half kept the other's products back
 //   warp 10     loads K and V by TMA, page by page, into rings of 3 and 2
 //               units, 128-byte swizzle
 //   warp 11     walks the line of items and hands them to the other warps
@@ -159,18 +157,29 @@ __device__ __forceinline__ constexpr uint32_t idesc_pv()
     return kIdescBase | (1u << 16) | ((uint32_t)(D >> 3) << 17);
 }
 
+// The warp's converged threads issue these together and one elected thread
+// takes effect: with the operands the same in every lane they stay in uniform
+// registers.  (Issued from a branch of one lane, each MMA took 70 to 80 cycles
+// to move its descriptors there.)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+    asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"(acc)
                  : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+    asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
                  "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                     smem_u32(bar))
                  : "memory");
 }
 
@@ -765,17 +774,21 @@ __device__ void loader(const smoe_attention_args &a, const Maps *maps, Smem &sm,
     }
 }
 
-// The MMAs of one half (one lane of warps 8 and 9).
+// The MMAs of one half (warps 8 and 9).
 template <int D>
 __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *status)
 {
-    const uint32_t ts = sm.tmem_base + col_s(half), to = sm.tmem_base + col_o<D>(half);
+    const uint32_t base = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
+    const uint32_t ts = base + col_s(half), to = base + col_o<D>(half);
     const uint64_t qd = sw128_desc(smem_u32(sq) + half * q_half_bytes(D)), kd = sw128_desc(smem_u32(ring));
     const uint64_t vd = sw128_desc_mn(smem_u32(ring) + kKStages * stage_bytes(D), kKeys * 128);
     constexpr uint64_t kStage = stage_bytes(D) >> 4;
     uint32_t g = 0, n = 0;    // units, items
     uint32_t qn = 0, pn = 0;  // items and units of this half
-    auto ok = [&](uint64_t *bar, unsigned parity) { return wait_for(sm, bar, parity, status); };
+    const int lane = threadIdx.x & 31;
+    auto ok = [&](uint64_t *bar, unsigned parity) {
+        return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
+    };
     // S of step x of the CTA, into its buffer
     auto qk = [&](uint32_t x) {
         const uint64_t bd = kd + (x / 2 % kKStages) * kStage + (x & 1) * (kStep * 128 >> 4);
@@ -790,8 +803,11 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
         const int slot = n % kItemSlots;
         if (!ok(&sm.item_full[slot], (n / kItemSlots) & 1u))
             return;
-        const int rows = sm.item[slot].rows, units = sm.item[slot].u1 - sm.item[slot].u0;
-        mbar_arrive(&sm.item_empty[slot]);
+        // the same in every lane, and known to be
+        const int rows = __shfl_sync(0xffffffffu, sm.item[slot].rows, 0);
+        const int units = __shfl_sync(0xffffffffu, sm.item[slot].u1 - sm.item[slot].u0, 0);
+        if (lane == 0)
+            mbar_arrive(&sm.item_empty[slot]);
         if (rows == 0)
             return;
         if (rows <= kHalf * half) {
@@ -799,7 +815,8 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
             for (int i = 0; i < units; ++i, ++g) {
                 if (!ok(&sm.kv_full[g % kVStages], (g / kVStages) & 1u))
                     return;
-                mbar_arrive(&sm.unit_done[g % kFree]);
+                if (lane == 0)
+                    mbar_arrive(&sm.unit_done[g % kFree]);
             }
             continue;
         }
@@ -810,12 +827,12 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             qk(2 * g + b);
-            umma_commit(&sm.s_done[half][b]);
+            commit_elected(&sm.s_done[half][b]);
         }
         for (int u = 0; u < units; ++u, ++g, ++pn) {
             const bool last = u + 1 == units;
             if (last)  // the item's last S are on their way: its queries are free after them
-                umma_commit(&sm.q_empty[half]);
+                commit_elected(&sm.q_empty[half]);
             if (!ok(&sm.kv_full[g % kVStages], (g / kVStages) & 1u))
                 return;
             const uint64_t bd = vd + (g % kVStages) * kStage;
@@ -832,9 +849,9 @@ __device__ void mma_issuer(Smem &sm, uint8_t *sq, uint8_t *ring, int half, int *
                 // MMAs of one thread run in order
                 if (!last)
                     qk(2 * (g + 1) + b);
-                umma_commit(&sm.s_done[half][b]);
+                commit_elected(&sm.s_done[half][b]);
             }
-            umma_commit(&sm.unit_done[g % kFree]);
+            commit_elected(&sm.unit_done[g % kFree]);
         }
     }
 }
@@ -1129,14 +1146,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kQueryWarp) {
         query_loader<D>(a, G, sm, sq, (warp - kQueryWarp) / 2, (warp - kQueryWarp) % 2, status);
     } else {
-        if (lane == 0) {
-            mma_issuer<D>(sm, sq, ring, warp - kMmaWarp, status);
-            // every MMA issued so far has completed once this commit lands
-            umma_commit(&sm.drain);
-            if (!mbar_wait_bounded(&sm.drain, 0)) {
-                set_status(status, kStatusTimeout);
-                *reinterpret_cast<volatile int *>(&sm.fail) = 1;
-            }
+        mma_issuer<D>(sm, sq, ring, __shfl_sync(0xffffffffu, warp, 0) - kMmaWarp, status);
+        __syncwarp();
+        // every MMA issued so far has completed once this commit lands
+        commit_elected(&sm.drain);
+        if (!mbar_wait_bounded(&sm.drain, 0)) {
+            set_status(status, kStatusTimeout);
+            *reinterpret_cast<volatile int *>(&sm.fail) = 1;
         }
     }
     __syncwarp();
