@@ -86,7 +86,7 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr)
 // is computed in parts.  Parts of one CTA are joined in shared memory, once,
 // at its end; what still is a part then goes to the workspace, and the CTA
 // that arrives last joins the item's parts, in CTA order.
-constexpr int kItemSteps = 3;
+constexpr int kItemSteps = 8;
 constexpr int kMaxCtas = 256;
 
 // A sequence of the batch in shared memory, with the place of its first item
