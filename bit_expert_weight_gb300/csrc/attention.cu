@@ -365,54 +365,68 @@ struct RowPart {
 // took 3,900 cycles, this 1,300), the one over other CTAs' parts, which waits
 // for the L2 cache, has the loads of four parts in flight.
 
-// Row r of the parts that warps wa .. wb of this CTA left (`tail`: warp wa's
-// is of an item begun in its share).
+// Rows r, r + 16, .. (T of them; those past nrows are not touched) of the
+// parts that warps wa .. wb of this CTA left (`tail`: warp wa's is of an item
+// begun in its share).
 template <int D, int T>
-__device__ __forceinline__ RowPart<D> join_near(const PartInfo (*parts)[2], int wa, int wb, bool tail, int r, int l16)
+__device__ __forceinline__ void join_near(RowPart<D> (&o)[T], const PartInfo (*parts)[2], int wa, int wb, bool tail,
+                                          int r, int nrows, int l16)
 {
-    RowPart<D> o;
-    o.clear();
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        o[t].clear();
 #pragma unroll 1
     for (int w = wa; w <= wb; ++w) {
         const float *p = parts[w][tail && w == wa ? 1 : 0].at;
-        float4 y[D / 64];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-            y[i] = *reinterpret_cast<const float4 *>(p + r * D + l16 * (D / 16) + 4 * i);
-        o.add(p[dec_rows(T) * D + r], p[dec_rows(T) * (D + 1) + r], y);
+        for (int t = 0; t < T; ++t) {
+            const int m = r + kMmaRows * t;
+            if (m >= nrows)
+                break;
+            float4 y[D / 64];
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+                y[i] = *reinterpret_cast<const float4 *>(p + m * D + l16 * (D / 16) + 4 * i);
+            o[t].add(p[dec_rows(T) * D + m], p[dec_rows(T) * (D + 1) + m], y);
+        }
     }
-    return o;
 }
 
-// Row r of n parts of other CTAs: the first at `first`, part k at rest + k
-// step.  They are read past the L1 cache.
+// The same rows of n parts of other CTAs: the first at `first`, part k at
+// rest + k step.  They are read past the L1 cache.
 template <int D, int T>
-__device__ __forceinline__ RowPart<D> join_far(const float *first, const float *rest, int64_t step, int n, int r,
-                                               int l16)
+__device__ __forceinline__ void join_far(RowPart<D> (&o)[T], const float *first, const float *rest, int64_t step,
+                                         int n, int r, int nrows, int l16)
 {
-    constexpr int kBatch = 4;
-    RowPart<D> o;
-    o.clear();
+    constexpr int kBatch = 4 / T;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        o[t].clear();
 #pragma unroll 1
     for (int k0 = 0; k0 < n; k0 += kBatch) {
-        float pm[kBatch], pl[kBatch];
-        float4 y[kBatch][D / 64];
+        float pm[kBatch][T], pl[kBatch][T];
+        float4 y[kBatch][T][D / 64];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             // past the end: the last part again, with no weight
             const int at = k0 + k < n ? k0 + k : n - 1;
             const float *p = at == 0 ? first : rest + at * step;
-            pm[k] = __ldcg(p + dec_rows(T) * D + r);
-            pl[k] = __ldcg(p + dec_rows(T) * (D + 1) + r);
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-                y[k][i] = __ldcg(reinterpret_cast<const float4 *>(p + r * D + l16 * (D / 16) + 4 * i));
+            for (int t = 0; t < T; ++t) {
+                const int m = r + kMmaRows * t < nrows ? r + kMmaRows * t : r;
+                pm[k][t] = __ldcg(p + dec_rows(T) * D + m);
+                pl[k][t] = __ldcg(p + dec_rows(T) * (D + 1) + m);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    y[k][t][i] = __ldcg(reinterpret_cast<const float4 *>(p + m * D + l16 * (D / 16) + 4 * i));
+            }
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            o.add(k0 + k < n ? pm[k] : -INFINITY, pl[k], y[k]);
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                o[t].add(k0 + k < n ? pm[k][t] : -INFINITY, pl[k][t], y[k][t]);
     }
-    return o;
 }
 
 template <int D, int T>
@@ -718,30 +732,39 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     constexpr int kPer = D / 16;  // outputs of a lane
     const uint32_t b0 = blockIdx.x * kDecWarps;
     const int hw = tid >> 4, l16 = lane & 15;
+    static_assert(2 * kDecWarps == kMmaRows, "half a warp per row of a tile");
     int base = 0;  // rows of the items so far
 #pragma unroll 1
     for (int j = -1; j < kDecWarps; ++j) {
         const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
         // rows go round over the half warps, whatever item they are of
-        const int r0 = (hw - base) & (2 * kDecWarps - 1);
-        base += pi.nrows;
+        const int r0 = (hw - base) & (kMmaRows - 1);
+        base += pi.nrows < kMmaRows ? pi.nrows : kMmaRows;
         const int wa = j < 0 ? 0 : j;
         const int wb = pi.last - b0 < kDecWarps ? static_cast<int>(pi.last - b0) : kDecWarps - 1;
-        for (int r = r0; r < pi.nrows; r += 2 * kDecWarps) {
-            const RowPart<D> o = join_near<D, T>(s_part, wa, wb, j >= 0, r, l16);
-            if (pi.first / kDecWarps == pi.last / kDecWarps) {
-                write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, o.v, o.l);
+        if (r0 >= pi.nrows)
+            continue;
+        RowPart<D> o[T];
+        join_near<D, T>(o, s_part, wa, wb, j >= 0, r0, pi.nrows, l16);
+        const bool whole = pi.first / kDecWarps == pi.last / kDecWarps;
+        float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D, T);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int r = r0 + kMmaRows * t;
+            if (r >= pi.nrows)
+                break;
+            if (whole) {
+                write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, o[t].v, o[t].l);
                 continue;
             }
             // the item goes over CTAs
-            float *out = cta_parts + (2 * (int64_t)blockIdx.x + (j < 0 ? 0 : 1)) * dec_part_floats(D, T);
 #pragma unroll
             for (int i = 0; i < kPer; i += 4)
                 __stcg(reinterpret_cast<float4 *>(out + r * D + l16 * kPer + i),
-                       make_float4(o.v[i], o.v[i + 1], o.v[i + 2], o.v[i + 3]));
+                       make_float4(o[t].v[i], o[t].v[i + 1], o[t].v[i + 2], o[t].v[i + 3]));
             if (l16 == 0) {
-                __stcg(out + kRows * D + r, o.m);
-                __stcg(out + kRows * (D + 1) + r, o.l);
+                __stcg(out + kRows * D + r, o[t].m);
+                __stcg(out + kRows * (D + 1) + r, o[t].l);
             }
         }
     }
@@ -755,19 +778,23 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
         s_final[tid] = pi.nrows > 0 && c_first != c_last && atomicAdd(arrived + c_first, 1u) == c_last - c_first;
     }
     __syncthreads();
+    __threadfence();
 #pragma unroll 1
     for (int j = -1; j < kDecWarps; ++j) {
         if (!s_final[j + 1])
             continue;
-        __threadfence();
         const PartInfo pi = s_part[j < 0 ? 0 : j][j < 0 ? 0 : 1];
         const int c_first = static_cast<int>(pi.first / kDecWarps), c_last = static_cast<int>(pi.last / kDecWarps);
-        for (int r = hw; r < pi.nrows; r += 2 * kDecWarps) {
+        if (hw < pi.nrows) {
             // the first CTA's part, then those of the CTAs after it
             const float *of = cta_parts + 2 * (int64_t)c_first * dec_part_floats(D, T);
-            const RowPart<D> o = join_far<D, T>(of + dec_part_floats(D, T), of, 2 * dec_part_floats(D, T),
-                                                c_last - c_first + 1, r, l16);
-            write_out<kPer>(a, G, pi.row0, pi.h, r, l16 * kPer, o.v, o.l);
+            RowPart<D> o[T];
+            join_far<D, T>(o, of + dec_part_floats(D, T), of, 2 * dec_part_floats(D, T), c_last - c_first + 1, hw,
+                           pi.nrows, l16);
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                if (hw + kMmaRows * t < pi.nrows)
+                    write_out<kPer>(a, G, pi.row0, pi.h, hw + kMmaRows * t, l16 * kPer, o[t].v, o[t].l);
         }
         if (tid == 0)
             arrived[c_first] = 0;  // for the next launch
