@@ -768,17 +768,15 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
             }
         }
     }
-    __threadfence();
     // ---- of the items that go over CTAs (the one begun before this CTA, the
     // last one begun in it), the last CTA to arrive joins the parts
     __syncthreads();
     if (tid <= kDecWarps) {
         const PartInfo &pi = s_part[tid ? tid - 1 : 0][tid ? 1 : 0];
         const uint32_t c_first = pi.first / kDecWarps, c_last = pi.last / kDecWarps;
-        s_final[tid] = pi.nrows > 0 && c_first != c_last && atomicAdd(arrived + c_first, 1u) == c_last - c_first;
+        s_final[tid] = pi.nrows > 0 && c_first != c_last && count_arrival(arrived + c_first) == c_last - c_first;
     }
     __syncthreads();
-    __threadfence();
 #pragma unroll 1
     for (int j = -1; j < kDecWarps; ++j) {
         if (!s_final[j + 1])

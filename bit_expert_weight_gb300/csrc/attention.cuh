@@ -26,6 +26,17 @@ cudaError_t allow_smem(Kernel kernel, int bytes, const DeviceFacts &dev, std::at
     return e;
 }
 
+// Counts an arrival at a counter in global memory: what the CTA's threads wrote
+// before the barrier in front of it is visible to whoever sees the count, and
+// what those who counted before wrote, to the threads behind the next barrier
+// (no fence of theirs is needed: the order is transitive).
+__device__ __forceinline__ unsigned count_arrival(unsigned *counter)
+{
+    unsigned v;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(counter) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;

@@ -1023,7 +1023,6 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
         if (whole)
             continue;
         // ---- the last of the item's CTAs to arrive joins its parts
-        __threadfence();
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sm.joined);
@@ -1031,7 +1030,7 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
             return;
         ++jn;
         if (threadIdx.x == 0)
-            sm.last = atomicAdd(arrived + c_first, 1u) == static_cast<unsigned>(c_last - c_first);
+            sm.last = count_arrival(arrived + c_first) == static_cast<unsigned>(c_last - c_first);
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sm.joined);
@@ -1039,7 +1038,6 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
             return;
         ++jn;
         if (*reinterpret_cast<volatile int *>(&sm.last)) {
-            __threadfence();
             // part j of the item
             auto part_of = [&](int j) {
                 return parts + (2 * (int64_t)j + (j == c_first ? 1 : 0)) * part_floats(D);
