@@ -214,6 +214,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes to global memory, in one piece where they are aligned to that: a
+// warp's lanes write rows of their own here, and a store takes a cycle per row.
+__device__ __forceinline__ void store32(void *p, const uint32_t *w, bool wide)
+{
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), SMOE_W8(w, 0) : "memory");
+    else
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<uint4 *>(static_cast<uint32_t *>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair(float x, float y)
 {
@@ -865,6 +877,8 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
     const int r = 32 * quarter + lane;  // row of the half, lane of tensor memory
     const uint32_t tl = sm.tmem_base + (static_cast<uint32_t>(32 * quarter) << 16);
     const float sc = a.scale * 1.44269504088896341f;
+    const int64_t esize = a.out_dtype == SMOE_F32 ? 4 : 2;
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.out_row_stride * esize | a.out_head_stride * esize) & 31) == 0;
     uint32_t sn = 0, jn = 0;  // commits of each s_done of this half, joins
     auto ok = [&](uint64_t *bar, unsigned parity) {
         return __all_sync(0xffffffffu, wait_for(sm, bar, parity, status));
@@ -976,20 +990,19 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
         const bool whole = c_first == c_last;
         auto write_out = [&](int col, const float *v, float inv) {  // 16 columns
             const int64_t at = token * a.out_row_stride + (int64_t)head * a.out_head_stride + col;
+            uint32_t w[16];
             if (a.out_dtype == SMOE_F32) {
-                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+                float *dst = static_cast<float *>(a.out) + at;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dst[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv,
-                                         v[4 * i + 3] * inv);
+                for (int i = 0; i < 16; ++i)
+                    w[i] = __float_as_uint(v[i] * inv);
+                store32(dst, w, wide);
+                store32(dst + 8, w + 8, wide);
             } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv),
-                                        pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                        pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                                        pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+                for (int i = 0; i < 8; ++i)
+                    w[i] = pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+                store32(static_cast<uint16_t *>(a.out) + at, w, wide);
             }
         };
         float *part = parts + (2 * (int64_t)blockIdx.x + (static_cast<int>(blockIdx.x) == c_first ? 1 : 0)) *
