@@ -264,6 +264,14 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, unsigned bytes)
                  : "memory");
 }
 
+// Bits lo .. hi - 1 of a word (any lo and hi).
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi)
+{
+    const uint32_t from = lo <= 0 ? ~0u : (lo < 32 ? ~0u << lo : 0u);
+    const uint32_t to = hi >= 32 ? ~0u : (hi > 0 ? (1u << hi) - 1u : 0u);
+    return from & to;
+}
+
 // Bounded wait that records a timeout in the CTA's fail flag.
 __device__ __forceinline__ bool wait_for(Smem &sm, uint64_t *bar, unsigned parity, int *status)
 {
@@ -914,11 +922,16 @@ __device__ void softmax(const smoe_attention_args &a, int G, Smem &sm, float *pa
                 pin32(s);
                 pin32(s + 32);
                 if (key0 < c.t_lo || key0 + kStep > c.t_hi) {
-                    const int first = lo - key0, end = hi - key0;
+                    // a bit per key: tested in place, it takes half the
+                    // instructions of two comparisons
 #pragma unroll
-                    for (int e = 0; e < kStep; ++e)
-                        if (e < first || e >= end)
-                            s[e] = 0xff800000u;  // -infinity
+                    for (int h = 0; h < kStep; h += 32) {
+                        const uint32_t unseen = ~bits_between(lo - key0 - h, hi - key0 - h);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (unseen & (1u << e))
+                                s[h + e] = 0xff800000u;  // -infinity
+                    }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
