@@ -61,7 +61,13 @@ constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11, kQueryWarp = 12;
 constexpr int kItemSlots = 4;
 constexpr int kThreads = 512;
-constexpr int kItemUnits = 4;           // an item's own cost, in units
+// An item's own cost, in units (queries, first products, output).  Heads of 64:
+// half the queries and output, while a unit takes about as long.  Measured at
+// 20 sequences, half chunks, half single rows, and one chunk of 3,000 rows: heads
+// of 64 with a cost of 4, 2, 1: 100.6, 95.7, 94.8 us and 45.8, 41.8, 41.5 us (two
+// long chunks 824, 800, 807); two prompts of heads of 128 with 4, 3, 2, 1: 1,074,
+// 1,078, 1,146, 1,332 us.
+__host__ __device__ constexpr int item_units(int D) { return D == 128 ? 4 : 2; }
 // Items of up to ten units are not cut: a cut costs about four units' time (a
 // part written and read, the join), and a part more one unit to read.
 constexpr int kWholeUnits = 10;
@@ -294,6 +300,7 @@ struct Tile {
     int b, t, h;
     int m0, rows;       // first packed row, packed rows (256 at most; 0: no tile)
     int units;
+    int own;            // its own cost, in units
     int64_t at;         // its first unit on the line
     int k_lo, k_hi;     // keys seen by any of its rows; unit 0 begins at kbase
     int t_lo, t_hi;     // keys seen by every row
@@ -324,6 +331,7 @@ __device__ __forceinline__ TileKeys keys_of(int window, int G, int seq_rows, int
 __device__ __forceinline__ void tile_keys(const smoe_attention_args &a, int G, Tile &c)
 {
     const TileKeys k = keys_of(a.window, G, c.s.rows, c.s.len, c.t);
+    c.own = item_units(a.cache.head_dim);
     c.m0 = c.t * kTileRows2;
     c.rows = k.rows;
     c.units = k.units;
@@ -337,7 +345,7 @@ __device__ __forceinline__ void tile_keys(const smoe_attention_args &a, int G, T
 // An item's length on the line.
 __device__ __forceinline__ int item_length(const Tile &c, int unit)
 {
-    return (c.units + kItemUnits + unit - 1) / unit * unit;
+    return (c.units + c.own + unit - 1) / unit * unit;
 }
 
 // To the next item; past the last one it has no rows.
@@ -361,7 +369,7 @@ __device__ __forceinline__ void tile_next(const smoe_attention_args &a, int G, i
 // Units [u0, u1) of the item that lie in the share [w0, w1).
 __device__ __forceinline__ void units_in(const Tile &c, int64_t w0, int64_t w1, int &u0, int &u1)
 {
-    const int64_t k = c.at + kItemUnits;
+    const int64_t k = c.at + c.own;
     u0 = w0 > k ? static_cast<int>(w0 - k) : 0;
     u1 = w1 - k < c.units ? static_cast<int>(w1 - k) : c.units;
 }
@@ -485,7 +493,7 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
             // Equal shares, but no item in so many parts that the joining costs
             // more than the sharing saves.
             q = ceil_div((int64_t)s.total * Hkv, gridDim.x);
-            const int64_t least = s.most <= kWholeUnits ? s.most + kItemUnits
+            const int64_t least = s.most <= kWholeUnits ? s.most + item_units(a.cache.head_dim)
                                                : static_cast<int64_t>(sqrtf(static_cast<float>(s.most)));
             q = q > least ? q : least;
             sum = l;
@@ -583,7 +591,7 @@ __device__ void item_walker(const smoe_attention_args &a, int G, Smem &sm, int64
             return;
         if (lane == 0) {
             Item &t = sm.item[slot];
-            const int64_t k = c.at + kItemUnits;
+            const int64_t k = c.at + c.own;
             t.row0 = c.s.row0;
             t.b = c.b;
             t.h = c.h;
