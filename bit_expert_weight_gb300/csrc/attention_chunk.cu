@@ -29,10 +29,10 @@
 // bound: two on each scheduler take 1,220 cycles for 64 keys of both (180 of
 // waiting, 290 the maximum, 680 the exponentials), with 44 % of the issue slots
 // and 36 % of the exponential unit in use: latencies that two warps don't fill.
-// Measured: 608 rows on 33,376 keys, 64 query and 4 kv heads of 128: 403 us,
-// 1,637 TFLOP/s; the same of 64: 880 TFLOP/s.  Prompts of 9,001 and 2,021 rows
-// (the second on 6,559 keys), heads of 128: 1.07 ms, 1,580 TFLOP/s; the rest are
-// items' starts and ends.
+// Measured: 608 rows on 33,376 keys, 64 query and 4 kv heads of 128: 403 to 414
+// us (from GPU to GPU), 1,590 to 1,640 TFLOP/s; the same of 64: 375 us, 880
+// TFLOP/s.  Prompts of 9,001 and 2,021 rows (the second on 6,559 keys), heads of
+// 128: 1.07 to 1.09 ms, 1,550 to 1,590 TFLOP/s; the rest are items' starts and ends.
 //
 // Roles of the 16 warps of a CTA, one CTA per SM:
 //   warps 0..3  half A, warps 4..7 half B: softmax, rescaling, output
