@@ -615,13 +615,8 @@ def _new_heads(x, dtype):
     """A contiguous [rows, heads, head_dim] tensor of x's shape: (tensor, pointer, row stride,
     head stride)."""
     T, H, D = x.shape
-    # the quicker call, where it does not copy x's order of dimensions
-    if x.stride(1) != D:
-        out = torch.empty((T, H, D), dtype=dtype, device=x.device)
-    elif dtype is x.dtype:
-        out = torch.empty_like(x)
-    else:
-        out = torch.empty_like(x, dtype=dtype)
+    # (x's own order of dimensions would be another one where its rows overlap)
+    out = torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
     return out, out.data_ptr(), H * D, D
 
 
