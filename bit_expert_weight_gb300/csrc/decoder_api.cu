@@ -20,6 +20,13 @@ inline bool valid_view(const void *p, int64_t row_stride, int64_t head_stride)
            head_stride % 8 == 0;
 }
 
+// Such a view to be written: its rows and its heads must not lie in one place.
+inline bool valid_out(const void *p, int64_t row_stride, int64_t head_stride, int64_t rows, int heads, int dim)
+{
+    return valid_view(p, row_stride, head_stride) && (rows == 1 || row_stride >= dim) &&
+           (heads == 1 || head_stride >= dim);
+}
+
 inline bool valid_dtype(int32_t t) { return t == SMOE_F32 || t == SMOE_BF16; }
 
 bool valid_rotation(int32_t rot_dim, int32_t head_dim, const int64_t *table, float rot_scale,
@@ -113,7 +120,8 @@ smoe_status smoe_rope(const smoe_rope_args *a, void *cuda_stream)
     if (a->num_rows == 0 || a->num_heads == 0)
         return SMOE_OK;
     if (!valid_view(a->x, a->x_row_stride, a->x_head_stride) ||
-        !valid_view(a->out, a->out_row_stride, a->out_head_stride) || !a->positions ||
+        !valid_out(a->out, a->out_row_stride, a->out_head_stride, a->num_rows, a->num_heads, a->head_dim) ||
+        !a->positions ||
         !valid_rotation(a->rot_dim, a->head_dim, a->table, a->rot_scale, a->eps) ||
         (a->norm_w && !aligned16(a->norm_w)))
         return SMOE_ERR_INVALID_ARG;
@@ -137,7 +145,8 @@ smoe_status smoe_kv_append(const smoe_kv_append_args *a, void *cuda_stream)
         !valid_view(a->v, a->v_row_stride, a->v_head_stride))
         return SMOE_ERR_INVALID_ARG;
     if (a->q && (a->num_heads < 1 || !valid_view(a->q, a->q_row_stride, a->q_head_stride) ||
-                 !valid_view(a->q_out, a->qo_row_stride, a->qo_head_stride)))
+                 !valid_out(a->q_out, a->qo_row_stride, a->qo_head_stride, a->batch.num_rows, a->num_heads,
+                            a->cache.head_dim)))
         return SMOE_ERR_INVALID_ARG;
     if (a->q && a->q_out == a->q &&
         (a->dtype != SMOE_BF16 || a->q_row_stride != a->qo_row_stride ||
@@ -168,7 +177,9 @@ smoe_status smoe_attention(const smoe_attention_args *a, void *workspace, size_t
     if (a->batch.num_rows == 0 || a->batch.num_seqs == 0)
         return SMOE_OK;
     if (a->max_rows < 1 || !batch_pointers(a->batch) || !valid_view(a->q, a->q_row_stride, a->q_head_stride) ||
-        !valid_view(a->out, a->out_row_stride, a->out_head_stride) || a->out == a->q)
+        !valid_out(a->out, a->out_row_stride, a->out_head_stride, a->batch.num_rows, a->num_heads,
+                   a->cache.head_dim) ||
+        a->out == a->q)
         return SMOE_ERR_INVALID_ARG;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
         return SMOE_ERR_INVALID_ARG;

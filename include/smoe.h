@@ -509,7 +509,11 @@ smoe_status smoe_moe_forward_noalloc(const smoe_layer_desc *layer, const void *x
  * Heads.  x, q, k and v are [rows, heads, head_dim] views: element (r, h, c)
  * lies at data + r * row_stride + h * head_stride + c (strides in elements),
  * so a slice of one projection's output needs no copy.  Pointers are 16-byte
- * aligned and strides are multiples of 8 elements.
+ * aligned and strides are multiples of 8 elements.  Rows or heads of an input
+ * may lie in one place (a stride below head_dim, or 0); those of an output may
+ * not: such strides are refused, other overlaps within an output, or of it with
+ * an input or the cache, are the caller's to avoid (but see smoe_rope and
+ * smoe_kv_append on working in place).
  *
  * Rotation.  Pair i (0 <= i < rot_dim / 2) of a head at position p turns by
  * t = p * f_i:

@@ -33,3 +33,24 @@ def test_new_outputs_have_the_strides_that_are_passed(S, shape, strides, dtype):
     assert out.shape == x.shape and out.dtype == dtype and out.data_ptr() == at
     assert out.is_contiguous() and (row, head) == (shape[1] * shape[2], shape[2])
     assert out.stride() == (row, head, 1)
+
+
+OVERLAPPING = [  # rows, heads, row stride, head stride of an output of heads of 128
+    (3, 4, 0, 128), (3, 4, 120, 128), (3, 4, 512, 0), (3, 4, 512, 64), (2, 1, 64, 128),
+    (1, 2, 512, 120),
+]
+
+
+@pytest.mark.parametrize("rows, heads, row, head", OVERLAPPING, ids=str)
+def test_outputs_that_overlap_themselves_are_refused(S, rows, heads, row, head):
+    """Two rows or two heads of one output in the same place: which one stays is left to
+    chance, so the library refuses (as the inputs do not, which are only read)."""
+    import ctypes
+    from test_decoder_args import append_args, attention_args, rope_args
+    L = S.load()
+    out = dict(out_row_stride=row, out_head_stride=head, num_rows=rows)
+    assert L.smoe_rope(ctypes.byref(rope_args(S, num_heads=heads, **out)), None) == -1
+    a = attention_args(S, num_heads=heads, num_kv_heads=1, **out)
+    assert L.smoe_attention(ctypes.byref(a), 4096, S.ATTENTION_WORKSPACE_BYTES, None) == -1
+    a = append_args(S, num_heads=heads, num_rows=rows, qo_row_stride=row, qo_head_stride=head)
+    assert L.smoe_kv_append(ctypes.byref(a), None) == -1
