@@ -594,17 +594,33 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _handle(stream, t):
-    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _heads(name, t):
-    """A [rows, heads, head_dim] fp32 or bf16 CUDA view with contiguous channels:
+def _device(name, t):
+    """The index of t's device, which the call's other tensors share: the library launches on
+    the current one."""
+    dev = t.get_device()               # -1: on the host
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    return dev
+
+
+def _handle(stream, dev):
+    if stream is None:
+        return _raw_stream(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError("the stream must be of the tensors' device")
+    return stream.cuda_stream
+
+
+def _heads(name, t, dev):
+    """A [rows, heads, head_dim] fp32 or bf16 view on device dev with contiguous channels:
     (pointer, row stride, head stride, smoe_dtype)."""
     st = t.stride()
-    if len(st) != 3 or st[2] != 1 or not t.is_cuda:
-        raise ValueError(f"{name} must be a [rows, heads, head_dim] CUDA tensor with contiguous "
-                         "channels")
+    if len(st) != 3 or st[2] != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor with contiguous "
+                         "channels, on the device of the call's other tensors")
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be fp32 or bf16")
@@ -620,27 +636,29 @@ def _new_heads(x, dtype):
     return out, out.data_ptr(), H * D, D
 
 
-def _device_array(name, t, dtype, numel):
-    """Pointer of a contiguous CUDA tensor of `dtype` with at least `numel` elements
+def _device_array(name, t, dtype, numel, dev):
+    """Pointer of a contiguous tensor of `dtype` on device dev with at least `numel` elements
     (None: no tensor, a null pointer)."""
     if t is None:
         return 0
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the device of the "
+                         "call's other tensors")
     if t.numel() < numel:
         raise ValueError(f"{name} must have {numel} elements")
     return t.data_ptr()
 
 
-def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows):
+def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows, dev):
     """The members of smoe_kv_cache and smoe_kv_batch."""
     P, Hkv, page, D = shape = k_pages.shape
     ks, vs = k_pages.stride(), v_pages.stride()
     if v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must have one shape")
-    if not (k_pages.dtype == v_pages.dtype == torch.bfloat16 and k_pages.is_cuda and
-            v_pages.is_cuda):
-        raise ValueError("k_pages and v_pages must be bf16 CUDA tensors")
+    if not (k_pages.dtype == v_pages.dtype == torch.bfloat16 and
+            k_pages.get_device() == v_pages.get_device() == dev):
+        raise ValueError("k_pages and v_pages must be bf16 tensors on the device of the call's "
+                         "other tensors")
     if not ks[1:] == vs[1:] == (page * D, D, 1):
         raise ValueError("k_pages, v_pages: the last three dimensions must be contiguous")
     B = kv_len.numel()
@@ -649,9 +667,9 @@ def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows):
         raise ValueError("page_table must be [sequences, pages]")
     i32 = torch.int32
     return (k_pages.data_ptr(), v_pages.data_ptr(), P, ks[0], vs[0], page, Hkv, D, 0,
-            _device_array("row_start", row_start, i32, B + 1),
-            _device_array("kv_len", kv_len, i32, B),
-            _device_array("page_table", page_table, i32, 0), rows, B, pages)
+            _device_array("row_start", row_start, i32, B + 1, dev),
+            _device_array("kv_len", kv_len, i32, B, dev),
+            _device_array("page_table", page_table, i32, 0, dev), rows, B, pages)
 
 
 def rope_table(rot_dim: int, theta: float, kind="plain", factor=1.0, original_len=4096.0,
@@ -677,19 +695,20 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, rot_scal
     [rows]), after a norm of each head where norm_w (bf16 [head_dim]) is given.  The first
     2 * table.numel() channels rotate.  out: a tensor of x's shape and dtype (x itself
     rotates in place)."""
-    xp, xr, xh, dt = _heads("x", x)
+    dev = _device("x", x)
+    xp, xr, xh, dt = _heads("x", x, dev)
     T, H, D = x.shape
     if out is None:
         out, op, orow, oh = _new_heads(x, x.dtype)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and dtype")
     else:
-        op, orow, oh, _ = _heads("out", out)
+        op, orow, oh, _ = _heads("out", out, dev)
     a = _pack_rope(xp, op, xr, xh, orow, oh, T, H, D, dt, 2 * table.numel(), interleaved,
-                   rot_scale, eps, _device_array("positions", positions, torch.int32, T),
-                   _device_array("table", table, torch.int64, 0),
-                   _device_array("norm_w", norm_w, torch.bfloat16, D))
-    _check(load().smoe_rope(a, _handle(stream, x)), "smoe_rope")
+                   rot_scale, eps, _device_array("positions", positions, torch.int32, T, dev),
+                   _device_array("table", table, torch.int64, 0, dev),
+                   _device_array("norm_w", norm_w, torch.bfloat16, D, dev))
+    _check(load().smoe_rope(a, _handle(stream, dev)), "smoe_rope")
     return out
 
 
@@ -704,8 +723,9 @@ def kv_append(q, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     int32 [sequences] (the new rows included), page_table int32 [sequences, pages].  table
     None: no rotation."""
     T, Hkv, D = k.shape
-    kp, kr, kh, dt = _heads("k", k)
-    vp, vr, vh, vdt = _heads("v", v)
+    dev = _device("k", k)
+    kp, kr, kh, dt = _heads("k", k, dev)
+    vp, vr, vh, vdt = _heads("v", v, dev)
     if v.shape != k.shape or (Hkv, D) != (k_pages.shape[1], k_pages.shape[3]):
         raise ValueError("k and v must be [rows, kv heads, head_dim] of the pages")
     qp = op = qr = qh = orow = oh = H = 0
@@ -714,29 +734,30 @@ def kv_append(q, k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         if q.shape[0] != T or q.shape[2] != D:
             raise ValueError("q must have k's rows and head_dim")
         H = q.shape[1]
-        qp, qr, qh, qdt = _heads("q", q)
+        qp, qr, qh, qdt = _heads("q", q, dev)
         if q_out is None:
             q_out, op, orow, oh = _new_heads(q, torch.bfloat16)
         elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16:
             raise ValueError("q_out must be bf16 of q's shape")
         else:
-            op, orow, oh, _ = _heads("q_out", q_out)
+            op, orow, oh, _ = _heads("q_out", q_out, dev)
     if not dt == vdt == qdt:
         raise TypeError("q, k and v must have one dtype")
-    a = _pack_append(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, kp, vp,
-                     op, qr, qh, kr, kh, vr, vh, orow, oh, H, dt,
+    a = _pack_append(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T, dev), qp, kp,
+                     vp, op, qr, qh, kr, kh, vr, vh, orow, oh, H, dt,
                      0 if table is None else 2 * table.numel(), interleaved, rot_scale, eps,
-                     _device_array("positions", positions, torch.int32, T),
-                     _device_array("table", table, torch.int64, 0),
-                     _device_array("q_norm", q_norm, torch.bfloat16, D),
-                     _device_array("k_norm", k_norm, torch.bfloat16, D))
-    _check(load().smoe_kv_append(a, _handle(stream, k)), "smoe_kv_append")
+                     _device_array("positions", positions, torch.int32, T, dev),
+                     _device_array("table", table, torch.int64, 0, dev),
+                     _device_array("q_norm", q_norm, torch.bfloat16, D, dev),
+                     _device_array("k_norm", k_norm, torch.bfloat16, D, dev))
+    _check(load().smoe_kv_append(a, _handle(stream, dev)), "smoe_kv_append")
     return q_out if q is not None else None
 
 
 def attention_workspace(device="cuda", stream=None):
     """A zeroed workspace for `attention`, the same for every shape."""
     ws = torch.empty(ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+    _device("the workspace", ws)
     _check(load().smoe_moe_workspace_init(_ptr(ws), ws.numel(), _stream(stream)),
            "workspace_init")
     return ws
@@ -751,7 +772,8 @@ def attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     window 0: every key up to the row's own; scale default head_dim ** -0.5.  Returns out
     [rows, heads, head_dim] in out_dtype (bf16 or fp32)."""
     T, H, D = q.shape
-    qp, qr, qh, qdt = _heads("q", q)
+    dev = _device("q", q)
+    qp, qr, qh, qdt = _heads("q", q, dev)
     if qdt != SMOE_BF16:
         raise TypeError("q must be bf16")
     if D != k_pages.shape[3]:
@@ -764,11 +786,13 @@ def attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     else:
-        op, orow, oh, odt = _heads("out", out)
-    a = _pack_attention(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T), qp, op,
-                        qr, qh, orow, oh, H, odt, max_rows, window,
+        op, orow, oh, odt = _heads("out", out, dev)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the device of the call's other tensors")
+    a = _pack_attention(*_cache_batch(k_pages, v_pages, row_start, kv_len, page_table, T, dev), qp,
+                        op, qr, qh, orow, oh, H, odt, max_rows, window,
                         D ** -0.5 if scale is None else scale)
-    _check(load().smoe_attention(a, ws.data_ptr(), ws.nbytes, _handle(stream, q)),
+    _check(load().smoe_attention(a, ws.data_ptr(), ws.nbytes, _handle(stream, dev)),
            "smoe_attention")
     return out
 

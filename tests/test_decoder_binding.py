@@ -54,3 +54,124 @@ def test_outputs_that_overlap_themselves_are_refused(S, rows, heads, row, head):
     assert L.smoe_attention(ctypes.byref(a), 4096, S.ATTENTION_WORKSPACE_BYTES, None) == -1
     a = append_args(S, num_heads=heads, num_rows=rows, qo_row_stride=row, qo_head_stride=head)
     assert L.smoe_kv_append(ctypes.byref(a), None) == -1
+
+
+class Placed:
+    """A host tensor that says it lies on CUDA device `index`."""
+
+    def __init__(self, t, index):
+        self.t, self.index = t, index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.index
+
+    @property
+    def is_cuda(self):
+        return self.index >= 0
+
+
+class Handle:
+    def __init__(self, index):
+        self.device_index, self.cuda_stream = index, 77
+
+
+class Calls:
+    """What reaches the library instead of it: name -> (packed arguments, the rest)."""
+
+    def __init__(self):
+        self.got = {}
+
+    def __getattr__(self, name):
+        def call(args, *rest):
+            self.got[name] = (args, rest)
+            return 0
+        return call
+
+
+@pytest.fixture
+def calls(S, monkeypatch):
+    lib = Calls()
+    monkeypatch.setattr(S, "load", lambda: lib)
+    monkeypatch.setattr(S, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(S, "_raw_stream", lambda dev: 1000 + dev)
+    return lib
+
+
+def operands(S):
+    """Arguments of the three calls by name; `where` says where each one lies."""
+    i32, bf = torch.int32, torch.bfloat16
+    pages = torch.zeros(4, 2, 16, 64, dtype=bf)
+    batch = dict(k_pages=pages, v_pages=pages.clone(),
+                 row_start=torch.zeros(2, dtype=i32), kv_len=torch.zeros(1, dtype=i32),
+                 page_table=torch.zeros(1, 3, dtype=i32))
+    x, kv = torch.zeros(5, 4, 64, dtype=bf), torch.zeros(5, 2, 64, dtype=bf)
+    table, norm = torch.zeros(32, dtype=torch.int64), torch.zeros(64, dtype=bf)
+    pos = torch.zeros(5, dtype=i32)
+    ws = torch.empty(S.ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8)
+    return {
+        "rope": (S.rope, dict(x=x, positions=pos, table=table, norm_w=norm, out=x.clone())),
+        "kv_append": (S.kv_append, dict(q=x, k=kv, v=kv.clone(), **batch, table=table, q_norm=norm,
+                                        k_norm=norm.clone(), positions=pos, q_out=x.clone())),
+        "attention": (S.attention, dict(q=x, **batch, ws=ws, out=x.clone())),
+    }
+
+
+def call(S, name, elsewhere=None, index=0, **kw):
+    """The call with every tensor on device 0 but `elsewhere`, which is on device `index`."""
+    f, args = operands(S)[name]
+    args = {k: Placed(t, index if k == elsewhere else 0) for k, t in args.items()}
+    if name == "attention":
+        args["max_rows"] = 1
+    args.update(kw)
+    return f(**args)
+
+
+NAMES = {
+    "rope": ["x", "positions", "table", "norm_w", "out"],
+    "kv_append": ["q", "k", "v", "k_pages", "v_pages", "row_start", "kv_len", "page_table", "table",
+                  "q_norm", "k_norm", "positions", "q_out"],
+    "attention": ["q", "k_pages", "v_pages", "row_start", "kv_len", "page_table", "ws", "out"],
+}
+
+
+@pytest.mark.parametrize("name", sorted(NAMES))
+def test_calls_on_one_device_reach_the_library(S, calls, name):
+    call(S, name)
+    assert calls.got["smoe_" + name][1][-1] == 1000
+    call(S, name, stream=Handle(0))
+    assert calls.got["smoe_" + name][1][-1] == 77
+
+
+@pytest.mark.parametrize("index", [-1, 1], ids=["host", "other device"])
+@pytest.mark.parametrize("name, arg", [(n, a) for n in sorted(NAMES) for a in NAMES[n]])
+def test_tensors_elsewhere_are_refused(S, calls, name, arg, index):
+    """The kernel would read or write another device's, or the host's, addresses."""
+    with pytest.raises(ValueError):
+        call(S, name, arg, index)
+    assert not calls.got
+
+
+@pytest.mark.parametrize("name", sorted(NAMES))
+def test_another_device_than_the_current_one_is_refused(S, calls, monkeypatch, name):
+    """The library launches on the current device, with its status word."""
+    with pytest.raises(ValueError):
+        call(S, name, stream=Handle(1))
+    monkeypatch.setattr(S, "_current_device", lambda: 1, raising=False)
+    with pytest.raises(ValueError):
+        call(S, name)
+    assert not calls.got
+
+
+def test_workspaces_of_another_layout_are_refused(S, calls):
+    n = S.ATTENTION_WORKSPACE_BYTES
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(n),
+               torch.empty(2 * n, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            call(S, "attention", ws=Placed(ws, 0))
+    assert not calls.got
+    with pytest.raises(ValueError):
+        S.attention_workspace("cpu")
+    assert not calls.got
