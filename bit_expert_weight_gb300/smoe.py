@@ -624,7 +624,11 @@ def _heads(name, t, dev):
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be fp32 or bf16")
-    return t.data_ptr(), st[0], st[1], dt
+    row, head = st[0], st[1]
+    if (row | head) & 7:  # refused by the library, but free where the dimension is of one
+        T, H, D = t.shape
+        row, head = row if T > 1 else H * D, head if H > 1 else D
+    return t.data_ptr(), row, head, dt
 
 
 def _new_heads(x, dtype):
@@ -660,13 +664,16 @@ def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows, dev):
         raise ValueError("k_pages and v_pages must be bf16 tensors on the device of the call's "
                          "other tensors")
     if not ks[1:] == vs[1:] == (page * D, D, 1):
-        raise ValueError("k_pages, v_pages: the last three dimensions must be contiguous")
+        # (a pool of one kv head or one page may have other strides there)
+        if not (k_pages[:1].is_contiguous() and v_pages[:1].is_contiguous()):
+            raise ValueError("k_pages, v_pages: the last three dimensions must be contiguous")
     B = kv_len.numel()
     tb, pages = page_table.shape
     if tb < B:
         raise ValueError("page_table must be [sequences, pages]")
     i32 = torch.int32
-    return (k_pages.data_ptr(), v_pages.data_ptr(), P, ks[0], vs[0], page, Hkv, D, 0,
+    kstep, vstep = (ks[0], vs[0]) if P > 1 else (Hkv * page * D,) * 2
+    return (k_pages.data_ptr(), v_pages.data_ptr(), P, kstep, vstep, page, Hkv, D, 0,
             _device_array("row_start", row_start, i32, B + 1, dev),
             _device_array("kv_len", kv_len, i32, B, dev),
             _device_array("page_table", page_table, i32, 0, dev), rows, B, pages)

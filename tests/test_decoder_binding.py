@@ -65,6 +65,9 @@ class Placed:
     def __getattr__(self, name):
         return getattr(self.t, name)
 
+    def __getitem__(self, at):
+        return Placed(self.t[at], self.index)
+
     def get_device(self):
         return self.index
 
@@ -174,4 +177,39 @@ def test_workspaces_of_another_layout_are_refused(S, calls):
     assert not calls.got
     with pytest.raises(ValueError):
         S.attention_workspace("cpu")
+    assert not calls.got
+
+
+def unpacked(cls, raw):
+    return cls.from_buffer_copy(raw)
+
+
+def test_strides_of_dimensions_of_one_are_free(S, calls):
+    """Nothing steps along a dimension of one, so its stride may be anything: one row out of
+    a wider buffer, one kv head stored after its slots."""
+    bf = torch.bfloat16
+    one = torch.as_strided(torch.zeros(1000, dtype=bf), (1, 4, 64), (259, 64, 1))
+    x = Placed(one, 0)
+    pos, table = Placed(torch.zeros(1, dtype=torch.int32), 0), Placed(torch.zeros(32).long(), 0)
+    S.rope(x, pos, table, out=x)
+    a = unpacked(S.RopeArgs, calls.got["smoe_rope"][0])
+    assert a.x_row_stride % 8 == 0 and a.out_row_stride == a.x_row_stride and a.x_head_stride == 64
+    head = Placed(torch.as_strided(torch.zeros(1000, dtype=bf), (3, 1, 64), (64, 7, 1)), 0)
+    S.rope(head, Placed(torch.zeros(3, dtype=torch.int32), 0), table, out=head)
+    a = unpacked(S.RopeArgs, calls.got["smoe_rope"][0])
+    assert a.x_head_stride % 8 == 0 and a.x_row_stride == 64
+    # pages of one kv head, its dimension after the slots' or of an odd stride; one page
+    pages = torch.zeros(4, 16, 1, 64, dtype=bf)
+    for p, stride in ((pages.transpose(1, 2), 1024), (pages[:, :, 0].unsqueeze(1), 1024),
+                      (torch.as_strided(pages, (4, 1, 16, 64), (1024, 5, 64, 1)), 1024),
+                      (torch.as_strided(pages, (1, 1, 16, 64), (3, 5, 64, 1)), 1024)):
+        call(S, "attention", k_pages=Placed(p, 0), v_pages=Placed(p, 0))
+        a = unpacked(S.AttentionArgs, calls.got["smoe_attention"][0])
+        assert (a.k_page_stride, a.v_page_stride) == (stride, stride) and a.num_kv_heads == 1
+    calls.got.clear()
+    wide = torch.zeros(4, 2, 32, 64, dtype=bf)
+    for p in (wide[:, :, :16], wide[:, :, ::2], torch.zeros(4, 2, 16, 128, dtype=bf)[..., :64],
+              torch.zeros(4, 16, 2, 64, dtype=bf).transpose(1, 2)):
+        with pytest.raises(ValueError):
+            call(S, "attention", k_pages=Placed(p, 0), v_pages=Placed(p, 0))
     assert not calls.got
