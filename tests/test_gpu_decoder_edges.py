@@ -55,3 +55,71 @@ def test_inputs_whose_rows_overlap(S, ws):
                        S.kv_append(x.contiguous(), k, k, *where, table))
     assert torch.equal(S.attention(x, *where, T, ws), S.attention(x.contiguous(), *where, T, ws))
     assert S.device_status() == 0
+
+
+def attend_paged(S, ws, p, max_rows=None, **kw):
+    return S.attention(p.q, p.k_pages, p.v_pages, p.row_start, p.kv_len, p.page_table,
+                       max_rows or p.max_rows, ws, **kw)
+
+
+@pytest.mark.parametrize("rows, G", [(64, 1), (300, 2), (1, 4), (6, 4)], ids=str)
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_large_size(S, ws, rows, G, D):
+    """Values of up to 2^118 under scores that grow by 2^29 and 2^6 along the keys.  Weights
+    that are relative to the largest score so far are at most 1, so that sums over 400 keys
+    stay below 2^127; were they 2^29, they would not."""
+    n = 400
+    p = Paged([rows], [n], 2 * G, 2, D, 16, DEV, seed=5)
+    i = torch.arange(n, device=DEV)
+    pg, at = p.page_table[0, i // 16].long(), i % 16
+    p.q.zero_()
+    p.q[..., 0] = 1
+    key = torch.zeros(n, 2, D, dtype=BF16, device=DEV)
+    key[:, :, 0] = torch.where(i < 100, 0.0, torch.where(i < 330, 20.0, 24.0))[:, None].to(BF16)
+    p.k_pages[pg, :, at] = key
+    sign = randn(n, 2, D, seed=1).add(0.5).sign()
+    p.v_pages[pg, :, at] = (sign * randn(n, 2, D, seed=2).abs().clamp(1, 2) * 2.0 ** 117).to(BF16)
+    for dtype in (F32, BF16):
+        out = attend_paged(S, ws, p, scale=1.0, out_dtype=dtype)
+        assert bool(torch.isfinite(out).all())
+        p.check(out, True, scale=1.0)
+    assert S.device_status() == 0
+
+
+@pytest.mark.parametrize("step", [9.0, 50.0])
+@pytest.mark.parametrize("rows, kv, Hq, Hkv, D", [
+    ([300], [2000], 2, 2, 64),
+    ([300], [2000], 2, 2, 128),
+    ([40, 9], [1500, 900], 16, 2, 128),
+    ([20], [60_001], 16, 2, 64),            # one tile of keys for many CTAs
+], ids=str)
+def test_maxima_that_keep_growing(S, ws, rows, kv, Hq, Hkv, D, step):
+    """Every other row's scores grow by 2^step at most 12 times along the keys, so that what
+    is summed so far has to be scaled again and again; the rows between, in the same warps,
+    see scores of one size and are not scaled."""
+    page = 64
+    p = Paged(rows, kv, Hq, Hkv, D, page, DEV, seed=11)
+    scale = math.log(2) / 4
+    odd = (torch.arange(p.T, device=DEV)[:, None] + torch.arange(Hq, device=DEV)) % 2 == 1
+    p.q[odd] = 0
+    p.q[..., 0] = torch.where(odd, 4.0, 0.0).to(BF16)       # odd rows: the key's channel 0
+    for b, n in enumerate(kv):
+        i = torch.arange(n, device=DEV)
+        pg, at = p.page_table[b, i // page].long(), i % page
+        block = i // 64
+        times = block * 12 // int(block[-1]) if n > 2000 else block.clamp(max=12)
+        key = p.k_pages[pg, :, at]
+        key[..., 0] = (times * step)[:, None].to(BF16)
+        p.k_pages[pg, :, at] = key
+        # what the rows see, in powers of two per 64 keys, of the last row
+        row = sum(rows[:b + 1]) - 1
+        q = p.q[row].double().view(Hkv, Hq // Hkv, D)
+        s = torch.einsum("hgd,nhd->hgn", q, key.double()).reshape(Hq, n) / 4
+        s = torch.nn.functional.pad(s, (0, -n % 64), value=-math.inf).view(Hq, -1, 64).amax(-1)
+        before = s.cummax(-1).values[:, :-1]
+        grown = ((s[:, 1:] - before) > 8).sum(-1)
+        assert bool((grown[odd[row]] >= 10).all())
+        assert bool((s.amax(-1) - s[:, 0] < 8)[~odd[row]].any())
+    for dtype in (F32, BF16):
+        p.check(attend_paged(S, ws, p, scale=scale, out_dtype=dtype), True, scale=scale)
+    assert S.device_status() == 0
