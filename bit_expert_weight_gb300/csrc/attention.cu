@@ -138,19 +138,21 @@ __device__ __forceinline__ uint32_t steps_per_worker(uint32_t total, int longest
     return q > least ? q : (least > 1 ? least : 1);
 }
 
+// Steps of the longest line, with room below 2^32 for the rounding of a sum in
+// fp32.
+constexpr float kMaxLine = 4.2e9f;
+
 // The batch into shared memory (n + 1 entries), and the shares.  Each thread
-// takes `per` sequences in a row.  The line has fewer than 2^32 steps; a batch
-// beyond that is recorded and not worked on.
+// takes `per` sequences in a row.  A batch whose line has more than kMaxLine
+// steps is recorded and not worked on.
 __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs, int *status)
 {
     __shared__ uint32_t s_sum[2][kDecWarps];
     __shared__ int s_max[kDecWarps];
-    __shared__ int s_over;
+    __shared__ float s_all[kDecWarps];
     constexpr int kThreads = 32 * kDecWarps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = a.batch.num_seqs, per = (n + kThreads - 1) / kThreads, Hkv = a.cache.num_kv_heads;
-    if (tid == 0)
-        s_over = 0;
     // Lengths as they are, and rounded up to the steps that a CTA takes at one
     // per worker: where the grid has room for the latter, every CTA works on
     // one item only and has one join.
@@ -171,7 +173,7 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
         if (k > 0) {
             sum[0] += item_length(k, 1);
             sum[1] += item_length(k, kDecWarps);
-            all += static_cast<float>(k + 2 * kDecWarps) * static_cast<float>(Hkv);
+            all += static_cast<float>(item_length(k, kDecWarps)) * static_cast<float>(Hkv);
         }
         mx = k > mx ? k : mx;
     }
@@ -185,16 +187,18 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
         }
         const int m = __shfl_xor_sync(0xffffffffu, mx, o);
         mx = m > mx ? m : mx;
+        all += __shfl_xor_sync(0xffffffffu, all, o);
     }
     if (lane == 31) {
         s_sum[0][warp] = incl[0];
         s_sum[1][warp] = incl[1];
     }
-    if (lane == 0)
+    if (lane == 0) {
         s_max[warp] = mx;
+        s_all[warp] = all;
+    }
     __syncthreads();
-    if (all > 1.6e7f)  // of a thread: 256 of them stay below 2^32
-        s_over = 1;
+    all = 0.f;
     uint32_t total[2] = {0, 0}, before[2] = {incl[0] - sum[0], incl[1] - sum[1]};
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
@@ -204,6 +208,7 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
             total[j] += s_sum[j][w];
         }
         mx = s_max[w] > mx ? s_max[w] : mx;
+        all += s_all[w];
     }
     Share sh;
     sh.q = steps_per_worker(total[0] * Hkv, mx);
@@ -225,7 +230,7 @@ __device__ __forceinline__ Share plan(const smoe_attention_args &a, RowSeq *seqs
         seqs[n].at = sh.total;
     }
     __syncthreads();
-    if (s_over) {
+    if (all > kMaxLine) {  // the sums above may have wrapped
         set_status(status, kStatusBadArg);
         sh.total = 0;
     }

@@ -677,7 +677,11 @@ typedef struct {
  * gives the same bits on every call.
  * A page id outside the pool, a length past the page table, rows out of
  * order and a sequence of more than max_rows rows are recorded
- * (SMOE_ERR_DEVICE_FAULT); that sequence's output is then unspecified.
+ * (SMOE_ERR_DEVICE_FAULT); that sequence's output is then unspecified.  So is
+ * a call of too much work, which then writes nothing: where a sequence's rows
+ * are few (max_rows * num_heads / num_kv_heads <= 32), the steps of 16 keys,
+ * and 8 to 16 more per sequence, summed over the sequences with rows and
+ * times num_kv_heads, may be 4.2e9.
  * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_WORKSPACE, SMOE_ERR_UNSUPPORTED
  * (device), SMOE_ERR_CUDA. */
 smoe_status smoe_attention(const smoe_attention_args *args, void *workspace,

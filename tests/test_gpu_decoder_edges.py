@@ -123,3 +123,53 @@ def test_maxima_that_keep_growing(S, ws, rows, kv, Hq, Hkv, D, step):
     for dtype in (F32, BF16):
         p.check(attend_paged(S, ws, p, scale=scale, out_dtype=dtype), True, scale=scale)
     assert S.device_status() == 0
+
+
+def aliased(kv, Hq, Hkv, D, rows, pool=3, page=256):
+    """A batch whose page tables name the same few pages over and over, so that long
+    sequences need little memory: (pages and index arrays, queries)."""
+    k, v = (randn(pool, Hkv, page, D, seed=s, dtype=BF16) for s in (kv[0] % 1000, 7))
+    width = max(-(-n // page) for n in kv)
+    table = torch.arange(width, device=DEV) % pool
+    i32 = dict(dtype=torch.int32, device=DEV)
+    where = (k, v, torch.arange(len(kv) + 1, **i32) * rows, torch.tensor(kv, **i32),
+             table.to(torch.int32).expand(len(kv), -1).contiguous())
+    return where, randn(rows * len(kv), Hq, D, seed=3, dtype=BF16)
+
+
+def aliased_reference(where, q, n):
+    """(out, size, spread) of one row on n such keys: each slot counts as often as a key
+    lies in it."""
+    pool, Hkv, page, D = where[0].shape
+    i = torch.arange(pool * page, device=DEV)
+    full, rest = divmod(n, pool * page)
+    count = (full + (i < rest)).double()
+    k, v = (x.transpose(1, 2).reshape(pool * page, Hkv, D).double() for x in where[:2])
+    x = q[0].double().view(Hkv, -1, D)
+    s = torch.einsum("hgd,nhd->hgn", x, k) * D ** -0.5
+    p = torch.softmax(s + count.log(), -1)
+    out = torch.einsum("hgn,nhd->hgd", p, v).reshape(1, -1, D)
+    size = torch.einsum("hgn,nhd->hgd", p, v.abs()).reshape(1, -1, D)
+    spread = (torch.einsum("hgd,nhd->hgn", x.abs(), k.abs()) * D ** -0.5).amax(-1)
+    return out, size, spread.reshape(1, -1, 1)
+
+
+@pytest.mark.parametrize("n, Hkv, D", [(4_100_003, 64, 64), (2_200_001, 128, 128),
+                                       (300_000_001, 1, 64)], ids=str)
+def test_long_lines_of_steps(S, ws, n, Hkv, D):
+    """One sequence whose keys times kv heads are more than 2^28, with few rows."""
+    where, q = aliased([n], Hkv, Hkv, D, 1)
+    out = S.attention(q, *where, 1, ws, out_dtype=F32)
+    assert S.device_status() == 0
+    ref, size, spread = aliased_reference(where, q, n)
+    assert bool(((out.double() - ref).abs() <=
+                 attend_bound(ref, size, spread, n, D, F32, False)).all())
+
+
+def test_too_long_a_line_of_steps_is_recorded(S, ws):
+    """2^27 steps of 32 kv heads: 2^32.  Nothing is written, and the workspace stays usable."""
+    where, q = aliased([2 ** 31 - 512], 32, 32, 64, 1)
+    out = torch.full_like(q, 5.0)
+    S.attention(q, *where, 1, ws, out=out)
+    assert S.device_status() == -5 and S.device_status() == 0
+    assert bool((out == 5.0).all()) and not bool(ws[:4096].any())
