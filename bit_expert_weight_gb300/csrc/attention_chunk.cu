@@ -139,7 +139,7 @@ struct Smem {
     uint32_t k_filled, kv_filled, raw_filled;  // phases of k_first, kv_full, v_raw (drain after a failure)
     int fail, last;
     // the work split
-    uint32_t scan[kThreads / 32];
+    uint32_t scan[kThreads / 32], grains[kThreads / 32];
     int scan_max[kThreads / 32];
     int64_t q, total, before;    // units per CTA, in all, before the CTA's first item's tile
     int64_t border[2];           // the CTA's share
@@ -392,10 +392,18 @@ __device__ __forceinline__ int tiles_of(const Seq &s, int G) { return (s.rows * 
 struct Scan {
     uint32_t before, total;
     int most;
+    bool over;  // the sum may not be below 2^32, and the two above have wrapped
 };
-__device__ __forceinline__ Scan scan_all(Smem &sm, uint32_t v, int mx)
+// The line of one kv head must stay below 2^32 units.  That is seen from the
+// threads' own sums in grains of 2^16, rounded up, which 32 bits hold whatever
+// the batch: a thread has 2^14 tiles of 2^24 units at most.
+constexpr int kGrainShift = 16;
+constexpr uint32_t kMaxGrains = 1u << (32 - kGrainShift);
+__device__ __forceinline__ Scan scan_all(Smem &sm, uint64_t own, int mx)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t v = static_cast<uint32_t>(own);
+    const uint32_t grains = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(own >> kGrainShift) + 1u);
     uint32_t incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -406,6 +414,7 @@ __device__ __forceinline__ Scan scan_all(Smem &sm, uint32_t v, int mx)
     __syncthreads();
     if (lane == 31) {
         sm.scan[warp] = incl;
+        sm.grains[warp] = grains;
         sm.scan_max[warp] = mx;
     }
     __syncthreads();
@@ -415,6 +424,7 @@ __device__ __forceinline__ Scan scan_all(Smem &sm, uint32_t v, int mx)
     s.before = incl - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
     s.total = __reduce_add_sync(0xffffffffu, w);
     s.most = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? sm.scan_max[lane] : 0);
+    s.over = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? sm.grains[lane] : 0) > kMaxGrains;
     return s;
 }
 
@@ -482,11 +492,10 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
         c.t = i - seqs[b].tiles;
         tile_keys(a, G, c);
     };
-    // the length of this thread's tiles on the line of one kv head (fewer than
-    // 2^32 units in all: 2^17 tiles of 2^15 units)
+    // the length of this thread's tiles on the line of one kv head
     int mx = 0;
     auto length = [&](int unit) {
-        uint32_t l = 0;
+        uint64_t l = 0;
 #pragma unroll 1
         for (int i = i0, b = b0; i < i1; ++i) {
             tile_at(i, b);
@@ -498,7 +507,7 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
     int unit = 1;
     int64_t q;
     for (int pass = 0;; ++pass) {
-        const uint32_t l = length(unit);
+        const uint64_t l = length(unit);
         const Scan s = scan_all(sm, l, mx);
         if (pass == 0) {
             // Equal shares, but no item in so many parts that the joining costs
@@ -507,16 +516,22 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
             const int64_t least = s.most <= kWholeUnits ? s.most + item_units(a.cache.head_dim)
                                                : static_cast<int64_t>(sqrtf(static_cast<float>(s.most)));
             q = q > least ? q : least;
-            sum = l;
+            sum = static_cast<uint32_t>(l);
             sc = s;
+            if (s.over) {  // recorded, and not worked on
+                if (tid == 0)
+                    set_status(status, kStatusBadArg);
+                sum = sc.before = sc.total = 0;
+                break;
+            }
             // Where the grid has room for it, every item begins a CTA's share,
             // so that none is cut for the sake of its neighbours.
             if (all * Hkv > static_cast<int>(gridDim.x))
                 break;
             unit = static_cast<int>(q);
         } else {
-            if ((int64_t)s.total * Hkv <= q * gridDim.x) {
-                sum = l;
+            if (!s.over && (int64_t)s.total * Hkv <= q * gridDim.x) {
+                sum = static_cast<uint32_t>(l);
                 sc = s;
             } else {
                 unit = 1;

@@ -172,7 +172,7 @@ smoe_status smoe_attention(const smoe_attention_args *a, void *workspace, size_t
     if (a->num_heads < 1 || a->num_heads % a->cache.num_kv_heads ||
         a->num_heads / a->cache.num_kv_heads > 128 || a->window < 0 ||
         !isfinite(a->scale) || !(a->scale > 0.0f) ||
-        a->batch.num_rows * a->num_heads > 0x7fffffff)
+        a->batch.num_rows * a->num_heads > 0x7fffffff - 511)  // (rounded up to tiles, they fit 31 bits)
         return SMOE_ERR_INVALID_ARG;
     if (a->batch.num_rows == 0 || a->batch.num_seqs == 0)
         return SMOE_OK;

@@ -656,7 +656,7 @@ typedef struct {
     int32_t num_heads;         /* a multiple of num_kv_heads, at most 128
                                   times as many: query head h reads kv head
                                   h / (num_heads / num_kv_heads); num_rows *
-                                  num_heads < 2^31                            */
+                                  num_heads <= 2^31 - 512                     */
     int32_t out_dtype;         /* smoe_dtype                                  */
     int32_t max_rows;          /* no sequence of the batch has more rows; the
                                   kernel is chosen by it                      */
@@ -681,7 +681,10 @@ typedef struct {
  * a call of too much work, which then writes nothing: where a sequence's rows
  * are few (max_rows * num_heads / num_kv_heads <= 32), the steps of 16 keys,
  * and 8 to 16 more per sequence, summed over the sequences with rows and
- * times num_kv_heads, may be 4.2e9.
+ * times num_kv_heads, may be 4.2e9; else the blocks of 128 keys that each 256
+ * rows of one kv head see (new rows times query heads per kv head), and 2 to 4
+ * more, summed over the batch, may be 4.2e9 (half a minute and more of work:
+ * longer chunks are for several calls).
  * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_WORKSPACE, SMOE_ERR_UNSUPPORTED
  * (device), SMOE_ERR_CUDA. */
 smoe_status smoe_attention(const smoe_attention_args *args, void *workspace,

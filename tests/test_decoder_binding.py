@@ -213,3 +213,11 @@ def test_strides_of_dimensions_of_one_are_free(S, calls):
         with pytest.raises(ValueError):
             call(S, "attention", k_pages=Placed(p, 0), v_pages=Placed(p, 0))
     assert not calls.got
+
+
+def test_attention_refuses_more_rows_than_tiles_are_counted_for(S):
+    """num_rows * num_heads is rounded up to whole tiles in 31 bits."""
+    import ctypes
+    from test_decoder_args import attention_args
+    a = attention_args(S, num_rows=(1 << 27) - 31, num_heads=16)
+    assert S.load().smoe_attention(ctypes.byref(a), 4096, S.ATTENTION_WORKSPACE_BYTES, None) == -1
