@@ -261,7 +261,7 @@ __device__ __forceinline__ Place place_of(const smoe_kv_append_args &a, int64_t 
     // is needed then is asked for at once.
     int b = row < n ? static_cast<int>(row) : n - 1;
     int first = a.batch.row_start[b], last = a.batch.row_start[b + 1], len = a.batch.kv_len[b];
-    if (row >= a.batch.row_start[n])
+    if (row >= a.batch.row_start[n] || row < a.batch.row_start[0])
         return {-1, -1};
     if (row < first || row >= last) {
         b = owner_of(a.batch.row_start, n, row, lane);
@@ -330,10 +330,25 @@ __global__ void __launch_bounds__(kRotThreads)
         }
     };
     load(raw);  // the first heads are on their way while the rows' places are looked up
+    // The first CTA looks whether the starts are in order; the loads are on
+    // their way with those of its rows' places.
+    const int seqs = a.batch.num_seqs;
+    const bool look = blockIdx.x == 0;
+    const int start = look && tid < seqs ? a.batch.row_start[tid] : 0;
+    const int end = look && tid < seqs ? a.batch.row_start[tid + 1] : 0;
     for (int r = tid >> 5; r < rows; r += kRotThreads / 32) {
         const Place p = place_of(a, row0 + r, tid & 31, status);
         if ((tid & 31) == 0)
             s_place[r] = p;
+    }
+    if (look) {
+        bool bad = end < start || start < 0 || end > a.batch.num_rows;
+        for (int b = tid + kRotThreads; b < seqs; b += kRotThreads) {
+            const int to = a.batch.row_start[b + 1];
+            bad = bad || to < a.batch.row_start[b] || to > a.batch.num_rows;
+        }
+        if (bad)
+            set_status(status, kStatusBadArg);
     }
     __syncthreads();
     if (tid >= kRotThreads - kRotRows && tid - (kRotThreads - kRotRows) < rows)

@@ -537,9 +537,9 @@ smoe_status smoe_moe_forward_noalloc(const smoe_layer_desc *layer, const void *x
  * fine) and has kv_len[b] keys, the new rows' own included: its row number j
  * of n is key i = kv_len[b] - n + j.  Key i lies in page
  * page_table[b * table_stride + i / page_size] at slot i % page_size.  Rows
- * from row_start[num_seqs] on belong to no sequence: they give and
- * get nothing (a captured graph may be replayed with a smaller batch).  All
- * of these arrays are DEVICE int32, read when the kernel runs. */
+ * before row_start[0] and from row_start[num_seqs] on belong to no sequence:
+ * they give and get nothing (a captured graph may be replayed with a smaller
+ * batch, a part of a batch used by itself).  All of these arrays are DEVICE int32, read when the kernel runs. */
 #define SMOE_MAX_HEAD_DIM 256
 #define SMOE_MAX_SEQS 2048
 
@@ -635,9 +635,10 @@ typedef struct {
  * rotated, goes to q_out.  One launch.  The slots of one call must be
  * distinct (no two sequences write one page).  A row whose key index is
  * negative (a chunk longer than kv_len) is not stored.  A page id outside
- * the pool, a key past the page table and a row_start out of order store
- * nothing and are recorded: SMOE_ERR_DEVICE_FAULT from
- * smoe_get_device_status.  Errors: SMOE_ERR_INVALID_ARG,
+ * the pool and a key past the page table store nothing and are recorded:
+ * SMOE_ERR_DEVICE_FAULT from smoe_get_device_status.  So are row starts that
+ * are negative, fall or pass num_rows; which of their rows are stored, in the
+ * pages that the table names, is then unspecified.  Errors: SMOE_ERR_INVALID_ARG,
  * SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
 smoe_status smoe_kv_append(const smoe_kv_append_args *args, void *cuda_stream);
 

@@ -207,3 +207,47 @@ def test_tiles_of_few_rows_of_long_sequences(S, ws):
         tol = attend_bound(ref, size, spread, 5 * 16 * units, 64, F32, True)
         assert bool(((out[r:r + 1].double() - ref).abs() <= tol).all())
         assert float((tol / size).max()) < 0.02
+
+
+@pytest.mark.parametrize("joined", [False, True])
+def test_append_to_a_part_of_a_batch(S, ws, joined):
+    """Rows before row_start[0] belong to no sequence, like those from the last start on: the
+    append and the attention both leave them alone, and nothing is recorded."""
+    p = Paged([2, 3], [5, 8], 4, 2, 64, 16, DEV, joined=joined)
+    n, T = 4, 4 + p.T + 60
+    q, k, v = (randn(T, h, 64, seed=s, dtype=BF16) for h, s in ((4, 1), (2, 2), (2, 3)))
+    starts = p.row_start + n
+    k0, v0 = p.k_pages.clone(), p.v_pages.clone()
+    out = torch.full_like(q, 3.0)
+    S.kv_append(q, k, v, p.k_pages, p.v_pages, starts, p.kv_len, p.page_table, q_out=out)
+    assert S.device_status() == 0
+    assert torch.equal(out[n:n + p.T], q[n:n + p.T])
+    assert bool((out[:n] == 3.0).all()) and bool((out[n + p.T:] == 3.0).all())
+    for b, (r, length) in enumerate(zip(p.rows, p.kv)):
+        i = torch.arange(length - r, length, device=DEV)
+        pg, at = p.page_table[b, i // 16].long(), i % 16
+        first = int(starts[b])
+        assert torch.equal(p.k_pages[pg, :, at], k[first:first + r])
+        k0[pg, :, at], v0[pg, :, at] = k[first:first + r], v[first:first + r]
+    for old, new in ((k0, p.k_pages), (v0, p.v_pages)):
+        assert torch.equal(old.view(torch.int16), new.view(torch.int16))
+    got = torch.full_like(q, 3.0)
+    S.attention(q, p.k_pages, p.v_pages, starts, p.kv_len, p.page_table, 3, ws, out=got)
+    assert S.device_status() == 0
+    p.check(got[n:n + p.T], True, q=q[n:n + p.T])
+    assert bool((got[:n] == 3.0).all()) and bool((got[n + p.T:] == 3.0).all())
+
+
+@pytest.mark.parametrize("starts", [[0, 5, 3], [0, 3, 2, 5, 6], [0, 2, 9], [-1, 2, 5], [0, -3, 5],
+                                    [0] * 700 + [4, 3, 6]], ids=lambda s: str(s[-5:]))
+@pytest.mark.parametrize("scale", [1, 66])
+def test_append_records_row_starts_out_of_order(S, starts, scale):
+    """Starts that are negative, fall or leave the rows are recorded, wherever they stand."""
+    T, B = 6 * scale, len(starts) - 1
+    p = Paged([1] * B, [400] * B, 4, 2, 64, 256, DEV)
+    k = randn(T, 2, 64, dtype=BF16)
+    good = [min(b * scale, T) for b in range(B + 1)]
+    for s, status in ((good, 0), ([x * scale for x in starts], -5)):
+        S.kv_append(None, k, k, p.k_pages, p.v_pages,
+                    torch.tensor(s, dtype=torch.int32, device=DEV), p.kv_len, p.page_table)
+        assert S.device_status() == status and S.device_status() == 0
