@@ -6,7 +6,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from attn_helpers import Paged, attend, attend_bound, turned, turned_bound  # noqa: E402
+from attn_helpers import Paged, attend_bound, turned, turned_bound  # noqa: E402
+from test_attn_bounds import FEW  # noqa: E402
 from test_decoder_args import freqs  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -251,3 +252,14 @@ def test_append_records_row_starts_out_of_order(S, starts, scale):
         S.kv_append(None, k, k, p.k_pages, p.v_pages,
                     torch.tensor(s, dtype=torch.int32, device=DEV), p.kv_len, p.page_table)
         assert S.device_status() == status and S.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("case", FEW, ids=str)
+def test_few_rows_keep_p_in_fp32(S, ws, case, dtype):
+    """The bound is for P as two bf16 halves; P rounded to bf16 is beyond it in each of these
+    cases (test_attn_bounds)."""
+    rows, kv, Hq, Hkv, D, page, window = case
+    p = Paged(rows, kv, Hq, Hkv, D, page, DEV, seed=21)
+    p.check(attend_paged(S, ws, p, window=window, out_dtype=dtype), False, window)
+    assert S.device_status() == 0
