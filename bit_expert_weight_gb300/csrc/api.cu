@@ -69,14 +69,9 @@ static int device_cc_minor()
     return g_minor[cur_device()];
 }
 
-bool device_supported()
-{
-    // The library is compiled for sm_103a only.
-    return device_cc_major() == 10 && device_cc_minor() == 3;
-}
-
 const DeviceFacts &device_facts()
 {
+    static_assert(kMaxDevices <= kMaxDeviceIndex, "device indices");
     static DeviceFacts facts[kMaxDevices];
     static std::atomic<bool> known[kMaxDevices];
     const int dev = cur_device();
@@ -116,6 +111,12 @@ namespace {
 
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool device_supported()
+{
+    // The library is compiled for sm_103a only.
+    return device_cc_major() == 10 && device_cc_minor() == 3;
+}
 
 smoe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SMOE_OK : SMOE_ERR_CUDA; }
 

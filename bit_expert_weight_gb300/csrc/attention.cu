@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1)
     static_assert(kPartsAt + (size_t)kMaxCtas * (kDecWarps + 2) * dec_part_floats(D, T) * 4 <=
                       SMOE_ATTENTION_WORKSPACE_BYTES,
                   "workspace");
+    static_assert(kMaxCtas <= kMaxCounters, "counters");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.num_heads / a.cache.num_kv_heads, page = a.cache.page_size;
     const int g = lane >> 2, c2 = 2 * (lane & 3);

@@ -84,13 +84,6 @@ __device__ __forceinline__ void seen_from(const smoe_attention_args &a, int i, i
     seen_from(a.window, i, lo, hi);
 }
 
-// Keys seen by new row `token` of s.
-__device__ __forceinline__ void seen(const smoe_attention_args &a, const Seq &s, int token, int &lo,
-                                     int &hi)
-{
-    seen_from(a, s.len - s.rows + token, lo, hi);
-}
-
 __device__ __forceinline__ Seq seq_or_none(const smoe_attention_args &a, int b, int *status)
 {
     Seq s;

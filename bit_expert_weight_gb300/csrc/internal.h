@@ -18,9 +18,7 @@ size_t moe_workspace_zero_bytes(const smoe_layer_desc *layer, int64_t num_tokens
 int device_sm_count();
 // Compute capability major of the current device (cached per device).
 int device_cc_major();
-// Whether the current device is the one the library is compiled for (sm_103a).
-bool device_supported();
-// The same facts of the current device in one look (cached per device).
+// Facts of the current device in one look (cached per device).
 struct DeviceFacts {
     int sms;         // streaming multiprocessors
     bool supported;  // the device the library is compiled for
