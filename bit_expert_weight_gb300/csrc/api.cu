@@ -78,6 +78,8 @@ const DeviceFacts &device_facts()
     if (!known[dev].load(std::memory_order_acquire)) {
         ensure_device_info();
         std::lock_guard<std::mutex> lk(g_mu);
+        if (known[dev].load(std::memory_order_relaxed))
+            return facts[dev];  // another thread was first, and its caller reads them
         facts[dev].sms = g_sms[dev];
         facts[dev].supported = g_major[dev] == 10 && g_minor[dev] == 3;
         facts[dev].status = g_status_ptr[dev];
