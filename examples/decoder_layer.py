@@ -3,9 +3,9 @@ several sequences at once, prompts in chunks beside the next tokens of others.
 
     python examples/decoder_layer.py
 
-Between the projections (plain matrix products) a step is three calls on the
-attention side, kv_append and attention on the paged cache and the expert
-layer's forward, with the sequences' lengths and pages on the device.  Weights
+Between the norms and projections (plain torch) a step is kv_append and
+attention on the paged cache and the expert layer's forward, with the sequences'
+lengths and pages on the device.  Weights
 are random; the layer is the synthetic generator's smallest workload.
 """
 from __future__ import annotations
@@ -60,6 +60,11 @@ class PagedCache:
         self.owned[b], self.lens[b] = [], 0
 
 
+def rms_norm(x, weight):
+    x = x.float()
+    return (x * torch.rsqrt(x.square().mean(-1, keepdim=True) + EPS) * weight.float()).bfloat16()
+
+
 class DecoderLayer:
     def __init__(self, wl, heads, kv_heads, head_dim, device, bits=4, seed=0):
         self.wl, self.heads, self.kv_heads, self.head_dim = wl, heads, kv_heads, head_dim
@@ -74,6 +79,8 @@ class DecoderLayer:
         self.w_out = randn(wl.d, heads * head_dim, 1.0)
         self.q_norm = (1 + 0.1 * torch.randn(head_dim, generator=g, device=device)).bfloat16()
         self.k_norm = (1 + 0.1 * torch.randn(head_dim, generator=g, device=device)).bfloat16()
+        self.attn_norm = (1 + 0.1 * torch.randn(wl.d, generator=g, device=device)).bfloat16()
+        self.experts_norm = (1 + 0.1 * torch.randn(wl.d, generator=g, device=device)).bfloat16()
         self.rope, self.rot_scale = S.rope_table(head_dim, 1e6, "parts", 4.0, device=device)
         codes, scales = [], []
         for e in range(wl.E):
@@ -97,7 +104,7 @@ class DecoderLayer:
     def __call__(self, x, cache, batch, max_rows):
         """x bf16 [rows, d]; batch: what cache.grow returned for these rows."""
         where = (cache.k_pages, cache.v_pages, *batch)
-        q, k, v = self.project(x)
+        q, k, v = self.project(rms_norm(x, self.attn_norm))
         q = S.kv_append(q, k, v, *where, self.rope, self.rot_scale, q_norm=self.q_norm,
                         k_norm=self.k_norm, eps=EPS)
         a = S.attention(q, *where, max_rows, self.attn_ws)
@@ -105,7 +112,7 @@ class DecoderLayer:
         T = x.shape[0]
         if T not in self.moe_ws:
             self.moe_ws[T] = S.workspace(self.experts, T)
-        y = S.forward(self.experts, h, self.moe_ws[T])
+        y = S.forward(self.experts, rms_norm(h, self.experts_norm), self.moe_ws[T])
         return (h + y).to(torch.bfloat16)
 
 
