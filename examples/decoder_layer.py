@@ -109,11 +109,17 @@ class DecoderLayer:
                         k_norm=self.k_norm, eps=EPS)
         a = S.attention(q, *where, max_rows, self.attn_ws)
         h = x + a.flatten(1) @ self.w_out.T
+        return (h + self.moe(rms_norm(h, self.experts_norm))).to(torch.bfloat16)
+
+    def moe(self, x):
+        """The experts' output of the rows.  A workspace is laid out for its number of rows, so
+        the rows are filled up to a power of two: a few workspaces serve every step."""
         T = x.shape[0]
-        if T not in self.moe_ws:
-            self.moe_ws[T] = S.workspace(self.experts, T)
-        y = S.forward(self.experts, rms_norm(h, self.experts_norm), self.moe_ws[T])
-        return (h + y).to(torch.bfloat16)
+        rows = 1 << max(0, T - 1).bit_length()
+        if rows not in self.moe_ws:
+            self.moe_ws[rows] = S.workspace(self.experts, rows)
+        x = torch.nn.functional.pad(x, (0, 0, 0, rows - T))
+        return S.forward(self.experts, x, self.moe_ws[rows])[:T]
 
 
 def main():

@@ -45,3 +45,20 @@ def test_what_a_layer_adds_does_not_grow_with_its_input(ex, layer):
     added = (one_step(ex, layer, x).double() - x.double()).abs().max()
     assert float((y - x.double()).abs().max()) <= float(x.abs().max()) * 2.0 ** -7 + 4 * added / 1024
     assert ex.S.device_status() == 0
+
+
+def test_few_workspaces_serve_every_number_of_rows(ex, layer):
+    """Steps of 1 to 40 rows keep at most a workspace per power of two, and a row's output
+    does not depend on what fills the rows up."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    x = torch.randn(40, layer.wl.d, generator=g, device=DEV).bfloat16()
+    layer.moe_ws.clear()
+    for T in range(1, 41):
+        assert one_step(ex, layer, x[:T]).shape == (T, layer.wl.d)
+    assert len(layer.moe_ws) <= 7
+    whole = ex.S.forward(layer.experts, x[:8], ex.S.workspace(layer.experts, 8))
+    assert torch.equal(layer.moe(x[:8]), whole)
+    part = layer.moe(x[:5])
+    assert bool(((part - whole[:5]).abs() <= 1e-4 * whole.abs().max()).all())
+    assert ex.S.device_status() == 0
