@@ -81,6 +81,9 @@ __host__ __device__ constexpr int item_units(int D) { return D == 128 ? 4 : 2; }
 // part written and read, the join), and a part more one unit to read.
 constexpr int kWholeUnits = 10;
 constexpr int kMaxCtas = 240;
+// The longest run of one item in one CTA, in units: other warps wait for its
+// end, and their waits are bounded at 4e9 cycles, 2.9 times as many.
+constexpr int kMaxRun = 1 << 19;
 // log2 of how far m is set above the maximum, which may grow by as much before
 // sums are rescaled.  P is then between 2^-8 and 1 for the largest score, and
 // bf16 and fp32 lose nothing by that.  Measured: without it every new maximum
@@ -518,7 +521,8 @@ __device__ __forceinline__ void find_share(const smoe_attention_args &a, int G, 
             q = q > least ? q : least;
             sum = static_cast<uint32_t>(l);
             sc = s;
-            if (s.over) {  // recorded, and not worked on
+            const int share = static_cast<int>(min(q, (int64_t)0x7fffffff));
+            if (s.over || min(s.most, share) > kMaxRun) {  // recorded, and not worked on
                 if (tid == 0)
                     set_status(status, kStatusBadArg);
                 sum = sc.before = sc.total = 0;

@@ -684,8 +684,10 @@ typedef struct {
  * and 8 to 16 more per sequence, summed over the sequences with rows and
  * times num_kv_heads, may be 4.2e9; else the blocks of 128 keys that each 256
  * rows of one kv head see (new rows times query heads per kv head), and 2 to 4
- * more, summed over the batch, may be 4.2e9 (half a minute and more of work:
- * longer chunks are for several calls).
+ * more, summed over the batch, may be 4.2e9; and where such 256 rows see more
+ * than 6.7e7 keys, that sum times num_kv_heads over the SMs may be 2^19 (most of
+ * a second of work: longer chunks are for several calls).  The sums are in fp32
+ * and lose up to 2^-23 of their size for each 16 keys that one SM adds up.
  * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_WORKSPACE, SMOE_ERR_UNSUPPORTED
  * (device), SMOE_ERR_CUDA. */
 smoe_status smoe_attention(const smoe_attention_args *args, void *workspace,

@@ -184,11 +184,15 @@ def test_too_long_a_line_of_steps_is_recorded(S, ws):
     assert bool((out == 5.0).all()) and not bool(ws[:4096].any())
 
 
-def test_too_long_a_line_of_units_is_recorded(S, ws):
-    """4,200 rows of 16 heads on 2^31 keys: 262 tiles of 2^24 units are more than 2^32."""
-    where, q = aliased([2 ** 31 - 512], 16, 1, 64, 4200)
+@pytest.mark.parametrize("keys, rows", [
+    (2 ** 31 - 512, 4200),     # 262 tiles of 2^24 units are more than 2^32
+    (2 ** 26 + 2 ** 22, 4200)  # 262 tiles of 2^19 units and more: over 2^19 for each SM
+], ids=str)
+def test_too_long_a_line_of_units_is_recorded(S, ws, keys, rows):
+    """Rows of 16 heads on one kv head, 256 a tile."""
+    where, q = aliased([keys], 16, 1, 64, rows)
     out = torch.full_like(q, 5.0)
-    S.attention(q, *where, 4200, ws, out=out)
+    S.attention(q, *where, rows, ws, out=out)
     assert S.device_status() == -5 and S.device_status() == 0
     assert bool((out == 5.0).all()) and not bool(ws[:4096].any())
 
