@@ -673,7 +673,12 @@ typedef struct {
  * A row that sees no key (kv_len 0, or a chunk longer than kv_len) gets
  * zeros.  Keys past kv_len are never used, whatever their slots hold; keys
  * and values below it must be finite.  Scores, maxima, sums and outputs are
- * accumulated in fp32.  Work is split along the keys so that every SM has
+ * held in fp32, and the weights p_j are summed in fp32.  For their product with
+ * v_j they are rounded to bf16 (2^-8 of each p_j), as the tensor cores take them,
+ * where max_rows * num_heads / num_kv_heads is above 32; up to there they are two
+ * bf16 halves (2^-16 of each).  Single rows in one call
+ * with a chunk get the chunk's rounding; in a call of their own, with their own
+ * max_rows, the finer one.  Work is split along the keys so that every SM has
  * the same share; the parts are joined in a fixed order, so the same batch
  * gives the same bits on every call.
  * A page id outside the pool, a length past the page table, rows out of
