@@ -17,8 +17,10 @@
 // products took turns.)  m is set a factor 2^8 above the row's maximum and
 // again once the maximum has passed it: P is at most 1, so that O stays in
 // range wherever a plain sum does, and O is hardly ever rescaled; the final
-// division by P's sum, kept in fp32, makes the choice of m drop out.  P is rounded to bf16 for the tensor cores (2^-9 of
-// each p), the sum is not.
+// division by P's sum, kept in fp32, makes the choice of m drop out.  P is rounded to bf16
+// (2^-8 of each p), the type that the tensor cores multiply V's bf16 with at
+// their full rate; a second half as in attention.cu would double the products
+// with V.  The sum is not rounded.
 //
 // Bounds, per unit of heads of 128: the queue of products.  One of Q and K
 // (128 x 64 x 16) reads 4 KB of Q and 2 KB of K, 48 cycles of shared memory at
@@ -29,10 +31,10 @@
 // bound: two on each scheduler take 1,220 cycles for 64 keys of both (180 of
 // waiting, 290 the maximum, 680 the exponentials), with 44 % of the issue slots
 // and 36 % of the exponential unit in use: latencies that two warps don't fill.
-// Measured: 608 rows on 33,376 keys, 64 query and 4 kv heads of 128: 403 to 414
-// us (from GPU to GPU), 1,590 to 1,640 TFLOP/s; the same of 64: 375 us, 880
+// Measured: 608 rows on 33,376 keys, 64 query and 4 kv heads of 128: 403 to 419
+// us (from GPU to GPU), 1,570 to 1,640 TFLOP/s; the same of 64: 377 us, 875
 // TFLOP/s.  Prompts of 9,001 and 2,021 rows (the second on 6,559 keys), heads of
-// 128: 1.07 to 1.09 ms, 1,550 to 1,590 TFLOP/s; the rest are items' starts and ends.
+// 128: 1.06 to 1.10 ms, 1,540 to 1,600 TFLOP/s; the rest are items' starts and ends.
 //
 // Roles of the 16 warps of a CTA, one CTA per SM:
 //   warps 0..3  half A, warps 4..7 half B: softmax, rescaling, output

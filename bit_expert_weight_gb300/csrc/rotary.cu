@@ -15,7 +15,7 @@
 // its threads go over the heads, 8 channels (4 pairs) at a time, four loads in
 // flight.  Measured: 16,411 rows of 40 bf16 heads of 128 with 32 channels turned
 // 60.6 us, 5.5 TB/s; an append of 11,011 rows of 32 + 8 + 8 fp32 heads of 128
-// 66.0 us, 6.1 TB/s.  One row: 4.5 us, a launch and a chain of three loads.
+// 66.4 us, 6.1 TB/s.  One row: 4.5 us, a launch and a chain of three loads.
 #include "common.cuh"
 #include "internal.h"
 
