@@ -25,7 +25,8 @@ NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "
 
 LIBS = {
     "libsmoe.so": ["api.cu", "quant.cu", "repack.cu", "router.cu", "layer.cu", "grouped.cu", "noalloc.cu",
-                   "vault.cu", "decoder_api.cu", "rotary.cu", "attention.cu", "attention_chunk.cu"],
+                   "vault.cu", "decoder_api.cu", "rotary.cu", "attention.cu", "attention_chunk.cu",
+                   "beam.cu", "pages.cu"],
     "libsmoe_synth.so": ["synth.cu"],
 }
 

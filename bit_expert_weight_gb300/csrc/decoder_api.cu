@@ -1,6 +1,6 @@
 // decoder_api.cu -- the C ABI of the operators beside the expert layer
-// (rotation, paged append, paged attention): argument validation, and the
-// host's frequency table.
+// (rotation, paged append, paged attention, beams and pages): argument
+// validation, and the host's frequency table.
 #include <math.h>
 
 #include "common.cuh"
@@ -36,9 +36,11 @@ bool valid_rotation(int32_t rot_dim, int32_t head_dim, const int64_t *table, flo
            isfinite(rot_scale) && isfinite(eps) && eps >= 0.0f;
 }
 
+inline bool valid_page_size(int32_t n) { return n >= 16 && n <= 256 && !(n & (n - 1)); }
+
 bool valid_cache(const smoe_kv_cache &c)
 {
-    if (c.page_size < 16 || c.page_size > 256 || (c.page_size & (c.page_size - 1)))
+    if (!valid_page_size(c.page_size))
         return false;
     if (c.head_dim != 64 && c.head_dim != 128)
         return false;
@@ -58,6 +60,17 @@ bool valid_batch(const smoe_kv_batch &b)
 }
 
 bool batch_pointers(const smoe_kv_batch &b) { return b.row_start && b.kv_len && b.page_table; }
+
+bool valid_pool(const smoe_page_pool &p)
+{
+    return p.num_pages >= 1 && p.num_pages <= (1 << 30) && valid_page_size(p.page_size) && p.num_seqs >= 0 &&
+           p.num_seqs <= SMOE_MAX_SEQS && p.table_stride >= 0 && p.table_stride <= (1 << 27) && p.refs &&
+           aligned16(p.refs) &&
+           (p.num_seqs == 0 || (p.kv_len && p.page_table));
+}
+
+// b is a itself, or no part of it.
+inline bool same_or_apart(const int32_t *a, const int32_t *b, int64_t n) { return a == b || a + n <= b || b + n <= a; }
 
 smoe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SMOE_OK : SMOE_ERR_CUDA; }
 
@@ -189,6 +202,101 @@ smoe_status smoe_attention(const smoe_attention_args *a, void *workspace, size_t
     if (!dev.supported)
         return SMOE_ERR_UNSUPPORTED;
     return cuda_status(launch_attention(*a, workspace, dev, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+smoe_status smoe_beam_select(const smoe_beam_args *a, void *workspace, size_t workspace_bytes, void *cuda_stream)
+{
+    if (!a || !valid_dtype(a->dtype) || a->vocab < 1 || a->vocab > (1 << 26) || a->num_groups < 0 ||
+        a->num_groups > SMOE_MAX_SEQS || a->beams < 1 || a->beams > SMOE_MAX_BEAMS || a->num_out < 1 ||
+        a->num_out > SMOE_MAX_BEAMS || a->end_token < -1 || a->end_token >= a->vocab || a->row_stride < 0 ||
+        a->row_stride > (1ll << 40))
+        return SMOE_ERR_INVALID_ARG;
+    if (a->num_groups == 0)
+        return SMOE_OK;
+    const uintptr_t unit = a->dtype == SMOE_F32 ? 4 : 2;
+    if (!a->logits || reinterpret_cast<uintptr_t>(a->logits) % unit || !a->scores || !a->scores_out ||
+        !a->parents || !a->tokens || a->parents == a->tokens || a->parents == a->last)
+        return SMOE_ERR_INVALID_ARG;
+    // in place: a group is written when all of it has been read, so it has to lie where it was
+    if (a->num_out != a->beams && (a->scores_out == a->scores || a->tokens == a->last))
+        return SMOE_ERR_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return SMOE_ERR_INVALID_ARG;
+    if (workspace_bytes < SMOE_BEAM_WORKSPACE_BYTES)
+        return SMOE_ERR_WORKSPACE;
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
+        return SMOE_ERR_UNSUPPORTED;
+    return cuda_status(launch_beam_select(*a, workspace, dev, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+smoe_status smoe_pages_fork(const smoe_page_pool *pool, const int32_t *parent, const int32_t *keep,
+                            void *cuda_stream)
+{
+    if (!pool || !valid_pool(*pool))
+        return SMOE_ERR_INVALID_ARG;
+    if (pool->num_seqs == 0)
+        return SMOE_OK;
+    if (!parent || parent == pool->kv_len || keep == pool->kv_len)
+        return SMOE_ERR_INVALID_ARG;
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
+        return SMOE_ERR_UNSUPPORTED;
+    return cuda_status(launch_pages_fork(*pool, parent, keep, dev, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+smoe_status smoe_pages_reserve(const smoe_page_pool *pool, const int32_t *row_start, int32_t *copies,
+                               int32_t *counts, void *cuda_stream)
+{
+    if (!pool || !valid_pool(*pool) || !counts)
+        return SMOE_ERR_INVALID_ARG;
+    if (pool->num_seqs > 0 && (!row_start || !copies))
+        return SMOE_ERR_INVALID_ARG;
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
+        return SMOE_ERR_UNSUPPORTED;
+    return cuda_status(
+        launch_pages_reserve(*pool, row_start, copies, counts, dev, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+smoe_status smoe_pages_copy(const smoe_kv_cache *caches, int32_t num_caches, const int32_t *copies,
+                            const int32_t *counts, int32_t max_copies, void *cuda_stream)
+{
+    if (num_caches < 0 || num_caches > SMOE_MAX_CACHES || max_copies < 0 || (num_caches > 0 && !caches))
+        return SMOE_ERR_INVALID_ARG;
+    for (int i = 0; i < num_caches; ++i) {
+        const smoe_kv_cache &c = caches[i], &first = caches[0];
+        if (!valid_cache(c) || c.num_pages != first.num_pages || c.k_page_stride != first.k_page_stride ||
+            c.v_page_stride != first.v_page_stride || c.page_size != first.page_size ||
+            c.num_kv_heads != first.num_kv_heads || c.head_dim != first.head_dim)
+            return SMOE_ERR_INVALID_ARG;
+    }
+    if (num_caches == 0 || max_copies == 0)
+        return SMOE_OK;
+    if (!copies || !counts)
+        return SMOE_ERR_INVALID_ARG;
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
+        return SMOE_ERR_UNSUPPORTED;
+    return cuda_status(launch_pages_copy(caches, num_caches, copies, counts, max_copies, dev,
+                                         static_cast<cudaStream_t>(cuda_stream)));
+}
+
+smoe_status smoe_pages_compact(const smoe_page_pool *pool, int32_t *refs_out, int32_t *table_out, int32_t *copies,
+                               int32_t max_copies, int32_t *counts, void *cuda_stream)
+{
+    if (!pool || !valid_pool(*pool) || !refs_out || !counts || max_copies < pool->num_pages / 2 ||
+        (max_copies > 0 && !copies) || !same_or_apart(pool->refs, refs_out, pool->num_pages))
+        return SMOE_ERR_INVALID_ARG;
+    if (pool->num_seqs > 0 &&
+        (!table_out ||
+         !same_or_apart(pool->page_table, table_out, (int64_t)pool->num_seqs * pool->table_stride)))
+        return SMOE_ERR_INVALID_ARG;
+    const DeviceFacts &dev = device_facts();
+    if (!dev.supported)
+        return SMOE_ERR_UNSUPPORTED;
+    return cuda_status(launch_pages_compact(*pool, refs_out, table_out, copies, counts, dev,
+                                            static_cast<cudaStream_t>(cuda_stream)));
 }
 
 }  // extern "C"

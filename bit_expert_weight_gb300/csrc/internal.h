@@ -210,6 +210,18 @@ cudaError_t launch_attention(const smoe_attention_args &a, void *workspace, cons
 cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *workspace, const DeviceFacts &dev,
                                    cudaStream_t stream);
 
+// ------------------------------------------------- beams, pages of the cache
+
+cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const DeviceFacts &dev, cudaStream_t stream);
+cudaError_t launch_pages_fork(const smoe_page_pool &p, const int32_t *parent, const int32_t *keep,
+                              const DeviceFacts &dev, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const smoe_page_pool &p, const int32_t *row_start, int32_t *copies,
+                                 int32_t *counts, const DeviceFacts &dev, cudaStream_t stream);
+cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int32_t *table_out, int32_t *copies,
+                                 int32_t *counts, const DeviceFacts &dev, cudaStream_t stream);
+cudaError_t launch_pages_copy(const smoe_kv_cache *caches, int num_caches, const int32_t *copies,
+                              const int32_t *counts, int max_copies, const DeviceFacts &dev, cudaStream_t stream);
+
 int layer_grid_ctas_max();
 cudaError_t launch_layer(const LayerArgs &a, cudaStream_t stream);
 cudaError_t launch_combine(const LayerArgs &a, cudaStream_t stream);

@@ -39,12 +39,17 @@ EXPORTED = [
     "smoe_moe_workspace_bytes_mixed", "smoe_moe_forward_mixed", "smoe_moe_forward_stage_mixed",
     "smoe_debug_set_waits", "smoe_moe_path_dtype",
     "smoe_rope_table", "smoe_rope", "smoe_kv_append", "smoe_attention",
+    "smoe_beam_select", "smoe_pages_fork", "smoe_pages_reserve", "smoe_pages_copy",
+    "smoe_pages_compact",
 ]
 
 # Bytes of smoe_attention's workspace (SMOE_ATTENTION_WORKSPACE_BYTES) and
 # the kinds of frequency tables (SMOE_ROPE_* in include/smoe.h).
 ATTENTION_WORKSPACE_BYTES = 64 << 20
 ROPE_KINDS = {"plain": 0, "linear": 1, "parts": 2, "bands": 3}
+
+# Bytes of smoe_beam_select's workspace (SMOE_BEAM_WORKSPACE_BYTES).
+BEAM_WORKSPACE_BYTES = 32 << 20
 
 # Execution paths (SMOE_PATH_* in include/smoe.h).
 PATH_AUTO, PATH_STREAM, PATH_GROUPED = 0, 1, 2
@@ -162,6 +167,29 @@ class AttentionArgs(ctypes.Structure):
         ("max_rows", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class BeamArgs(ctypes.Structure):
+    """smoe_beam_args (include/smoe.h)."""
+    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("scores", ctypes.c_void_p), ("last", ctypes.c_void_p),
+                ("scores_out", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("tokens", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("num_groups", ctypes.c_int32), ("beams", ctypes.c_int32),
+                ("num_out", ctypes.c_int32), ("end_token", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    """smoe_page_pool (include/smoe.h)."""
+    _fields_ = [("refs", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    """smoe_kv_cache (include/smoe.h)."""
+    _fields_ = _CACHE_BATCH[:9]
+
+
 _lib = None
 _synth = None
 
@@ -253,6 +281,16 @@ def load(path: str | None = None):
     L.smoe_kv_append.restype = I
     L.smoe_attention.argtypes = [P, P, S, P]
     L.smoe_attention.restype = I
+    L.smoe_beam_select.argtypes = [P, P, S, P]
+    L.smoe_beam_select.restype = I
+    L.smoe_pages_fork.argtypes = [P, P, P, P]
+    L.smoe_pages_fork.restype = I
+    L.smoe_pages_reserve.argtypes = [P, P, P, P, P]
+    L.smoe_pages_reserve.restype = I
+    L.smoe_pages_copy.argtypes = [P, I32, P, P, I32, P]
+    L.smoe_pages_copy.restype = I
+    L.smoe_pages_compact.argtypes = [P, P, P, P, I32, P, P]
+    L.smoe_pages_compact.restype = I
     L.smoe_debug_set_waits.argtypes = [ctypes.c_longlong, I]
     L.smoe_debug_set_waits.restype = None
     _lib = L
@@ -653,8 +691,8 @@ def _device_array(name, t, dtype, numel, dev):
     return t.data_ptr()
 
 
-def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows, dev):
-    """The members of smoe_kv_cache and smoe_kv_batch."""
+def _cache(k_pages, v_pages, dev):
+    """The members of smoe_kv_cache."""
     P, Hkv, page, D = shape = k_pages.shape
     ks, vs = k_pages.stride(), v_pages.stride()
     if v_pages.shape != shape:
@@ -667,14 +705,19 @@ def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows, dev):
         # (a pool of one kv head or one page may have other strides there)
         if not (k_pages[:1].is_contiguous() and v_pages[:1].is_contiguous()):
             raise ValueError("k_pages, v_pages: the last three dimensions must be contiguous")
+    kstep, vstep = (ks[0], vs[0]) if P > 1 else (Hkv * page * D,) * 2
+    return k_pages.data_ptr(), v_pages.data_ptr(), P, kstep, vstep, page, Hkv, D, 0
+
+
+def _cache_batch(k_pages, v_pages, row_start, kv_len, page_table, rows, dev):
+    """The members of smoe_kv_cache and smoe_kv_batch."""
+    cache = _cache(k_pages, v_pages, dev)
     B = kv_len.numel()
     tb, pages = page_table.shape
     if tb < B:
         raise ValueError("page_table must be [sequences, pages]")
     i32 = torch.int32
-    kstep, vstep = (ks[0], vs[0]) if P > 1 else (Hkv * page * D,) * 2
-    return (k_pages.data_ptr(), v_pages.data_ptr(), P, kstep, vstep, page, Hkv, D, 0,
-            _device_array("row_start", row_start, i32, B + 1, dev),
+    return (*cache, _device_array("row_start", row_start, i32, B + 1, dev),
             _device_array("kv_len", kv_len, i32, B, dev),
             _device_array("page_table", page_table, i32, 0, dev), rows, B, pages)
 
@@ -802,6 +845,135 @@ def attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     _check(load().smoe_attention(a, ws.data_ptr(), ws.nbytes, _handle(stream, dev)),
            "smoe_attention")
     return out
+
+
+# ------------------------------------------- beams, pages of the cache
+
+_pack_beam, _pack_pool, _pack_cache = map(_packer, (BeamArgs, PagePool, KvCache))
+
+
+def beam_workspace(device="cuda", stream=None):
+    """A zeroed workspace for `beam_select`, the same for every shape."""
+    ws = torch.empty(BEAM_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+    _device("the workspace", ws)
+    _check(load().smoe_moe_workspace_init(_ptr(ws), ws.numel(), _stream(stream)),
+           "workspace_init")
+    return ws
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, ws: torch.Tensor,
+                last=None, end_token=-1, out=None, stream=None):
+    """smoe_beam_select: the num_out best continuations of each group's beams, best first.
+    logits fp32 or bf16 [groups * beams, vocab] with contiguous rows; scores fp32 [groups,
+    beams]; last int32 [groups, beams]: a beam whose last token is end_token is finished.
+    Returns (scores fp32, parents int32, tokens int32), each [groups, num_out]; out: such
+    tensors (with num_out == beams, scores and last may be among them: in place)."""
+    dev = _device("logits", logits)
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
+        raise TypeError("logits must be fp32 or bf16")
+    st = logits.stride()
+    G, K = scores.shape
+    if len(st) != 2 or logits.shape[0] != G * K or (st[1] != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [groups * beams, vocab] with contiguous rows, "
+                         "scores [groups, beams]")
+    f32, i32, n = torch.float32, torch.int32, G * num_out
+    if out is None:
+        out = (torch.empty((G, num_out), dtype=f32, device=logits.device),
+               torch.empty((G, num_out), dtype=i32, device=logits.device),
+               torch.empty((G, num_out), dtype=i32, device=logits.device))
+    to_scores, parents, tokens = out
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the device of the call's other tensors")
+    a = _pack_beam(logits.data_ptr(), st[0] if G * K > 1 else 0,
+                   _device_array("scores", scores, f32, 0, dev),
+                   _device_array("last", last, i32, G * K, dev),
+                   _device_array("out[0]", to_scores, f32, n, dev),
+                   _device_array("out[1]", parents, i32, n, dev),
+                   _device_array("out[2]", tokens, i32, n, dev), dt, logits.shape[1], G, K,
+                   num_out, end_token)
+    _check(load().smoe_beam_select(a, ws.data_ptr(), ws.nbytes, _handle(stream, dev)),
+           "smoe_beam_select")
+    return out
+
+
+def _pool(refs, kv_len, page_table, page_size, dev):
+    """smoe_page_pool as bytes."""
+    i32, S = torch.int32, kv_len.numel()
+    rows, width = page_table.shape
+    if rows < S:
+        raise ValueError("page_table must be [sequences, pages]")
+    return _pack_pool(_device_array("refs", refs, i32, 0, dev),
+                      _device_array("kv_len", kv_len, i32, 0, dev),
+                      _device_array("page_table", page_table, i32, 0, dev), refs.numel(),
+                      page_size, S, width)
+
+
+def pages_fork(refs: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+               page_size: int, parent: torch.Tensor, keep=None, stream=None):
+    """smoe_pages_fork, in place: sequence s becomes a copy of what sequence parent[s] was
+    (-1: an empty one), of its first keep[s] keys where keep is given.  refs int32 [pages],
+    kv_len int32 [sequences], page_table int32 [sequences, pages], parent and keep int32
+    [sequences]."""
+    dev = _device("refs", refs)
+    S = kv_len.numel()
+    _check(load().smoe_pages_fork(_pool(refs, kv_len, page_table, page_size, dev),
+                                  _device_array("parent", parent, torch.int32, S, dev),
+                                  _device_array("keep", keep, torch.int32, S, dev),
+                                  _handle(stream, dev)), "smoe_pages_fork")
+
+
+def pages_reserve(refs: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                  page_size: int, row_start: torch.Tensor, copies: torch.Tensor,
+                  counts: torch.Tensor, stream=None):
+    """smoe_pages_reserve, in place: room for row_start[s + 1] - row_start[s] more keys of
+    each sequence.  copies int32 [sequences, 2] gets the pages to copy first, counts int32 [2]
+    how many and how many pages are left (below 0: short of so many, nothing changed)."""
+    dev = _device("refs", refs)
+    S, i32 = kv_len.numel(), torch.int32
+    _check(load().smoe_pages_reserve(_pool(refs, kv_len, page_table, page_size, dev),
+                                     _device_array("row_start", row_start, i32, S + 1, dev),
+                                     _device_array("copies", copies, i32, 2 * S, dev),
+                                     _device_array("counts", counts, i32, 2, dev),
+                                     _handle(stream, dev)), "smoe_pages_reserve")
+
+
+def pages_copy(k_pages, v_pages, copies: torch.Tensor, counts: torch.Tensor, stream=None):
+    """smoe_pages_copy: page copies[i, 0] to copies[i, 1], i < counts[0], in every layer's
+    cache.  k_pages and v_pages: a tensor, or a list of one per layer, bf16 [pages, kv heads,
+    page size, head_dim]; copies int32 [at most, 2], counts int32."""
+    if not isinstance(k_pages, (list, tuple)):
+        k_pages, v_pages = [k_pages], [v_pages]
+    if len(k_pages) != len(v_pages):
+        raise ValueError("k_pages and v_pages must be of as many layers")
+    if copies.dim() != 2 or copies.shape[1] != 2:
+        raise ValueError("copies must be [at most, 2]")
+    dev = _device("copies", copies)
+    caches = b"".join(_pack_cache(*_cache(k, v, dev)) for k, v in zip(k_pages, v_pages))
+    _check(load().smoe_pages_copy(caches, len(k_pages),
+                                  _device_array("copies", copies, torch.int32, 0, dev),
+                                  _device_array("counts", counts, torch.int32, 1, dev),
+                                  copies.shape[0], _handle(stream, dev)), "smoe_pages_copy")
+
+
+def pages_compact(refs: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                  page_size: int, copies: torch.Tensor, counts: torch.Tensor, refs_out=None,
+                  page_table_out=None, stream=None):
+    """smoe_pages_compact: the held pages become the pool's first ones.  In place, or into
+    refs_out and page_table_out; copies int32 [at least pages / 2, 2] gets the moves for
+    `pages_copy`, counts int32 [2] how many and how many pages are held."""
+    dev = _device("refs", refs)
+    i32 = torch.int32
+    refs_out = refs if refs_out is None else refs_out
+    page_table_out = page_table if page_table_out is None else page_table_out
+    if copies.dim() != 2 or copies.shape[1] != 2:
+        raise ValueError("copies must be [at most, 2]")
+    _check(load().smoe_pages_compact(
+        _pool(refs, kv_len, page_table, page_size, dev),
+        _device_array("refs_out", refs_out, i32, refs.numel(), dev),
+        _device_array("page_table_out", page_table_out, i32, page_table.numel(), dev),
+        _device_array("copies", copies, i32, 0, dev), copies.shape[0],
+        _device_array("counts", counts, i32, 2, dev), _handle(stream, dev)), "smoe_pages_compact")
 
 
 def device_status(stream=None) -> int:

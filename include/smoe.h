@@ -698,6 +698,158 @@ typedef struct {
 smoe_status smoe_attention(const smoe_attention_args *args, void *workspace,
                            size_t workspace_bytes, void *cuda_stream);
 
+/* ------------------------------------------- beams, pages of the cache */
+
+/* What a serving program does between two steps of the attention above: choose
+ * the next tokens of its beams, let sequences become copies of others, make
+ * room for their next rows, and keep the pool of pages in order.  Everything
+ * is decided on the device from the arrays' contents: nothing is read back,
+ * each call is one launch and may be captured.  Inference only.
+ *
+ * A step of a beam search, of S = num_groups * beams sequences:
+ *   smoe_pages_reserve   room for the new rows; what is shared and about to
+ *                        be written is listed for
+ *   smoe_pages_copy      once for all layers; then smoe_kv_append and
+ *                        smoe_attention in each
+ *   smoe_beam_select     the best continuations
+ *   smoe_pages_fork      each sequence becomes its parent's copy
+ * Without beams a program forks to let finished sequences go (parent -1) and
+ * to take refused rows back (keep). */
+
+/* Largest numbers of beams and of outputs of a group. */
+#define SMOE_MAX_BEAMS 32
+/* Bytes of smoe_beam_select's workspace, for every shape: 256-byte aligned,
+ * zeroed once (smoe_moe_workspace_init) and again after a call that returned an
+ * error; calls that can overlap on the device need a workspace each. */
+#define SMOE_BEAM_WORKSPACE_BYTES (32u << 20)
+
+typedef struct {
+    const void *logits;        /* [num_groups * beams, vocab]: element (r, v) at
+                                  logits + r * row_stride + v (elements), aligned
+                                  to its type; rows may overlap                */
+    int64_t row_stride;        /* >= 0                                        */
+    const float *scores;       /* [num_groups, beams]                         */
+    const int32_t *last;       /* nullable [num_groups, beams]: each beam's
+                                  last token                                  */
+    float *scores_out;         /* [num_groups, num_out]                       */
+    int32_t *parents;          /* out [num_groups, num_out]                   */
+    int32_t *tokens;           /* out [num_groups, num_out]                   */
+    int32_t dtype;             /* smoe_dtype of logits                        */
+    int32_t vocab;             /* 1 .. 2^26                                   */
+    int32_t num_groups;        /* 0 .. SMOE_MAX_SEQS                          */
+    int32_t beams;             /* 1 .. SMOE_MAX_BEAMS                         */
+    int32_t num_out;           /* 1 .. SMOE_MAX_BEAMS                         */
+    int32_t end_token;         /* -1: none; else < vocab                      */
+} smoe_beam_args;
+
+/* The num_out best continuations of each group's beams, best first:
+ *   value(k, v) = scores[k] + x_kv - log(sum_u exp(x_ku))
+ * over the group's beams k and all tokens v; of equal values the lower k comes
+ * first, and within a beam the larger logit, then the lower v.  parents gets the beam's row in logits (group *
+ * beams + k), tokens v, scores_out the value.
+ * A beam whose last token is end_token is finished: its logits are not read,
+ * and it has one continuation, end_token at its own score.  A logit of -inf or
+ * NaN is never chosen and has no part in the sum; +inf counts as the largest
+ * finite fp32.  A beam whose score is not finite has no continuation, nor has
+ * one without a logit above -inf.  Where a group has fewer than num_out
+ * continuations the rest get score -inf, parent -1 and token -1.
+ * exp and its sums are in fp32 (a row's normaliser is off by a few 2^-24, by
+ * the same in equal rows of equal alignment to 16 bytes), the rest, and the
+ * comparison of values, in 64 bits: continuations of different beams that are
+ * nearer than that may come in either order.  Work is split over the
+ * vocabulary and joined in a fixed order: the same inputs give the same bits.
+ * With num_out == beams, scores_out may be scores and tokens may be last (a
+ * captured step works in place); no other overlap of an output with anything.
+ * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_WORKSPACE, SMOE_ERR_UNSUPPORTED
+ * (device), SMOE_ERR_CUDA. */
+smoe_status smoe_beam_select(const smoe_beam_args *args, void *workspace, size_t workspace_bytes,
+                             void *cuda_stream);
+
+/* The pages of a pool and the sequences that hold them, for the caches of all
+ * layers alike.  Sequence s has kv_len[s] keys, in the pages that the first
+ * ceil(kv_len[s] / page_size) entries of its table row name; refs[p] counts
+ * the sequences whose row names page p there, and whatever else of the
+ * program holds it (a prefix kept for later requests adds 1 itself).  A page
+ * is free where that is not above 0.  All arrays are DEVICE int32 and belong to
+ * one stream at a time.  Entries of a row past a sequence's pages are neither
+ * read nor changed. */
+typedef struct {
+    int32_t *refs;             /* [num_pages], 16-byte aligned                */
+    int32_t *kv_len;           /* [num_seqs]                                  */
+    int32_t *page_table;       /* [num_seqs, table_stride]                    */
+    int32_t num_pages;         /* 1 .. 2^30                                   */
+    int32_t page_size;         /* 16, 32, 64, 128 or 256                      */
+    int32_t num_seqs;          /* 0 .. SMOE_MAX_SEQS                          */
+    int32_t table_stride;      /* 0 .. 2^27; kv_len is at most table_stride *
+                                  page_size, and 2^31 - 512                   */
+} smoe_page_pool;
+
+/* Sequence s becomes what sequence parent[s] was: its table row (of the pages
+ * that it uses) and its length, min(that length, keep[s]) where keep is given.
+ * parent -1: an empty sequence, whose pages are let go.  All at once, in
+ * place; pages are shared, not copied, and refs follows.  keep below 0 counts
+ * as 0.  A parent outside -1 .. num_seqs - 1 and a length that is negative or
+ * past its row are recorded (SMOE_ERR_DEVICE_FAULT from
+ * smoe_get_device_status) and then nothing changes; an entry that names no
+ * page of the pool is recorded and not counted.
+ *   parent  [num_seqs]       keep  nullable [num_seqs]
+ * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
+smoe_status smoe_pages_fork(const smoe_page_pool *pool, const int32_t *parent, const int32_t *keep,
+                            void *cuda_stream);
+
+/* Room for row_start[s + 1] - row_start[s] more keys of each sequence: kv_len
+ * grows by that, and the arrays are then those that smoe_kv_append and
+ * smoe_attention take for these rows.  New pages are the free ones of lowest
+ * number, given out in order of the sequences and of their rows' entries.  A
+ * sequence whose last page is partly filled and held by others too gets a page
+ * of its own for it first, and the pair (old page, new page) is listed, in
+ * order of the sequences: smoe_pages_copy has to follow before the append.
+ * (Where all that hold such a page are sequences that get rows in this call,
+ * the first of them keeps it.)
+ *   row_start  [num_seqs + 1]
+ *   copies     out [num_seqs, 2]; entries past the count are left alone
+ *   counts     out [2]: how many copies; how many pages are still free
+ * If fewer pages are free than needed nothing changes, counts is (0, free -
+ * needed, at least -2^30), and that is recorded, for an append would overwrite older keys.
+ * Row starts that fall, lengths that leave the table row or 2^31 - 512, and a
+ * last page that is not in the pool or that nobody holds are recorded too:
+ * nothing changes, and counts is (0, -1).
+ * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
+smoe_status smoe_pages_reserve(const smoe_page_pool *pool, const int32_t *row_start,
+                               int32_t *copies, int32_t *counts, void *cuda_stream);
+
+/* Caches of one call of smoe_pages_copy. */
+#define SMOE_MAX_CACHES 128
+
+/* Copy whole pages, keys and values, in the caches of several layers (one pool
+ * each, of the same sizes and strides): page copies[i][0] to page copies[i][1]
+ * for i < counts[0], at most max_copies.  No page is the target of two pairs,
+ * or a source and a target.  A page outside the pool is recorded, and its pair
+ * skipped; so is a count below 0 or above max_copies (then what fits is copied).
+ *   caches   HOST array of num_caches (0 .. SMOE_MAX_CACHES)
+ *   copies   [max_copies, 2]      counts  [1 or more]
+ * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
+smoe_status smoe_pages_copy(const smoe_kv_cache *caches, int32_t num_caches, const int32_t *copies,
+                            const int32_t *counts, int32_t max_copies, void *cuda_stream);
+
+/* Close the pool up: with n pages held, the i-th held page of number n or more
+ * moves to the i-th free page below n, so that the held ones are 0 .. n - 1.
+ * refs and the tables follow, and the moves are listed for smoe_pages_copy, in
+ * that order.  A holder that is not in the tables finds its page in the list.
+ *   refs_out   [num_pages]: pool->refs itself, or apart from it
+ *   table_out  [num_seqs, table_stride]: pool->page_table itself, or apart
+ *              from it (entries past a sequence's pages are left alone there)
+ *   copies     out [max_copies, 2], max_copies >= num_pages / 2; entries past
+ *              the count are left alone
+ *   counts     out [2]: how many moves; n
+ * A length that is negative or past its row is recorded, and that row stays as
+ * it is; so is, and does, an entry that names no page of the pool, or one of
+ * number n or more that nobody holds.
+ * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
+smoe_status smoe_pages_compact(const smoe_page_pool *pool, int32_t *refs_out, int32_t *table_out,
+                               int32_t *copies, int32_t max_copies, int32_t *counts,
+                               void *cuda_stream);
+
 /* Testing only: make the layer kernel's bounded waits short and, if
  * stall_routing is nonzero, make its routing step wait for logits that no
  * CTA ever writes.  The layer kernel (the streaming path) hands every value
