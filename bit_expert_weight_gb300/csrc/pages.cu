@@ -374,20 +374,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     unsigned long long before = threads_before(sh, own, tid);
     for (int s = 2 * tid; s < 2 * tid + 2 && s < n && !bad; ++s) {
-        sh.base[s] = static_cast<int>(before);  // (used only where the total fits)
+        sh.base[s] = static_cast<int>(before & ((1ull << 40) - 1));
         const bool apart = sh.holders[s] == 0;
         sh.holders[s] = apart ? static_cast<int>(before >> 40) : -1;
         before += sh.need[s] + (static_cast<unsigned long long>(apart) << 40);
     }
     __syncthreads();
-    const int64_t needed = sh.total & ((1ull << 40) - 1);
+    // (row starts are of 32 bits: no more than 2^28 pages and one per sequence)
+    const int needed = static_cast<int>(sh.total & ((1ull << 40) - 1));
     const int num_free = counted(sh.runs);
     const bool lead = cluster_rank() == 0;
     if (bad || needed > num_free) {
         if (lead && tid == 0) {
             set_status(status, kStatusBadArg);
             counts[0] = 0;
-            counts[1] = bad ? -1 : static_cast<int>(max((int64_t)num_free - needed, -(int64_t)(1 << 30)));
+            counts[1] = bad ? -1 : num_free - needed;
         }
         return;
     }
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.kv_len[s] += row_start[s + 1] - row_start[s];
         if (tid == 0) {
             counts[0] = static_cast<int>(sh.total >> 40);
-            counts[1] = num_free - static_cast<int>(needed);
+            counts[1] = num_free - needed;
         }
     }
     int rank = counted_before(sh.runs, tid >> 5);

@@ -746,7 +746,7 @@ typedef struct {
  *   value(k, v) = scores[k] + x_kv - log(sum_u exp(x_ku))
  * over the group's beams k and all tokens v; of equal values the lower k comes
  * first, and within a beam the larger logit, then the lower v.  parents gets the beam's row in logits (group *
- * beams + k), tokens v, scores_out the value.
+ * beams + k), tokens v, scores_out the value rounded to fp32.
  * A beam whose last token is end_token is finished: its logits are not read,
  * and it has one continuation, end_token at its own score.  A logit of -inf or
  * NaN is never chosen and has no part in the sum; +inf counts as the largest
@@ -810,7 +810,7 @@ smoe_status smoe_pages_fork(const smoe_page_pool *pool, const int32_t *parent, c
  *   copies     out [num_seqs, 2]; entries past the count are left alone
  *   counts     out [2]: how many copies; how many pages are still free
  * If fewer pages are free than needed nothing changes, counts is (0, free -
- * needed, at least -2^30), and that is recorded, for an append would overwrite older keys.
+ * needed), and that is recorded, for an append would overwrite older keys.
  * Row starts that fall, lengths that leave the table row or 2^31 - 512, and a
  * last page that is not in the pool or that nobody holds are recorded too:
  * nothing changes, and counts is (0, -1).
