@@ -6,11 +6,10 @@
 // logits: one pass over a row finds them, and the sum, together.
 //
 // Work: a row is cut into parts, a CTA has one of them.  A logit that may be
-// among the part's largest goes to its warp's queue in shared memory, and from
-// there, 32 at a time, sorted, into the warp's list (lane i the i-th largest),
-// as 64-bit keys (logit, then the lower index).  A part's sum and list go to
-// the workspace; the CTA that arrives last of a group's joins its rows' parts
-// in order, and then the rows' candidates by their values in 64 bits.
+// among the part's largest goes to the CTA's queue in shared memory, as a 64-bit
+// key (logit, then the lower index).  A part's sum and its largest keys, in
+// order, go to the workspace; the CTA that arrives last of a group's joins its
+// rows' parts, and then the rows' candidates by their values in 64 bits.
 #include <float.h>
 #include <math.h>
 
@@ -27,8 +26,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kWords = 4;                         // of 16 bytes, of a thread and step
 constexpr int kStepWords = kThreads * kWords;     // of a CTA and step
 constexpr size_t kStatsAt = SMOE_MAX_SEQS * sizeof(unsigned);  // after the groups' counters
-constexpr int kMaxWave = 4096;                    // CTAs that a launch is cut into, beyond one per row
-static_assert(kStatsAt + (size_t)(SMOE_MAX_SEQS * SMOE_MAX_BEAMS + kMaxWave) *
+constexpr int kMaxSteps = 24;                     // of a part
+constexpr int kMaxWave = 4096;                    // CTAs that a launch is cut into, beyond what kMaxSteps asks
+static_assert(kStatsAt + (size_t)(SMOE_MAX_SEQS * ((SMOE_MAX_VOCAB / 4 + 1) / (kStepWords * kMaxSteps) + 1) + kMaxWave) *
                              (sizeof(float2) + SMOE_MAX_BEAMS * sizeof(unsigned long long)) <=
                   SMOE_BEAM_WORKSPACE_BYTES,
               "parts in the workspace");
@@ -38,9 +38,6 @@ constexpr float kSlack = 40.0f;
 // A sum's reference stays within this: sums of rows whose largest logit is
 // beyond it come out as 0 or infinite, and are taken again (row_sum).
 constexpr float kMaxRef = 2097152.0f;
-// Warps tell their rank-th largest where rank is at most this (four steps of a
-// few cycles); more is asked of parts of few warps with words only.
-constexpr int kMaxRank = 4;
 
 using Key = unsigned long long;
 
@@ -63,19 +60,6 @@ __device__ __forceinline__ Key key_of(float x, int index)
 }
 __device__ __forceinline__ float logit_of(Key k) { return from_ordered(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int index_of(Key k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
-
-// Both lists sorted, largest first, one key a lane: the 32 largest of both.
-__device__ __forceinline__ Key merged(Key a, Key b, int lane)
-{
-    const Key r = __shfl_sync(0xffffffffu, b, 31 - lane);
-    a = a > r ? a : r;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Key y = __shfl_xor_sync(0xffffffffu, a, o);
-        a = ((lane & o) == 0) == (a > y) ? a : y;
-    }
-    return a;
-}
 
 struct BeamArgs {
     smoe_beam_args a;
@@ -100,12 +84,6 @@ __device__ __forceinline__ int state_of(const smoe_beam_args &a, int64_t row)
 // A logit as it counts: NaN as -inf, +inf as the largest finite one.
 __device__ __forceinline__ float counted_logit(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
 
-// Next larger number (of a finite one or -inf).
-__device__ __forceinline__ float next_up(float x)
-{
-    const int b = __float_as_int(x);
-    return __int_as_float(x == 0.0f ? 1 : b > 0 ? b + 1 : b - 1);
-}
 template <bool F32>
 constexpr int kPer = F32 ? 4 : 8;  // logits of a word
 
@@ -246,207 +224,408 @@ __device__ __forceinline__ float sum_of(const uint4 (&v)[kWords], float ref)
     return a + b;
 }
 
-constexpr int kQueue = 31 + 32 * kPer<false>;  // what is left of a sort, and a word of every lane
+// Groups (a thread's words of one step) that are looked at again, and keys
+// taken from them.  A part's num_out largest groups hold no more.
+constexpr int kHits = 256;
+constexpr int kKeys = 1024;
+static_assert(SMOE_MAX_BEAMS * kWords * kPer<false> <= kKeys && SMOE_MAX_BEAMS <= kHits, "the largest groups fit");
 
 struct PartShared {
     Sum sum[kWarps];
-    Key list[kWarps][32];
     uint32_t rank[kWarps];   // see scan_part
-    int queued[kWarps];
-    Key queue[kWarps][kQueue];
+    int count[kWarps];
+    int hits, queued;
+    int hit[kHits];          // groups: step * kThreads + thread
+    Key queue[kKeys];
+    float most[kMaxSteps][kThreads];  // the largest logit of every group
 };
 
-// Sorted over the lanes, largest first.
-__device__ __forceinline__ Key sorted(Key a, int lane)
+// A part of a row, in words of 16 bytes from the one that the row begins in.
+struct Part {
+    const uint8_t *base;
+    int first;      // logits of word 0 before the row
+    int vocab;
+    int w0, w1;     // words
+    int steps;
+};
+
+template <bool F32>
+__device__ __forceinline__ uint4 load_word(const Part &p, int w)
 {
-#pragma unroll
-    for (int n = 2; n <= 32; n *= 2)
-#pragma unroll
-        for (int o = n / 2; o > 0; o >>= 1) {
-            const Key y = __shfl_xor_sync(0xffffffffu, a, o);
-            const bool larger = ((lane & o) == 0) == ((lane & n) == 0);
-            a = larger == (a > y) ? a : y;
-        }
-    return a;
+    return load_word<F32>(p.base, p.first, p.vocab, w, p.w1);
 }
 
-// What waits in the warp's queue into its list, 32 keys at a time, until fewer
-// than `keep` are left.
-__device__ __forceinline__ void drain(PartShared &sh, int warp, int lane, int num_out, int keep, Key &list, Key &bar)
+// Sum over the CTA, in every thread.
+__device__ __forceinline__ int sum_over_cta(PartShared &sh, int v, int tid)
 {
-    int n = *static_cast<volatile int *>(&sh.queued[warp]);
-    while (n >= keep) {
-        const int m = n < 32 ? n : 32;
-        Key k = lane < m ? sh.queue[warp][n - m + lane] : 0;
-        n -= m;
-        if (__any_sync(0xffffffffu, k > bar)) {
-            list = merged(list, sorted(k, lane), lane);
-            bar = __shfl_sync(0xffffffffu, list, num_out - 1);
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((tid & 31) == 0)
+        sh.count[tid >> 5] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i)
+        v += sh.count[i];
+    return v;
+}
+
+// The logits of a part that are not below `bar` (or, strictly, above it) into
+// the queue, of the groups whose largest is: true if both had room.
+template <bool F32>
+__device__ __forceinline__ bool collect(PartShared &sh, const Part &p, float bar, bool strictly, int tid)
+{
+    constexpr int kP = kPer<F32>;
+    for (int i = 0; i < p.steps; ++i) {
+        const float m = sh.most[i][tid];
+        if (strictly ? m > bar : m >= bar) {
+            const int at = atomicAdd(&sh.hits, 1);
+            if (at < kHits)
+                sh.hit[at] = i * kThreads + tid;
         }
     }
-    __syncwarp();
-    if (lane == 0)
-        sh.queued[warp] = n;
-    __syncwarp();
+    __syncthreads();
+    const int hits = sh.hits;
+    if (hits > kHits)
+        return false;
+    for (int u = tid; u < hits * kWords; u += kThreads) {
+        const int g = sh.hit[u / kWords];
+        const int w = p.w0 + g / kThreads * kStepWords + u % kWords * kThreads + g % kThreads;
+        const uint4 v = load_word<F32>(p, w);
+#pragma unroll
+        for (int e = 0; e < kP; ++e) {
+            const float x = logit_at<F32>(v, e);
+            if (strictly ? x > bar : x >= bar) {
+                const int at = atomicAdd(&sh.queued, 1);
+                if (at < kKeys)
+                    sh.queue[at] = key_of(fminf(x, FLT_MAX), w * kP - p.first + e);
+            }
+        }
+    }
+    __syncthreads();
+    return sh.queued <= kKeys;
+}
+
+// What collect had no room for: logits of which very many are large, or alike.
+// Where many are at the bar itself (masked ones), those above it are few.  Else
+// the bar becomes the num_out-th largest group's (bit by bit): then fewer than
+// num_out groups are above it.  Of the logits that are equal to the bar the
+// first ones are taken in order, where they are needed.
+template <bool F32>
+__device__ __noinline__ void collect_crowd(PartShared &sh, const Part &p, float bar, int num_out, int tid)
+{
+    constexpr int kP = kPer<F32>;
+    const int lane = tid & 31, warp = tid >> 5;
+    for (int turn = 0; turn < 2; ++turn) {
+        if (turn == 1) {
+            uint32_t o = 0;
+            for (int bit = 31; bit >= 0; --bit) {
+                const uint32_t t = o | 1u << bit;
+                int n = 0;
+                for (int i = 0; i < p.steps; ++i)
+                    n += ordered(sh.most[i][tid]) >= t;
+                if (sum_over_cta(sh, n, tid) >= num_out)
+                    o = t;
+            }
+            bar = fmaxf(from_ordered(o), -FLT_MAX);
+        }
+        __syncthreads();
+        if (tid == 0)
+            sh.hits = sh.queued = 0;
+        __syncthreads();
+        if (collect<F32>(sh, p, bar, true, tid))
+            break;
+    }
+    int need = num_out - sh.queued, found = sh.queued;
+    for (int i = 0; i < p.steps && need > 0; ++i) {
+        const bool maybe = sh.most[i][tid] >= bar;  // (if its largest is above, it may hold some too)
+        if (!__syncthreads_or(maybe))
+            continue;
+        for (int j = 0; j < kWords && need > 0; ++j) {
+            const int w = p.w0 + i * kStepWords + j * kThreads + tid;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            int mine = 0;
+            if (maybe) {
+                v = load_word<F32>(p, w);
+#pragma unroll
+                for (int e = 0; e < kP; ++e)
+                    mine += fminf(logit_at<F32>(v, e), FLT_MAX) == bar;
+            }
+            int at = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, at, d);
+                at += lane >= d ? up : 0;
+            }
+            __syncthreads();
+            if (lane == 31)
+                sh.count[warp] = at;
+            __syncthreads();
+            at -= mine;
+            int all = 0;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                at += x < warp ? sh.count[x] : 0;
+                all += sh.count[x];
+            }
+            if (mine) {
+#pragma unroll
+                for (int e = 0; e < kP; ++e)
+                    if (fminf(logit_at<F32>(v, e), FLT_MAX) == bar && at++ < need)
+                        sh.queue[found + at - 1] = key_of(bar, w * kP - p.first + e);
+            }
+            found += min(all, need);
+            need -= min(all, need);
+        }
+    }
+    __syncthreads();
+    if (tid == 0)
+        sh.queued = found;
+    __syncthreads();
+}
+
+// The num_out largest of n keys to `out`, in order (0 where there are fewer): a
+// key's place is the number of larger ones, for all keys differ.
+__device__ __forceinline__ void rank_keys(const Key *keys, int n, int num_out, Key *out, int tid)
+{
+    for (int i = tid; i < n; i += kThreads) {
+        const Key k = keys[i];
+        int above = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j)
+            above += keys[j] > k;
+        if (above < num_out)
+            out[above] = k;
+    }
+    if (tid >= n && tid < num_out)
+        out[tid] = 0;
 }
 
 // One part of one row: its sum and its largest logits, by the whole CTA.
 //
-// What may be among the row's num_out largest is at least `bar`:
-// - strictly more than the last of the warp's own list, which is full of
-//   logits of lower index (a warp meets its words in their order);
-// - at least the least, over the warps, of their rank-th largest, where rank
-//   times the warps is num_out: that many logits are not smaller.  A lane's
-//   largest logit so far stands for the lane (other lanes' are other logits).
-// The first words of a part are looked at only when every warp has told its
-// own rank-th, so that nearly all of what passes from then on is wanted.
+// The part is read once, and nothing is chosen meanwhile: each thread only
+// notes the largest logit of its words of every step.  Then a bar is set that
+// num_out logits reach: the least, over the warps, of the rank-th largest of
+// their threads' largest, where rank times the warps is num_out.  Few words
+// reach it; they are read again (they lie in L2), and their logits ranked.
 template <bool F32>
 __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int part, PartShared &sh)
 {
     const smoe_beam_args &a = b.a;
     constexpr int kP = kPer<F32>, kBytes = F32 ? 4 : 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.num_out;
-    // words of 16 bytes from the one that the row begins in
     const uint8_t *begin = static_cast<const uint8_t *>(a.logits) + row * a.row_stride * kBytes;
-    const int first = static_cast<int>(reinterpret_cast<uintptr_t>(begin) & 15) / kBytes;
-    const uint8_t *base = begin - first * kBytes;
-    const int words = (first + a.vocab + kP - 1) / kP;
-    const int w0 = part * b.part_words, w1 = min(w0 + b.part_words, words);
-    const int busy = max(1, min(kWarps, (w1 - w0 + 32 * kWords - 1) / (32 * kWords)));  // warps with words
-    const int rank = (N + busy - 1) / busy;
-    if (lane == 0)
-        sh.queued[warp] = 0;
-    Key list = 0, bar = 0;
-    float own = -FLT_MAX;     // what is not less may be among the list's largest
-    float top = -INFINITY;    // the lane's largest
-    Sum s = {-kMaxRef, 0.0f};
-    int w = w0 + warp * 32 * kWords + lane;
+    Part p;
+    p.first = static_cast<int>(reinterpret_cast<uintptr_t>(begin) & 15) / kBytes;
+    p.base = begin - p.first * kBytes;
+    p.vocab = a.vocab;
+    p.w0 = part * b.part_words;
+    p.w1 = min(p.w0 + b.part_words, (p.first + a.vocab + kP - 1) / kP);
+    p.steps = max(0, p.w1 - p.w0 + kStepWords - 1) / kStepWords;
+    int w = p.w0 + tid;
     uint4 next[kWords];
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-        next[i] = load_word<F32>(base, first, a.vocab, w + 32 * i, w1);
-    for (int step = w0; step < w1; step += kStepWords, w += kStepWords) {
+        next[i] = load_word<F32>(p, w + kThreads * i);
+    // (the first words are on their way while the beam's state is looked up)
+    if (state_of(a, row) != kLive)
+        return;
+    float top = -INFINITY;
+    Sum s = {-kMaxRef, 0.0f};
+    for (int step = 0; step < p.steps; ++step, w += kStepWords) {
         uint4 v[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
             v[i] = next[i];
-        if (step + kStepWords < w1) {
+        if (step + 1 < p.steps) {
 #pragma unroll
             for (int i = 0; i < kWords; ++i)
-                next[i] = load_word<F32>(base, first, a.vocab, w + kStepWords + 32 * i, w1);
+                next[i] = load_word<F32>(p, w + kStepWords + kThreads * i);
         }
-        const float most = largest<F32>(v, kWords);
-        if (rank <= kMaxRank && (step == w0 || __any_sync(0xffffffffu, most > top))) {
-            uint32_t o = ordered(fmaxf(top, most)), r = 0;
-            for (int i = 0; i < rank; ++i) {
-                r = __reduce_max_sync(0xffffffffu, o);
-                const unsigned m = __ballot_sync(0xffffffffu, o == r);
-                o = lane == __ffs(m) - 1 ? 0 : o;
-            }
-            if (lane == 0)
-                sh.rank[warp] = r;
-        }
+        const float most = fminf(largest<F32>(v, kWords), FLT_MAX);
+        sh.most[step][tid] = most;
         top = fmaxf(top, most);
         s.raise(most);
         s.sum += sum_of<F32>(v, s.ref);
-        if (step == w0)
-            __syncthreads();
-        float least = own;
-        if (rank <= kMaxRank) {
-            const uint32_t r = lane < busy ? *static_cast<volatile uint32_t *>(&sh.rank[lane]) : 0xffffffffu;
-            least = fmaxf(least, from_ordered(__reduce_min_sync(0xffffffffu, r)));
-        }
-        if (!__any_sync(0xffffffffu, most >= least))
-            continue;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            if (!__any_sync(0xffffffffu, largest<F32>(&v[i], 1) >= least))
-                continue;
-#pragma unroll
-            for (int e = 0; e < kP; ++e) {
-                const float x = logit_at<F32>(v[i], e);
-                if (x >= least) {
-                    const int at = atomicAdd(&sh.queued[warp], 1);
-                    sh.queue[warp][at] = key_of(fminf(x, FLT_MAX), (w + 32 * i) * kP - first + e);
-                }
-            }
-            __syncwarp();
-            if (*static_cast<volatile int *>(&sh.queued[warp]) >= 32) {
-                drain(sh, warp, lane, N, 32, list, bar);
-                own = bar ? next_up(logit_of(bar)) : -FLT_MAX;
-                least = fmaxf(least, own);
-            }
-        }
     }
-    drain(sh, warp, lane, N, 1, list, bar);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Sum other;
-        other.ref = __shfl_xor_sync(0xffffffffu, s.ref, o);
-        other.sum = __shfl_xor_sync(0xffffffffu, s.sum, o);
-        s = joined(s, other);
+    const int busy = max(1, min(kWarps, (p.w1 - p.w0 + 31) / 32));  // warps with words
+    uint32_t o = ordered(top), r = 0;
+    for (int i = 0; i < N; i += busy) {
+        r = __reduce_max_sync(0xffffffffu, o);
+        o = lane == __ffs(__ballot_sync(0xffffffffu, o == r)) - 1 ? 0 : o;
     }
-    sh.list[warp][lane] = list;
-    if (lane == 0)
+    const float ref = static_cast<float>(__reduce_max_sync(0xffffffffu, static_cast<int>(s.ref)));
+    s = {ref, s.sum * power_of_two(s.ref - ref)};
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        s.sum += __shfl_xor_sync(0xffffffffu, s.sum, d);
+    if (lane == 0) {
+        sh.rank[warp] = r;
         sh.sum[warp] = s;
-    // the warps' lists are joined two by two
-    for (int o = 1; o < kWarps; o *= 2) {
-        __syncthreads();
-        if (warp % (2 * o) == 0) {
-            s = joined(s, sh.sum[warp + o]);
-            list = merged(list, sh.list[warp + o][lane], lane);
-            sh.list[warp][lane] = list;
-            if (lane == 0)
-                sh.sum[warp] = s;
-        }
     }
-    if (warp == 0) {
-        const int64_t at = row * b.parts + part;
-        if (lane == 0)
-            b.stats[at] = make_float2(s.ref, s.sum);
-        if (lane < N)
-            b.keys[at * N + lane] = list;
-    }
-}
-
-// A candidate of a group, as an integer that grows with its value in 64 bits
-// (0: none), and 32 times its beam plus its rank there.
-struct Candidate {
-    unsigned long long value;
-    int place;
-};
-__device__ __forceinline__ bool before(const Candidate &x, const Candidate &y)
-{
-    return x.value > y.value || (x.value == y.value && x.place < y.place);
-}
-__device__ __forceinline__ unsigned long long ordered_value(double x)
-{
-    const unsigned long long b = __double_as_longlong(x + 0.0);
-    return b >> 63 ? ~b : b | 1ull << 63;
-}
-__device__ __forceinline__ double value_of(unsigned long long o)
-{
-    return __longlong_as_double(o >> 63 ? o & ~(1ull << 63) : ~o);
-}
-
-// c and the 32 of r, both sorted, in r's order reversed: the first 32 of both.
-__device__ __forceinline__ Candidate merged(Candidate c, const Candidate &reversed, int lane)
-{
-    c = before(c, reversed) ? c : reversed;
+    if (tid == 0)
+        sh.hits = sh.queued = 0;
+    __syncthreads();
+    r = lane < busy ? sh.rank[lane] : 0xffffffffu;
+    const float bar = fmaxf(from_ordered(__reduce_min_sync(0xffffffffu, r)), -FLT_MAX);
+    if (!collect<F32>(sh, p, bar, false, tid))
+        collect_crowd<F32>(sh, p, bar, N, tid);
+    const int64_t at = row * b.parts + part;
+    rank_keys(sh.queue, sh.queued, N, b.keys + at * N, tid);
+    if (tid == 0) {
+        s = sh.sum[0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Candidate y = {__shfl_xor_sync(0xffffffffu, c.value, o), __shfl_xor_sync(0xffffffffu, c.place, o)};
-        c = ((lane & o) == 0) == before(c, y) ? c : y;
+        for (int i = 1; i < kWarps; ++i)
+            s = joined(s, sh.sum[i]);
+        b.stats[at] = make_float2(s.ref, s.sum);
     }
-    return c;
 }
+
+// ------------------------------------------------- a group's candidates
+
+// Values are sums of a large and a small fp32 number: the double format's
+// units are so few on this part that a logarithm there takes 2,800 cycles.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b)  // exactly a + b
+{
+    Two r;
+    r.hi = a + b;
+    const float v = r.hi - a;
+    r.lo = (a - (r.hi - v)) + (b - v);
+    return r;
+}
+__device__ __forceinline__ Two settled(Two t)
+{
+    Two r;
+    r.hi = t.hi + t.lo;
+    r.lo = t.lo - (r.hi - t.hi);
+    return r;
+}
+
+// c near 1 / (1 + (i + 1/2) / 32), of 8 bits, and -log c as two numbers.
+__constant__ float kLogTable[32][3] = {
+    {0.984375f, 0.015748357f, -4.3215895e-10f}, {0.95703125f, 0.043919235f, -1.5330752e-09f},
+    {0.92578125f, 0.0771173f, 1.8207458e-09f}, {0.90234375f, 0.102759734f, 1.6164925e-10f},
+    {0.875f, 0.13353139f, 1.0038866e-09f}, {0.8515625f, 0.16068238f, 1.4910411e-09f},
+    {0.83203125f, 0.18388528f, 2.4525408e-09f}, {0.80859375f, 0.21245866f, -4.023958e-09f},
+    {0.7890625f, 0.23690975f, -4.536055e-11f}, {0.76953125f, 0.2619737f, 6.873547e-09f},
+    {0.75390625f, 0.28248724f, 1.21607515e-08f}, {0.734375f, 0.3087355f, -8.195663e-09f},
+    {0.71875f, 0.33024168f, 6.725313e-09f}, {0.703125f, 0.3522206f, -1.293613e-09f},
+    {0.6875f, 0.37469345f, -3.8705092e-09f}, {0.671875f, 0.39768296f, 2.8643212e-09f},
+    {0.66015625f, 0.41527873f, -3.2201528e-09f}, {0.64453125f, 0.43923196f, 8.613421e-09f},
+    {0.6328125f, 0.4575811f, 6.3991252e-09f}, {0.62109375f, 0.47627324f, 3.600426e-09f},
+    {0.609375f, 0.49532142f, 1.4414702e-08f}, {0.59765625f, 0.5147395f, 9.68991e-09f},
+    {0.5859375f, 0.53454214f, 7.0384276e-09f}, {0.578125f, 0.54796517f, 1.7625055e-09f},
+    {0.56640625f, 0.5684437f, -1.3513369e-08f}, {0.5546875f, 0.5893504f, -1.5476893e-08f},
+    {0.546875f, 0.603535f, 2.5360706e-08f}, {0.5390625f, 0.61792374f, 2.2750092e-08f},
+    {0.52734375f, 0.63990265f, 1.4731166e-08f}, {0.51953125f, 0.6548283f, 6.244991e-09f},
+    {0.51171875f, 0.6699801f, 1.25404656e-08f}, {0.50390625f, 0.685365f, 1.88891e-08f},
+};
+
+// The logarithm of (sum.hi + sum.lo) 2^ref, of a normal number and a whole one,
+// to 2^-29 or so: by a table, as P. T. P. Tang's "Table-driven implementation
+// of the logarithm function" has it: with m in [1, 2) and c m = 1 + r, |r| < 2^-5,
+// log m = -log c + r - r^2 / 2 + r^3 / 3 - ...
+__device__ __forceinline__ Two log_of(Two sum, float ref)
+{
+    const int bits = __float_as_int(sum.hi);
+    const int e = (bits >> 23) - 127;
+    const float m = __int_as_float((bits & 0x7fffff) | 0x3f800000);
+    const float *t = kLogTable[(bits >> 18) & 31];
+    const float r = fmaf(m, t[0], -1.0f);
+    const float small = sum.lo * power_of_two(static_cast<float>(-e)) * t[0];
+    const float q = r * r * fmaf(r, fmaf(r, fmaf(r, fmaf(r, -1.0f / 6, 0.2f), -0.25f), 1.0f / 3), -0.5f);
+    const float n = ref + static_cast<float>(e), ln2 = 0.693147182464599609375f, rest = -1.904654323148236e-9f;
+    const float p = n * ln2;
+    float lo = fmaf(n, rest, fmaf(n, ln2, -p));
+    Two s = two_sum(p, t[1]);
+    lo += s.lo + t[2];
+    s = two_sum(s.hi, r);
+    s.lo += lo + (q + small);
+    return settled(s);
+}
+
+// Integers that grow with a value, in 2^-45 of it or so; never 0.
+using Value = unsigned long long;
+__device__ __forceinline__ Value ordered_value(Two t)
+{
+    // (large enough, the rest is below what 64 bits would hold)
+    const float lo = fabsf(t.hi) > 0x1p64f ? 0.0f : t.lo;
+    return static_cast<Value>(ordered(t.hi + 0.0f)) << 32 | ordered(lo + 0.0f);
+}
+
+constexpr int kCands = 512;
+constexpr int kSamples = 1024;
 
 struct JoinShared {
-    Candidate best[kWarps][32];
-    int token[SMOE_MAX_BEAMS][32];
+    // of each beam: a quarter of its score, and of its normaliser (base + off);
+    // values may be three times fp32's largest number
+    float score[SMOE_MAX_BEAMS], base[SMOE_MAX_BEAMS];
+    Two off[SMOE_MAX_BEAMS];
+    int state[SMOE_MAX_BEAMS];
+    float again[SMOE_MAX_BEAMS];   // the largest logit where the sum has to be taken again, else NaN
     float sum[kWarps];
-    int again;               // a beam whose sum has to be taken again
+    int queued;
+    Value bar;
+    Value sample[kSamples];        // the first values of each part, 0 of beams that are not live
+    // candidates
+    Value value[kCands];
+    Key key[kCands];
+    int beam[kCands];
+    // the best of each warp (select_crowd)
+    Value best_value[kWarps];
+    Key best_key[kWarps];
+    int best_beam[kWarps];
 };
+
+__device__ __forceinline__ Value value_of(const JoinShared &sh, int k, Key key)
+{
+    Two t = two_sum(0.25f * logit_of(key), -sh.base[k]);
+    const Two u = two_sum(t.hi, -sh.off[k].hi);
+    const float lo = u.lo + (t.lo - sh.off[k].lo);
+    t = two_sum(u.hi, sh.score[k]);
+    t.lo += lo;
+    return ordered_value(settled(t));
+}
+__device__ __forceinline__ float score_of(Value v) { return 4.0f * from_ordered(static_cast<uint32_t>(v >> 32)); }
+
+// Whether candidate a comes before b.
+__device__ __forceinline__ bool before(Value av, int ak, Key a, Value bv, int bk, Key b)
+{
+    return av != bv ? av > bv : ak != bk ? ak < bk : a > b;
+}
+
+__device__ __forceinline__ void put(const smoe_beam_args &a, int group, int place, bool found, Value value, int beam,
+                                    Key key)
+{
+    const int64_t at = (int64_t)group * a.num_out + place;
+    a.scores_out[at] = found ? score_of(value) : -INFINITY;
+    a.parents[at] = found ? group * a.beams + beam : -1;
+    a.tokens[at] = found ? index_of(key) : -1;
+}
+
+// Candidate i of a group's beams * parts * num_out (and a finished beam's own):
+// false where there is none.
+__device__ __forceinline__ bool candidate(const BeamArgs &b, int group, const JoinShared &sh, int i, Value &value,
+                                          int &beam, Key &key)
+{
+    const smoe_beam_args &a = b.a;
+    const int per = b.parts * a.num_out;
+    beam = i / per;
+    const int rest = i - beam * per;
+    if (sh.state[beam] == kFinished) {
+        key = key_of(0.0f, a.end_token);
+        value = ordered_value({sh.score[beam], 0.0f});
+        return rest == 0;
+    }
+    if (sh.state[beam] != kLive)
+        return false;
+    key = __ldcg(b.keys + (int64_t)group * a.beams * per + i);
+    value = value_of(sh, beam, key);
+    return key != 0;
+}
 
 // The sum of exp(x - most) over a row, by the whole CTA: of rows with a NaN or
 // +inf, or whose largest logit is out of the range of references.
@@ -474,95 +653,202 @@ __device__ float row_sum(const smoe_beam_args &a, int64_t row, float most, JoinS
     return s;
 }
 
+// The smallest of the lanes' keys.
+__device__ __forceinline__ Key least_of(Key k)
+{
+    const uint32_t hi = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo =
+        __reduce_min_sync(0xffffffffu, hi == static_cast<uint32_t>(k >> 32) ? static_cast<uint32_t>(k) : 0xffffffffu);
+    return static_cast<Key>(hi) << 32 | lo;
+}
+
+// The outputs of a group with very many candidates that are alike: the best of
+// all, then the best of what comes after it, and so on.
+__device__ __noinline__ void select_crowd(const BeamArgs &b, int group, JoinShared &sh)
+{
+    const smoe_beam_args &a = b.a;
+    const int tid = threadIdx.x, lane = tid & 31, all = a.beams * b.parts * a.num_out;
+    Value last_value = ~0ull;
+    Key last_key = ~0ull;
+    int last_beam = -1;
+    for (int place = 0; place < a.num_out; ++place) {
+        Value value = 0;
+        Key key = 0;
+        int beam = 0;
+        for (int i = tid; i < all; i += kThreads) {
+            Value v;
+            Key k;
+            int m;
+            if (candidate(b, group, sh, i, v, m, k) && before(last_value, last_beam, last_key, v, m, k) &&
+                before(v, m, k, value, beam, key)) {
+                value = v;
+                key = k;
+                beam = m;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const Value v = __shfl_xor_sync(0xffffffffu, value, o);
+            const Key k = __shfl_xor_sync(0xffffffffu, key, o);
+            const int m = __shfl_xor_sync(0xffffffffu, beam, o);
+            if (before(v, m, k, value, beam, key)) {
+                value = v;
+                key = k;
+                beam = m;
+            }
+        }
+        __syncthreads();
+        if (lane == 0) {
+            sh.best_value[tid >> 5] = value;
+            sh.best_key[tid >> 5] = key;
+            sh.best_beam[tid >> 5] = beam;
+        }
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w)
+            if (before(sh.best_value[w], sh.best_beam[w], sh.best_key[w], value, beam, key)) {
+                value = sh.best_value[w];
+                key = sh.best_key[w];
+                beam = sh.best_beam[w];
+            }
+        if (tid == 0)
+            put(a, group, place, value != 0, value, beam, key);
+        last_value = value;
+        last_key = key;
+        last_beam = beam;
+    }
+}
+
+// A group's outputs from its rows' parts, by the CTA that arrived last.  As in
+// a part: a bar that num_out candidates reach, and the few that do are ranked.
+// The bar is the num_out-th largest of some first values of each part, four
+// times as many as that in all.
 template <bool F32>
 __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinShared &sh)
 {
     const smoe_beam_args &a = b.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.num_out;
-    Candidate best = {0, 0x7fffffff};
-    for (int k0 = 0; k0 < a.beams; k0 += kWarps) {
-        const int k = k0 + warp;
-        const int64_t row = (int64_t)group * a.beams + k;
-        const int state = k < a.beams ? state_of(a, row) : kDead;
-        double score = 0.0, base = 0.0, off = 0.0;  // off: the normaliser, less base
-        Key list = 0;
-        bool again = false;
-        if (state == kLive) {
-            score = a.scores[row];
-            const float2 *stats = b.stats + row * b.parts;
-            const Key *keys = b.keys + row * b.parts * N;
-            list = lane < N ? __ldcg(keys + lane) : 0;
-            float ref = -kMaxRef;
-            for (int p = lane; p < b.parts; p += 32)
-                ref = fmaxf(ref, __ldcg(&stats[p].x));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-            double sum = 0.0;
-            for (int p = lane; p < b.parts; p += 32) {
-                const float2 s = __ldcg(stats + p);
-                sum += s.y * power_of_two(s.x - ref);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.num_out, P = b.parts;
+    const int64_t row0 = (int64_t)group * a.beams;
+    const int depth = min(N, (4 * N + a.beams * P - 1) / (a.beams * P));  // values of a part
+    const int each = P * depth, samples = min(a.beams * each, kSamples);
+    if (tid == 0) {
+        sh.queued = 0;
+        sh.bar = 0;
+    }
+    bool again = false;
+    for (int k = warp; k < a.beams; k += kWarps) {
+        const float2 *stats = b.stats + (row0 + k) * P;
+        const Key *keys = b.keys + (row0 + k) * P * N;
+        // (all of these are on their way at once; those of beams that are not live mean nothing)
+        Key top = 0;
+        Two sum = {0.0f, 0.0f};
+        float ref = -kMaxRef;
+        for (int p = lane; p < P; p += 32) {
+            const Key t = __ldcg(keys + (int64_t)p * N);
+            const float2 s = __ldcg(stats + p);
+            const float to = fmaxf(ref, s.x);
+            sum.hi *= power_of_two(ref - to);
+            sum.lo *= power_of_two(ref - to);
+            const Two u = two_sum(sum.hi, s.y * power_of_two(s.x - to));
+            sum = {u.hi, sum.lo + u.lo};
+            ref = to;
+            top = t > top ? t : top;
+        }
+        const int state = state_of(a, row0 + k);
+        if (lane == 0) {
+            sh.state[k] = state;
+            sh.score[k] = 0.25f * a.scores[row0 + k];
+        }
+        if (state != kLive) {
+            for (int i = lane; i < each && k * each + i < kSamples; i += 32)
+                sh.sample[k * each + i] = 0;
+            continue;
+        }
+        const float all = static_cast<float>(__reduce_max_sync(0xffffffffu, static_cast<int>(ref)));
+        sum.hi *= power_of_two(ref - all);
+        sum.lo *= power_of_two(ref - all);
+        for (int o = 16; o > 0; o >>= 1) {
+            const Two t = two_sum(sum.hi, __shfl_xor_sync(0xffffffffu, sum.hi, o));
+            sum = {t.hi, t.lo + (sum.lo + __shfl_xor_sync(0xffffffffu, sum.lo, o))};
+        }
+        top = ~least_of(~top);
+        // the largest logit's term is at least 2^-1
+        const bool wrong = !(sum.hi >= 0.25f && sum.hi <= FLT_MAX) && top != 0;
+        const Two log = log_of(settled(sum), all);
+        if (lane == 0) {
+            sh.base[k] = 0.0f;
+            sh.off[k] = {0.25f * log.hi, 0.25f * log.lo};
+            sh.again[k] = wrong ? logit_of(top) : NAN;
+        }
+        again = again || wrong;
+        __syncwarp();
+        if (!wrong)
+            for (int i = lane; i < each && k * each + i < kSamples; i += 32) {
+                const Key t = __ldcg(keys + (i / depth) * N + i % depth);
+                sh.sample[k * each + i] = t ? value_of(sh, k, t) : 0;
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            for (int p = 1; p < b.parts; ++p) {
-                const Key other = lane < N ? __ldcg(keys + (int64_t)p * N + lane) : 0;
-                list = merged(list, other, lane);
+    }
+    if (__syncthreads_or(again))
+        for (int k = 0; k < a.beams; ++k) {
+            const float most = sh.again[k];
+            if (sh.state[k] != kLive || isnan(most))
+                continue;
+            const float s = row_sum<F32>(a, row0 + k, most, sh);
+            const Two log = log_of({s, 0.0f}, 0.0f);
+            if (tid == 0) {
+                sh.base[k] = 0.25f * most;
+                sh.off[k] = {0.25f * log.hi, 0.25f * log.lo};
             }
-            list = lane < N ? list : 0;
-            // in whole sums of normal numbers the largest logit's term is one of at least 2^-1
-            again = !(sum >= 0.25 && sum <= FLT_MAX) && __shfl_sync(0xffffffffu, list, 0) != 0;
-            off = (ref + log2(sum)) * 0.6931471805599453;
+            for (int i = tid; i < each && k * each + i < kSamples; i += kThreads)
+                sh.sample[k * each + i] = 0;
+            __syncthreads();
         }
-        // (rare: rows one after the other, by all warps)
-        if (__syncthreads_or(again)) {
-            for (int w = 0; w < kWarps; ++w) {
-                if (warp == w && lane == 0)
-                    sh.again = again ? __float_as_int(logit_of(list)) : 0x7fffffff;
-                __syncthreads();
-                const int most = sh.again;
-                __syncthreads();
-                if (most == 0x7fffffff)  // (no logit's bits)
-                    continue;
-                const float s = row_sum<F32>(a, (int64_t)group * a.beams + k0 + w, __int_as_float(most), sh);
-                if (warp == w) {
-                    base = __int_as_float(most);
-                    off = log(static_cast<double>(s));
-                }
-            }
-        }
-        Candidate c = {0, 0x7fffffff};
-        int token = -1;
-        if (list) {
-            c.value = ordered_value(score + ((logit_of(list) - base) - off));
-            token = index_of(list);
-        } else if (state == kFinished && lane == 0) {
-            c.value = ordered_value(a.scores[row]);
-            token = a.end_token;
-        }
-        if (k < a.beams) {
-            sh.token[k][lane] = token;
-            c.place = 32 * k + lane;
-        }
-        const Candidate r = {__shfl_sync(0xffffffffu, c.value, 31 - lane), __shfl_sync(0xffffffffu, c.place, 31 - lane)};
-        best = merged(best, r, lane);
+    for (int i = tid; i < samples; i += kThreads) {
+        const Value v = sh.sample[i];
+        int place = 0;
+#pragma unroll 8
+        for (int j = 0; j < samples; ++j)
+            place += sh.sample[j] > v || (sh.sample[j] == v && j < i);
+        if (place == N - 1)
+            sh.bar = v;
     }
     __syncthreads();
-    for (int o = 1; o < kWarps && o < a.beams; o *= 2) {
-        sh.best[warp][lane] = best;
-        __syncthreads();
-        if (warp % (2 * o) == 0)
-            best = merged(best, sh.best[warp + o][31 - lane], lane);
-        __syncthreads();
+    const Value bar = sh.bar;
+    for (int i = tid; i < a.beams * P * N; i += kThreads) {
+        Value value;
+        Key key;
+        int beam;
+        if (candidate(b, group, sh, i, value, beam, key) && value >= bar) {
+            const int at = atomicAdd(&sh.queued, 1);
+            if (at < kCands) {
+                sh.value[at] = value;
+                sh.key[at] = key;
+                sh.beam[at] = beam;
+            }
+        }
     }
-    if (warp == 0 && lane < N) {
-        const int64_t at = (int64_t)group * N + lane;
-        const bool found = best.value != 0;
-        a.scores_out[at] = found ? static_cast<float>(value_of(best.value)) : -INFINITY;
-        a.parents[at] = found ? group * a.beams + (best.place >> 5) : -1;
-        a.tokens[at] = found ? sh.token[best.place >> 5][best.place & 31] : -1;
+    __syncthreads();
+    const int n = sh.queued;
+    if (n > kCands) {
+        select_crowd(b, group, sh);
+        return;
     }
+    for (int i = tid; i < n; i += kThreads) {
+        const Value value = sh.value[i];
+        const Key key = sh.key[i];
+        const int beam = sh.beam[i];
+        int place = 0, same = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+            place += sh.value[j] > value;
+            same += sh.value[j] == value;
+        }
+        for (int j = 0; j < n && same > 1; ++j)
+            place += sh.value[j] == value && before(value, sh.beam[j], sh.key[j], value, beam, key);
+        if (place < N)
+            put(a, group, place, true, value, beam, key);
+    }
+    if (tid >= n && tid < N)
+        put(a, group, tid, false, 0, 0, 0);
 }
 
 union BeamShared {
@@ -571,14 +857,13 @@ union BeamShared {
 };
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 3) beam_kernel(const BeamArgs b)
+__global__ void __launch_bounds__(kThreads, 4) beam_kernel(const BeamArgs b)
 {
     __shared__ BeamShared sh;
     __shared__ bool s_last;
     const int64_t row = blockIdx.x / b.parts;
     const int part = blockIdx.x % b.parts, group = static_cast<int>(row / b.a.beams);
-    if (state_of(b.a, row) == kLive)
-        scan_part<F32>(b, row, part, sh.part);
+    scan_part<F32>(b, row, part, sh.part);
     __syncthreads();
     if (threadIdx.x == 0) {
         const unsigned all = b.a.beams * b.parts;
@@ -606,7 +891,8 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     // parts: about six CTAs per SM, of a step at least
     const int64_t wave = dev.sms * 6 < kMaxWave ? dev.sms * 6 : kMaxWave;
     int64_t parts = (wave + rows - 1) / rows;
-    parts = parts < steps ? parts : steps;
+    const int least = (steps + kMaxSteps - 1) / kMaxSteps;
+    parts = parts < least ? least : parts < steps ? parts : steps;
     const int each = static_cast<int>((steps + parts - 1) / parts);
     b.part_words = each * kStepWords;
     b.parts = (steps + each - 1) / each;

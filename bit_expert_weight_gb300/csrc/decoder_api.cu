@@ -206,8 +206,8 @@ smoe_status smoe_attention(const smoe_attention_args *a, void *workspace, size_t
 
 smoe_status smoe_beam_select(const smoe_beam_args *a, void *workspace, size_t workspace_bytes, void *cuda_stream)
 {
-    if (!a || !valid_dtype(a->dtype) || a->vocab < 1 || a->vocab > (1 << 26) || a->num_groups < 0 ||
-        a->num_groups > SMOE_MAX_SEQS || a->beams < 1 || a->beams > SMOE_MAX_BEAMS || a->num_out < 1 ||
+    if (!a || !valid_dtype(a->dtype) || a->vocab < 1 || a->vocab > SMOE_MAX_VOCAB || a->num_groups < 0 ||
+        a->beams < 1 || a->beams > SMOE_MAX_BEAMS || a->num_groups > SMOE_MAX_SEQS / a->beams || a->num_out < 1 ||
         a->num_out > SMOE_MAX_BEAMS || a->end_token < -1 || a->end_token >= a->vocab || a->row_stride < 0 ||
         a->row_stride > (1ll << 40))
         return SMOE_ERR_INVALID_ARG;

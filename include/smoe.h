@@ -718,6 +718,7 @@ smoe_status smoe_attention(const smoe_attention_args *args, void *workspace,
 
 /* Largest numbers of beams and of outputs of a group. */
 #define SMOE_MAX_BEAMS 32
+#define SMOE_MAX_VOCAB (1 << 22)
 /* Bytes of smoe_beam_select's workspace, for every shape: 256-byte aligned,
  * zeroed once (smoe_moe_workspace_init) and again after a call that returned an
  * error; calls that can overlap on the device need a workspace each. */
@@ -735,8 +736,8 @@ typedef struct {
     int32_t *parents;          /* out [num_groups, num_out]                   */
     int32_t *tokens;           /* out [num_groups, num_out]                   */
     int32_t dtype;             /* smoe_dtype of logits                        */
-    int32_t vocab;             /* 1 .. 2^26                                   */
-    int32_t num_groups;        /* 0 .. SMOE_MAX_SEQS                          */
+    int32_t vocab;             /* 1 .. SMOE_MAX_VOCAB                         */
+    int32_t num_groups;        /* num_groups * beams <= SMOE_MAX_SEQS         */
     int32_t beams;             /* 1 .. SMOE_MAX_BEAMS                         */
     int32_t num_out;           /* 1 .. SMOE_MAX_BEAMS                         */
     int32_t end_token;         /* -1: none; else < vocab                      */

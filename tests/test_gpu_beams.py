@@ -47,7 +47,7 @@ def select(S, ws, x, scores, n, **kw):
 @pytest.mark.parametrize("G, K, V, N", [
     (1, 1, 1, 1), (1, 1, 5, 3), (2, 3, 7, 32), (1, 4, 8, 4), (3, 2, 31, 2), (1, 32, 100, 32),
     (5, 4, 1_001, 8), (2, 5, 4_099, 10), (1, 4, 32_000, 4), (7, 1, 8_192, 1), (2, 16, 8_193, 32),
-    (1, 2, 300_007, 32), (40, 8, 3_000, 16), (2048, 1, 40, 3), (2048, 32, 9, 32),
+    (1, 2, 300_007, 32), (40, 8, 3_000, 16), (2048, 1, 40, 3), (64, 32, 9, 32),
     (1, 1, 3_000_001, 5),
 ], ids=str)
 def test_select(S, ws, G, K, V, N, dtype):

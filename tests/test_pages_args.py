@@ -32,8 +32,8 @@ def beam_args(S, **kw):
 @pytest.mark.parametrize("kw", [
     dict(logits=None), dict(logits=PTR + 1), dict(logits=PTR + 2, dtype=0), dict(row_stride=-1),
     dict(row_stride=(1 << 40) + 1), dict(scores=None), dict(scores_out=None), dict(parents=None),
-    dict(tokens=None), dict(dtype=2), dict(vocab=0), dict(vocab=(1 << 26) + 1),
-    dict(num_groups=-1), dict(num_groups=2049), dict(beams=0), dict(beams=33), dict(num_out=0),
+    dict(tokens=None), dict(dtype=2), dict(vocab=0), dict(vocab=(1 << 22) + 1),
+    dict(num_groups=-1), dict(num_groups=513), dict(beams=0), dict(beams=33), dict(num_out=0),
     dict(num_out=33), dict(end_token=-2), dict(end_token=100), dict(scores_out=2 * PTR),
     dict(tokens=3 * PTR), dict(parents=6 * PTR), dict(parents=3 * PTR, num_out=4),
 ], ids=str)
