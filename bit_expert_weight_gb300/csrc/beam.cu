@@ -276,13 +276,15 @@ template <bool F32>
 __device__ __forceinline__ bool collect(PartShared &sh, const Part &p, float bar, bool strictly, int tid)
 {
     constexpr int kP = kPer<F32>;
+    unsigned mine = 0;  // by step
     for (int i = 0; i < p.steps; ++i) {
         const float m = sh.most[i][tid];
-        if (strictly ? m > bar : m >= bar) {
-            const int at = atomicAdd(&sh.hits, 1);
-            if (at < kHits)
-                sh.hit[at] = i * kThreads + tid;
-        }
+        mine |= (strictly ? m > bar : m >= bar) ? 1u << i : 0u;
+    }
+    if (mine) {
+        int at = atomicAdd(&sh.hits, __popc(mine));
+        for (; mine && at < kHits; mine &= mine - 1)
+            sh.hit[at++] = (__ffs(mine) - 1) * kThreads + tid;
     }
     __syncthreads();
     const int hits = sh.hits;
@@ -292,15 +294,19 @@ __device__ __forceinline__ bool collect(PartShared &sh, const Part &p, float bar
         const int g = sh.hit[u / kWords];
         const int w = p.w0 + g / kThreads * kStepWords + u % kWords * kThreads + g % kThreads;
         const uint4 v = load_word<F32>(p, w);
+        unsigned pass = 0;
 #pragma unroll
         for (int e = 0; e < kP; ++e) {
             const float x = logit_at<F32>(v, e);
-            if (strictly ? x > bar : x >= bar) {
-                const int at = atomicAdd(&sh.queued, 1);
-                if (at < kKeys)
-                    sh.queue[at] = key_of(fminf(x, FLT_MAX), w * kP - p.first + e);
-            }
+            pass |= (strictly ? x > bar : x >= bar) ? 1u << e : 0u;
         }
+        if (!pass)
+            continue;
+        int at = atomicAdd(&sh.queued, __popc(pass));
+#pragma unroll
+        for (int e = 0; e < kP; ++e)
+            if ((pass >> e & 1) && at < kKeys)
+                sh.queue[at++] = key_of(fminf(logit_at<F32>(v, e), FLT_MAX), w * kP - p.first + e);
     }
     __syncthreads();
     return sh.queued <= kKeys;
@@ -472,7 +478,7 @@ __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int pa
         collect_crowd<F32>(sh, p, bar, N, tid);
     const int64_t at = row * b.parts + part;
     rank_keys(sh.queue, sh.queued, N, b.keys + at * N, tid);
-    if (tid == 0) {
+    if (tid == kThreads - 32) {  // (a warp that seldom has keys to rank)
         s = sh.sum[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i)
@@ -558,6 +564,7 @@ __device__ __forceinline__ Value ordered_value(Two t)
 
 constexpr int kCands = 512;
 constexpr int kSamples = 1024;
+constexpr int kFirst = 4;  // candidates of a thread that are loaded early
 
 struct JoinShared {
     // of each beam: a quarter of its score, and of its normaliser (base + off);
@@ -606,25 +613,18 @@ __device__ __forceinline__ void put(const smoe_beam_args &a, int group, int plac
     a.tokens[at] = found ? index_of(key) : -1;
 }
 
-// Candidate i of a group's beams * parts * num_out (and a finished beam's own):
-// false where there is none.
-__device__ __forceinline__ bool candidate(const BeamArgs &b, int group, const JoinShared &sh, int i, Value &value,
-                                          int &beam, Key &key)
+// Candidate `rest` of a beam's parts * num_out, whose key was `key` (a finished
+// beam has one, of its own): false where there is none.
+__device__ __forceinline__ bool candidate(const smoe_beam_args &a, const JoinShared &sh, int beam, int rest,
+                                          Value &value, Key &key)
 {
-    const smoe_beam_args &a = b.a;
-    const int per = b.parts * a.num_out;
-    beam = i / per;
-    const int rest = i - beam * per;
     if (sh.state[beam] == kFinished) {
         key = key_of(0.0f, a.end_token);
         value = ordered_value({sh.score[beam], 0.0f});
         return rest == 0;
     }
-    if (sh.state[beam] != kLive)
-        return false;
-    key = __ldcg(b.keys + (int64_t)group * a.beams * per + i);
     value = value_of(sh, beam, key);
-    return key != 0;
+    return sh.state[beam] == kLive && key != 0;
 }
 
 // The sum of exp(x - most) over a row, by the whole CTA: of rows with a NaN or
@@ -667,7 +667,8 @@ __device__ __forceinline__ Key least_of(Key k)
 __device__ __noinline__ void select_crowd(const BeamArgs &b, int group, JoinShared &sh)
 {
     const smoe_beam_args &a = b.a;
-    const int tid = threadIdx.x, lane = tid & 31, all = a.beams * b.parts * a.num_out;
+    const int tid = threadIdx.x, lane = tid & 31, per = b.parts * a.num_out, all = a.beams * per;
+    const Key *keys = b.keys + (int64_t)group * all;
     Value last_value = ~0ull;
     Key last_key = ~0ull;
     int last_beam = -1;
@@ -677,9 +678,9 @@ __device__ __noinline__ void select_crowd(const BeamArgs &b, int group, JoinShar
         int beam = 0;
         for (int i = tid; i < all; i += kThreads) {
             Value v;
-            Key k;
-            int m;
-            if (candidate(b, group, sh, i, v, m, k) && before(last_value, last_beam, last_key, v, m, k) &&
+            Key k = __ldcg(keys + i);
+            const int m = i / per;
+            if (candidate(a, sh, m, i - m * per, v, k) && before(last_value, last_beam, last_key, v, m, k) &&
                 before(v, m, k, value, beam, key)) {
                 value = v;
                 key = k;
@@ -734,16 +735,27 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         sh.queued = 0;
         sh.bar = 0;
     }
+    // All that a beam's warp needs is on its way at once, and so are the first
+    // candidates of every thread (what belongs to beams that are not live means
+    // nothing).
+    const int per = P * N, all = a.beams * per;
+    const Key *group_keys = b.keys + row0 * per;
+    Key first[kFirst];
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j)
+        first[j] = tid + j * kThreads < all ? __ldcg(group_keys + tid + j * kThreads) : 0;
     bool again = false;
     for (int k = warp; k < a.beams; k += kWarps) {
         const float2 *stats = b.stats + (row0 + k) * P;
-        const Key *keys = b.keys + (row0 + k) * P * N;
-        // (all of these are on their way at once; those of beams that are not live mean nothing)
+        const Key *keys = group_keys + k * per;
+        const float score = a.scores[row0 + k];
+        const int state = state_of(a, row0 + k);
+        const Key sample = lane < each ? __ldcg(keys + lane / depth * N + lane % depth) : 0;
         Key top = 0;
         Two sum = {0.0f, 0.0f};
         float ref = -kMaxRef;
         for (int p = lane; p < P; p += 32) {
-            const Key t = __ldcg(keys + (int64_t)p * N);
+            const Key t = __ldcg(keys + p * N);
             const float2 s = __ldcg(stats + p);
             const float to = fmaxf(ref, s.x);
             sum.hi *= power_of_two(ref - to);
@@ -753,19 +765,18 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
             ref = to;
             top = t > top ? t : top;
         }
-        const int state = state_of(a, row0 + k);
         if (lane == 0) {
             sh.state[k] = state;
-            sh.score[k] = 0.25f * a.scores[row0 + k];
+            sh.score[k] = 0.25f * score;
         }
         if (state != kLive) {
             for (int i = lane; i < each && k * each + i < kSamples; i += 32)
                 sh.sample[k * each + i] = 0;
             continue;
         }
-        const float all = static_cast<float>(__reduce_max_sync(0xffffffffu, static_cast<int>(ref)));
-        sum.hi *= power_of_two(ref - all);
-        sum.lo *= power_of_two(ref - all);
+        const float to = static_cast<float>(__reduce_max_sync(0xffffffffu, static_cast<int>(ref)));
+        sum.hi *= power_of_two(ref - to);
+        sum.lo *= power_of_two(ref - to);
         for (int o = 16; o > 0; o >>= 1) {
             const Two t = two_sum(sum.hi, __shfl_xor_sync(0xffffffffu, sum.hi, o));
             sum = {t.hi, t.lo + (sum.lo + __shfl_xor_sync(0xffffffffu, sum.lo, o))};
@@ -773,7 +784,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         top = ~least_of(~top);
         // the largest logit's term is at least 2^-1
         const bool wrong = !(sum.hi >= 0.25f && sum.hi <= FLT_MAX) && top != 0;
-        const Two log = log_of(settled(sum), all);
+        const Two log = log_of(settled(sum), to);
         if (lane == 0) {
             sh.base[k] = 0.0f;
             sh.off[k] = {0.25f * log.hi, 0.25f * log.lo};
@@ -783,7 +794,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         __syncwarp();
         if (!wrong)
             for (int i = lane; i < each && k * each + i < kSamples; i += 32) {
-                const Key t = __ldcg(keys + (i / depth) * N + i % depth);
+                const Key t = i < 32 ? sample : __ldcg(keys + i / depth * N + i % depth);
                 sh.sample[k * each + i] = t ? value_of(sh, k, t) : 0;
             }
     }
@@ -813,11 +824,10 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
     }
     __syncthreads();
     const Value bar = sh.bar;
-    for (int i = tid; i < a.beams * P * N; i += kThreads) {
+    const auto offer = [&](int i, Key key) {
         Value value;
-        Key key;
-        int beam;
-        if (candidate(b, group, sh, i, value, beam, key) && value >= bar) {
+        const int beam = i / per;
+        if (candidate(a, sh, beam, i - beam * per, value, key) && value >= bar) {
             const int at = atomicAdd(&sh.queued, 1);
             if (at < kCands) {
                 sh.value[at] = value;
@@ -825,7 +835,13 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
                 sh.beam[at] = beam;
             }
         }
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j)
+        if (tid + j * kThreads < all)
+            offer(tid + j * kThreads, first[j]);
+    for (int i = tid + kFirst * kThreads; i < all; i += kThreads)
+        offer(i, __ldcg(group_keys + i));
     __syncthreads();
     const int n = sh.queued;
     if (n > kCands) {
@@ -889,8 +905,8 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     const int words = (a.vocab + 2 * per - 2) / per;
     const int steps = (words + kStepWords - 1) / kStepWords;
     // parts: about six CTAs per SM, of a step at least
-    const int64_t wave = dev.sms * 6 < kMaxWave ? dev.sms * 6 : kMaxWave;
-    int64_t parts = (wave + rows - 1) / rows;
+    const int64_t wave = dev.sms * 4 < kMaxWave ? dev.sms * 4 : kMaxWave;
+    int64_t parts = wave / rows;
     const int least = (steps + kMaxSteps - 1) / kMaxSteps;
     parts = parts < least ? least : parts < steps ? parts : steps;
     const int each = static_cast<int>((steps + parts - 1) / parts);
