@@ -286,7 +286,7 @@ smoe_status smoe_pages_compact(const smoe_page_pool *pool, int32_t *refs_out, in
                                int32_t max_copies, int32_t *counts, void *cuda_stream)
 {
     if (!pool || !valid_pool(*pool) || !refs_out || !counts || max_copies < pool->num_pages / 2 ||
-        (max_copies > 0 && !copies) || !same_or_apart(pool->refs, refs_out, pool->num_pages))
+        (max_copies > 0 && !copies) || (reinterpret_cast<uintptr_t>(copies) & 7) || !same_or_apart(pool->refs, refs_out, pool->num_pages))
         return SMOE_ERR_INVALID_ARG;
     if (pool->num_seqs > 0 &&
         (!table_out ||

@@ -9,7 +9,6 @@
 // next to find.
 #include <atomic>
 
-#include "attention.cuh"
 #include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -20,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kMaxKeys = 0x7fffffff - 511;  // of a sequence
 
 __device__ __forceinline__ int log2_of(int power) { return 31 - __clz(power); }
@@ -41,7 +40,7 @@ __device__ __forceinline__ bool valid_len(const smoe_page_pool &p, int len)
 // child that does: for entry j of an old sequence the two come to (children
 // with more than j pages) - 1, one atomic addition where that is not 0 (whole
 // numbers: their order does not matter).
-constexpr int kForkEntries = 16;  // of a thread and tile
+constexpr int kForkEntries = 8;  // of a thread and tile
 
 struct ForkShared {
     int parent[SMOE_MAX_SEQS], was[SMOE_MAX_SEQS], len[SMOE_MAX_SEQS];
@@ -99,37 +98,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     most = s_most;
     // columns of a tile: a power of two, so that a tile's entries fit the threads
-    int width = 8;
+    int width = 4;
     while (width * 2 * n <= kThreads * kForkEntries && width < 4096)
         width *= 2;
     const int wshift = log2_of(width);
     for (int j0 = cluster_rank() * width; j0 < most; j0 += cluster_size() * width) {
-        int moved[kForkEntries];
+        // (first what is to be read, all at once; then what is done with it)
+        int moved[kForkEntries], own[kForkEntries], by[kForkEntries];
+        unsigned moves = 0;
 #pragma unroll
         for (int i = 0; i < kForkEntries; ++i) {
             const int e = tid + i * kThreads, s = e >> wshift, j = j0 + (e & (width - 1));
+            by[i] = moved[i] = own[i] = 0;
             if (s >= n)
                 continue;
             const int a = sh.parent[s];
-            if (a >= 0 && a != s && j < pages_of(sh.len[s], shift))
+            if (a >= 0 && a != s && j < pages_of(sh.len[s], shift)) {
+                moves |= 1u << i;
                 moved[i] = p.page_table[(int64_t)a * p.table_stride + j];
+            }
             if (j < pages_of(sh.was[s], shift)) {
                 const int c = sh.children[s];
-                const int by = (j < sh.least[s] ? c : c == 1 ? 0 : children_above(sh, n, s, j, shift)) - 1;
-                if (by != 0) {
-                    const int page = p.page_table[(int64_t)s * p.table_stride + j];
-                    if (page >= 0 && page < p.num_pages)
-                        atomicAdd(p.refs + page, by);
-                    else
-                        set_status(status, kStatusBadArg);
-                }
+                by[i] = (j < sh.least[s] ? c : c == 1 ? 0 : children_above(sh, n, s, j, shift)) - 1;
+                if (by[i] != 0)
+                    own[i] = p.page_table[(int64_t)s * p.table_stride + j];
             }
         }
+#pragma unroll
+        for (int i = 0; i < kForkEntries; ++i)
+            if (by[i] != 0) {
+                if (own[i] >= 0 && own[i] < p.num_pages)
+                    atomicAdd(p.refs + own[i], by[i]);
+                else
+                    set_status(status, kStatusBadArg);
+            }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kForkEntries; ++i) {
             const int e = tid + i * kThreads, s = e >> wshift, j = j0 + (e & (width - 1));
-            if (s < n && sh.parent[s] >= 0 && sh.parent[s] != s && j < pages_of(sh.len[s], shift))
+            if (moves >> i & 1)
                 p.page_table[(int64_t)s * p.table_stride + j] = moved[i];
         }
     }
@@ -142,33 +149,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------- runs of a pool's pages
 
 // Reserve and compact go over refs in runs: a CTA of the cluster has some
-// consecutive pages, and each of its warps a run of them, 4 pages a lane and
-// step.
+// consecutive pages, and each of its warps a run of them, 1024 pages (8 loads in
+// flight) at a time.
+constexpr int kChunk = 1024;
+
 struct Runs {
     int64_t first, last;  // the warp's pages
 };
 
-__device__ __forceinline__ int64_t run_length(int num_pages)
-{
-    const int64_t runs = (int64_t)cluster_size() * kWarps;
-    return (num_pages + runs * 128 - 1) / (runs * 128) * 128;
-}
-
 __device__ __forceinline__ Runs run_of_warp(int num_pages)
 {
-    const int64_t len = run_length(num_pages);
+    const int64_t runs = (int64_t)cluster_size() * kWarps;
+    const int64_t len = (num_pages + runs * kChunk - 1) / (runs * kChunk) * kChunk;
     Runs r;
     r.first = ((int64_t)cluster_rank() * kWarps + (threadIdx.x >> 5)) * len;
     r.last = min(r.first + len, (int64_t)num_pages);
     return r;
 }
 
-// Four pages' holders from page `at` on (a multiple of 4); -1 past `last`.
+// Four pages' holders from page `at` on (a multiple of 4); 0 past `last`.
 __device__ __forceinline__ int4 refs_at(const int32_t *refs, int64_t at, int64_t last)
 {
     if (at + 4 <= last)
         return __ldcg(reinterpret_cast<const int4 *>(refs + at));
-    int4 v = make_int4(-1, -1, -1, -1);
+    int4 v = make_int4(0, 0, 0, 0);
     if (at < last)
         v.x = __ldcg(refs + at);
     if (at + 1 < last)
@@ -178,15 +182,35 @@ __device__ __forceinline__ int4 refs_at(const int32_t *refs, int64_t at, int64_t
     return v;
 }
 
-// Bit i: page i of the four is held.
-__device__ __forceinline__ unsigned held_of(int4 v)
+// Nibble i of a lane's word: which of pages at + 128 i + 4 lane + (0 .. 3) are held.
+__device__ __forceinline__ uint32_t held_nibbles(const int32_t *refs, int64_t at, int64_t last, int lane)
 {
-    return (v.x > 0) | (v.y > 0) << 1 | (v.z > 0) << 2 | (v.w > 0) << 3;
+    int4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = refs_at(refs, at + 128 * i + 4 * lane, last);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w |= static_cast<uint32_t>((v[i].x > 0) | (v[i].y > 0) << 1 | (v[i].z > 0) << 2 | (v[i].w > 0) << 3) << (4 * i);
+    return w;
 }
-// Bit i: page at + i is below `end`.
-__device__ __forceinline__ unsigned below(int64_t at, int64_t end)
+
+// Bit j of a lane's word: whether page at + 32 lane + j is held.
+__device__ __forceinline__ uint32_t held_pages(const int32_t *refs, int64_t at, int64_t last, int lane)
 {
-    return end - at >= 4 ? 15u : end > at ? (1u << (end - at)) - 1u : 0u;
+    const uint32_t w = held_nibbles(refs, at, last, lane);
+    uint32_t m = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+        m |= (__shfl_sync(0xffffffffu, w, 8 * (lane & 3) + t) >> (4 * (lane >> 2)) & 15u) << (4 * t);
+    return m;
+}
+
+// Bit j: page at + j is below `end`.
+__device__ __forceinline__ uint32_t below(int64_t at, int64_t end)
+{
+    return end - at >= 32 ? 0xffffffffu : end > at ? (1u << (end - at)) - 1u : 0u;
 }
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
@@ -208,15 +232,8 @@ __device__ __forceinline__ int lanes_before(int v, int lane, int *total)
 __device__ __forceinline__ int count_held(const int32_t *refs, Runs r, int lane)
 {
     int n = 0;
-    for (int64_t at = r.first + 4 * lane; at < r.last; at += 4 * 128) {
-        int4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = refs_at(refs, at + 128 * i, r.last);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            n += __popc(held_of(v[i]));
-    }
+    for (int64_t at = r.first; at < r.last; at += kChunk)
+        n += __popc(held_nibbles(refs, at, r.last, lane));
     return warp_sum(n);
 }
 
@@ -401,31 +418,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     int rank = counted_before(sh.runs, tid >> 5);
-    for (int64_t at = run.first; at < run.last && rank < needed; at += 128) {
-        const int64_t q = at + 4 * lane;
-        unsigned free = ~held_of(refs_at(p.refs, q, run.last)) & below(q, run.last);
+    for (int64_t at = run.first; at < run.last && rank < needed; at += kChunk) {
+        const int64_t page0 = at + 32 * lane;
+        uint32_t free = ~held_pages(p.refs, at, run.last, lane) & below(page0, run.last);
         int all;
         int r = rank + lanes_before(__popc(free), lane, &all);
         rank += all;
+        if (!free || r >= needed)
+            continue;
+        // the last sequence whose pages begin at rank r or before; the next ones follow
+        int s = 0, end = n;
+        while (end - s > 1) {
+            const int mid = (s + end) / 2;
+            if (sh.base[mid] <= r)
+                s = mid;
+            else
+                end = mid;
+        }
+        int base = sh.base[s], next = base + sh.need[s];
         for (; free && r < needed; free &= free - 1, ++r) {
-            const int page = static_cast<int>(q) + __ffs(free) - 1;
-            // the last sequence whose pages begin at rank r or before
-            int lo = 0, hi = n;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (sh.base[mid] <= r)
-                    lo = mid;
-                else
-                    hi = mid;
+            const int page = static_cast<int>(page0) + __ffs(free) - 1;
+            while (r >= next) {
+                base = next;
+                next += sh.need[++s];
             }
-            const int copy = sh.holders[lo];
-            const int j = sh.had[lo] + (r - sh.base[lo]) - (copy >= 0);
-            if (copy >= 0 && r == sh.base[lo]) {
-                copies[2 * copy] = sh.page[lo];
+            const int copy = sh.holders[s];
+            if (copy >= 0 && r == base) {
+                copies[2 * copy] = sh.page[s];
                 copies[2 * copy + 1] = page;
-                atomicAdd(p.refs + sh.page[lo], -1);
+                atomicAdd(p.refs + sh.page[s], -1);
             }
-            p.page_table[(int64_t)lo * p.table_stride + j] = page;
+            p.page_table[(int64_t)s * p.table_stride + sh.had[s] + (r - base) - (copy >= 0)] = page;
             p.refs[page] = 1;
         }
     }
@@ -435,11 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 struct CompactShared {
     RunCounts runs;
-    int under;  // held pages below n
+    int under;                 // held pages below n
+    int most;                  // pages of the longest sequence
+    int pages[SMOE_MAX_SEQS];  // of each one
 };
 
-// While the tables are looked through, the entry of a moved page in refs_out
-// (which will be 0) says where it went.
+// The two ends of the moves are found by rank, each for itself; then the moves
+// are gone through as a list.  While the tables are looked through, the entry
+// of a moved page in refs_out (which will be 0) says where it went.
 __device__ __forceinline__ int went_to(int page) { return -1 - page; }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -450,89 +476,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, shift = log2_of(p.page_size);
     const Runs run = run_of_warp(p.num_pages);
     cluster_arrive();
+    if (tid == 0)
+        sh.most = 0;
     const int mine = count_held(p.refs, run, lane);
     share_counts(sh.runs, mine, tid);
     const int n = counted(sh.runs), before = counted_before(sh.runs, tid >> 5);
     // The free pages below n, by their rank among the free.
     int held_before = before;
-    for (int64_t at = run.first; at < run.last && at < n; at += 128) {
-        const int64_t q = at + 4 * lane;
-        const unsigned in = below(q, min(run.last, (int64_t)n));
-        const unsigned held = held_of(refs_at(p.refs, q, run.last)) & in;
+    for (int64_t at = run.first; at < run.last && at < n; at += kChunk) {
+        const int64_t page0 = at + 32 * lane;
+        const uint32_t in = below(page0, min(run.last, (int64_t)n));
+        const uint32_t held = held_pages(p.refs, at, run.last, lane) & in;
         int all;
-        const int h = held_before + lanes_before(__popc(held), lane, &all);
+        int64_t to = page0 - held_before - lanes_before(__popc(held), lane, &all);
         held_before += all;
-        for (unsigned free = ~held & in; free; free &= free - 1) {
+        for (uint32_t free = ~held & in; free; free &= free - 1) {
             const int i = __ffs(free) - 1;
-            copies[2 * (q + i - h - __popc(held & ((1u << i) - 1))) + 1] = static_cast<int>(q) + i;
+            copies[2 * (to + i - __popc(held & ((1u << i) - 1))) + 1] = static_cast<int>(page0) + i;
         }
     }
     // The run that page n lies in (or the end of the last one) tells how many are held below n.
     if (lane == 0 && run.first < run.last && n >= run.first && (n < run.last || run.last == p.num_pages))
         for (unsigned r = 0; r < cluster_size(); ++r)
             store_to_rank(&sh.under, r, held_before);
+    for (int s = tid; s < p.num_seqs; s += kThreads) {
+        const int len = p.kv_len[s];
+        const bool ok = valid_len(p, len);
+        sh.pages[s] = ok ? pages_of(len, shift) : 0;
+        if (!ok)
+            set_status(status, kStatusBadArg);
+        atomicMax(&sh.most, sh.pages[s]);
+    }
     cluster_sync();
     const int moves = n - sh.under;
     if (cluster_rank() == 0 && tid == 0) {
         counts[0] = moves;
         counts[1] = n;
     }
-    // Pages below n stay, those above go to the free ones, by their rank.  (In
-    // place, what is below n may be a page that has just come: it is not read.)
-    const bool apart = refs_out != p.refs;
+    // The held pages from n on, by their rank.
     int rank = max(before - sh.under, 0);
-    for (int64_t at = run.first; at < run.last; at += 128) {
-        const int64_t q = at + 4 * lane;
-        const unsigned in = below(q, run.last), stay = below(q, min(run.last, (int64_t)n));
-        const int4 v = refs_at(p.refs, q, run.last);
-        const unsigned moved = held_of(v) & in & ~stay;
-        int all;
-        int r = rank + lanes_before(__popc(moved), lane, &all);
-        rank += all;
-        const int c[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (moved >> i & 1) {
-                const int to = __ldcg(copies + 2 * (int64_t)r + 1);
-                copies[2 * (int64_t)r] = static_cast<int>(q) + i;
-                refs_out[to] = c[i];
-                refs_out[q + i] = went_to(to);
-                ++r;
-            } else if (apart && (in >> i & 1) && (!(stay >> i & 1) || c[i] > 0)) {
-                refs_out[q + i] = stay >> i & 1 ? c[i] : 0;
-            }
-        }
-    }
-    cluster_sync();
-    // The tables: a warp takes a row after the other.
-    const int warps = cluster_size() * kWarps;
-    for (int s = cluster_rank() * kWarps + (tid >> 5); s < p.num_seqs; s += warps) {
-        const int len = p.kv_len[s];
-        if (!valid_len(p, len)) {
-            set_status(status, kStatusBadArg);
+    for (int64_t at = run.first; at < run.last; at += kChunk) {
+        if (at + kChunk <= n)
             continue;
+        const int64_t page0 = at + 32 * lane;
+        uint32_t held = held_pages(p.refs, at, run.last, lane) & ~below(page0, n);
+        int all;
+        int r = rank + lanes_before(__popc(held), lane, &all);
+        rank += all;
+        for (; held; held &= held - 1, ++r)
+            copies[2 * (int64_t)r] = static_cast<int>(page0) + __ffs(held) - 1;
+    }
+    // What stays where it is (the free pages below n are written below).
+    const int first = cluster_rank() * kThreads + tid, step = cluster_size() * kThreads;
+    if (refs_out != p.refs)
+        for (int64_t q = first; q < p.num_pages; q += step) {
+            const int c = __ldcg(p.refs + q);
+            if (q >= n || c > 0)
+                refs_out[q] = q < n ? c : 0;
         }
-        const int pages = pages_of(len, shift);
+    cluster_sync();
+    for (int i = first; i < moves; i += step) {
+        const int2 m = __ldcg(reinterpret_cast<const int2 *>(copies) + i);
+        refs_out[m.y] = __ldcg(p.refs + m.x);
+        refs_out[m.x] = went_to(m.y);
+    }
+    cluster_sync();
+    // The tables: some columns of a row for each warp.
+    constexpr int kEach = 8;
+    const int warps = cluster_size() * kWarps, wide = (sh.most + 32 * kEach - 1) / (32 * kEach);
+    for (int u = cluster_rank() * kWarps + (tid >> 5); u < wide * p.num_seqs; u += warps) {
+        const int s = u % p.num_seqs, pages = sh.pages[s];
+        const int j0 = u / p.num_seqs * 32 * kEach + lane;
         const int64_t row = (int64_t)s * p.table_stride;
-        for (int j = lane; j < pages; j += 32) {
-            const int page = p.page_table[row + j];
-            int to = page;
-            if (page < 0 || page >= p.num_pages) {
+        int page[kEach], to[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            page[i] = j0 + 32 * i < pages ? p.page_table[row + j0 + 32 * i] : 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            to[i] = -1;
+            if (page[i] >= n && page[i] < p.num_pages)
+                to[i] = __ldcg(refs_out + page[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (j0 + 32 * i >= pages)
+                continue;
+            int now = page[i];
+            if (now < 0 || now >= p.num_pages || (now >= n && to[i] >= 0))
                 set_status(status, kStatusBadArg);
-            } else if (page >= n) {
-                const int went = __ldcg(refs_out + page);
-                if (went < 0)
-                    to = went_to(went);
-                else
-                    set_status(status, kStatusBadArg);
-            }
-            if (to != page || table_out != p.page_table)
-                table_out[row + j] = to;
+            else if (now >= n)
+                now = went_to(to[i]);
+            if (now != page[i] || table_out != p.page_table)
+                table_out[row + j0 + 32 * i] = now;
         }
     }
     cluster_sync();
-    for (int64_t q = max(run.first, (int64_t)n) + lane; q < run.last; q += 32)
-        refs_out[q] = 0;
+    for (int i = first; i < moves; i += step)
+        refs_out[__ldcg(copies + 2 * (int64_t)i)] = 0;
 }
 
 // ------------------------------------------------------------------- copy
@@ -593,8 +634,18 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 // One cluster of at most kMaxCluster CTAs.
 template <class... Params, class... Args>
-cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, cudaStream_t stream, Args... args)
+cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const DeviceFacts &dev, cudaStream_t stream,
+                           Args... args)
 {
+    static std::atomic<bool> allowed[kMaxDeviceIndex];  // (of each kernel: they differ in their parameters)
+    if (!allowed[dev.index].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess && smem > 0)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+        allowed[dev.index].store(true, std::memory_order_release);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
@@ -624,26 +675,21 @@ cudaError_t launch_pages_fork(const smoe_page_pool &p, const int32_t *parent, co
                               const DeviceFacts &dev, cudaStream_t stream)
 {
     const int64_t entries = (int64_t)p.num_seqs * p.table_stride;
-    return launch_cluster(fork_kernel, cluster_for(entries / 4096), 0, stream, p, parent, keep, dev.status);
+    return launch_cluster(fork_kernel, cluster_for(entries / 4096), 0, dev, stream, p, parent, keep, dev.status);
 }
 
 cudaError_t launch_pages_reserve(const smoe_page_pool &p, const int32_t *row_start, int32_t *copies,
                                  int32_t *counts, const DeviceFacts &dev, cudaStream_t stream)
 {
-    static std::atomic<bool> allowed[kMaxDeviceIndex];
-    const int smem = static_cast<int>(sizeof(ReserveShared));
-    const cudaError_t e = allow_smem(reserve_kernel, smem, dev, allowed);
-    if (e != cudaSuccess)
-        return e;
-    return launch_cluster(reserve_kernel, cluster_for(p.num_pages / 8192), smem, stream, p, row_start, copies,
-                          counts, dev.status);
+    return launch_cluster(reserve_kernel, cluster_for(p.num_pages / 8192), sizeof(ReserveShared), dev, stream, p,
+                          row_start, copies, counts, dev.status);
 }
 
 cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int32_t *table_out, int32_t *copies,
                                  int32_t *counts, const DeviceFacts &dev, cudaStream_t stream)
 {
     const int64_t work = p.num_pages / 8192 + (int64_t)p.num_seqs * p.table_stride / 8192;
-    return launch_cluster(compact_kernel, cluster_for(work), 0, stream, p, refs_out, table_out, copies, counts,
+    return launch_cluster(compact_kernel, cluster_for(work), 0, dev, stream, p, refs_out, table_out, copies, counts,
                           dev.status);
 }
 

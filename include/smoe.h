@@ -840,8 +840,8 @@ smoe_status smoe_pages_copy(const smoe_kv_cache *caches, int32_t num_caches, con
  *   refs_out   [num_pages]: pool->refs itself, or apart from it
  *   table_out  [num_seqs, table_stride]: pool->page_table itself, or apart
  *              from it (entries past a sequence's pages are left alone there)
- *   copies     out [max_copies, 2], max_copies >= num_pages / 2; entries past
- *              the count are left alone
+ *   copies     out [max_copies, 2], max_copies >= num_pages / 2, 8-byte
+ *              aligned; entries past the count are left alone
  *   counts     out [2]: how many moves; n
  * A length that is negative or past its row is recorded, and that row stays as
  * it is; so is, and does, an entry that names no page of the pool, or one of

@@ -87,7 +87,7 @@ def test_compact_refuses(S):
     L, p = S.load(), ctypes.byref(pool_args(S))
     far = 100 * PTR
     for bad in ((None, far, far, 500, far), (far, None, far, 500, far), (far, far, None, 500, far),
-                (far, far, far, 499, far), (far, far, far, 500, None),
+                (far, far, far, 499, far), (far, far, far, 500, None), (far, far, far + 4, 500, far),
                 (PTR + 16, far, far, 500, far), (PTR - 400, far, far, 500, far),
                 (PTR + 3984, far, far, 500, far), (far, 3 * PTR + 64, far, 500, far),
                 (far, 3 * PTR - 64, far, 500, far)):
