@@ -35,42 +35,55 @@ __device__ __forceinline__ bool valid_len(const smoe_page_pool &p, int len)
 // ------------------------------------------------------------------- fork
 
 // Rows are rewritten in place, so one CTA owns some columns of the table for
-// all sequences: it reads what moves, waits for its own threads, and writes.
-// A page loses a holder with each sequence that used it and gains one with each
-// child that does: for entry j of an old sequence the two come to (children
-// with more than j pages) - 1, one atomic addition where that is not 0 (whole
-// numbers: their order does not matter).
-constexpr int kForkEntries = 8;  // of a thread and tile
+// all sequences: it reads what was there, waits for its own threads, and writes.
+// An entry that changes takes a holder from its old page and gives one to the
+// new (whole numbers: the order of the additions does not matter).  Beams share
+// most of their pages, and entries that stay the same cost two reads only.
+//
+// A tile is a row's 32 columns to a warp (16 or 8 of two or four rows where
+// there are many sequences, so that kForkRows of a thread are all of them).
+constexpr int kForkRows = 16;
+constexpr int kNone = -0x7fffffff - 1;
+static_assert(kForkRows * kWarps * 4 >= SMOE_MAX_SEQS, "tiles of 8 columns hold all sequences");
 
-struct ForkShared {
-    int parent[SMOE_MAX_SEQS], was[SMOE_MAX_SEQS], len[SMOE_MAX_SEQS];
-    int children[SMOE_MAX_SEQS], least[SMOE_MAX_SEQS];  // and the fewest pages of a child
+struct ForkRow {
+    int parent, was, now;  // pages
+    int len;               // keys
 };
 
-__device__ int children_above(const ForkShared &sh, int n, int s, int j, int shift)
+struct ForkShared {
+    ForkRow row[SMOE_MAX_SEQS];
+    int most;  // pages of the longest sequence
+};
+
+__device__ __forceinline__ void add_holder(const smoe_page_pool &p, int page, int by, int *status)
 {
-    int c = 0;
-    for (int t = 0; t < n; ++t)
-        c += sh.parent[t] == s && pages_of(sh.len[t], shift) > j;
-    return c;
+    if (page >= 0 && page < p.num_pages)
+        atomicAdd(p.refs + page, by);
+    else
+        set_status(status, kStatusBadArg);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     fork_kernel(const smoe_page_pool p, const int32_t *parent, const int32_t *keep, int *status)
 {
     __shared__ ForkShared sh;
-    const int tid = threadIdx.x, n = p.num_seqs, shift = log2_of(p.page_size);
+    const int tid = threadIdx.x, lane = tid & 31, n = p.num_seqs, shift = log2_of(p.page_size);
     bool bad = false;
-    int most = 0;
-    for (int s = tid; s < n; s += kThreads) {
+    int most = 0, cut[2];  // a thread has sequences tid and tid + kThreads
+    if (tid == 0)
+        sh.most = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = tid + i * kThreads;
+        if (s >= n)
+            continue;
         const int a = parent[s], len = p.kv_len[s];
-        sh.parent[s] = a;
-        sh.was[s] = len;
-        sh.children[s] = 0;
-        sh.least[s] = 0x7fffffff;
-        bad = bad || a < -1 || a >= n || !valid_len(p, len);
-        if (!bad)
-            most = max(most, pages_of(len, shift));
+        cut[i] = keep ? max(keep[s], 0) : 0x7fffffff;
+        const bool ok = a >= -1 && a < n && valid_len(p, len);
+        bad = bad || !ok;
+        sh.row[s] = {a, ok ? pages_of(len, shift) : 0, 0, len};
+        most = max(most, sh.row[s].was);
     }
     // (the same answer in every CTA: none of the arrays has been written yet)
     if (__syncthreads_or(bad)) {
@@ -78,94 +91,90 @@ __global__ void __launch_bounds__(kThreads, 1)
             set_status(status, kStatusBadArg);
         return;
     }
-    for (int s = tid; s < n; s += kThreads) {
-        const int a = sh.parent[s];
-        int len = a < 0 ? 0 : sh.was[a];
-        if (keep)
-            len = min(len, max(keep[s], 0));
-        sh.len[s] = len;
-        if (a >= 0) {
-            atomicAdd(&sh.children[a], 1);
-            atomicMin(&sh.least[a], pages_of(len, shift));
-        }
-    }
     cluster_arrive();  // this CTA has read every length
-    __shared__ int s_most;
-    if (tid == 0)
-        s_most = 0;
-    __syncthreads();
-    atomicMax(&s_most, most);
-    __syncthreads();
-    most = s_most;
-    // columns of a tile: a power of two, so that a tile's entries fit the threads
-    int width = 4;
-    while (width * 2 * n <= kThreads * kForkEntries && width < 4096)
-        width *= 2;
-    const int wshift = log2_of(width);
-    for (int j0 = cluster_rank() * width; j0 < most; j0 += cluster_size() * width) {
-        // (first what is to be read, all at once; then what is done with it)
-        int moved[kForkEntries], own[kForkEntries], by[kForkEntries];
-        unsigned moves = 0;
+    int len[2];
 #pragma unroll
-        for (int i = 0; i < kForkEntries; ++i) {
-            const int e = tid + i * kThreads, s = e >> wshift, j = j0 + (e & (width - 1));
-            by[i] = moved[i] = own[i] = 0;
+    for (int i = 0; i < 2; ++i) {
+        const int s = tid + i * kThreads;
+        if (s >= n)
+            continue;
+        const int a = sh.row[s].parent;
+        len[i] = a < 0 ? 0 : min(sh.row[a].len, cut[i]);
+        sh.row[s].now = pages_of(len[i], shift);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0)
+        atomicMax(&sh.most, most);
+    __syncthreads();
+    most = sh.most;
+    const int wshift = n <= kForkRows * kWarps ? 5 : n <= 2 * kForkRows * kWarps ? 4 : 3;
+    const int width = 1 << wshift, rows = kThreads >> wshift;  // of the CTA at a time
+    const int s0 = tid >> wshift;
+    for (int j0 = cluster_rank() * width; j0 < most; j0 += cluster_size() * width) {
+        const int j = j0 + (tid & (width - 1));
+        int from[kForkRows], to[kForkRows];  // the entry as it was and as it will be, or kNone
+#pragma unroll
+        for (int i = 0; i < kForkRows; ++i) {
+            const int s = s0 + i * rows;
+            from[i] = to[i] = kNone;
             if (s >= n)
                 continue;
-            const int a = sh.parent[s];
-            if (a >= 0 && a != s && j < pages_of(sh.len[s], shift)) {
-                moves |= 1u << i;
-                moved[i] = p.page_table[(int64_t)a * p.table_stride + j];
-            }
-            if (j < pages_of(sh.was[s], shift)) {
-                const int c = sh.children[s];
-                by[i] = (j < sh.least[s] ? c : c == 1 ? 0 : children_above(sh, n, s, j, shift)) - 1;
-                if (by[i] != 0)
-                    own[i] = p.page_table[(int64_t)s * p.table_stride + j];
-            }
+            const ForkRow r = sh.row[s];
+            const bool comes = r.parent != s && j < r.now;
+            if (j < r.was && (r.parent != s || j >= r.now))
+                from[i] = max(p.page_table[(int64_t)s * p.table_stride + j], kNone + 1);
+            if (comes)
+                to[i] = max(p.page_table[(int64_t)r.parent * p.table_stride + j], kNone + 1);
         }
-#pragma unroll
-        for (int i = 0; i < kForkEntries; ++i)
-            if (by[i] != 0) {
-                if (own[i] >= 0 && own[i] < p.num_pages)
-                    atomicAdd(p.refs + own[i], by[i]);
-                else
-                    set_status(status, kStatusBadArg);
-            }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kForkEntries; ++i) {
-            const int e = tid + i * kThreads, s = e >> wshift, j = j0 + (e & (width - 1));
-            if (moves >> i & 1)
-                p.page_table[(int64_t)s * p.table_stride + j] = moved[i];
+        for (int i = 0; i < kForkRows; ++i) {
+            if (from[i] == to[i])
+                continue;
+            if (from[i] != kNone)
+                add_holder(p, from[i], -1, status);
+            if (to[i] != kNone) {
+                add_holder(p, to[i], 1, status);
+                p.page_table[(int64_t)(s0 + i * rows) * p.table_stride + j] = to[i];
+            }
         }
     }
     cluster_wait();
     if (cluster_rank() == 0)
-        for (int s = tid; s < n; s += kThreads)
-            p.kv_len[s] = sh.len[s];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (tid + i * kThreads < n)
+                p.kv_len[tid + i * kThreads] = len[i];
 }
 
 // ------------------------------------------------- runs of a pool's pages
 
-// Reserve and compact go over refs in runs: a CTA of the cluster has some
-// consecutive pages, and each of its warps a run of them, 1024 pages (8 loads in
-// flight) at a time.
-constexpr int kChunk = 1024;
+// Reserve and compact go over refs in runs of consecutive pages, one for each
+// warp of the cluster, dealt to its CTAs in turn (what is asked of pages is often
+// asked of the lowest), and in each run in chunks of 128 pages (L = 1) or of 1024
+// (L = 8 loads in flight), by the size of the pool.
+constexpr int chunk(int L) { return 128 * L; }
 
-struct Runs {
-    int64_t first, last;  // the warp's pages
+struct Run {
+    int64_t first, last;  // pages
 };
 
-__device__ __forceinline__ Runs run_of_warp(int num_pages)
+// The length of a run.
+template <int L>
+__device__ __forceinline__ int64_t run_length(int num_pages)
 {
-    const int64_t runs = (int64_t)cluster_size() * kWarps;
-    const int64_t len = (num_pages + runs * kChunk - 1) / (runs * kChunk) * kChunk;
-    Runs r;
-    r.first = ((int64_t)cluster_rank() * kWarps + (threadIdx.x >> 5)) * len;
-    r.last = min(r.first + len, (int64_t)num_pages);
-    return r;
+    const unsigned round = cluster_size() * kWarps * chunk(L);
+    return (int64_t)((static_cast<unsigned>(num_pages) + round - 1) / round) * chunk(L);
 }
+
+// Run number r.
+__device__ __forceinline__ Run run_at(int64_t length, int r, int num_pages)
+{
+    return {r * length, min((r + 1) * length, (int64_t)num_pages)};
+}
+
+// Warp w's run.
+__device__ __forceinline__ int run_of_warp(int w) { return w * cluster_size() + cluster_rank(); }
 
 // Four pages' holders from page `at` on (a multiple of 4); 0 past `last`.
 __device__ __forceinline__ int4 refs_at(const int32_t *refs, int64_t at, int64_t last)
@@ -183,99 +192,120 @@ __device__ __forceinline__ int4 refs_at(const int32_t *refs, int64_t at, int64_t
 }
 
 // Nibble i of a lane's word: which of pages at + 128 i + 4 lane + (0 .. 3) are held.
+template <int L>
 __device__ __forceinline__ uint32_t held_nibbles(const int32_t *refs, int64_t at, int64_t last, int lane)
 {
-    int4 v[8];
+    int4 v[L];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < L; ++i)
         v[i] = refs_at(refs, at + 128 * i + 4 * lane, last);
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < L; ++i)
         w |= static_cast<uint32_t>((v[i].x > 0) | (v[i].y > 0) << 1 | (v[i].z > 0) << 2 | (v[i].w > 0) << 3) << (4 * i);
     return w;
 }
 
-// Bit j of a lane's word: whether page at + 32 lane + j is held.
-__device__ __forceinline__ uint32_t held_pages(const int32_t *refs, int64_t at, int64_t last, int lane)
+// Those nibbles' pages that are below `end`.
+template <int L>
+__device__ __forceinline__ uint32_t nibbles_below(int64_t at, int64_t end, int lane)
 {
-    const uint32_t w = held_nibbles(refs, at, last, lane);
-    uint32_t m = 0;
+    const int n = static_cast<int>(min(max(end - at, (int64_t)0), (int64_t)chunk(L)));
+    uint32_t w = 0;
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
-        m |= (__shfl_sync(0xffffffffu, w, 8 * (lane & 3) + t) >> (4 * (lane >> 2)) & 15u) << (4 * t);
-    return m;
-}
-
-// Bit j: page at + j is below `end`.
-__device__ __forceinline__ uint32_t below(int64_t at, int64_t end)
-{
-    return end - at >= 32 ? 0xffffffffu : end > at ? (1u << (end - at)) - 1u : 0u;
+    for (int i = 0; i < L; ++i) {
+        const int d = n - 128 * i - 4 * lane;
+        w |= (d >= 4 ? 15u : d > 0 ? (1u << d) - 1u : 0u) << (4 * i);
+    }
+    return w;
 }
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// The lanes' v before this one, and all lanes' in total.
-__device__ __forceinline__ int lanes_before(int v, int lane, int *total)
-{
-    int x = v;
+// Where the set pages of a chunk stand among themselves, in the order of the
+// pages: those of each nibble's word (32 lanes) one after the other.
+template <int L>
+struct Ranks {
+    uint32_t before[2], total[2];  // a byte for each nibble: of the lanes before, of all lanes (at most 128)
+    __device__ __forceinline__ Ranks(uint32_t w, int lane)
+    {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        x += lane >= o ? y : 0;
+        for (int h = 0; h < (L + 3) / 4; ++h) {
+            uint32_t own = 0;
+#pragma unroll
+            for (int i = 4 * h; i < L && i < 4 * h + 4; ++i)
+                own |= static_cast<uint32_t>(__popc(w >> (4 * i) & 15u)) << (8 * (i & 3));
+            uint32_t x = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                x += lane >= o ? y : 0;
+            }
+            before[h] = x - own;
+            total[h] = __shfl_sync(0xffffffffu, x, 31);
+        }
     }
-    *total = __shfl_sync(0xffffffffu, x, 31);
-    return x - v;
-}
+    // Set pages before nibble i's first one of this lane.
+    __device__ __forceinline__ int at(int i) const
+    {
+        int n = before[i / 4] >> (8 * (i & 3)) & 255u;
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            n += j < i ? static_cast<int>(total[j / 4] >> (8 * (j & 3)) & 255u) : 0;
+        return n;
+    }
+    __device__ __forceinline__ int all() const
+    {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            n += total[j / 4] >> (8 * (j & 3)) & 255u;
+        return n;
+    }
+};
 
-// Held pages of the warp's run.
-__device__ __forceinline__ int count_held(const int32_t *refs, Runs r, int lane)
+// Held pages of a run.
+template <int L>
+__device__ __forceinline__ int count_held(const int32_t *refs, Run r, int lane)
 {
     int n = 0;
-    for (int64_t at = r.first; at < r.last; at += kChunk)
-        n += __popc(held_nibbles(refs, at, r.last, lane));
+    for (int64_t at = r.first; at < r.last; at += chunk(L))
+        n += __popc(held_nibbles<L>(refs, at, r.last, lane));
     return warp_sum(n);
 }
 
-// Counts of every warp of the cluster, and what comes before this warp's run.
+// Counts of every run.
 struct RunCounts {
-    int cta[kMaxCluster];  // by rank
-    int warp[kWarps];      // of this CTA
+    int own[kWarps];
+    int run[kMaxCluster * kWarps];
 };
 
-// `mine`: the warp's count, the same in all its lanes.  The kernel has arrived
-// at the cluster's barrier at its start (every CTA has begun where that ends).
-// A barrier of the cluster.
+// `mine`: the count of the warp's run, the same in all its lanes.  The kernel
+// has arrived at the cluster's barrier at its start (every CTA has begun where
+// that ends).  A barrier of the cluster.
 __device__ __forceinline__ void share_counts(RunCounts &rc, int mine, int tid)
 {
     if ((tid & 31) == 0)
-        rc.warp[tid >> 5] = mine;
+        rc.own[tid >> 5] = mine;
     __syncthreads();
     cluster_wait();
-    if (tid < 32) {
-        const int all = warp_sum(tid < kWarps ? rc.warp[tid] : 0);
-        if (tid < static_cast<int>(cluster_size()))
-            store_to_rank(&rc.cta[cluster_rank()], tid, all);
-    }
+    if (tid < static_cast<int>(cluster_size()) * kWarps)
+        store_to_rank(&rc.run[run_of_warp(tid % kWarps)], tid / kWarps, rc.own[tid % kWarps]);
     cluster_sync();
 }
 
-__device__ __forceinline__ int counted_before(const RunCounts &rc, int warp)
+// What the runs before r counted, by a warp.
+__device__ __forceinline__ int counted_before(const RunCounts &rc, int r, int lane)
 {
     int n = 0;
-    for (unsigned r = 0; r < cluster_rank(); ++r)
-        n += rc.cta[r];
-    for (int w = 0; w < warp; ++w)
-        n += rc.warp[w];
-    return n;
+    for (int i = lane; i < r; i += 32)
+        n += rc.run[i];
+    return warp_sum(n);
 }
 
-__device__ __forceinline__ int counted(const RunCounts &rc)
+__device__ __forceinline__ int counted(const RunCounts &rc, int lane)
 {
-    int n = 0;
-    for (unsigned r = 0; r < cluster_size(); ++r)
-        n += rc.cta[r];
-    return n;
+    return counted_before(rc, static_cast<int>(cluster_size()) * kWarps, lane);
 }
 
 // ---------------------------------------------------------------- reserve
@@ -285,39 +315,34 @@ __device__ __forceinline__ int counted(const RunCounts &rc)
 // the number needed looks up whose it is.
 constexpr int kSlots = 2 * SMOE_MAX_SEQS;  // of the table of shared last pages
 
-struct ReserveShared {
-    RunCounts runs;
-    int page[SMOE_MAX_SEQS];      // a partly filled last page that is to be written, else -1
-    int holders[SMOE_MAX_SEQS];   // of it; later: the place of its copy in the list, else -1
-    int had[SMOE_MAX_SEQS];       // pages
-    int need[SMOE_MAX_SEQS];
-    int base[SMOE_MAX_SEQS];      // free pages given to the sequences before
-    int key[kSlots], writers[kSlots], first[kSlots];
-    unsigned long long warp[kWarps], total;
+// What a sequence gets, as the ranks' owners look it up.
+struct Given {
+    int end;    // free pages given to the sequences up to it
+    int entry;  // of its row: the first one's
+    int copy;   // the place of its copy in the list, -1: none
+    int page;   // the page that is copied
 };
 
-// Sums over the threads before this one, and over all.
-__device__ __forceinline__ unsigned long long threads_before(ReserveShared &sh, unsigned long long v, int tid)
+struct ReserveShared {
+    RunCounts runs;
+    Given given[SMOE_MAX_SEQS];
+    int page[SMOE_MAX_SEQS];      // a partly filled last page that is to be written, else -1
+    int holders[SMOE_MAX_SEQS];   // of it
+    int had[SMOE_MAX_SEQS];       // pages
+    int need[SMOE_MAX_SEQS];
+    int key[kSlots], writers[kSlots], first[kSlots];
+    int warp_need[kWarps], warp_copies[kWarps];
+};
+
+// The lanes' v up to this one.
+__device__ __forceinline__ int lanes_up_to(int v, int lane)
 {
-    const int lane = tid & 31, w = tid >> 5;
-    unsigned long long x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-        x += lane >= o ? y : 0;
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        v += lane >= o ? y : 0;
     }
-    if (lane == 31)
-        sh.warp[w] = x;
-    __syncthreads();
-    unsigned long long before = 0, all = 0;
-    for (int i = 0; i < kWarps; ++i) {
-        before += i < w ? sh.warp[i] : 0;
-        all += sh.warp[i];
-    }
-    if (tid == 0)
-        sh.total = all;
-    __syncthreads();
-    return before + x - v;
+    return v;
 }
 
 __device__ __forceinline__ int slot_of_page(ReserveShared &sh, int page)
@@ -333,13 +358,15 @@ __device__ __forceinline__ int slot_of_page(ReserveShared &sh, int page)
     return static_cast<int>(h);
 }
 
+template <int L>
 __global__ void __launch_bounds__(kThreads, 1)
     reserve_kernel(const smoe_page_pool p, const int32_t *row_start, int32_t *copies, int32_t *counts, int *status)
 {
     extern __shared__ __align__(16) uint8_t s_raw[];
     ReserveShared &sh = *reinterpret_cast<ReserveShared *>(s_raw);
-    const int tid = threadIdx.x, lane = tid & 31, n = p.num_seqs, shift = log2_of(p.page_size);
-    const Runs run = run_of_warp(p.num_pages);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.num_seqs, shift = log2_of(p.page_size);
+    const int64_t length = run_length<L>(p.num_pages);
+    const Run run = run_at(length, run_of_warp(warp), p.num_pages);
     cluster_arrive();
     bool bad = false;
     for (int i = tid; i < kSlots; i += kThreads) {
@@ -368,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.page[s] = page;
         sh.holders[s] = holders;
     }
-    const int mine = static_cast<int>(max(run.last - run.first, (int64_t)0)) - count_held(p.refs, run, lane);
+    const int mine = static_cast<int>(max(run.last - run.first, (int64_t)0)) - count_held<L>(p.refs, run, lane);
     bad = __syncthreads_or(bad);
     for (int s = tid; s < n && !bad; s += kThreads)
         if (sh.holders[s] > 1) {
@@ -377,29 +404,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicMin(&sh.first[at], s);
         }
     share_counts(sh.runs, mine, tid);  // (also: every CTA has read the lengths and the holders)
-    // pages needed in the low 40 bits, copies above; a thread has two consecutive sequences
-    unsigned long long own = 0;
-    for (int s = 2 * tid; s < 2 * tid + 2 && s < n && !bad; ++s) {
-        bool apart = false;
-        if (sh.holders[s] > 1) {
-            const int at = slot_of_page(sh, sh.page[s]);
-            apart = sh.writers[at] < sh.holders[s] || sh.first[at] != s;
+    // A thread has two consecutive sequences.
+    int need[2] = {0, 0}, copy[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = 2 * tid + i;
+        if (s < n && !bad) {
+            if (sh.holders[s] > 1) {
+                const int at = slot_of_page(sh, sh.page[s]);
+                copy[i] = sh.writers[at] < sh.holders[s] || sh.first[at] != s;
+            }
+            need[i] = sh.need[s] + copy[i];
         }
-        sh.need[s] += apart;
-        sh.holders[s] = apart ? 0 : -1;
-        own += sh.need[s] + (static_cast<unsigned long long>(apart) << 40);
     }
-    unsigned long long before = threads_before(sh, own, tid);
-    for (int s = 2 * tid; s < 2 * tid + 2 && s < n && !bad; ++s) {
-        sh.base[s] = static_cast<int>(before & ((1ull << 40) - 1));
-        const bool apart = sh.holders[s] == 0;
-        sh.holders[s] = apart ? static_cast<int>(before >> 40) : -1;
-        before += sh.need[s] + (static_cast<unsigned long long>(apart) << 40);
+    // (row starts are of 32 bits: no more than 2^28 pages and one per sequence)
+    int end = lanes_up_to(need[0] + need[1], lane), place = lanes_up_to(copy[0] + copy[1], lane);
+    if (lane == 31) {
+        sh.warp_need[warp] = end;
+        sh.warp_copies[warp] = place;
     }
     __syncthreads();
-    // (row starts are of 32 bits: no more than 2^28 pages and one per sequence)
-    const int needed = static_cast<int>(sh.total & ((1ull << 40) - 1));
-    const int num_free = counted(sh.runs);
+    const int others = sh.warp_need[lane], other_copies = sh.warp_copies[lane];
+    const int needed = warp_sum(others), num_copies = warp_sum(other_copies);
+    end += warp_sum(lane < warp ? others : 0);
+    place += warp_sum(lane < warp ? other_copies : 0) - copy[0] - copy[1];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = 2 * tid + i;
+        if (s < n && !bad) {
+            const Given g = {i == 0 ? end - need[1] : end, sh.had[s] - copy[i], copy[i] ? place : -1, sh.page[s]};
+            sh.given[s] = g;
+            place += copy[i];
+        }
+    }
+    __syncthreads();
+    const int num_free = counted(sh.runs, lane);
     const bool lead = cluster_rank() == 0;
     if (bad || needed > num_free) {
         if (lead && tid == 0) {
@@ -413,48 +452,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = tid; s < n; s += kThreads)
             p.kv_len[s] += row_start[s + 1] - row_start[s];
         if (tid == 0) {
-            counts[0] = static_cast<int>(sh.total >> 40);
+            counts[0] = num_copies;
             counts[1] = num_free - needed;
         }
     }
-    int rank = counted_before(sh.runs, tid >> 5);
-    for (int64_t at = run.first; at < run.last && rank < needed; at += kChunk) {
-        const int64_t page0 = at + 32 * lane;
-        uint32_t free = ~held_pages(p.refs, at, run.last, lane) & below(page0, run.last);
-        int all;
-        int r = rank + lanes_before(__popc(free), lane, &all);
-        rank += all;
-        if (!free || r >= needed)
-            continue;
-        // the last sequence whose pages begin at rank r or before; the next ones follow
-        int s = 0, end = n;
-        while (end - s > 1) {
-            const int mid = (s + end) / 2;
-            if (sh.base[mid] <= r)
-                s = mid;
-            else
-                end = mid;
-        }
-        int base = sh.base[s], next = base + sh.need[s];
-        for (; free && r < needed; free &= free - 1, ++r) {
-            const int page = static_cast<int>(page0) + __ffs(free) - 1;
-            while (r >= next) {
-                base = next;
-                next += sh.need[++s];
+    // A run's nibbles are dealt to L warps, so that no lane has more than 4 pages
+    // of a chunk to give.
+    for (int t = warp; t < kWarps * L; t += kWarps) {
+        const int number = run_of_warp(t / L), slice = t % L;
+        int rank = counted_before(sh.runs, number, lane);
+        if (rank >= needed)
+            break;
+        const Run r = run_at(length, number, p.num_pages);
+        for (int64_t at = r.first; at < r.last && rank < needed; at += chunk(L)) {
+            const uint32_t w = ~held_nibbles<L>(p.refs, at, r.last, lane) & nibbles_below<L>(at, r.last, lane);
+            const Ranks<L> ranks(w, lane);
+            int k = rank + ranks.at(slice);
+            rank += ranks.all();
+            unsigned free = w >> (4 * slice) & 15u;
+            if (!free || k >= needed)
+                continue;
+            // the first sequence whose pages end behind rank k; the next ones follow
+            int s = 0;
+            for (int hi = n - 1; s < hi;) {
+                const int mid = (s + hi) / 2;
+                if (sh.given[mid].end > k)
+                    hi = mid;
+                else
+                    s = mid + 1;
             }
-            const int copy = sh.holders[s];
-            if (copy >= 0 && r == base) {
-                copies[2 * copy] = sh.page[s];
-                copies[2 * copy + 1] = page;
-                atomicAdd(p.refs + sh.page[s], -1);
+            Given g = sh.given[s];
+            int begin = s > 0 ? sh.given[s - 1].end : 0;
+            for (; free && k < needed; free &= free - 1, ++k) {
+                const int page = static_cast<int>(at) + 128 * slice + 4 * lane + __ffs(free) - 1;
+                while (k >= g.end) {
+                    begin = g.end;
+                    g = sh.given[++s];
+                }
+                if (g.copy >= 0 && k == begin) {
+                    copies[2 * g.copy] = g.page;
+                    copies[2 * g.copy + 1] = page;
+                    atomicAdd(p.refs + g.page, -1);
+                }
+                p.page_table[(int64_t)s * p.table_stride + g.entry + (k - begin)] = page;
+                p.refs[page] = 1;
             }
-            p.page_table[(int64_t)s * p.table_stride + sh.had[s] + (r - base) - (copy >= 0)] = page;
-            p.refs[page] = 1;
         }
     }
 }
 
 // ---------------------------------------------------------------- compact
+
+constexpr int kBatch = 8;  // loads of a thread that are in flight together
 
 struct CompactShared {
     RunCounts runs;
@@ -468,37 +517,41 @@ struct CompactShared {
 // of a moved page in refs_out (which will be 0) says where it went.
 __device__ __forceinline__ int went_to(int page) { return -1 - page; }
 
+template <int L>
 __global__ void __launch_bounds__(kThreads, 1)
     compact_kernel(const smoe_page_pool p, int32_t *refs_out, int32_t *table_out, int32_t *copies,
                    int32_t *counts, int *status)
 {
     __shared__ CompactShared sh;
-    const int tid = threadIdx.x, lane = tid & 31, shift = log2_of(p.page_size);
-    const Runs run = run_of_warp(p.num_pages);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = log2_of(p.page_size);
+    const Run run = run_at(run_length<L>(p.num_pages), run_of_warp(warp), p.num_pages);
     cluster_arrive();
     if (tid == 0)
         sh.most = 0;
-    const int mine = count_held(p.refs, run, lane);
+    const int mine = count_held<L>(p.refs, run, lane);
     share_counts(sh.runs, mine, tid);
-    const int n = counted(sh.runs), before = counted_before(sh.runs, tid >> 5);
+    const int n = counted(sh.runs, lane), before = counted_before(sh.runs, run_of_warp(warp), lane);
     // The free pages below n, by their rank among the free.
-    int held_before = before;
-    for (int64_t at = run.first; at < run.last && at < n; at += kChunk) {
-        const int64_t page0 = at + 32 * lane;
-        const uint32_t in = below(page0, min(run.last, (int64_t)n));
-        const uint32_t held = held_pages(p.refs, at, run.last, lane) & in;
-        int all;
-        int64_t to = page0 - held_before - lanes_before(__popc(held), lane, &all);
-        held_before += all;
-        for (uint32_t free = ~held & in; free; free &= free - 1) {
-            const int i = __ffs(free) - 1;
-            copies[2 * (to + i - __popc(held & ((1u << i) - 1))) + 1] = static_cast<int>(page0) + i;
+    int64_t held_before = before;
+    for (int64_t at = run.first; at < run.last && at < n; at += chunk(L)) {
+        const uint32_t in = nibbles_below<L>(at, min(run.last, (int64_t)n), lane);
+        const uint32_t held = held_nibbles<L>(p.refs, at, run.last, lane) & in;
+        const Ranks<L> ranks(~held & in, lane);
+        const int64_t to = at - held_before;  // free pages before the chunk
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            int64_t k = to + ranks.at(i);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                if ((~held & in) >> (4 * i + d) & 1)
+                    copies[2 * k++ + 1] = static_cast<int>(at) + 128 * i + 4 * lane + d;
         }
+        held_before += warp_sum(__popc(held));
     }
     // The run that page n lies in (or the end of the last one) tells how many are held below n.
-    if (lane == 0 && run.first < run.last && n >= run.first && (n < run.last || run.last == p.num_pages))
-        for (unsigned r = 0; r < cluster_size(); ++r)
-            store_to_rank(&sh.under, r, held_before);
+    if (lane < static_cast<int>(cluster_size()) && run.first < run.last && n >= run.first &&
+        (n < run.last || run.last == p.num_pages))
+        store_to_rank(&sh.under, lane, static_cast<int>(held_before));
     for (int s = tid; s < p.num_seqs; s += kThreads) {
         const int len = p.kv_len[s];
         const bool ok = valid_len(p, len);
@@ -514,52 +567,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         counts[1] = n;
     }
     // The held pages from n on, by their rank.
-    int rank = max(before - sh.under, 0);
-    for (int64_t at = run.first; at < run.last; at += kChunk) {
-        if (at + kChunk <= n)
+    int64_t rank = max(before - sh.under, 0);
+    for (int64_t at = run.first; at < run.last; at += chunk(L)) {
+        if (at + chunk(L) <= n)
             continue;
-        const int64_t page0 = at + 32 * lane;
-        uint32_t held = held_pages(p.refs, at, run.last, lane) & ~below(page0, n);
-        int all;
-        int r = rank + lanes_before(__popc(held), lane, &all);
-        rank += all;
-        for (; held; held &= held - 1, ++r)
-            copies[2 * (int64_t)r] = static_cast<int>(page0) + __ffs(held) - 1;
+        const uint32_t held = held_nibbles<L>(p.refs, at, run.last, lane) & ~nibbles_below<L>(at, n, lane);
+        const Ranks<L> ranks(held, lane);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            int64_t k = rank + ranks.at(i);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                if (held >> (4 * i + d) & 1)
+                    copies[2 * k++] = static_cast<int>(at) + 128 * i + 4 * lane + d;
+        }
+        rank += ranks.all();
     }
     // What stays where it is (the free pages below n are written below).
     const int first = cluster_rank() * kThreads + tid, step = cluster_size() * kThreads;
+    const bool whole = (reinterpret_cast<uintptr_t>(refs_out) & 15) == 0;
     if (refs_out != p.refs)
-        for (int64_t q = first; q < p.num_pages; q += step) {
-            const int c = __ldcg(p.refs + q);
-            if (q >= n || c > 0)
-                refs_out[q] = q < n ? c : 0;
+        for (int64_t q0 = 4 * (int64_t)first; q0 < p.num_pages; q0 += 4 * kBatch * (int64_t)step) {
+            int4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                v[i] = refs_at(p.refs, q0 + 4 * i * (int64_t)step, p.num_pages);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t q = q0 + 4 * i * (int64_t)step;
+                const int c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                if (q >= n && q + 4 <= p.num_pages && whole) {
+                    *reinterpret_cast<int4 *>(refs_out + q) = make_int4(0, 0, 0, 0);
+                    continue;
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (q + d < p.num_pages && (q + d >= n || c[d] > 0))
+                        refs_out[q + d] = q + d < n ? c[d] : 0;
+            }
         }
     cluster_sync();
-    for (int i = first; i < moves; i += step) {
-        const int2 m = __ldcg(reinterpret_cast<const int2 *>(copies) + i);
-        refs_out[m.y] = __ldcg(p.refs + m.x);
-        refs_out[m.x] = went_to(m.y);
+    for (int i0 = first; i0 < moves; i0 += kBatch * step) {
+        int2 m[kBatch];
+        int c[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            m[i] = i0 + i * step < moves ? __ldcg(reinterpret_cast<const int2 *>(copies) + i0 + i * step) : make_int2(0, 0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            c[i] = __ldcg(p.refs + m[i].x);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i0 + i * step < moves) {
+                refs_out[m[i].y] = c[i];
+                refs_out[m[i].x] = went_to(m[i].y);
+            }
     }
     cluster_sync();
     // The tables: some columns of a row for each warp.
-    constexpr int kEach = 8;
-    const int warps = cluster_size() * kWarps, wide = (sh.most + 32 * kEach - 1) / (32 * kEach);
+    const int warps = cluster_size() * kWarps, wide = (sh.most + 32 * kBatch - 1) / (32 * kBatch);
     for (int u = cluster_rank() * kWarps + (tid >> 5); u < wide * p.num_seqs; u += warps) {
         const int s = u % p.num_seqs, pages = sh.pages[s];
-        const int j0 = u / p.num_seqs * 32 * kEach + lane;
+        const int j0 = u / p.num_seqs * 32 * kBatch + lane;
         const int64_t row = (int64_t)s * p.table_stride;
-        int page[kEach], to[kEach];
+        int page[kBatch], to[kBatch];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < kBatch; ++i)
             page[i] = j0 + 32 * i < pages ? p.page_table[row + j0 + 32 * i] : 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
             to[i] = -1;
             if (page[i] >= n && page[i] < p.num_pages)
                 to[i] = __ldcg(refs_out + page[i]);
         }
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
             if (j0 + 32 * i >= pages)
                 continue;
             int now = page[i];
@@ -572,8 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     cluster_sync();
-    for (int i = first; i < moves; i += step)
-        refs_out[__ldcg(copies + 2 * (int64_t)i)] = 0;
+    for (int i0 = first; i0 < moves; i0 += kBatch * step) {
+        int from[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            from[i] = i0 + i * step < moves ? __ldcg(copies + 2 * (int64_t)(i0 + i * step)) : -1;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (from[i] >= 0)
+                refs_out[from[i]] = 0;
+    }
 }
 
 // ------------------------------------------------------------------- copy
@@ -634,10 +724,9 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 // One cluster of at most kMaxCluster CTAs.
 template <class... Params, class... Args>
-cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const DeviceFacts &dev, cudaStream_t stream,
-                           Args... args)
+cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const DeviceFacts &dev,
+                           std::atomic<bool> *allowed, cudaStream_t stream, Args... args)
 {
-    static std::atomic<bool> allowed[kMaxDeviceIndex];  // (of each kernel: they differ in their parameters)
     if (!allowed[dev.index].load(std::memory_order_acquire)) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess && smem > 0)
@@ -669,28 +758,46 @@ int cluster_for(int64_t n)
     return c;
 }
 
+// Pools that one cluster goes over in chunks of 128 pages at once.
+constexpr int kSmallPool = kMaxCluster * kWarps * chunk(1);
+bool small_pool(const smoe_page_pool &p) { return p.num_pages <= kSmallPool; }
+int pool_cluster(const smoe_page_pool &p)
+{
+    const int64_t pages = p.num_pages / (kWarps * chunk(1)), entries = (int64_t)p.num_seqs * p.table_stride / 8192;
+    return cluster_for(pages > entries ? pages : entries);
+}
+
 }  // namespace
 
 cudaError_t launch_pages_fork(const smoe_page_pool &p, const int32_t *parent, const int32_t *keep,
                               const DeviceFacts &dev, cudaStream_t stream)
 {
     const int64_t entries = (int64_t)p.num_seqs * p.table_stride;
-    return launch_cluster(fork_kernel, cluster_for(entries / 4096), 0, dev, stream, p, parent, keep, dev.status);
+    static std::atomic<bool> allowed[kMaxDeviceIndex];
+    return launch_cluster(fork_kernel, cluster_for(entries / 4096), 0, dev, allowed, stream, p, parent, keep,
+                          dev.status);
 }
 
 cudaError_t launch_pages_reserve(const smoe_page_pool &p, const int32_t *row_start, int32_t *copies,
                                  int32_t *counts, const DeviceFacts &dev, cudaStream_t stream)
 {
-    return launch_cluster(reserve_kernel, cluster_for(p.num_pages / 8192), sizeof(ReserveShared), dev, stream, p,
-                          row_start, copies, counts, dev.status);
+    const auto go = [&](auto *kernel, std::atomic<bool> *allowed) {
+        return launch_cluster(kernel, pool_cluster(p), sizeof(ReserveShared), dev, allowed, stream, p, row_start, copies,
+                              counts, dev.status);
+    };
+    static std::atomic<bool> allowed[2][kMaxDeviceIndex];
+    return small_pool(p) ? go(reserve_kernel<1>, allowed[0]) : go(reserve_kernel<8>, allowed[1]);
 }
 
 cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int32_t *table_out, int32_t *copies,
                                  int32_t *counts, const DeviceFacts &dev, cudaStream_t stream)
 {
-    const int64_t work = p.num_pages / 8192 + (int64_t)p.num_seqs * p.table_stride / 8192;
-    return launch_cluster(compact_kernel, cluster_for(work), 0, dev, stream, p, refs_out, table_out, copies, counts,
-                          dev.status);
+    const auto go = [&](auto *kernel, std::atomic<bool> *allowed) {
+        return launch_cluster(kernel, pool_cluster(p), 0, dev, allowed, stream, p, refs_out, table_out, copies, counts,
+                              dev.status);
+    };
+    static std::atomic<bool> allowed[2][kMaxDeviceIndex];
+    return small_pool(p) ? go(compact_kernel<1>, allowed[0]) : go(compact_kernel<8>, allowed[1]);
 }
 
 cudaError_t launch_pages_copy(const smoe_kv_cache *caches, int num_caches, const int32_t *copies,

@@ -791,8 +791,8 @@ typedef struct {
  * place; pages are shared, not copied, and refs follows.  keep below 0 counts
  * as 0.  A parent outside -1 .. num_seqs - 1 and a length that is negative or
  * past its row are recorded (SMOE_ERR_DEVICE_FAULT from
- * smoe_get_device_status) and then nothing changes; an entry that names no
- * page of the pool is recorded and not counted.
+ * smoe_get_device_status) and then nothing changes; an entry that comes or goes
+ * and names no page of the pool is recorded and not counted.
  *   parent  [num_seqs]       keep  nullable [num_seqs]
  * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_UNSUPPORTED (device), SMOE_ERR_CUDA. */
 smoe_status smoe_pages_fork(const smoe_page_pool *pool, const int32_t *parent, const int32_t *keep,
