@@ -255,6 +255,23 @@ __device__ __forceinline__ uint4 load_word(const Part &p, int w)
     return load_word<F32>(p.base, p.first, p.vocab, w, p.w1);
 }
 
+// A thread's words of the step that begins at word w.  Where all of the step's
+// words are the row's, which is so but for its first and last ones, the loads
+// are not under conditions, which would make them wait for one another.
+template <bool F32>
+__device__ __forceinline__ void load_step(uint4 (&v)[kWords], const Part &p, int w, int tid)
+{
+    if (w + kStepWords <= p.w1 && w * kPer<F32> >= p.first && (w + kStepWords) * kPer<F32> <= p.first + p.vocab) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            v[i] = __ldcs(reinterpret_cast<const uint4 *>(p.base) + w + kThreads * i + tid);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            v[i] = load_word<F32>(p, w + kThreads * i + tid);
+    }
+}
+
 // Sum over the CTA, in every thread.
 __device__ __forceinline__ int sum_over_cta(PartShared &sh, int v, int tid)
 {
@@ -428,11 +445,9 @@ __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int pa
     p.w0 = part * b.part_words;
     p.w1 = min(p.w0 + b.part_words, (p.first + a.vocab + kP - 1) / kP);
     p.steps = max(0, p.w1 - p.w0 + kStepWords - 1) / kStepWords;
-    int w = p.w0 + tid;
+    int w = p.w0;
     uint4 next[kWords];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-        next[i] = load_word<F32>(p, w + kThreads * i);
+    load_step<F32>(next, p, w, tid);
     // (the first words are on their way while the beam's state is looked up)
     if (state_of(a, row) != kLive)
         return;
@@ -443,11 +458,8 @@ __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int pa
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
             v[i] = next[i];
-        if (step + 1 < p.steps) {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                next[i] = load_word<F32>(p, w + kStepWords + kThreads * i);
-        }
+        if (step + 1 < p.steps)
+            load_step<F32>(next, p, w + kStepWords, tid);
         const float most = fminf(largest<F32>(v, kWords), FLT_MAX);
         sh.most[step][tid] = most;
         top = fmaxf(top, most);
@@ -743,14 +755,15 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
     Key first[kFirst];
 #pragma unroll
     for (int j = 0; j < kFirst; ++j)
-        first[j] = tid + j * kThreads < all ? __ldcg(group_keys + tid + j * kThreads) : 0;
+        first[j] = __ldcg(group_keys + min(tid + j * kThreads, all - 1));
     bool again = false;
     for (int k = warp; k < a.beams; k += kWarps) {
         const float2 *stats = b.stats + (row0 + k) * P;
         const Key *keys = group_keys + k * per;
         const float score = a.scores[row0 + k];
         const int state = state_of(a, row0 + k);
-        const Key sample = lane < each ? __ldcg(keys + lane / depth * N + lane % depth) : 0;
+        const int at = min(lane, each - 1);
+        const Key sample = __ldcg(keys + at / depth * N + at % depth);
         Key top = 0;
         Two sum = {0.0f, 0.0f};
         float ref = -kMaxRef;

@@ -40,21 +40,34 @@ __device__ __forceinline__ bool valid_len(const smoe_page_pool &p, int len)
 // new (whole numbers: the order of the additions does not matter).  Beams share
 // most of their pages, and entries that stay the same cost two reads only.
 //
-// A tile is a row's 32 columns to a warp (16 or 8 of two or four rows where
-// there are many sequences, so that kForkRows of a thread are all of them).
-constexpr int kForkRows = 16;
-constexpr int kNone = -0x7fffffff - 1;
-static_assert(kForkRows * kWarps * 4 >= SMOE_MAX_SEQS, "tiles of 8 columns hold all sequences");
+// The rows that may change are listed; of a tile of columns, their entries as
+// they were and those of their parents come to shared memory together, by
+// cp.async.
+constexpr int kForkBytes = 96 << 10;  // of both, unless 8 columns take more
 
 struct ForkRow {
-    int parent, was, now;  // pages
-    int len;               // keys
+    int seq, parent, was, now;  // pages
 };
 
 struct ForkShared {
     ForkRow row[SMOE_MAX_SEQS];
-    int most;  // pages of the longest sequence
+    int len[SMOE_MAX_SEQS];
+    int rows, most;  // rows listed, pages of the longest of them
 };
+
+// Columns of a tile (its logarithm).
+__host__ __device__ inline int fork_columns(int num_seqs)
+{
+    int shift = 3;
+    while (shift < 9 && (8 * num_seqs << (shift + 1)) <= kForkBytes)
+        ++shift;
+    return shift;
+}
+
+__device__ __forceinline__ void copy_word(int *to, const int32_t *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
 
 __device__ __forceinline__ void add_holder(const smoe_page_pool &p, int page, int by, int *status)
 {
@@ -68,22 +81,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     fork_kernel(const smoe_page_pool p, const int32_t *parent, const int32_t *keep, int *status)
 {
     __shared__ ForkShared sh;
-    const int tid = threadIdx.x, lane = tid & 31, n = p.num_seqs, shift = log2_of(p.page_size);
-    bool bad = false;
-    int most = 0, cut[2];  // a thread has sequences tid and tid + kThreads
+    extern __shared__ __align__(16) int s_entries[];
+    const int tid = threadIdx.x, n = p.num_seqs, shift = log2_of(p.page_size);
     if (tid == 0)
-        sh.most = 0;
+        sh.rows = sh.most = 0;
+    bool bad = false;
+    int from_seq[2], was[2], len[2];  // a thread has sequences tid and tid + kThreads
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int s = tid + i * kThreads;
         if (s >= n)
             continue;
-        const int a = parent[s], len = p.kv_len[s];
-        cut[i] = keep ? max(keep[s], 0) : 0x7fffffff;
-        const bool ok = a >= -1 && a < n && valid_len(p, len);
-        bad = bad || !ok;
-        sh.row[s] = {a, ok ? pages_of(len, shift) : 0, 0, len};
-        most = max(most, sh.row[s].was);
+        from_seq[i] = parent[s];
+        was[i] = p.kv_len[s];
+        len[i] = keep ? max(keep[s], 0) : 0x7fffffff;
+        sh.len[s] = was[i];
+        bad = bad || from_seq[i] < -1 || from_seq[i] >= n || !valid_len(p, was[i]);
     }
     // (the same answer in every CTA: none of the arrays has been written yet)
     if (__syncthreads_or(bad)) {
@@ -92,52 +105,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     cluster_arrive();  // this CTA has read every length
-    int len[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int s = tid + i * kThreads;
         if (s >= n)
             continue;
-        const int a = sh.row[s].parent;
-        len[i] = a < 0 ? 0 : min(sh.row[a].len, cut[i]);
-        sh.row[s].now = pages_of(len[i], shift);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0)
-        atomicMax(&sh.most, most);
-    __syncthreads();
-    most = sh.most;
-    const int wshift = n <= kForkRows * kWarps ? 5 : n <= 2 * kForkRows * kWarps ? 4 : 3;
-    const int width = 1 << wshift, rows = kThreads >> wshift;  // of the CTA at a time
-    const int s0 = tid >> wshift;
-    for (int j0 = cluster_rank() * width; j0 < most; j0 += cluster_size() * width) {
-        const int j = j0 + (tid & (width - 1));
-        int from[kForkRows], to[kForkRows];  // the entry as it was and as it will be, or kNone
-#pragma unroll
-        for (int i = 0; i < kForkRows; ++i) {
-            const int s = s0 + i * rows;
-            from[i] = to[i] = kNone;
-            if (s >= n)
-                continue;
-            const ForkRow r = sh.row[s];
-            const bool comes = r.parent != s && j < r.now;
-            if (j < r.was && (r.parent != s || j >= r.now))
-                from[i] = max(p.page_table[(int64_t)s * p.table_stride + j], kNone + 1);
-            if (comes)
-                to[i] = max(p.page_table[(int64_t)r.parent * p.table_stride + j], kNone + 1);
+        len[i] = from_seq[i] < 0 ? 0 : min(sh.len[from_seq[i]], len[i]);
+        const ForkRow r = {s, from_seq[i], pages_of(was[i], shift), pages_of(len[i], shift)};
+        if (r.parent != s ? r.was + r.now > 0 : r.was > r.now) {
+            sh.row[atomicAdd(&sh.rows, 1)] = r;
+            atomicMax(&sh.most, max(r.was, r.now));
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kForkRows; ++i) {
-            if (from[i] == to[i])
+    }
+    __syncthreads();
+    const int most = sh.most, wshift = fork_columns(n), width = 1 << wshift, entries = sh.rows << wshift;
+    int *before = s_entries, *after = s_entries + (n << wshift);
+    for (int j0 = cluster_rank() * width; j0 < most; j0 += cluster_size() * width) {
+        for (int e = tid; e < entries; e += kThreads) {
+            const ForkRow r = sh.row[e >> wshift];
+            const int j = j0 + (e & (width - 1));
+            if (j >= r.was && j >= r.now)
                 continue;
-            if (from[i] != kNone)
-                add_holder(p, from[i], -1, status);
-            if (to[i] != kNone) {
-                add_holder(p, to[i], 1, status);
-                p.page_table[(int64_t)(s0 + i * rows) * p.table_stride + j] = to[i];
+            if (j < r.was && (r.parent != r.seq || j >= r.now))
+                copy_word(before + e, p.page_table + (int64_t)r.seq * p.table_stride + j);
+            if (j < r.now && r.parent != r.seq)
+                copy_word(after + e, p.page_table + (int64_t)r.parent * p.table_stride + j);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();  // (every thread's entries are here, and nothing of these columns is written yet)
+        for (int e = tid; e < entries; e += kThreads) {
+            const ForkRow r = sh.row[e >> wshift];
+            const int j = j0 + (e & (width - 1));
+            const bool goes = j < r.was && (r.parent != r.seq || j >= r.now), comes = j < r.now && r.parent != r.seq;
+            if (!goes && !comes)
+                continue;
+            const int from = before[e], to = after[e];
+            if (goes && comes && from == to)
+                continue;
+            if (goes)
+                add_holder(p, from, -1, status);
+            if (comes) {
+                add_holder(p, to, 1, status);
+                p.page_table[(int64_t)r.seq * p.table_stride + j] = to;
             }
         }
+        __syncthreads();
     }
     cluster_wait();
     if (cluster_rank() == 0)
@@ -196,9 +208,15 @@ template <int L>
 __device__ __forceinline__ uint32_t held_nibbles(const int32_t *refs, int64_t at, int64_t last, int lane)
 {
     int4 v[L];
+    if (at + chunk(L) <= last) {  // (loads under conditions of their own would wait for one another)
 #pragma unroll
-    for (int i = 0; i < L; ++i)
-        v[i] = refs_at(refs, at + 128 * i + 4 * lane, last);
+        for (int i = 0; i < L; ++i)
+            v[i] = __ldcg(reinterpret_cast<const int4 *>(refs + at) + 32 * i + lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            v[i] = refs_at(refs, at + 128 * i + 4 * lane, last);
+    }
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < L; ++i)
@@ -248,19 +266,15 @@ struct Ranks {
     // Set pages before nibble i's first one of this lane.
     __device__ __forceinline__ int at(int i) const
     {
-        int n = before[i / 4] >> (8 * (i & 3)) & 255u;
-#pragma unroll
-        for (int j = 0; j < L; ++j)
-            n += j < i ? static_cast<int>(total[j / 4] >> (8 * (j & 3)) & 255u) : 0;
-        return n;
+        const uint32_t low = i < 4 ? (1u << (8 * i)) - 1u : 0xffffffffu;
+        const unsigned lanes = (L > 4 && i >= 4 ? before[1] : before[0]) >> (8 * (i & 3)) & 255u;
+        const unsigned n = __dp4a(total[0] & low, 0x01010101u, lanes);
+        return L > 4 && i > 4 ? __dp4a(total[1] & ((1u << (8 * (i - 4))) - 1u), 0x01010101u, n) : n;
     }
     __device__ __forceinline__ int all() const
     {
-        int n = 0;
-#pragma unroll
-        for (int j = 0; j < L; ++j)
-            n += total[j / 4] >> (8 * (j & 3)) & 255u;
-        return n;
+        const unsigned n = __dp4a(total[0], 0x01010101u, 0u);
+        return L > 4 ? __dp4a(total[1], 0x01010101u, n) : n;
     }
 };
 
@@ -374,28 +388,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.writers[i] = 0;
         sh.first[i] = 0x7fffffff;
     }
-    for (int s = tid; s < n; s += kThreads) {
+    // A thread has sequences tid and tid + kThreads.  Their lengths, last pages
+    // and those pages' holders come one after the other; the pool is counted meanwhile.
+    int had[2], page[2], new_pages[2], holders[2], grown[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = tid + i * kThreads;
+        had[i] = new_pages[i] = holders[i] = grown[i] = 0;
+        page[i] = -1;
+        if (s >= n)
+            continue;
         const int len = p.kv_len[s];
         const int64_t rows = (int64_t)row_start[s + 1] - row_start[s];
-        int had = 0, need = 0, page = -1, holders = 0;
         if (!valid_len(p, len) || rows < 0 || rows > kMaxKeys - len || !valid_len(p, len + static_cast<int>(rows))) {
             bad = true;
-        } else {
-            had = pages_of(len, shift);
-            need = pages_of(len + static_cast<int>(rows), shift) - had;
-            if (rows > 0 && (len & (p.page_size - 1))) {
-                page = p.page_table[(int64_t)s * p.table_stride + had - 1];
-                if (page >= 0 && page < p.num_pages)
-                    holders = __ldcg(p.refs + page);
-                bad = bad || holders <= 0;
-            }
+            continue;
         }
-        sh.had[s] = had;
-        sh.need[s] = need;
-        sh.page[s] = page;
-        sh.holders[s] = holders;
+        grown[i] = len + static_cast<int>(rows);
+        had[i] = pages_of(len, shift);
+        new_pages[i] = pages_of(len + static_cast<int>(rows), shift) - had[i];
+        if (rows > 0 && (len & (p.page_size - 1))) {
+            page[i] = __ldcg(p.page_table + (int64_t)s * p.table_stride + had[i] - 1);
+            holders[i] = -1;  // (to be looked up)
+        }
     }
     const int mine = static_cast<int>(max(run.last - run.first, (int64_t)0)) - count_held<L>(p.refs, run, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (holders[i] < 0 && page[i] >= 0 && page[i] < p.num_pages)
+            holders[i] = __ldcg(p.refs + page[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = tid + i * kThreads;
+        if (s >= n)
+            continue;
+        bad = bad || holders[i] < 0 || (page[i] >= 0 && holders[i] == 0);
+        sh.had[s] = had[i];
+        sh.need[s] = new_pages[i];
+        sh.page[s] = page[i];
+        sh.holders[s] = holders[i];
+    }
     bad = __syncthreads_or(bad);
     for (int s = tid; s < n && !bad; s += kThreads)
         if (sh.holders[s] > 1) {
@@ -449,8 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (lead) {
-        for (int s = tid; s < n; s += kThreads)
-            p.kv_len[s] += row_start[s + 1] - row_start[s];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (tid + i * kThreads < n)
+                p.kv_len[tid + i * kThreads] = grown[i];
         if (tid == 0) {
             counts[0] = num_copies;
             counts[1] = num_free - needed;
@@ -503,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- compact
 
-constexpr int kBatch = 8;  // loads of a thread that are in flight together
+constexpr int kBatch = 4;  // loads of a thread that are in flight together
 
 struct CompactShared {
     RunCounts runs;
@@ -583,27 +617,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         rank += ranks.all();
     }
-    // What stays where it is (the free pages below n are written below).
+    // What stays where it is (of the free pages below n the moves are told afterwards).
     const int first = cluster_rank() * kThreads + tid, step = cluster_size() * kThreads;
     const bool whole = (reinterpret_cast<uintptr_t>(refs_out) & 15) == 0;
     if (refs_out != p.refs)
         for (int64_t q0 = 4 * (int64_t)first; q0 < p.num_pages; q0 += 4 * kBatch * (int64_t)step) {
             int4 v[kBatch];
+            if (q0 + 4 * ((kBatch - 1) * (int64_t)step + 1) <= p.num_pages) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                v[i] = refs_at(p.refs, q0 + 4 * i * (int64_t)step, p.num_pages);
+                for (int i = 0; i < kBatch; ++i)
+                    v[i] = __ldcg(reinterpret_cast<const int4 *>(p.refs + q0) + i * (int64_t)step);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    v[i] = refs_at(p.refs, q0 + 4 * i * (int64_t)step, p.num_pages);
+            }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int64_t q = q0 + 4 * i * (int64_t)step;
-                const int c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                if (q >= n && q + 4 <= p.num_pages && whole) {
-                    *reinterpret_cast<int4 *>(refs_out + q) = make_int4(0, 0, 0, 0);
-                    continue;
-                }
+                const int m = static_cast<int>(min(max(n - q, (int64_t)0), (int64_t)4));  // of them below n
+                v[i] = make_int4(m > 0 ? v[i].x : 0, m > 1 ? v[i].y : 0, m > 2 ? v[i].z : 0, m > 3 ? v[i].w : 0);
+                if (whole && q + 4 <= p.num_pages) {
+                    *reinterpret_cast<int4 *>(refs_out + q) = v[i];
+                } else {
+                    const int c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    if (q + d < p.num_pages && (q + d >= n || c[d] > 0))
-                        refs_out[q + d] = q + d < n ? c[d] : 0;
+                    for (int d = 0; d < 4; ++d)
+                        if (q + d < p.num_pages)
+                            refs_out[q + d] = c[d];
+                }
             }
         }
     cluster_sync();
@@ -612,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int c[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            m[i] = i0 + i * step < moves ? __ldcg(reinterpret_cast<const int2 *>(copies) + i0 + i * step) : make_int2(0, 0);
+            m[i] = __ldcg(reinterpret_cast<const int2 *>(copies) + min(i0 + i * step, moves - 1));
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             c[i] = __ldcg(p.refs + m[i].x);
@@ -629,26 +671,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = cluster_rank() * kWarps + (tid >> 5); u < wide * p.num_seqs; u += warps) {
         const int s = u % p.num_seqs, pages = sh.pages[s];
         const int j0 = u / p.num_seqs * 32 * kBatch + lane;
+        if (j0 - lane >= pages)
+            continue;
         const int64_t row = (int64_t)s * p.table_stride;
         int page[kBatch], to[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            page[i] = j0 + 32 * i < pages ? p.page_table[row + j0 + 32 * i] : 0;
+            page[i] = __ldcg(p.page_table + row + (j0 + 32 * i < pages ? j0 + 32 * i : 0));
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            to[i] = -1;
-            if (page[i] >= n && page[i] < p.num_pages)
-                to[i] = __ldcg(refs_out + page[i]);
-        }
+        for (int i = 0; i < kBatch; ++i)
+            to[i] = __ldcg(refs_out + (page[i] >= n && page[i] < p.num_pages ? page[i] : 0));
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             if (j0 + 32 * i >= pages)
                 continue;
-            int now = page[i];
-            if (now < 0 || now >= p.num_pages || (now >= n && to[i] >= 0))
+            const bool above = page[i] >= n && page[i] < p.num_pages, went = above && to[i] < 0;
+            if (page[i] < 0 || page[i] >= p.num_pages || (above && !went))
                 set_status(status, kStatusBadArg);
-            else if (now >= n)
-                now = went_to(to[i]);
+            const int now = went ? went_to(to[i]) : page[i];
             if (now != page[i] || table_out != p.page_table)
                 table_out[row + j0 + 32 * i] = now;
         }
@@ -658,11 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int from[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            from[i] = i0 + i * step < moves ? __ldcg(copies + 2 * (int64_t)(i0 + i * step)) : -1;
+            from[i] = __ldcg(copies + 2 * (int64_t)min(i0 + i * step, moves - 1));
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            if (from[i] >= 0)
-                refs_out[from[i]] = 0;
+            refs_out[from[i]] = 0;  // (the last one more than once)
     }
 }
 
@@ -707,20 +746,20 @@ __global__ void __launch_bounds__(kCopyThreads)
         const int end = min((unit + 1) * kUnitWords, a.page_words);
         constexpr int kEach = kUnitWords / kCopyThreads;
         uint4 w[kEach];
+        const int first = unit * kUnitWords + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int at = unit * kUnitWords + k * kCopyThreads + threadIdx.x;
-            if (at < end)
-                w[k] = __ldcs(src + at);
-        }
+        for (int k = 0; k < kEach; ++k)
+            w[k] = __ldcs(src + min(first + k * kCopyThreads, end - 1));
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            const int at = unit * kUnitWords + k * kCopyThreads + threadIdx.x;
-            if (at < end)
-                dst[at] = w[k];
-        }
+        for (int k = 0; k < kEach; ++k)
+            if (first + k * kCopyThreads < end)
+                dst[first + k * kCopyThreads] = w[k];
     }
 }
+
+// Dynamic shared memory of a CTA at most (fork: 8 columns of SMOE_MAX_SEQS rows).
+constexpr int kMaxSmem = 64 * SMOE_MAX_SEQS;
+static_assert(kForkBytes <= kMaxSmem && sizeof(ReserveShared) <= kMaxSmem, "shared memory");
 
 // One cluster of at most kMaxCluster CTAs.
 template <class... Params, class... Args>
@@ -729,8 +768,8 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const 
 {
     if (!allowed[dev.index].load(std::memory_order_acquire)) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess && smem > 0)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess)
             return e;
         allowed[dev.index].store(true, std::memory_order_release);
@@ -774,7 +813,8 @@ cudaError_t launch_pages_fork(const smoe_page_pool &p, const int32_t *parent, co
 {
     const int64_t entries = (int64_t)p.num_seqs * p.table_stride;
     static std::atomic<bool> allowed[kMaxDeviceIndex];
-    return launch_cluster(fork_kernel, cluster_for(entries / 4096), 0, dev, allowed, stream, p, parent, keep,
+    const int smem = 8 * p.num_seqs << fork_columns(p.num_seqs);
+    return launch_cluster(fork_kernel, cluster_for(entries / 4096), smem, dev, allowed, stream, p, parent, keep,
                           dev.status);
 }
 
