@@ -240,6 +240,17 @@ __device__ __forceinline__ uint32_t nibbles_below(int64_t at, int64_t end, int l
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
+// The lanes' v up to this one.
+__device__ __forceinline__ int lanes_up_to(int v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        v += lane >= o ? y : 0;
+    }
+    return v;
+}
+
 // Where the set pages of a chunk stand among themselves, in the order of the
 // pages: those of each nibble's word (32 lanes) one after the other.
 template <int L>
@@ -253,12 +264,7 @@ struct Ranks {
 #pragma unroll
             for (int i = 4 * h; i < L && i < 4 * h + 4; ++i)
                 own |= static_cast<uint32_t>(__popc(w >> (4 * i) & 15u)) << (8 * (i & 3));
-            uint32_t x = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-                x += lane >= o ? y : 0;
-            }
+            const uint32_t x = lanes_up_to(own, lane);
             before[h] = x - own;
             total[h] = __shfl_sync(0xffffffffu, x, 31);
         }
@@ -329,12 +335,12 @@ __device__ __forceinline__ int counted(const RunCounts &rc, int lane)
 // the number needed looks up whose it is.
 constexpr int kSlots = 2 * SMOE_MAX_SEQS;  // of the table of shared last pages
 
-// What a sequence gets, as the ranks' owners look it up.
+// What a sequence gets, for those that get any.
 struct Given {
     int end;    // free pages given to the sequences up to it
+    int seq;
     int entry;  // of its row: the first one's
     int copy;   // the place of its copy in the list, -1: none
-    int page;   // the page that is copied
 };
 
 struct ReserveShared {
@@ -347,17 +353,6 @@ struct ReserveShared {
     int key[kSlots], writers[kSlots], first[kSlots];
     int warp_need[kWarps], warp_copies[kWarps];
 };
-
-// The lanes' v up to this one.
-__device__ __forceinline__ int lanes_up_to(int v, int lane)
-{
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
-        v += lane >= o ? y : 0;
-    }
-    return v;
-}
 
 __device__ __forceinline__ int slot_of_page(ReserveShared &sh, int page)
 {
@@ -450,23 +445,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     // (row starts are of 32 bits: no more than 2^28 pages and one per sequence)
-    int end = lanes_up_to(need[0] + need[1], lane), place = lanes_up_to(copy[0] + copy[1], lane);
+    // (copies, and above them in the same words, sequences that get pages)
+    const int own = copy[0] + copy[1] + ((need[0] > 0) + (need[1] > 0) << 16);
+    int end = lanes_up_to(need[0] + need[1], lane), place = lanes_up_to(own, lane);
     if (lane == 31) {
         sh.warp_need[warp] = end;
         sh.warp_copies[warp] = place;
     }
     __syncthreads();
     const int others = sh.warp_need[lane], other_copies = sh.warp_copies[lane];
-    const int needed = warp_sum(others), num_copies = warp_sum(other_copies);
+    const int needed = warp_sum(others), counted_all = warp_sum(other_copies);
+    const int num_copies = counted_all & 0xffff, num_given = counted_all >> 16;
     end += warp_sum(lane < warp ? others : 0);
-    place += warp_sum(lane < warp ? other_copies : 0) - copy[0] - copy[1];
+    place += warp_sum(lane < warp ? other_copies : 0) - own;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int s = 2 * tid + i;
-        if (s < n && !bad) {
-            const Given g = {i == 0 ? end - need[1] : end, sh.had[s] - copy[i], copy[i] ? place : -1, sh.page[s]};
-            sh.given[s] = g;
-            place += copy[i];
+        if (need[i] > 0) {
+            sh.given[place >> 16] = {i == 0 ? end - need[1] : end, s, sh.had[s] - copy[i],
+                                     copy[i] ? place & 0xffff : -1};
+            place += copy[i] + (1 << 16);
         }
     }
     __syncthreads();
@@ -507,28 +505,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!free || k >= needed)
                 continue;
             // the first sequence whose pages end behind rank k; the next ones follow
-            int s = 0;
-            for (int hi = n - 1; s < hi;) {
-                const int mid = (s + hi) / 2;
+            int at_given = 0;
+            for (int hi = num_given - 1; at_given < hi;) {
+                const int mid = (at_given + hi) / 2;
                 if (sh.given[mid].end > k)
                     hi = mid;
                 else
-                    s = mid + 1;
+                    at_given = mid + 1;
             }
-            Given g = sh.given[s];
-            int begin = s > 0 ? sh.given[s - 1].end : 0;
+            Given g = sh.given[at_given];
+            int begin = at_given > 0 ? sh.given[at_given - 1].end : 0;
             for (; free && k < needed; free &= free - 1, ++k) {
                 const int page = static_cast<int>(at) + 128 * slice + 4 * lane + __ffs(free) - 1;
-                while (k >= g.end) {
+                if (k >= g.end) {
                     begin = g.end;
-                    g = sh.given[++s];
+                    g = sh.given[++at_given];
                 }
                 if (g.copy >= 0 && k == begin) {
-                    copies[2 * g.copy] = g.page;
+                    const int old = sh.page[g.seq];
+                    copies[2 * g.copy] = old;
                     copies[2 * g.copy + 1] = page;
-                    atomicAdd(p.refs + g.page, -1);
+                    atomicAdd(p.refs + old, -1);
                 }
-                p.page_table[(int64_t)s * p.table_stride + g.entry + (k - begin)] = page;
+                p.page_table[(int64_t)g.seq * p.table_stride + g.entry + (k - begin)] = page;
                 p.refs[page] = 1;
             }
         }
@@ -538,12 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- compact
 
 constexpr int kBatch = 4;  // loads of a thread that are in flight together
+constexpr int kColumns = 128;
 
 struct CompactShared {
     RunCounts runs;
     int under;                 // held pages below n
-    int most;                  // pages of the longest sequence
     int pages[SMOE_MAX_SEQS];  // of each one
+    int chunks[SMOE_MAX_SEQS]; // of kColumns entries, of the sequences up to it
+    int warp[kWarps];
 };
 
 // The two ends of the moves are found by rank, each for itself; then the moves
@@ -560,8 +561,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = log2_of(p.page_size);
     const Run run = run_at(run_length<L>(p.num_pages), run_of_warp(warp), p.num_pages);
     cluster_arrive();
-    if (tid == 0)
-        sh.most = 0;
     const int mine = count_held<L>(p.refs, run, lane);
     share_counts(sh.runs, mine, tid);
     const int n = counted(sh.runs, lane), before = counted_before(sh.runs, run_of_warp(warp), lane);
@@ -574,11 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t to = at - held_before;  // free pages before the chunk
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            int64_t k = to + ranks.at(i);
+            int32_t *k = copies + 2 * (to + ranks.at(i)) + 1;
 #pragma unroll
             for (int d = 0; d < 4; ++d)
-                if ((~held & in) >> (4 * i + d) & 1)
-                    copies[2 * k++ + 1] = static_cast<int>(at) + 128 * i + 4 * lane + d;
+                if ((~held & in) >> (4 * i + d) & 1) {
+                    *k = static_cast<int>(at) + 128 * i + 4 * lane + d;
+                    k += 2;
+                }
         }
         held_before += warp_sum(__popc(held));
     }
@@ -586,14 +587,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane < static_cast<int>(cluster_size()) && run.first < run.last && n >= run.first &&
         (n < run.last || run.last == p.num_pages))
         store_to_rank(&sh.under, lane, static_cast<int>(held_before));
-    for (int s = tid; s < p.num_seqs; s += kThreads) {
+    // A thread has two consecutive sequences.
+    int chunks[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = 2 * tid + i;
+        if (s >= p.num_seqs)
+            continue;
         const int len = p.kv_len[s];
         const bool ok = valid_len(p, len);
-        sh.pages[s] = ok ? pages_of(len, shift) : 0;
         if (!ok)
             set_status(status, kStatusBadArg);
-        atomicMax(&sh.most, sh.pages[s]);
+        sh.pages[s] = ok ? pages_of(len, shift) : 0;
+        chunks[i] = (sh.pages[s] + kColumns - 1) / kColumns;
     }
+    int end = lanes_up_to(chunks[0] + chunks[1], lane);
+    if (lane == 31)
+        sh.warp[warp] = end;
+    __syncthreads();
+    end += warp_sum(lane < warp ? sh.warp[lane] : 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (2 * tid + i < p.num_seqs)
+            sh.chunks[2 * tid + i] = i == 0 ? end - chunks[1] : end;
     cluster_sync();
     const int moves = n - sh.under;
     if (cluster_rank() == 0 && tid == 0) {
@@ -609,11 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Ranks<L> ranks(held, lane);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            int64_t k = rank + ranks.at(i);
+            int32_t *k = copies + 2 * (rank + ranks.at(i));
 #pragma unroll
             for (int d = 0; d < 4; ++d)
-                if (held >> (4 * i + d) & 1)
-                    copies[2 * k++] = static_cast<int>(at) + 128 * i + 4 * lane + d;
+                if (held >> (4 * i + d) & 1) {
+                    *k = static_cast<int>(at) + 128 * i + 4 * lane + d;
+                    k += 2;
+                }
         }
         rank += ranks.all();
     }
@@ -666,32 +684,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
     }
     cluster_sync();
-    // The tables: some columns of a row for each warp.
-    const int warps = cluster_size() * kWarps, wide = (sh.most + 32 * kBatch - 1) / (32 * kBatch);
-    for (int u = cluster_rank() * kWarps + (tid >> 5); u < wide * p.num_seqs; u += warps) {
-        const int s = u % p.num_seqs, pages = sh.pages[s];
-        const int j0 = u / p.num_seqs * 32 * kBatch + lane;
-        if (j0 - lane >= pages)
-            continue;
+    // The tables: kColumns of a row for each warp and turn.  (Past a row's last
+    // entry the lanes do that one again.)
+    const int warps = cluster_size() * kWarps, units = p.num_seqs > 0 ? sh.chunks[p.num_seqs - 1] : 0;
+    for (int u = cluster_rank() * kWarps + warp; u < units; u += warps) {
+        int s = 0;  // the first row whose chunks end behind u
+        for (int hi = p.num_seqs - 1; s < hi;) {
+            const int mid = (s + hi) / 2;
+            if (sh.chunks[mid] > u)
+                hi = mid;
+            else
+                s = mid + 1;
+        }
+        const int last = sh.pages[s] - 1, j0 = (u - (s > 0 ? sh.chunks[s - 1] : 0)) * kColumns + lane;
         const int64_t row = (int64_t)s * p.table_stride;
-        int page[kBatch], to[kBatch];
+        const int32_t *from = p.page_table + row;
+        int32_t *out = table_out + row;
+        int page[kColumns / 32], to[kColumns / 32];
+        bool bad = false;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            page[i] = __ldcg(p.page_table + row + (j0 + 32 * i < pages ? j0 + 32 * i : 0));
+        for (int i = 0; i < kColumns / 32; ++i)
+            page[i] = __ldcg(from + min(j0 + 32 * i, last));
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
+        for (int i = 0; i < kColumns / 32; ++i)
             to[i] = __ldcg(refs_out + (page[i] >= n && page[i] < p.num_pages ? page[i] : 0));
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (j0 + 32 * i >= pages)
-                continue;
-            const bool above = page[i] >= n && page[i] < p.num_pages, went = above && to[i] < 0;
-            if (page[i] < 0 || page[i] >= p.num_pages || (above && !went))
-                set_status(status, kStatusBadArg);
-            const int now = went ? went_to(to[i]) : page[i];
-            if (now != page[i] || table_out != p.page_table)
-                table_out[row + j0 + 32 * i] = now;
+        for (int i = 0; i < kColumns / 32; ++i) {
+            const bool above = page[i] >= n && page[i] < p.num_pages;
+            bad = bad || static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.num_pages) || (above && to[i] >= 0);
+            out[min(j0 + 32 * i, last)] = above && to[i] < 0 ? went_to(to[i]) : page[i];
         }
+        if (bad)
+            set_status(status, kStatusBadArg);
     }
     cluster_sync();
     for (int i0 = first; i0 < moves; i0 += kBatch * step) {
