@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 #pragma unroll
         for (int k = 0; k < kEach; ++k)
             if (first + k * kCopyThreads < end)
-                dst[first + k * kCopyThreads] = w[k];
+                __stcs(dst + first + k * kCopyThreads, w[k]);
     }
 }
 
@@ -882,8 +882,8 @@ cudaError_t launch_pages_copy(const smoe_kv_cache *caches, int num_caches, const
     a.max_copies = max_copies;
     a.num_pages = static_cast<int>(c.num_pages);
     const int64_t units = (int64_t)max_copies * num_caches * 2 * a.units;
-    const int64_t wave = (int64_t)dev.sms * 8;
-    copy_kernel<<<static_cast<unsigned>(units < wave ? units : wave), kCopyThreads, 0, stream>>>(a, copies, counts,
+    const int64_t most = (int64_t)dev.sms * 32;
+    copy_kernel<<<static_cast<unsigned>(units < most ? units : most), kCopyThreads, 0, stream>>>(a, copies, counts,
                                                                                               dev.status);
     return cudaGetLastError();
 }

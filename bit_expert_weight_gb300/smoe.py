@@ -683,7 +683,7 @@ def _device_array(name, t, dtype, numel, dev):
     (None: no tensor, a null pointer)."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on the device of the "
                          "call's other tensors")
     if t.numel() < numel:
@@ -850,6 +850,7 @@ def attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
 # ------------------------------------------- beams, pages of the cache
 
 _pack_beam, _pack_pool, _pack_cache = map(_packer, (BeamArgs, PagePool, KvCache))
+_POINTERS = struct.Struct("@PP")       # the first members of smoe_kv_cache
 
 
 def beam_workspace(device="cuda", stream=None):
@@ -949,8 +950,22 @@ def pages_copy(k_pages, v_pages, copies: torch.Tensor, counts: torch.Tensor, str
     if copies.dim() != 2 or copies.shape[1] != 2:
         raise ValueError("copies must be [at most, 2]")
     dev = _device("copies", copies)
-    caches = b"".join(_pack_cache(*_cache(k, v, dev)) for k, v in zip(k_pages, v_pages))
-    _check(load().smoe_pages_copy(caches, len(k_pages),
+    caches = []
+    if k_pages:
+        # the first layer's are looked at closely, and others that are like them only for that
+        k0, v0, bf = k_pages[0], v_pages[0], torch.bfloat16
+        first = _pack_cache(*_cache(k0, v0, dev))
+        rest = first[_POINTERS.size:]
+        shape, ks, vs = k0.shape, k0.stride(), v0.stride()
+        caches.append(first)
+        for k, v in zip(k_pages[1:], v_pages[1:]):
+            if (k.dtype is bf and v.dtype is bf and k.shape == shape and v.shape == shape and
+                    k.stride() == ks and v.stride() == vs and
+                    k.get_device() == dev and v.get_device() == dev):
+                caches.append(_POINTERS.pack(k.data_ptr(), v.data_ptr()) + rest)
+            else:
+                caches.append(_pack_cache(*_cache(k, v, dev)))
+    _check(load().smoe_pages_copy(b"".join(caches), len(caches),
                                   _device_array("copies", copies, torch.int32, 0, dev),
                                   _device_array("counts", counts, torch.int32, 1, dev),
                                   copies.shape[0], _handle(stream, dev)), "smoe_pages_copy")
