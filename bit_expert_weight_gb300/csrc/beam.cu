@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 3;
 constexpr int kWords = 4;                         // of 16 bytes, of a thread and step
 constexpr int kStepWords = kThreads * kWords;     // of a CTA and step
 constexpr size_t kStatsAt = SMOE_MAX_SEQS * sizeof(unsigned);  // after the groups' counters
@@ -32,6 +33,11 @@ static_assert(kStatsAt + (size_t)(SMOE_MAX_SEQS * ((SMOE_MAX_VOCAB / 4 + 1) / (k
                              (sizeof(float2) + SMOE_MAX_BEAMS * sizeof(unsigned long long)) <=
                   SMOE_BEAM_WORKSPACE_BYTES,
               "parts in the workspace");
+// Logits of more bytes than this are read as passing by (first to leave L2):
+// those of less may lie there, from the product that made them, and the few
+// words read again do (60 fp32 rows of 100,003: 12.5 us, 14.0 as passing by; 512
+// rows of 151,936: 36.9 us, 33.6 as passing by).
+constexpr int64_t kPassing = 32 << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 // A sum's largest term may be 2^40: few steps have to rescale.
 constexpr float kSlack = 40.0f;
@@ -103,7 +109,7 @@ __device__ __forceinline__ uint4 load_word(const uint8_t *base, int first, int v
     constexpr int kP = kPer<F32>;
     const int at = w * kP - first;  // index of the word's first logit
     if (w < end && at >= 0 && at + kP <= vocab)
-        return __ldcs(reinterpret_cast<const uint4 *>(base) + w);
+        return __ldg(reinterpret_cast<const uint4 *>(base) + w);
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -258,13 +264,14 @@ __device__ __forceinline__ uint4 load_word(const Part &p, int w)
 // A thread's words of the step that begins at word w.  Where all of the step's
 // words are the row's, which is so but for its first and last ones, the loads
 // are not under conditions, which would make them wait for one another.
-template <bool F32>
+template <bool F32, bool PASSING>
 __device__ __forceinline__ void load_step(uint4 (&v)[kWords], const Part &p, int w, int tid)
 {
     if (w + kStepWords <= p.w1 && w * kPer<F32> >= p.first && (w + kStepWords) * kPer<F32> <= p.first + p.vocab) {
+        const uint4 *from = reinterpret_cast<const uint4 *>(p.base) + w + tid;
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
-            v[i] = __ldcs(reinterpret_cast<const uint4 *>(p.base) + w + kThreads * i + tid);
+            v[i] = PASSING ? __ldcs(from + kThreads * i) : __ldg(from + kThreads * i);
     } else {
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
@@ -431,7 +438,7 @@ __device__ __forceinline__ void rank_keys(const Key *keys, int n, int num_out, K
 // num_out logits reach: the least, over the warps, of the rank-th largest of
 // their threads' largest, where rank times the warps is num_out.  Few words
 // reach it; they are read again (they lie in L2), and their logits ranked.
-template <bool F32>
+template <bool F32, bool PASSING>
 __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int part, PartShared &sh)
 {
     const smoe_beam_args &a = b.a;
@@ -447,7 +454,7 @@ __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int pa
     p.steps = max(0, p.w1 - p.w0 + kStepWords - 1) / kStepWords;
     int w = p.w0;
     uint4 next[kWords];
-    load_step<F32>(next, p, w, tid);
+    load_step<F32, PASSING>(next, p, w, tid);
     // (the first words are on their way while the beam's state is looked up)
     if (state_of(a, row) != kLive)
         return;
@@ -459,7 +466,7 @@ __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int pa
         for (int i = 0; i < kWords; ++i)
             v[i] = next[i];
         if (step + 1 < p.steps)
-            load_step<F32>(next, p, w + kStepWords, tid);
+            load_step<F32, PASSING>(next, p, w + kStepWords, tid);
         const float most = fminf(largest<F32>(v, kWords), FLT_MAX);
         sh.most[step][tid] = most;
         top = fmaxf(top, most);
@@ -885,14 +892,14 @@ union BeamShared {
     JoinShared join;
 };
 
-template <bool F32>
-__global__ void __launch_bounds__(kThreads, 4) beam_kernel(const BeamArgs b)
+template <bool F32, bool PASSING>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_kernel(const BeamArgs b)
 {
     __shared__ BeamShared sh;
     __shared__ bool s_last;
     const int64_t row = blockIdx.x / b.parts;
     const int part = blockIdx.x % b.parts, group = static_cast<int>(row / b.a.beams);
-    scan_part<F32>(b, row, part, sh.part);
+    scan_part<F32, PASSING>(b, row, part, sh.part);
     __syncthreads();
     if (threadIdx.x == 0) {
         const unsigned all = b.a.beams * b.parts;
@@ -917,8 +924,8 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     const int per = f32 ? 4 : 8;
     const int words = (a.vocab + 2 * per - 2) / per;
     const int steps = (words + kStepWords - 1) / kStepWords;
-    // parts: about six CTAs per SM, of a step at least
-    const int64_t wave = dev.sms * 4 < kMaxWave ? dev.sms * 4 : kMaxWave;
+    // parts: up to two CTAs per SM, of a step at least
+    const int64_t wave = dev.sms * 2 < kMaxWave ? dev.sms * 2 : kMaxWave;
     int64_t parts = wave / rows;
     const int least = (steps + kMaxSteps - 1) / kMaxSteps;
     parts = parts < least ? least : parts < steps ? parts : steps;
@@ -929,7 +936,9 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     b.arrivals = reinterpret_cast<unsigned *>(ws);
     b.stats = reinterpret_cast<float2 *>(ws + kStatsAt);
     b.keys = reinterpret_cast<Key *>(ws + kStatsAt + rows * b.parts * sizeof(float2));
-    auto k = f32 ? beam_kernel<true> : beam_kernel<false>;
+    const bool passing = rows * a.vocab * (f32 ? 4 : 2) > kPassing;
+    auto k = f32 ? (passing ? beam_kernel<true, true> : beam_kernel<true, false>)
+                 : (passing ? beam_kernel<false, true> : beam_kernel<false, false>);
     k<<<static_cast<unsigned>(rows * b.parts), kThreads, 0, stream>>>(b);
     return cudaGetLastError();
 }
