@@ -66,7 +66,7 @@ bool valid_pool(const smoe_page_pool &p)
     return p.num_pages >= 1 && p.num_pages <= (1 << 30) && valid_page_size(p.page_size) && p.num_seqs >= 0 &&
            p.num_seqs <= SMOE_MAX_SEQS && p.table_stride >= 0 && p.table_stride <= (1 << 27) && p.refs &&
            aligned16(p.refs) &&
-           (p.num_seqs == 0 || (p.kv_len && p.page_table));
+           (p.num_seqs == 0 || (p.kv_len && (p.page_table || p.table_stride == 0)));
 }
 
 // b is a itself, or no part of it.
@@ -288,7 +288,7 @@ smoe_status smoe_pages_compact(const smoe_page_pool *pool, int32_t *refs_out, in
     if (!pool || !valid_pool(*pool) || !refs_out || !counts || max_copies < pool->num_pages / 2 ||
         (max_copies > 0 && !copies) || (reinterpret_cast<uintptr_t>(copies) & 7) || !same_or_apart(pool->refs, refs_out, pool->num_pages))
         return SMOE_ERR_INVALID_ARG;
-    if (pool->num_seqs > 0 &&
+    if (pool->num_seqs > 0 && pool->table_stride > 0 &&
         (!table_out ||
          !same_or_apart(pool->page_table, table_out, (int64_t)pool->num_seqs * pool->table_stride)))
         return SMOE_ERR_INVALID_ARG;

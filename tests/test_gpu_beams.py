@@ -202,3 +202,66 @@ def test_two_streams_at_once(S):
     for i in (0, 1):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_few_of_the_vocabulary_allowed(S, ws, dtype):
+    """Fewer tokens allowed than asked for, the rest at the type's lowest value: the lowest
+    tokens of those make up the number."""
+    x = torch.full((8, 60_001), torch.finfo(dtype).min, dtype=dtype, device=DEV)
+    for r in range(8):
+        x[r, torch.randperm(60_001, device=DEV)[:r]] = rand(r, seed=r, dtype=dtype)
+    for K, n in ((1, 32), (2, 20), (8, 32)):
+        select(S, ws, x, rand(8 // K, K, seed=1), n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("spread", [0.0, 1e-2, 30.0])
+def test_large_logits_close_together(S, ws, dtype, spread):
+    """The large logits all lie where one warp reads them, or a few hundred words hold nothing
+    else; many are alike in bf16, all where spread is 0."""
+    V = 90_000
+    i = torch.arange(V, device=DEV)
+    per = 4 if dtype == F32 else 8
+    near = rand(4, V, seed=3, spread=max(spread, 1e-9))
+    x = torch.where((i // per) % 256 < 32, 100.0, 0.0) + near
+    x[1] = torch.where(i < 3_000, 50.0, 0.0) + near[1]
+    x[2] = torch.where(i > V - 3_000, 50.0, 0.0) + near[2]
+    x[3] = torch.where((i // per) % 256 == 7, 50.0, 0.0) + near[3]
+    if spread == 0:
+        x = x.round()
+    for K in (1, 4):
+        for n in (2, 32):
+            select(S, ws, x.to(dtype), rand(4 // K, K, seed=K), n)
+
+
+def test_first_call_in_a_capture(S):
+    """A process whose first calls are made while a graph is captured."""
+    import subprocess
+    import sys
+    code = """
+import torch, bit_expert_weight_gb300.smoe as S
+d = dict(dtype=torch.int32, device="cuda:0")
+ws, aws = torch.zeros(S.BEAM_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda:0"), None
+x, sc = torch.randn(4, 5000, device="cuda:0"), torch.zeros(2, 2, device="cuda:0")
+out = (torch.zeros(2, 2, device="cuda:0"), torch.zeros(2, 2, **d), torch.zeros(2, 2, **d))
+refs, kv, table = torch.zeros(64, **d), torch.zeros(4, **d), torch.zeros(4, 8, **d)
+start, copies, counts = torch.arange(5, **d) * 20, torch.zeros(32, 2, **d), torch.zeros(2, **d)
+k, v = torch.zeros(64, 1, 16, 64, dtype=torch.bfloat16, device="cuda:0"), None
+v = k.clone()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    S.beam_select(x, sc, 2, ws, out=out)
+    S.pages_fork(refs, kv, table, 16, out[1].view(-1))
+    S.pages_reserve(refs, kv, table, 16, start, copies, counts)
+    S.pages_copy(k, v, copies[:4], counts)
+    S.pages_compact(refs, kv, table, 16, copies, counts)
+g.replay()
+torch.cuda.synchronize()
+assert kv.tolist() == [20] * 4 and counts.tolist() == [0, 8], (kv, counts)
+assert out[1].tolist()[0][0] in (0, 1) and S.device_status() == 0
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]

@@ -275,6 +275,17 @@ def test_no_sequences_and_full_pools(S):
     assert S.device_status() == 0
 
 
+def test_tables_of_no_columns(S):
+    p = Pool(20, 16, 3, 0)
+    d = OnDevice(p)
+    S.pages_fork(*d.pool, ints([2, -1, 0]))
+    assert reserve(S, d, [0, 0, 0]) == ([[-5, -5]] * 3, [0, 20])
+    S.pages_compact(*d.pool, torch.zeros(10, 2, dtype=I32, device=DEV), ints([0, 0]))
+    assert S.device_status() == 0
+    assert reserve(S, d, [0, 1, 0]) == ([[-5, -5]] * 3, [0, -1]) and S.device_status() == -5
+    d.check(p)
+
+
 # --------------------------------------------------------------- copies
 
 def caches(layers, P, Hkv, page, D, joined, seed=0):
