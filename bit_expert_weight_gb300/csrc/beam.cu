@@ -39,8 +39,6 @@ static_assert(kStatsAt + (size_t)(SMOE_MAX_SEQS * ((SMOE_MAX_VOCAB / 4 + 1) / (k
 // rows of 151,936: 36.9 us, 33.6 as passing by).
 constexpr int64_t kPassing = 32 << 20;
 constexpr float kLog2e = 1.4426950408889634f;
-// A sum's largest term may be 2^40: few steps have to rescale.
-constexpr float kSlack = 40.0f;
 // A sum's reference stays within this: sums of rows whose largest logit is
 // beyond it come out as 0 or infinite, and are taken again (row_sum).
 constexpr float kMaxRef = 2097152.0f;
@@ -186,13 +184,14 @@ __device__ __forceinline__ float power_of_two(float n)
 
 // The sum of 2^(x log2 e - ref) over logits x, for a whole number ref, so that
 // sums of different references are joined without any rounding but that of
-// their addition.
+// their addition.  The largest exponent is above -1 and at most 0, where its
+// rounding is least.
 struct Sum {
     float ref, sum;
     __device__ __forceinline__ void raise(float most)
     {
         const float to = fminf(fmaxf(ceilf(most * kLog2e), -kMaxRef), kMaxRef);
-        if (to > ref + kSlack) {
+        if (to > ref) {
             sum *= power_of_two(ref - to);
             ref = to;
         }

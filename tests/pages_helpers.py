@@ -138,12 +138,17 @@ def values(logits, scores, last=None, end_token=-1):
     return torch.where(torch.isinf(score)[..., None], score[..., None], score[..., None] + v)
 
 
-def values_bound(vocab):
+def values_bound(logits):
     """What a row's normaliser may be off by, in every one of its values alike.  A term
-    exp(x - ref): ex2 within 2 ulp (2^-22), its argument a rounded difference times a rounded
-    constant (d e^-d 3 2^-24 / ln 2 < 2^-22 for d = ref - x); sums of at most vocab / 256 + 64
-    terms in one thread, half a step each; eight joins of sums, 2^-21 each."""
-    return (vocab / 256 + 64) * U32 + 10 * 2.0 ** -21
+    2^(x log2 e - ref) with an exponent y <= 0: ex2 within 2 ulp (2^-22), y's two roundings
+    (|y| 2^y 2 2^-24 ln 2 < 2^-24); chains of 16 terms of a step, 24 steps, 5 and 8 joins, half a
+    step each; the logarithm and the value itself, 2^-22.  Rows with a NaN or +inf, or whose
+    largest logit is beyond 2^20, are summed by each thread on its own: chains of vocab / 256."""
+    vocab = logits.shape[-1]
+    x = torch.where(logits.isnan(), torch.full_like(logits, math.inf), logits).amax(-1)
+    plain = bool((x.abs() <= 2.0 ** 20).all())
+    chain = 53 if plain else vocab / 256 + 13
+    return chain * U32 + 2.0 ** -22 + 2.0 ** -24 + 2.0 ** -22 + (0 if plain else 2.0 ** -21)
 
 
 def check_selection(out, logits, scores, num_out, last=None, end_token=-1):
@@ -157,8 +162,8 @@ def check_selection(out, logits, scores, num_out, last=None, end_token=-1):
     val = values(logits, scores, last, end_token)
     # a beam's own order is exact: larger logits, then lower tokens
     x = torch.where(logits.isnan(), torch.full_like(logits, -math.inf), logits).view(G, K, V)
-    bound = values_bound(V)
     for g in range(G):
+        bound = values_bound(logits[g * K:(g + 1) * K])
         found = min(num_out, int((val[g] > -math.inf).sum()))
         parents, tokens = got_p[g].tolist(), got_t[g].tolist()
         assert parents[found:] == tokens[found:] == [-1] * (num_out - found), (g, found)
