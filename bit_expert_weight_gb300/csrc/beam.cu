@@ -896,6 +896,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_kernel(const BeamAr
 {
     __shared__ BeamShared sh;
     __shared__ bool s_last;
+    pdl_wait();
+    pdl_launch_dependents();
     const int64_t row = blockIdx.x / b.parts;
     const int part = blockIdx.x % b.parts, group = static_cast<int>(row / b.a.beams);
     scan_part<F32, PASSING>(b, row, part, sh.part);
@@ -938,8 +940,14 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     const bool passing = rows * a.vocab * (f32 ? 4 : 2) > kPassing;
     auto k = f32 ? (passing ? beam_kernel<true, true> : beam_kernel<true, false>)
                  : (passing ? beam_kernel<false, true> : beam_kernel<false, false>);
-    k<<<static_cast<unsigned>(rows * b.parts), kThreads, 0, stream>>>(b);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1] = {launch_ahead()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * b.parts));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, b);
 }
 
 }  // namespace smoe

@@ -212,6 +212,18 @@ cudaError_t launch_attention_chunk(const smoe_attention_args &a, uint8_t *worksp
 
 // ------------------------------------------------- beams, pages of the cache
 
+// The kernels of these calls are launched ahead of the end of the one before
+// them in the stream (programmatic dependent launch) and wait for it before
+// they touch memory: a serving step is a chain of short ones, and a launch
+// after a full stop costs more than 1 us.
+inline cudaLaunchAttribute launch_ahead()
+{
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const DeviceFacts &dev, cudaStream_t stream);
 cudaError_t launch_pages_fork(const smoe_page_pool &p, const int32_t *parent, const int32_t *keep,
                               const DeviceFacts &dev, cudaStream_t stream);

@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, n = p.num_seqs, shift = log2_of(p.page_size);
     if (tid == 0)
         sh.rows = sh.most = 0;
+    pdl_wait();
+    pdl_launch_dependents();
     bool bad = false;
     int from_seq[2], was[2], len[2];  // a thread has sequences tid and tid + kThreads
 #pragma unroll
@@ -383,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.writers[i] = 0;
         sh.first[i] = 0x7fffffff;
     }
+    pdl_wait();
+    pdl_launch_dependents();
     // A thread has sequences tid and tid + kThreads.  Their lengths, last pages
     // and those pages' holders come one after the other; the pool is counted meanwhile.
     int had[2], page[2], new_pages[2], holders[2], grown[2];
@@ -561,6 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = log2_of(p.page_size);
     const Run run = run_at(run_length<L>(p.num_pages), run_of_warp(warp), p.num_pages);
     cluster_arrive();
+    pdl_wait();
+    pdl_launch_dependents();
     const int mine = count_held<L>(p.refs, run, lane);
     share_counts(sh.runs, mine, tid);
     const int n = counted(sh.runs, lane), before = counted_before(sh.runs, run_of_warp(warp), lane);
@@ -736,16 +742,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kCopyThreads = 256;
 constexpr int kUnitWords = 1024;  // of 16 bytes
 
+// (arguments for 8 caches or for all: 2 KB of them make a launch longer)
+template <int MOST>
 struct CopyArgs {
-    const uint4 *k[SMOE_MAX_CACHES], *v[SMOE_MAX_CACHES];
+    const uint4 *k[MOST], *v[MOST];
     int64_t k_stride, v_stride;  // words
     int page_words, units;       // of a page's keys
     int num_caches, max_copies, num_pages;
 };
 
+template <int MOST>
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_kernel(const __grid_constant__ CopyArgs a, const int32_t *copies, const int32_t *counts, int *status)
+    copy_kernel(const __grid_constant__ CopyArgs<MOST> a, const int32_t *copies, const int32_t *counts, int *status)
 {
+    pdl_wait();
+    pdl_launch_dependents();
     const int asked = counts[0];
     const int n = min(max(asked, 0), a.max_copies);
     if (asked != n && blockIdx.x == 0 && threadIdx.x == 0)
@@ -798,7 +809,8 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const 
             return e;
         allowed[dev.index].store(true, std::memory_order_release);
     }
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1] = launch_ahead();
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -808,7 +820,7 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const 
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -864,10 +876,13 @@ cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int
     return small_pool(p) ? go(compact_kernel<1>, allowed[0]) : go(compact_kernel<8>, allowed[1]);
 }
 
-cudaError_t launch_pages_copy(const smoe_kv_cache *caches, int num_caches, const int32_t *copies,
-                              const int32_t *counts, int max_copies, const DeviceFacts &dev, cudaStream_t stream)
+namespace {
+
+template <int MOST>
+cudaError_t launch_copy(const smoe_kv_cache *caches, int num_caches, const int32_t *copies, const int32_t *counts,
+                        int max_copies, const DeviceFacts &dev, cudaStream_t stream)
 {
-    CopyArgs a;
+    CopyArgs<MOST> a;
     const smoe_kv_cache &c = caches[0];
     for (int i = 0; i < num_caches; ++i) {
         a.k[i] = static_cast<const uint4 *>(caches[i].k_pages);
@@ -883,9 +898,23 @@ cudaError_t launch_pages_copy(const smoe_kv_cache *caches, int num_caches, const
     a.num_pages = static_cast<int>(c.num_pages);
     const int64_t units = (int64_t)max_copies * num_caches * 2 * a.units;
     const int64_t most = (int64_t)dev.sms * 32;
-    copy_kernel<<<static_cast<unsigned>(units < most ? units : most), kCopyThreads, 0, stream>>>(a, copies, counts,
-                                                                                              dev.status);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1] = {launch_ahead()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(units < most ? units : most));
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, copy_kernel<MOST>, a, copies, counts, dev.status);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_copy(const smoe_kv_cache *caches, int num_caches, const int32_t *copies,
+                              const int32_t *counts, int max_copies, const DeviceFacts &dev, cudaStream_t stream)
+{
+    return (num_caches <= 8 ? launch_copy<8> : launch_copy<SMOE_MAX_CACHES>)(caches, num_caches, copies, counts,
+                                                                            max_copies, dev, stream);
 }
 
 }  // namespace smoe
