@@ -540,29 +540,107 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- compact
 
+// The two ends of the moves are found by rank, each for itself, by a cluster;
+// then the moves are gone through as a list, and the tables.  Meanwhile the
+// entry of a moved page in refs_out (which will be 0) says where it went.  A
+// small pool's are done with by the same cluster; a large one's by launches of
+// the whole device, which one cluster's 16 SMs would take longer for.
 constexpr int kBatch = 4;  // loads of a thread that are in flight together
 constexpr int kColumns = 128;
 
-struct CompactShared {
-    RunCounts runs;
-    int under;                 // held pages below n
-    int pages[SMOE_MAX_SEQS];  // of each one
-    int chunks[SMOE_MAX_SEQS]; // of kColumns entries, of the sequences up to it
-    int warp[kWarps];
-};
-
-// The two ends of the moves are found by rank, each for itself; then the moves
-// are gone through as a list.  While the tables are looked through, the entry
-// of a moved page in refs_out (which will be 0) says where it went.
 __device__ __forceinline__ int went_to(int page) { return -1 - page; }
 
-template <int L>
+// What stays where it is, into other refs: a thread of `step` has number `first`.
+__device__ __forceinline__ void stay_pass(const smoe_page_pool &p, int32_t *refs_out, int n, int64_t first, int64_t step)
+{
+    const bool whole = (reinterpret_cast<uintptr_t>(refs_out) & 15) == 0;
+    for (int64_t q = 4 * first; q < p.num_pages; q += 4 * step) {
+        const int4 v = refs_at(p.refs, q, p.num_pages);
+        if (whole && q >= n && q + 4 <= p.num_pages && v.x <= 0 && v.y <= 0 && v.z <= 0 && v.w <= 0) {
+            *reinterpret_cast<int4 *>(refs_out + q) = make_int4(0, 0, 0, 0);
+            continue;
+        }
+        const int c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int d = 0; d < 4; ++d)  // (moved pages and those that they come to are told by move_pass)
+            if (q + d < p.num_pages && (q + d < n) == (c[d] > 0))
+                refs_out[q + d] = q + d < n ? c[d] : 0;
+    }
+}
+
+__device__ __forceinline__ void move_pass(const smoe_page_pool &p, int32_t *refs_out, const int32_t *copies, int moves,
+                                          int first, int step)
+{
+    for (int i0 = first; i0 < moves; i0 += kBatch * step) {
+        int2 m[kBatch];
+        int c[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            m[i] = __ldcg(reinterpret_cast<const int2 *>(copies) + min(i0 + i * step, moves - 1));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            c[i] = __ldcg(p.refs + m[i].x);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i0 + i * step < moves) {
+                refs_out[m[i].y] = c[i];
+                refs_out[m[i].x] = went_to(m[i].y);
+            }
+    }
+}
+
+// Entries j0 + 32 i of a row of `pages`, by a warp.  (Past the last entry the
+// lanes do that one again.)
+__device__ __forceinline__ void table_pass(const smoe_page_pool &p, const int32_t *refs_out, int32_t *table_out, int n,
+                                           int s, int pages, int j0, int *status)
+{
+    const int64_t row = (int64_t)s * p.table_stride;
+    const int32_t *from = p.page_table + row;
+    int32_t *out = table_out + row;
+    int page[kColumns / 32], to[kColumns / 32];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kColumns / 32; ++i)
+        page[i] = __ldcg(from + min(j0 + 32 * i, pages - 1));
+#pragma unroll
+    for (int i = 0; i < kColumns / 32; ++i)
+        to[i] = __ldcg(refs_out + (page[i] >= n && page[i] < p.num_pages ? page[i] : 0));
+#pragma unroll
+    for (int i = 0; i < kColumns / 32; ++i) {
+        const bool above = page[i] >= n && page[i] < p.num_pages;
+        bad = bad || static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.num_pages) || (above && to[i] >= 0);
+        out[min(j0 + 32 * i, pages - 1)] = above && to[i] < 0 ? went_to(to[i]) : page[i];
+    }
+    if (bad)
+        set_status(status, kStatusBadArg);
+}
+
+__device__ __forceinline__ void clear_pass(int32_t *refs_out, const int32_t *copies, int moves, int first, int step)
+{
+    for (int i0 = first; i0 < moves; i0 += kBatch * step) {
+        int from[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            from[i] = __ldcg(copies + 2 * (int64_t)min(i0 + i * step, moves - 1));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            refs_out[from[i]] = 0;  // (the last one more than once)
+    }
+}
+
+struct CompactShared {
+    RunCounts runs;
+    int under;  // held pages below n
+};
+
+// ALONE: with the passes.
+template <int L, bool ALONE>
 __global__ void __launch_bounds__(kThreads, 1)
     compact_kernel(const smoe_page_pool p, int32_t *refs_out, int32_t *table_out, int32_t *copies,
                    int32_t *counts, int *status)
 {
     __shared__ CompactShared sh;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = log2_of(p.page_size);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Run run = run_at(run_length<L>(p.num_pages), run_of_warp(warp), p.num_pages);
     cluster_arrive();
     pdl_wait();
@@ -593,29 +671,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane < static_cast<int>(cluster_size()) && run.first < run.last && n >= run.first &&
         (n < run.last || run.last == p.num_pages))
         store_to_rank(&sh.under, lane, static_cast<int>(held_before));
-    // A thread has two consecutive sequences.
-    int chunks[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int s = 2 * tid + i;
-        if (s >= p.num_seqs)
-            continue;
-        const int len = p.kv_len[s];
-        const bool ok = valid_len(p, len);
-        if (!ok)
-            set_status(status, kStatusBadArg);
-        sh.pages[s] = ok ? pages_of(len, shift) : 0;
-        chunks[i] = (sh.pages[s] + kColumns - 1) / kColumns;
-    }
-    int end = lanes_up_to(chunks[0] + chunks[1], lane);
-    if (lane == 31)
-        sh.warp[warp] = end;
-    __syncthreads();
-    end += warp_sum(lane < warp ? sh.warp[lane] : 0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (2 * tid + i < p.num_seqs)
-            sh.chunks[2 * tid + i] = i == 0 ? end - chunks[1] : end;
     cluster_sync();
     const int moves = n - sh.under;
     if (cluster_rank() == 0 && tid == 0) {
@@ -641,98 +696,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         rank += ranks.all();
     }
-    // What stays where it is (of the free pages below n the moves are told afterwards).
+    if (!ALONE)
+        return;
+    cluster_sync();
     const int first = cluster_rank() * kThreads + tid, step = cluster_size() * kThreads;
-    const bool whole = (reinterpret_cast<uintptr_t>(refs_out) & 15) == 0;
     if (refs_out != p.refs)
-        for (int64_t q0 = 4 * (int64_t)first; q0 < p.num_pages; q0 += 4 * kBatch * (int64_t)step) {
-            int4 v[kBatch];
-            if (q0 + 4 * ((kBatch - 1) * (int64_t)step + 1) <= p.num_pages) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    v[i] = __ldcg(reinterpret_cast<const int4 *>(p.refs + q0) + i * (int64_t)step);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    v[i] = refs_at(p.refs, q0 + 4 * i * (int64_t)step, p.num_pages);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int64_t q = q0 + 4 * i * (int64_t)step;
-                const int m = static_cast<int>(min(max(n - q, (int64_t)0), (int64_t)4));  // of them below n
-                v[i] = make_int4(m > 0 ? v[i].x : 0, m > 1 ? v[i].y : 0, m > 2 ? v[i].z : 0, m > 3 ? v[i].w : 0);
-                if (whole && q + 4 <= p.num_pages) {
-                    *reinterpret_cast<int4 *>(refs_out + q) = v[i];
-                } else {
-                    const int c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        if (q + d < p.num_pages)
-                            refs_out[q + d] = c[d];
-                }
-            }
-        }
+        stay_pass(p, refs_out, n, first, step);
+    move_pass(p, refs_out, copies, moves, first, step);
     cluster_sync();
-    for (int i0 = first; i0 < moves; i0 += kBatch * step) {
-        int2 m[kBatch];
-        int c[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            m[i] = __ldcg(reinterpret_cast<const int2 *>(copies) + min(i0 + i * step, moves - 1));
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            c[i] = __ldcg(p.refs + m[i].x);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (i0 + i * step < moves) {
-                refs_out[m[i].y] = c[i];
-                refs_out[m[i].x] = went_to(m[i].y);
-            }
-    }
-    cluster_sync();
-    // The tables: kColumns of a row for each warp and turn.  (Past a row's last
-    // entry the lanes do that one again.)
-    const int warps = cluster_size() * kWarps, units = p.num_seqs > 0 ? sh.chunks[p.num_seqs - 1] : 0;
-    for (int u = cluster_rank() * kWarps + warp; u < units; u += warps) {
-        int s = 0;  // the first row whose chunks end behind u
-        for (int hi = p.num_seqs - 1; s < hi;) {
-            const int mid = (s + hi) / 2;
-            if (sh.chunks[mid] > u)
-                hi = mid;
-            else
-                s = mid + 1;
-        }
-        const int last = sh.pages[s] - 1, j0 = (u - (s > 0 ? sh.chunks[s - 1] : 0)) * kColumns + lane;
-        const int64_t row = (int64_t)s * p.table_stride;
-        const int32_t *from = p.page_table + row;
-        int32_t *out = table_out + row;
-        int page[kColumns / 32], to[kColumns / 32];
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < kColumns / 32; ++i)
-            page[i] = __ldcg(from + min(j0 + 32 * i, last));
-#pragma unroll
-        for (int i = 0; i < kColumns / 32; ++i)
-            to[i] = __ldcg(refs_out + (page[i] >= n && page[i] < p.num_pages ? page[i] : 0));
-#pragma unroll
-        for (int i = 0; i < kColumns / 32; ++i) {
-            const bool above = page[i] >= n && page[i] < p.num_pages;
-            bad = bad || static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.num_pages) || (above && to[i] >= 0);
-            out[min(j0 + 32 * i, last)] = above && to[i] < 0 ? went_to(to[i]) : page[i];
-        }
-        if (bad)
+    const int shift = log2_of(p.page_size), warps = cluster_size() * kWarps;
+    const int wide = (p.table_stride + kColumns - 1) / kColumns;
+    for (int u = cluster_rank() * kWarps + warp; u < wide * p.num_seqs; u += warps) {
+        const int s = u / wide, j0 = u % wide * kColumns, len = p.kv_len[s];
+        if (!valid_len(p, len))
             set_status(status, kStatusBadArg);
+        else if (j0 < pages_of(len, shift))
+            table_pass(p, refs_out, table_out, n, s, pages_of(len, shift), j0 + lane, status);
     }
     cluster_sync();
-    for (int i0 = first; i0 < moves; i0 += kBatch * step) {
-        int from[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            from[i] = __ldcg(copies + 2 * (int64_t)min(i0 + i * step, moves - 1));
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            refs_out[from[i]] = 0;  // (the last one more than once)
+    clear_pass(refs_out, copies, moves, first, step);
+}
+
+constexpr int kPassThreads = 256;
+
+// The passes of a large pool.
+__global__ void __launch_bounds__(kPassThreads)
+    move_kernel(const smoe_page_pool p, int32_t *refs_out, const int32_t *copies, const int32_t *counts)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int first = blockIdx.x * kPassThreads + threadIdx.x, step = gridDim.x * kPassThreads;
+    if (refs_out != p.refs)
+        stay_pass(p, refs_out, counts[1], first, step);
+    move_pass(p, refs_out, copies, counts[0], first, step);
+}
+
+__global__ void __launch_bounds__(kPassThreads)
+    table_kernel(const smoe_page_pool p, const int32_t *refs_out, int32_t *table_out, const int32_t *counts, int *status)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int s = blockIdx.y, len = p.kv_len[s], n = counts[1];
+    if (!valid_len(p, len)) {
+        set_status(status, kStatusBadArg);
+        return;
     }
+    const int pages = pages_of(len, log2_of(p.page_size)), lane = threadIdx.x & 31;
+    const int warps = gridDim.x * (kPassThreads / 32);
+    for (int j0 = (blockIdx.x * (kPassThreads / 32) + (threadIdx.x >> 5)) * kColumns; j0 < pages; j0 += warps * kColumns)
+        table_pass(p, refs_out, table_out, n, s, pages, j0 + lane, status);
+}
+
+__global__ void __launch_bounds__(kPassThreads)
+    clear_kernel(int32_t *refs_out, const int32_t *copies, const int32_t *counts)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    clear_pass(refs_out, copies, counts[0], blockIdx.x * kPassThreads + threadIdx.x, gridDim.x * kPassThreads);
 }
 
 // ------------------------------------------------------------------- copy
@@ -824,6 +844,19 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <class... Params, class... Args>
+cudaError_t launch_grid(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args)
+{
+    cudaLaunchAttribute attr[1] = {launch_ahead()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The power of two that n pieces of work keep busy.
 int cluster_for(int64_t n)
 {
@@ -835,6 +868,7 @@ int cluster_for(int64_t n)
 
 // Pools that one cluster goes over in chunks of 128 pages at once.
 constexpr int kSmallPool = kMaxCluster * kWarps * chunk(1);
+constexpr int kSmallTables = 1 << 16;  // entries
 bool small_pool(const smoe_page_pool &p) { return p.num_pages <= kSmallPool; }
 int pool_cluster(const smoe_page_pool &p)
 {
@@ -868,12 +902,28 @@ cudaError_t launch_pages_reserve(const smoe_page_pool &p, const int32_t *row_sta
 cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int32_t *table_out, int32_t *copies,
                                  int32_t *counts, const DeviceFacts &dev, cudaStream_t stream)
 {
+    const bool alone = small_pool(p) && (int64_t)p.num_seqs * p.table_stride <= kSmallTables;
     const auto go = [&](auto *kernel, std::atomic<bool> *allowed) {
         return launch_cluster(kernel, pool_cluster(p), 0, dev, allowed, stream, p, refs_out, table_out, copies, counts,
                               dev.status);
     };
-    static std::atomic<bool> allowed[2][kMaxDeviceIndex];
-    return small_pool(p) ? go(compact_kernel<1>, allowed[0]) : go(compact_kernel<8>, allowed[1]);
+    static std::atomic<bool> allowed[3][kMaxDeviceIndex];
+    cudaError_t e = alone           ? go(compact_kernel<1, true>, allowed[0])
+                    : small_pool(p) ? go(compact_kernel<1, false>, allowed[1])
+                                    : go(compact_kernel<8, false>, allowed[2]);
+    if (alone)
+        return e;
+    const auto pass = [&](dim3 grid, auto *kernel, auto... args) {
+        if (e == cudaSuccess)
+            e = launch_grid(kernel, grid, kPassThreads, stream, args...);
+    };
+    pass(dim3(dev.sms * 2), move_kernel, p, refs_out, copies, counts);
+    if (p.num_seqs > 0 && p.table_stride > 0) {
+        const int columns = kPassThreads / 32 * kColumns, wide = (p.table_stride + columns - 1) / columns;
+        pass(dim3(wide < 64 ? wide : 64, p.num_seqs), table_kernel, p, refs_out, table_out, counts, dev.status);
+    }
+    pass(dim3(dev.sms), clear_kernel, refs_out, copies, counts);
+    return e;
 }
 
 namespace {
@@ -898,14 +948,8 @@ cudaError_t launch_copy(const smoe_kv_cache *caches, int num_caches, const int32
     a.num_pages = static_cast<int>(c.num_pages);
     const int64_t units = (int64_t)max_copies * num_caches * 2 * a.units;
     const int64_t most = (int64_t)dev.sms * 32;
-    cudaLaunchAttribute attr[1] = {launch_ahead()};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units < most ? units : most));
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, copy_kernel<MOST>, a, copies, counts, dev.status);
+    return launch_grid(copy_kernel<MOST>, dim3(static_cast<unsigned>(units < most ? units : most)), kCopyThreads, stream,
+                       a, copies, counts, dev.status);
 }
 
 }  // namespace

@@ -704,7 +704,8 @@ smoe_status smoe_attention(const smoe_attention_args *args, void *workspace,
  * the next tokens of its beams, let sequences become copies of others, make
  * room for their next rows, and keep the pool of pages in order.  Everything
  * is decided on the device from the arrays' contents: nothing is read back,
- * each call is one launch and may be captured.  Inference only.
+ * each call is one launch (smoe_pages_compact of a large pool: four) and may be
+ * captured.  Inference only.
  *
  * A step of a beam search, of S = num_groups * beams sequences:
  *   smoe_pages_reserve   room for the new rows; what is shared and about to
