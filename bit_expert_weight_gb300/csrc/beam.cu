@@ -69,6 +69,7 @@ struct BeamArgs {
     smoe_beam_args a;
     int parts;             // of a row
     int part_words;        // a multiple of kStepWords
+    int depth;             // first values of a part that join_group's bar goes by
     unsigned *arrivals;    // [groups], 0 between launches
     float2 *stats;         // [rows][parts]: reference and sum
     Key *keys;             // [rows][parts][num_out]
@@ -79,10 +80,11 @@ enum : int { kDead, kFinished, kLive };
 
 __device__ __forceinline__ int state_of(const smoe_beam_args &a, int64_t row)
 {
-    const float score = a.scores[row];
+    const float score = a.scores[row];  // (both loads at once)
+    const int last = a.last && a.end_token >= 0 ? a.last[row] : -1;
     if (!(fabsf(score) <= FLT_MAX))
         return kDead;
-    return a.end_token >= 0 && a.last && a.last[row] == a.end_token ? kFinished : kLive;
+    return a.end_token >= 0 && last == a.end_token ? kFinished : kLive;
 }
 
 // A logit as it counts: NaN as -inf, +inf as the largest finite one.
@@ -739,16 +741,15 @@ __device__ __noinline__ void select_crowd(const BeamArgs &b, int group, JoinShar
 
 // A group's outputs from its rows' parts, by the CTA that arrived last.  As in
 // a part: a bar that num_out candidates reach, and the few that do are ranked.
-// The bar is the num_out-th largest of some first values of each part, four
-// times as many as that in all.
+// The bar is the num_out-th largest of the first `depth` values of each part,
+// four times as many as that in all.
 template <bool F32>
 __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinShared &sh)
 {
     const smoe_beam_args &a = b.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.num_out, P = b.parts;
     const int64_t row0 = (int64_t)group * a.beams;
-    const int depth = min(N, (4 * N + a.beams * P - 1) / (a.beams * P));  // values of a part
-    const int each = P * depth, samples = min(a.beams * each, kSamples);
+    const int depth = b.depth, each = P * depth, samples = min(a.beams * each, kSamples);
     if (tid == 0) {
         sh.queued = 0;
         sh.bar = 0;
@@ -933,6 +934,8 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     const int each = static_cast<int>((steps + parts - 1) / parts);
     b.part_words = each * kStepWords;
     b.parts = (steps + each - 1) / each;
+    const int depth = (4 * a.num_out + a.beams * b.parts - 1) / (a.beams * b.parts);
+    b.depth = depth < a.num_out ? depth : a.num_out;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     b.arrivals = reinterpret_cast<unsigned *>(ws);
     b.stats = reinterpret_cast<float2 *>(ws + kStatsAt);
@@ -940,14 +943,7 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     const bool passing = rows * a.vocab * (f32 ? 4 : 2) > kPassing;
     auto k = f32 ? (passing ? beam_kernel<true, true> : beam_kernel<true, false>)
                  : (passing ? beam_kernel<false, true> : beam_kernel<false, false>);
-    cudaLaunchAttribute attr[1] = {launch_ahead()};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * b.parts));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, b);
+    return launch_ahead(k, dim3(static_cast<unsigned>(rows * b.parts)), kThreads, 0, 0, stream, b);
 }
 
 }  // namespace smoe

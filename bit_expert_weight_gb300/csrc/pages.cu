@@ -825,36 +825,13 @@ cudaError_t launch_cluster(void (*kernel)(Params...), int ctas, int smem, const 
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-        if (e != cudaSuccess)
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
             return e;
+        }
         allowed[dev.index].store(true, std::memory_order_release);
     }
-    cudaLaunchAttribute attr[2];
-    attr[1] = launch_ahead();
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <class... Params, class... Args>
-cudaError_t launch_grid(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args)
-{
-    cudaLaunchAttribute attr[1] = {launch_ahead()};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    return launch_ahead(kernel, dim3(ctas), kThreads, smem, ctas, stream, args...);
 }
 
 // The power of two that n pieces of work keep busy.
@@ -915,7 +892,7 @@ cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int
         return e;
     const auto pass = [&](dim3 grid, auto *kernel, auto... args) {
         if (e == cudaSuccess)
-            e = launch_grid(kernel, grid, kPassThreads, stream, args...);
+            e = launch_ahead(kernel, grid, kPassThreads, 0, 0, stream, args...);
     };
     pass(dim3(dev.sms * 2), move_kernel, p, refs_out, copies, counts);
     if (p.num_seqs > 0 && p.table_stride > 0) {
@@ -948,8 +925,8 @@ cudaError_t launch_copy(const smoe_kv_cache *caches, int num_caches, const int32
     a.num_pages = static_cast<int>(c.num_pages);
     const int64_t units = (int64_t)max_copies * num_caches * 2 * a.units;
     const int64_t most = (int64_t)dev.sms * 32;
-    return launch_grid(copy_kernel<MOST>, dim3(static_cast<unsigned>(units < most ? units : most)), kCopyThreads, stream,
-                       a, copies, counts, dev.status);
+    return launch_ahead(copy_kernel<MOST>, dim3(static_cast<unsigned>(units < most ? units : most)), kCopyThreads, 0, 0,
+                        stream, a, copies, counts, dev.status);
 }
 
 }  // namespace
