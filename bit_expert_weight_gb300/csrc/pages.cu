@@ -2,11 +2,21 @@
 // smoe_pages_reserve, smoe_pages_compact (whole numbers only) and
 // smoe_pages_copy.
 //
-// The first three change a few arrays of a pool at most of some MB, in steps
+// The first three change a few arrays of a pool, at most of some MB, in steps
 // that need one another's results.  Each runs as one thread-block cluster: its
 // barrier is the hardware's and its words pass through shared memory, so a call
 // is one launch, needs no workspace, and nothing of one launch is left for the
-// next to find.
+// next to find.  Clusters have up to 16 CTAs (8: a pool of 400,000 pages
+// compacted in 84 us instead of 43, all else alike).
+//
+// Bound: chains of loads and barriers (an L2 load 700 to 1,000 cycles, a barrier
+// of the cluster with what was written before it about as much), and issue
+// slots where one cluster goes over a whole table.  Measured on the device:
+// 4 sequences reordered 2.6 us, 512 of up to 16,001 keys 5.7 us; a step of 240
+// beams cut back, reordered and extended 11.3 us in two calls (fork 3.8, reserve
+// of no rows 4.0); chunks of 200 prompts in a pool of 430,000 pages 10.2 us in
+// two calls; a pool of 1,100 pages compacted 8.4 us, one of 336,000 with 32,500
+// moves 15.2 us.
 #include <atomic>
 
 #include "cluster.cuh"
@@ -166,7 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Reserve and compact go over refs in runs of consecutive pages, one for each
 // warp of the cluster, dealt to its CTAs in turn (what is asked of pages is often
 // asked of the lowest), and in each run in chunks of 128 pages (L = 1) or of 1024
-// (L = 8 loads in flight), by the size of the pool.
+// (L = 8 loads in flight), by the size of the pool: of up to two chunks of 128 for
+// each warp, or more (a step of 240 beams in a pool of 100,000 pages: 10.6 us
+// with 128, 11.3 with 1024; chunks of 200 prompts in one of 430,000: 17.2 and 10.2).
 constexpr int chunk(int L) { return 128 * L; }
 
 struct Run {
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // then the moves are gone through as a list, and the tables.  Meanwhile the
 // entry of a moved page in refs_out (which will be 0) says where it went.  A
 // small pool's are done with by the same cluster; a large one's by launches of
-// the whole device, which one cluster's 16 SMs would take longer for.
+// the whole device (336,000 pages, 480 sequences: 15.2 us; by the cluster 20.3).
 constexpr int kBatch = 4;  // loads of a thread that are in flight together
 constexpr int kColumns = 128;
 
@@ -758,7 +770,10 @@ __global__ void __launch_bounds__(kPassThreads)
 // ------------------------------------------------------------------- copy
 
 // Bound: HBM, each page is read and written once.  A unit is 16 KB of one
-// page's keys or values in one cache.
+// page's keys or values in one cache.  Many CTAs of one to a few units each keep
+// the most loads in flight: 601 pages in two layers (630 MB read and written) take
+// 93.9 us, 6.7 TB/s, with 32 CTAs per SM, 102 us with 8 that go on and on; more than
+// 32 would cost calls of few pages.  12 pages in four layers: 2.1 us.
 constexpr int kCopyThreads = 256;
 constexpr int kUnitWords = 1024;  // of 16 bytes
 
@@ -843,10 +858,15 @@ int cluster_for(int64_t n)
     return c;
 }
 
-// Pools that one cluster goes over in chunks of 128 pages at once.
-constexpr int kSmallPool = kMaxCluster * kWarps * chunk(1);
-constexpr int kSmallTables = 1 << 16;  // entries
-bool small_pool(const smoe_page_pool &p) { return p.num_pages <= kSmallPool; }
+constexpr int kRound = kMaxCluster * kWarps * chunk(1);
+bool small_chunks(const smoe_page_pool &p) { return p.num_pages <= 2 * kRound; }
+// A pool of one round, with tables of few entries, is also compacted by the one
+// launch: 1,100 pages take 8.4 us a call, and 12.6 by four launches, which the
+// host takes longer for (8.3 us on the device).
+bool compact_alone(const smoe_page_pool &p)
+{
+    return p.num_pages <= kRound && (int64_t)p.num_seqs * p.table_stride <= 1 << 16;
+}
 int pool_cluster(const smoe_page_pool &p)
 {
     const int64_t pages = p.num_pages / (kWarps * chunk(1)), entries = (int64_t)p.num_seqs * p.table_stride / 8192;
@@ -873,21 +893,21 @@ cudaError_t launch_pages_reserve(const smoe_page_pool &p, const int32_t *row_sta
                               counts, dev.status);
     };
     static std::atomic<bool> allowed[2][kMaxDeviceIndex];
-    return small_pool(p) ? go(reserve_kernel<1>, allowed[0]) : go(reserve_kernel<8>, allowed[1]);
+    return small_chunks(p) ? go(reserve_kernel<1>, allowed[0]) : go(reserve_kernel<8>, allowed[1]);
 }
 
 cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int32_t *table_out, int32_t *copies,
                                  int32_t *counts, const DeviceFacts &dev, cudaStream_t stream)
 {
-    const bool alone = small_pool(p) && (int64_t)p.num_seqs * p.table_stride <= kSmallTables;
+    const bool alone = compact_alone(p);
     const auto go = [&](auto *kernel, std::atomic<bool> *allowed) {
         return launch_cluster(kernel, pool_cluster(p), 0, dev, allowed, stream, p, refs_out, table_out, copies, counts,
                               dev.status);
     };
     static std::atomic<bool> allowed[3][kMaxDeviceIndex];
-    cudaError_t e = alone           ? go(compact_kernel<1, true>, allowed[0])
-                    : small_pool(p) ? go(compact_kernel<1, false>, allowed[1])
-                                    : go(compact_kernel<8, false>, allowed[2]);
+    cudaError_t e = alone             ? go(compact_kernel<1, true>, allowed[0])
+                    : small_chunks(p) ? go(compact_kernel<1, false>, allowed[1])
+                                      : go(compact_kernel<8, false>, allowed[2]);
     if (alone)
         return e;
     const auto pass = [&](dim3 grid, auto *kernel, auto... args) {

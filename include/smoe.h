@@ -749,17 +749,20 @@ typedef struct {
  * over the group's beams k and all tokens v; of equal values the lower k comes
  * first, and within a beam the larger logit, then the lower v.  parents gets the beam's row in logits (group *
  * beams + k), tokens v, scores_out the value rounded to fp32.
- * A beam whose last token is end_token is finished: its logits are not read,
+ * A beam whose last token is end_token is finished: its logits do not matter,
  * and it has one continuation, end_token at its own score.  A logit of -inf or
  * NaN is never chosen and has no part in the sum; +inf counts as the largest
  * finite fp32.  A beam whose score is not finite has no continuation, nor has
  * one without a logit above -inf.  Where a group has fewer than num_out
  * continuations the rest get score -inf, parent -1 and token -1.
- * exp and its sums are in fp32 (a row's normaliser is off by a few 2^-24, by
- * the same in equal rows of equal alignment to 16 bytes), the rest, and the
- * comparison of values, in 64 bits: continuations of different beams that are
- * nearer than that may come in either order.  Work is split over the
- * vocabulary and joined in a fixed order: the same inputs give the same bits.
+ * Exponentials and their sums are in fp32: a row's normaliser is off by 1e-7 or
+ * so, at most 2^-18, and by the same in equal rows of equal alignment to 16
+ * bytes (rows with a NaN or +inf, or whose largest logit is beyond 2^20: by
+ * 2^-24 for each 256 tokens more).  What follows is held and compared to 2^-45
+ * of its size (values beyond 2^64 as fp32): continuations of different beams
+ * that are nearer to one another than all this may come in either order.  Work
+ * is split over the vocabulary and joined in a fixed order: the same inputs
+ * give the same bits.
  * With num_out == beams, scores_out may be scores and tokens may be last (a
  * captured step works in place); no other overlap of an output with anything.
  * Errors: SMOE_ERR_INVALID_ARG, SMOE_ERR_WORKSPACE, SMOE_ERR_UNSUPPORTED

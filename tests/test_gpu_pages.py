@@ -72,7 +72,7 @@ def reserve(S, d, rows):
 SIZES = [  # pages, page size, sequences, table width
     (1, 16, 1, 1), (7, 16, 2, 5), (60, 32, 9, 12), (300, 16, 40, 23), (1_000, 128, 17, 70),
     (5_000, 16, 300, 40), (40_000, 256, 33, 513), (9_000, 64, 2_048, 9), (70_001, 16, 5, 4_500),
-    (300_003, 16, 64, 900),
+    (300_003, 16, 64, 900), (30_000, 32, 100, 700), (140_001, 64, 7, 300), (1_200_007, 16, 50, 900),
 ]
 
 
