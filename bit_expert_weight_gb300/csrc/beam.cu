@@ -120,7 +120,7 @@ __device__ __forceinline__ uint4 load_word(const uint8_t *base, int first, int v
     constexpr int kP = kPer<F32>;
     const int at = w * kP - first;  // index of the word's first logit
     if (w < end && at >= 0 && at + kP <= vocab)
-        return __ldg(reinterpret_cast<const uint4 *>(base) + w);
+        return __ldcg(reinterpret_cast<const uint4 *>(base) + w);
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -283,7 +283,7 @@ __device__ __forceinline__ void load_step(uint4 (&v)[kWords], const Part &p, int
         const uint4 *from = reinterpret_cast<const uint4 *>(p.base) + w + tid;
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
-            v[i] = PASSING ? __ldcs(from + kThreads * i) : __ldg(from + kThreads * i);
+            v[i] = PASSING ? __ldcs(from + kThreads * i) : __ldcg(from + kThreads * i);
     } else {
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
