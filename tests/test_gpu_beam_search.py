@@ -89,3 +89,30 @@ def test_example_runs(ex):
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "done:" in r.stdout and r.stdout.count("request") == 3
+
+
+def test_a_captured_step(ex):
+    """The whole step of a search (room, copies, append, attention, choice, reordering) as one
+    graph, replayed: what it comes to is the same as call by call, to the bit."""
+    def begin():
+        model = ex.TinyModel(300, 4, 2, 64, torch.device(DEV), seed=9)
+        search = ex.BeamSearch(model, 3, 4, 300, 16, 16, 64, 2, torch.device(DEV))
+        search.prompts([[5] * 40, list(range(3, 20)), [7]])
+        return search
+
+    eager, replayed = begin(), begin()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    eager.step()                              # (libraries are ready before the capture)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        replayed.step()
+    for step in range(40):
+        if step:
+            eager.step()
+        graph.replay()
+        for a, b in ((eager.parents, replayed.parents), (eager.tokens, replayed.tokens),
+                     (eager.refs, replayed.refs), (eager.kv_len, replayed.kv_len),
+                     (eager.table, replayed.table), (eager.counts, replayed.counts),
+                     (eager.scores, replayed.scores)):
+            assert torch.equal(a, b), step
+    assert ex.S.device_status() == 0
