@@ -274,8 +274,8 @@ __device__ __forceinline__ uint4 load_word(const Part &p, int w)
 }
 
 // A thread's words of the step that begins at word w.  Where all of the step's
-// words are the row's, which is so but for its first and last ones, the loads
-// are not under conditions, which would make them wait for one another.
+// words are the row's, which is so but for its first and last ones, one
+// condition does for all loads.
 template <bool F32, bool PASSING>
 __device__ __forceinline__ void load_step(uint4 (&v)[kWords], const Part &p, int w, int tid)
 {

@@ -6,16 +6,16 @@
 // that need one another's results.  Each runs as one thread-block cluster: its
 // barrier is the hardware's and its words pass through shared memory, so a call
 // is one launch, needs no workspace, and nothing of one launch is left for the
-// next to find.  Clusters have up to 16 CTAs (8: a pool of 400,000 pages
-// compacted in 84 us instead of 43, all else alike).
+// next to find.  Clusters have up to 16 CTAs (8: 13.3 us instead of 10.3 for the
+// chunks below, 18.2 instead of 15.2 for the larger compaction).
 //
 // Bound: chains of loads and barriers (an L2 load 700 to 1,000 cycles, a barrier
 // of the cluster with what was written before it about as much), and issue
 // slots where one cluster goes over a whole table.  Measured on the device:
-// 4 sequences reordered 2.6 us, 512 of up to 16,001 keys 5.7 us; a step of 240
-// beams cut back, reordered and extended 11.3 us in two calls (fork 3.8, reserve
-// of no rows 4.0); chunks of 200 prompts in a pool of 430,000 pages 10.2 us in
-// two calls; a pool of 1,100 pages compacted 8.4 us, one of 336,000 with 32,500
+// 4 sequences reordered 2.5 us, 512 of up to 16,001 keys 5.7 us; a step of 240
+// beams cut back, reordered and extended 10.6 us in two calls (fork 3.8, reserve
+// of no rows 4.2); chunks of 200 prompts in a pool of 430,000 pages 10.3 us in
+// two calls; a pool of 1,100 pages compacted 8.1 us, one of 336,000 with 32,500
 // moves 15.2 us.
 #include <atomic>
 
@@ -222,7 +222,7 @@ template <int L>
 __device__ __forceinline__ uint32_t held_nibbles(const int32_t *refs, int64_t at, int64_t last, int lane)
 {
     int4 v[L];
-    if (at + chunk(L) <= last) {  // (loads under conditions of their own would wait for one another)
+    if (at + chunk(L) <= last) {  // (one condition for all loads)
 #pragma unroll
         for (int i = 0; i < L; ++i)
             v[i] = __ldcg(reinterpret_cast<const int4 *>(refs + at) + 32 * i + lane);
