@@ -597,6 +597,13 @@ constexpr int kCands = 512;
 constexpr int kSamples = 1024;
 constexpr int kFirst = 4;  // candidates of a thread that are loaded early
 
+// A candidate of a group, or none (0, 0): of equal values the one with the
+// larger `tie` comes first: the lower beam, the larger logit, the lower token.
+struct alignas(16) Candidate {
+    Value value;
+    unsigned long long tie;
+};
+
 struct JoinShared {
     // of each beam: a quarter of its score, and of its normaliser (base + off);
     // values may be three times fp32's largest number
@@ -606,16 +613,11 @@ struct JoinShared {
     float again[SMOE_MAX_BEAMS];   // the largest logit where the sum has to be taken again, else NaN
     float sum[kWarps];
     int queued;
-    Value bar;
-    Value sample[kSamples];        // the first values of each part, 0 of beams that are not live
-    // candidates
-    Value value[kCands];
-    Key key[kCands];
-    int beam[kCands];
-    // the best of each warp (select_crowd)
-    Value best_value[kWarps];
-    Key best_key[kWarps];
-    int best_beam[kWarps];
+    uint32_t bar;                  // upper half of a value
+    // upper halves of the first values of each part; 0: none, and of beams that are not live
+    alignas(16) uint32_t sample[kSamples];
+    Candidate queue[kCands];
+    Candidate best[kWarps];        // of each warp (select_crowd)
 };
 
 __device__ __forceinline__ Value value_of(const JoinShared &sh, int k, Key key)
@@ -629,33 +631,47 @@ __device__ __forceinline__ Value value_of(const JoinShared &sh, int k, Key key)
 }
 __device__ __forceinline__ float score_of(Value v) { return 4.0f * from_ordered(static_cast<uint32_t>(v >> 32)); }
 
-// Whether candidate a comes before b.
-__device__ __forceinline__ bool before(Value av, int ak, Key a, Value bv, int bk, Key b)
+// The parts of a candidate's tie.
+constexpr int kTokenBits = 22, kBeamAt = 32 + kTokenBits;
+static_assert(1 << kTokenBits == SMOE_MAX_VOCAB && SMOE_MAX_BEAMS <= 1 << (64 - kBeamAt), "bits of a tie");
+
+__device__ __forceinline__ unsigned long long tie_of(int beam, Key key)
 {
-    return av != bv ? av > bv : ak != bk ? ak < bk : a > b;
+    return static_cast<unsigned long long>(SMOE_MAX_BEAMS - 1 - beam) << kBeamAt | (key >> 32) << kTokenBits |
+           (SMOE_MAX_VOCAB - 1 - index_of(key));
+}
+__device__ __forceinline__ int beam_of(unsigned long long tie) { return SMOE_MAX_BEAMS - 1 - static_cast<int>(tie >> kBeamAt); }
+__device__ __forceinline__ int token_of(unsigned long long tie)
+{
+    return SMOE_MAX_VOCAB - 1 - static_cast<int>(tie & (SMOE_MAX_VOCAB - 1));
 }
 
-__device__ __forceinline__ void put(const smoe_beam_args &a, int group, int place, bool found, Value value, int beam,
-                                    Key key)
+__device__ __forceinline__ bool before(const Candidate &x, const Candidate &y)
+{
+    // (no branches: two threads of a warp hardly ever agree)
+    return (x.value > y.value) | ((x.value == y.value) & (x.tie > y.tie));
+}
+
+// Output number `place` of a group: a candidate, or none where its value is 0.
+__device__ __forceinline__ void put(const smoe_beam_args &a, int group, int place, const Candidate &c)
 {
     const int64_t at = (int64_t)group * a.num_out + place;
-    a.scores_out[at] = found ? score_of(value) : -INFINITY;
-    a.parents[at] = found ? group * a.beams + beam : -1;
-    a.tokens[at] = found ? index_of(key) : -1;
+    const bool found = c.value != 0;
+    a.scores_out[at] = found ? score_of(c.value) : -INFINITY;
+    a.parents[at] = found ? group * a.beams + beam_of(c.tie) : -1;
+    a.tokens[at] = found ? token_of(c.tie) : -1;
 }
 
 // Candidate `rest` of a beam's parts * num_out, whose key was `key` (a finished
-// beam has one, of its own): false where there is none.
-__device__ __forceinline__ bool candidate(const smoe_beam_args &a, const JoinShared &sh, int beam, int rest,
-                                          Value &value, Key &key)
+// beam has one, of its own).
+__device__ __forceinline__ Candidate candidate(const smoe_beam_args &a, const JoinShared &sh, int beam, int rest, Key key)
 {
-    if (sh.state[beam] == kFinished) {
-        key = key_of(0.0f, a.end_token);
-        value = ordered_value({sh.score[beam], 0.0f});
-        return rest == 0;
-    }
-    value = value_of(sh, beam, key);
-    return sh.state[beam] == kLive && key != 0;
+    const int state = sh.state[beam];
+    if (state == kFinished && rest == 0)
+        return {ordered_value({sh.score[beam], 0.0f}), tie_of(beam, key_of(0.0f, a.end_token))};
+    if (state != kLive || key == 0)
+        return {0, 0};
+    return {value_of(sh, beam, key), tie_of(beam, key)};
 }
 
 // The sum of exp(x - most) over a row, by the whole CTA: of rows with a NaN or
@@ -700,53 +716,29 @@ __device__ __noinline__ void select_crowd(const BeamArgs &b, int group, JoinShar
     const smoe_beam_args &a = b.a;
     const int tid = threadIdx.x, lane = tid & 31, per = b.parts * a.num_out, all = a.beams * per;
     const Key *keys = b.keys + (int64_t)group * all;
-    Value last_value = ~0ull;
-    Key last_key = ~0ull;
-    int last_beam = -1;
+    Candidate last = {~0ull, ~0ull};
     for (int place = 0; place < a.num_out; ++place) {
-        Value value = 0;
-        Key key = 0;
-        int beam = 0;
+        Candidate best = {0, 0};
         for (int i = tid; i < all; i += kThreads) {
-            Value v;
-            Key k = __ldcg(keys + i);
-            const int m = i / per;
-            if (candidate(a, sh, m, i - m * per, v, k) && before(last_value, last_beam, last_key, v, m, k) &&
-                before(v, m, k, value, beam, key)) {
-                value = v;
-                key = k;
-                beam = m;
-            }
+            const int beam = i / per;
+            const Candidate c = candidate(a, sh, beam, i - beam * per, __ldcg(keys + i));
+            if (before(last, c) && before(c, best))
+                best = c;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const Value v = __shfl_xor_sync(0xffffffffu, value, o);
-            const Key k = __shfl_xor_sync(0xffffffffu, key, o);
-            const int m = __shfl_xor_sync(0xffffffffu, beam, o);
-            if (before(v, m, k, value, beam, key)) {
-                value = v;
-                key = k;
-                beam = m;
-            }
+            const Candidate c = {__shfl_xor_sync(0xffffffffu, best.value, o), __shfl_xor_sync(0xffffffffu, best.tie, o)};
+            best = before(c, best) ? c : best;
         }
         __syncthreads();
-        if (lane == 0) {
-            sh.best_value[tid >> 5] = value;
-            sh.best_key[tid >> 5] = key;
-            sh.best_beam[tid >> 5] = beam;
-        }
+        if (lane == 0)
+            sh.best[tid >> 5] = best;
         __syncthreads();
         for (int w = 0; w < kWarps; ++w)
-            if (before(sh.best_value[w], sh.best_beam[w], sh.best_key[w], value, beam, key)) {
-                value = sh.best_value[w];
-                key = sh.best_key[w];
-                beam = sh.best_beam[w];
-            }
+            best = before(sh.best[w], best) ? sh.best[w] : best;
         if (tid == 0)
-            put(a, group, place, value != 0, value, beam, key);
-        last_value = value;
-        last_key = key;
-        last_beam = beam;
+            put(a, group, place, best);
+        last = best;
     }
 }
 
@@ -765,6 +757,8 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         sh.queued = 0;
         sh.bar = 0;
     }
+    if (tid < 4 && samples + tid < kSamples)
+        sh.sample[samples + tid] = 0;
     // All that a beam's warp needs is on its way at once, and so are the first
     // candidates of every thread (what belongs to beams that are not live means
     // nothing).
@@ -826,7 +820,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         if (!wrong)
             for (int i = lane; i < each && k * each + i < kSamples; i += 32) {
                 const Key t = i < 32 ? sample : __ldcg(keys + i / depth * N + i % depth);
-                sh.sample[k * each + i] = t ? value_of(sh, k, t) : 0;
+                sh.sample[k * each + i] = t ? static_cast<uint32_t>(value_of(sh, k, t) >> 32) : 0;
             }
     }
     if (__syncthreads_or(again))
@@ -845,26 +839,27 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
             __syncthreads();
         }
     for (int i = tid; i < samples; i += kThreads) {
-        const Value v = sh.sample[i];
+        // (of equal ones the earlier comes first; what is behind the samples is 0)
+        const uint32_t v = sh.sample[i];
         int place = 0;
-#pragma unroll 8
-        for (int j = 0; j < samples; ++j)
-            place += sh.sample[j] > v || (sh.sample[j] == v && j < i);
+#pragma unroll 4
+        for (int j = 0; j < samples; j += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(sh.sample + j);
+            place += ((x.x > v) | ((x.x == v) & (j < i))) + ((x.y > v) | ((x.y == v) & (j + 1 < i))) +
+                     ((x.z > v) | ((x.z == v) & (j + 2 < i))) + ((x.w > v) | ((x.w == v) & (j + 3 < i)));
+        }
         if (place == N - 1)
             sh.bar = v;
     }
     __syncthreads();
-    const Value bar = sh.bar;
+    const Value bar = static_cast<Value>(sh.bar) << 32;
     const auto offer = [&](int i, Key key) {
-        Value value;
         const int beam = i / per;
-        if (candidate(a, sh, beam, i - beam * per, value, key) && value >= bar) {
+        const Candidate c = candidate(a, sh, beam, i - beam * per, key);
+        if (c.value != 0 && c.value >= bar) {
             const int at = atomicAdd(&sh.queued, 1);
-            if (at < kCands) {
-                sh.value[at] = value;
-                sh.key[at] = key;
-                sh.beam[at] = beam;
-            }
+            if (at < kCands)
+                sh.queue[at] = c;
         }
     };
 #pragma unroll
@@ -880,22 +875,16 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         return;
     }
     for (int i = tid; i < n; i += kThreads) {
-        const Value value = sh.value[i];
-        const Key key = sh.key[i];
-        const int beam = sh.beam[i];
-        int place = 0, same = 0;
+        const Candidate c = sh.queue[i];
+        int place = 0;
 #pragma unroll 8
-        for (int j = 0; j < n; ++j) {
-            place += sh.value[j] > value;
-            same += sh.value[j] == value;
-        }
-        for (int j = 0; j < n && same > 1; ++j)
-            place += sh.value[j] == value && before(value, sh.beam[j], sh.key[j], value, beam, key);
+        for (int j = 0; j < n; ++j)
+            place += before(sh.queue[j], c);
         if (place < N)
-            put(a, group, place, true, value, beam, key);
+            put(a, group, place, c);
     }
     if (tid >= n && tid < N)
-        put(a, group, tid, false, 0, 0, 0);
+        put(a, group, tid, {0, 0});
 }
 
 union BeamShared {
