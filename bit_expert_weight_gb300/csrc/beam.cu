@@ -433,7 +433,7 @@ __device__ __forceinline__ void rank_keys(const Key *keys, int n, int num_out, K
     for (int i = tid; i < n; i += kThreads) {
         const Key k = keys[i];
         int above = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < n; ++j)
             above += keys[j] > k;
         if (above < num_out)
@@ -842,7 +842,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         // (of equal ones the earlier comes first; what is behind the samples is 0)
         const uint32_t v = sh.sample[i];
         int place = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < samples; j += 4) {
             const uint4 x = *reinterpret_cast<const uint4 *>(sh.sample + j);
             place += ((x.x > v) | ((x.x == v) & (j < i))) + ((x.y > v) | ((x.y == v) & (j + 1 < i))) +
