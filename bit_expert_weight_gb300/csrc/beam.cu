@@ -10,15 +10,15 @@
 // fp32); the few words whose largest is among the part's are read again, and
 // their logits ranked, as 64-bit keys (logit, then the lower index).  (Choosing
 // while reading, by sorted lists or queues of each warp, took 52 to 127 us for 512
-// rows of 151,936 instead of 32.)  A part's sum and its largest keys, in order,
+// rows of 151,936 instead of 31.)  A part's sum and its largest keys, in order,
 // go to the workspace; the CTA that arrives last of a group's joins its rows'
 // parts, and then the rows' candidates by their values.
 //
 // Bound: HBM while the rows are read (12 logits of bf16 per cycle and SM, all
 // that comes), then a chain of latencies: words read again, the arrival, the
 // join.  Measured: 512 rows of 151,936 bf16 logits, 16 of each group of 8, 433 of
-// them read: 31.6 us, 4.2 TB/s; 60 fp32 rows of 100,003 11.7 us; 320 rows of 65,536
-// of which 0.3 % are allowed 19.9 us; 4 rows of 32,000 6.7 us.
+// them read: 30.7 us, 4.3 TB/s; 60 fp32 rows of 100,003 11.5 us; 320 rows of 65,536
+// of which 0.3 % are allowed 18.1 us; 4 rows of 32,000 6.6 us.
 #include <float.h>
 #include <math.h>
 

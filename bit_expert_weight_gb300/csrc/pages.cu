@@ -14,9 +14,9 @@
 // slots where one cluster goes over a whole table.  Measured on the device:
 // 4 sequences reordered 2.5 us, 512 of up to 16,001 keys 5.7 us; a step of 240
 // beams cut back, reordered and extended 10.6 us in two calls (fork 3.8, reserve
-// of no rows 4.2); chunks of 200 prompts in a pool of 430,000 pages 10.3 us in
-// two calls; a pool of 1,100 pages compacted 8.1 us, one of 336,000 with 32,500
-// moves 15.2 us.
+// of no rows 4.2); chunks of 200 prompts in a pool of 430,000 pages 10.2 us in
+// two calls; a pool of 1,100 pages compacted 7.3 us, one of 336,000 with 32,500
+// moves 15.3 us.
 #include <atomic>
 
 #include "cluster.cuh"

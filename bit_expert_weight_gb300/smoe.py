@@ -686,7 +686,7 @@ def _device_array(name, t, dtype, numel, dev):
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on the device of the "
                          "call's other tensors")
-    if t.numel() < numel:
+    if numel and t.numel() < numel:
         raise ValueError(f"{name} must have {numel} elements")
     return t.data_ptr()
 
