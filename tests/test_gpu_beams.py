@@ -235,6 +235,36 @@ def test_large_logits_close_together(S, ws, dtype, spread):
             select(S, ws, x.to(dtype), rand(4 // K, K, seed=K), n)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_largest_vocabulary(S, ws, dtype):
+    """2^22 tokens, the best ones at both ends and alike."""
+    V = 1 << 22
+    x = rand(2, V, seed=6, dtype=dtype)
+    x[0, [0, V // 2, V - 1]] = 30.0
+    x[1, [V - 2, V - 1]] = 30.0
+    for K in (1, 2):
+        s, p, t = select(S, ws, x, torch.zeros(2 // K, K, device=DEV), 5)
+        if K == 1:
+            assert t[0, :3].tolist() == [0, V // 2, V - 1] and t[1, :2].tolist() == [V - 2, V - 1]
+
+
+def test_rows_far_apart(S, ws):
+    """Rows whose offsets pass 32 bits."""
+    buf = torch.empty(2 ** 32 + 20_000, dtype=BF16, device=DEV)
+    x = torch.as_strided(buf, (3, 9_001), (2 ** 31 + 1, 1), 5)
+    x.copy_(rand(3, 9_001, seed=2, dtype=BF16))
+    a = S.beam_select(x, rand(1, 3, seed=3), 8, ws)
+    assert S.device_status() == 0
+    check_selection(a, x.clone(), rand(1, 3, seed=3), 8)
+
+
+def test_end_token_without_last_tokens(S, ws):
+    x = rand(6, 500, seed=1)
+    a = select(S, ws, x, rand(2, 3, seed=2), 3, end_token=2)
+    b = S.beam_select(x, rand(2, 3, seed=2), 3, ws)
+    assert all(torch.equal(y, z) for y, z in zip(a, b))
+
+
 def test_first_call_in_a_capture(S):
     """A process whose first calls are made while a graph is captured."""
     import subprocess

@@ -286,6 +286,72 @@ def test_tables_of_no_columns(S):
     d.check(p)
 
 
+def test_tables_past_32_bits(S):
+    """The last rows' entries are more than 2^31 entries from the first."""
+    n, W, P = 1_100, 2_000_000, 300
+    table = torch.full((n, W), -9, dtype=I32, device=DEV)
+    refs, kv = torch.zeros(P, dtype=I32, device=DEV), torch.zeros(n, dtype=I32, device=DEV)
+    start = torch.zeros(n + 1, dtype=I32, device=DEV)
+    start[1:] += 3                            # rows of the first and of the last two sequences
+    start[n - 1:] += 40
+    start[n:] += 30
+    copies, counts = torch.zeros(n, 2, dtype=I32, device=DEV), ints([0, 0])
+    S.pages_reserve(refs, kv, table, 16, start, copies, counts)
+    assert counts.tolist() == [0, P - 6]
+    assert table[0, :2].tolist() == [0, -9]
+    assert table[n - 2, :4].tolist() == [1, 2, 3, -9] and table[n - 1, :3].tolist() == [4, 5, -9]
+    parent = torch.arange(n, dtype=I32, device=DEV)
+    parent[0], parent[n - 1] = n - 2, -1
+    S.pages_fork(refs, kv, table, 16, parent)
+    assert table[0, :4].tolist() == [1, 2, 3, -9] and refs[:7].tolist() == [0, 2, 2, 2, 0, 0, 0]
+    moves = torch.zeros(P // 2, 2, dtype=I32, device=DEV)
+    S.pages_compact(refs, kv, table, 16, moves, counts)
+    assert counts.tolist() == [1, 3] and moves[0].tolist() == [3, 0]
+    assert table[n - 2, :4].tolist() == [1, 2, 0, -9] and table[0, :4].tolist() == [1, 2, 0, -9]
+    assert S.device_status() == 0
+
+
+def test_large_pools(S):
+    """70 million pages: the free ones far behind, and a compaction of half of them."""
+    P, page = 70_000_001, 16
+    refs = torch.ones(P, dtype=I32, device=DEV)
+    free = [5, 12_345_678, P - 3, P - 1]
+    refs[free] = 0
+    kv, table = ints([0, 0]), torch.full((2, 9), -9, dtype=I32, device=DEV)
+    copies, counts = torch.zeros(P // 2, 2, dtype=I32, device=DEV), ints([0, 0])
+    S.pages_reserve(refs, kv, table, page, ints([0, 17, 50]), copies, counts)
+    assert counts.tolist() == [0, -1] and S.device_status() == -5 and kv.tolist() == [0, 0]
+    S.pages_reserve(refs, kv, table, page, ints([0, 17, 40]), copies, counts)
+    assert counts.tolist() == [0, 0] and bool((refs == 1).all())
+    assert table[:, :3].tolist() == [free[:2] + [-9], free[2:] + [-9]]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    refs.copy_(torch.randint(0, 3, (P,), generator=g, device=DEV, dtype=I32))
+    refs[free] = 1
+    was = refs.clone()
+    held = (was > 0).nonzero()[:, 0]
+    n = held.numel()
+    source = held[held >= n]
+    target = (was[:n] <= 0).nonzero()[:, 0]
+    for out in (None, torch.full((P,), 9, dtype=I32, device=DEV)):
+        refs.copy_(was)
+        before = table.clone()
+        into = torch.empty_like(table) if out is not None else None
+        S.pages_compact(refs, kv, table if out is not None else before, page, copies, counts,
+                        refs_out=out, page_table_out=into)
+        assert S.device_status() == 0 and counts.tolist() == [source.numel(), n]
+        m = copies[:source.numel()].long()
+        assert torch.equal(m[:, 0], source) and torch.equal(m[:, 1], target)
+        want = was.clone()
+        want[target] = was[source]
+        want[n:] = 0
+        assert torch.equal(want, refs if out is None else out)
+        now = (before if out is None else into)[:, :2]
+        moved = {int(a): int(b) for a, b in zip(source[-3:], target[-3:])}
+        assert now[0, 0] == 5 and now[1, 1] == moved.get(P - 1, P - 1)
+        assert now[0, 1] == (12_345_678 if 12_345_678 < n else None)
+
+
 # --------------------------------------------------------------- copies
 
 def caches(layers, P, Hkv, page, D, joined, seed=0):
@@ -349,6 +415,21 @@ def test_copy_records_bad_pages_and_counts(S):
         assert S.device_status() == -5 and S.device_status() == 0
         for xs, ws in zip((k, v), want):
             assert all(same_bits(a, b) for a, b in zip(xs, ws))
+
+
+def test_copies_past_32_bits(S):
+    """Pages that are more than 2^31 elements from the first."""
+    P = 2_200_000
+    k = torch.zeros(P, 1, 16, 64, dtype=BF16, device=DEV)
+    v = torch.zeros(P, 1, 16, 64, dtype=BF16, device=DEV)
+    (a,), (b,) = caches(1, 3, 1, 16, 64, False)
+    k[:3], v[:3] = a, b
+    S.pages_copy(k, v, ints([[0, P - 1], [2, P - 2]]), ints([2]))
+    S.pages_copy(k, v, ints([[P - 1, 7]]), ints([1]))
+    assert S.device_status() == 0
+    for x, y in ((k, a), (v, b)):
+        assert same_bits(x[P - 1], y[0]) and same_bits(x[P - 2], y[2]) and same_bits(x[7], y[0])
+        assert not bool(x[8:P - 2].view(torch.int16).any())
 
 
 def test_captured_steps(S):
