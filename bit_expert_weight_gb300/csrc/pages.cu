@@ -298,12 +298,13 @@ struct Ranks {
     }
 };
 
-// Held pages of a run.
+// Held pages of a run, and (first_held) the nibbles of its first chunk.
 template <int L>
-__device__ __forceinline__ int count_held(const int32_t *refs, Run r, int lane)
+__device__ __forceinline__ int count_held(const int32_t *refs, Run r, int lane, uint32_t &first_held)
 {
-    int n = 0;
-    for (int64_t at = r.first; at < r.last; at += chunk(L))
+    first_held = r.first < r.last ? held_nibbles<L>(refs, r.first, r.last, lane) : 0;
+    int n = __popc(first_held);
+    for (int64_t at = r.first + chunk(L); at < r.last; at += chunk(L))
         n += __popc(held_nibbles<L>(refs, at, r.last, lane));
     return warp_sum(n);
 }
@@ -366,6 +367,8 @@ struct ReserveShared {
     int need[SMOE_MAX_SEQS];
     int key[kSlots], writers[kSlots], first[kSlots];
     int warp_need[kWarps], warp_copies[kWarps];
+    uint32_t free[kWarps][32];    // of each run's chunk: the lanes' nibbles
+    int rank[kWarps];             // of its first free page
 };
 
 __device__ __forceinline__ int slot_of_page(ReserveShared &sh, int page)
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             holders[i] = -1;  // (to be looked up)
         }
     }
-    const int mine = static_cast<int>(max(run.last - run.first, (int64_t)0)) - count_held<L>(p.refs, run, lane);
+    uint32_t held;
+    const int mine = static_cast<int>(max(run.last - run.first, (int64_t)0)) - count_held<L>(p.refs, run, lane, held);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (holders[i] < 0 && page[i] >= 0 && page[i] < p.num_pages)
@@ -504,49 +508,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             counts[1] = num_free - needed;
         }
     }
-    // A run's nibbles are dealt to L warps, so that no lane has more than 4 pages
-    // of a chunk to give.
-    for (int t = warp; t < kWarps * L; t += kWarps) {
-        const int number = run_of_warp(t / L), slice = t % L;
-        int rank = counted_before(sh.runs, number, lane);
-        if (rank >= needed)
-            break;
-        const Run r = run_at(length, number, p.num_pages);
-        for (int64_t at = r.first; at < r.last && rank < needed; at += chunk(L)) {
-            const uint32_t w = ~held_nibbles<L>(p.refs, at, r.last, lane) & nibbles_below<L>(at, r.last, lane);
-            const Ranks<L> ranks(w, lane);
-            int k = rank + ranks.at(slice);
-            rank += ranks.all();
-            unsigned free = w >> (4 * slice) & 15u;
-            if (!free || k >= needed)
-                continue;
-            // the first sequence whose pages end behind rank k; the next ones follow
-            int at_given = 0;
-            for (int hi = num_given - 1; at_given < hi;) {
-                const int mid = (at_given + hi) / 2;
-                if (sh.given[mid].end > k)
-                    hi = mid;
-                else
-                    at_given = mid + 1;
-            }
-            Given g = sh.given[at_given];
-            int begin = at_given > 0 ? sh.given[at_given - 1].end : 0;
-            for (; free && k < needed; free &= free - 1, ++k) {
-                const int page = static_cast<int>(at) + 128 * slice + 4 * lane + __ffs(free) - 1;
-                if (k >= g.end) {
-                    begin = g.end;
-                    g = sh.given[++at_given];
-                }
-                if (g.copy >= 0 && k == begin) {
-                    const int old = sh.page[g.seq];
-                    copies[2 * g.copy] = old;
-                    copies[2 * g.copy + 1] = page;
-                    atomicAdd(p.refs + old, -1);
-                }
-                p.page_table[(int64_t)g.seq * p.table_stride + g.entry + (k - begin)] = page;
-                p.refs[page] = 1;
-            }
+    // Gives the free pages of a chunk's slice away; w: the chunk's free ones,
+    // the first of rank `rank`.
+    const auto give = [&](int64_t at, int slice, uint32_t w, int rank) {
+        int k = rank + Ranks<L>(w, lane).at(slice);
+        unsigned free = w >> (4 * slice) & 15u;
+        if (!free || k >= needed)
+            return;
+        // the first sequence whose pages end behind rank k; the next ones follow
+        int at_given = 0;
+        for (int hi = num_given - 1; at_given < hi;) {
+            const int mid = (at_given + hi) / 2;
+            if (sh.given[mid].end > k)
+                hi = mid;
+            else
+                at_given = mid + 1;
         }
+        Given g = sh.given[at_given];
+        int begin = at_given > 0 ? sh.given[at_given - 1].end : 0;
+        for (; free && k < needed; free &= free - 1, ++k) {
+            const int page = static_cast<int>(at) + 128 * slice + 4 * lane + __ffs(free) - 1;
+            if (k >= g.end) {
+                begin = g.end;
+                g = sh.given[++at_given];
+            }
+            if (g.copy >= 0 && k == begin) {
+                const int old = sh.page[g.seq];
+                copies[2 * g.copy] = old;
+                copies[2 * g.copy + 1] = page;
+                atomicAdd(p.refs + old, -1);
+            }
+            p.page_table[(int64_t)g.seq * p.table_stride + g.entry + (k - begin)] = page;
+            p.refs[page] = 1;
+        }
+    };
+    // Each warp looks at its own run, chunk by chunk, before any page of the
+    // chunk is given away: what is given is held from then on.  With L > 1 the
+    // chunks of the CTA's runs are then dealt out by slices, so that no lane has
+    // more than 4 pages to give.
+    int rank = counted_before(sh.runs, run_of_warp(warp), lane);
+    for (int64_t at = run.first;; at += chunk(L)) {
+        const bool more = at < run.last && rank < needed;
+        if (L > 1 ? !__syncthreads_or(more) : !more)
+            break;
+        if (more && at > run.first)
+            held = held_nibbles<L>(p.refs, at, run.last, lane);
+        const uint32_t free = more ? ~held & nibbles_below<L>(at, run.last, lane) : 0;
+        const int first = rank;
+        rank += warp_sum(__popc(free));
+        if (L == 1) {
+            give(at, 0, free, first);
+            continue;
+        }
+        sh.free[warp][lane] = free;
+        sh.rank[warp] = first;
+        __syncthreads();
+        for (int t = warp; t < kWarps * L && sh.rank[t / L] < needed; t += kWarps)
+            give(run_of_warp(t / L) * length + (at - run.first), t % L, sh.free[t / L][lane], sh.rank[t / L]);
     }
 }
 
@@ -657,7 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
-    const int mine = count_held<L>(p.refs, run, lane);
+    uint32_t first_held;
+    const int mine = count_held<L>(p.refs, run, lane, first_held);
     share_counts(sh.runs, mine, tid);
     const int n = counted(sh.runs, lane), before = counted_before(sh.runs, run_of_warp(warp), lane);
     // The free pages below n, by their rank among the free.

@@ -354,6 +354,37 @@ def test_large_pools(S):
 
 # --------------------------------------------------------------- copies
 
+@pytest.mark.parametrize("P, n, W, chance", [
+    (140_003, 40, 1_500, 0.5), (430_000, 200, 1_000, 0.5), (524_288, 2_000, 130, 0.3),
+    (1_700_011, 100, 9_000, 0.5), (5_000_000, 64, 50_000, 0.1), (9_000_001, 2_048, 4_000, 0.05)], ids=str)
+def test_many_pages_given_at_once(S, P, n, W, chance):
+    """Almost all that a large pool has left, given away by one call, time after time: each
+    page of the pool is looked at while others are given."""
+    gen = torch.Generator(device=DEV).manual_seed(P)
+    for turn in range(6):
+        refs = (torch.rand(P, device=DEV, generator=gen) < chance).to(I32)
+        refs[:(turn * P) // 7] *= turn % 2
+        free = (refs <= 0).nonzero()[:, 0]
+        need = torch.randint(0, 2 * min(W, len(free) // n), (n,), device=DEV, generator=gen).clamp(max=W)
+        need = (need * min(1.0, len(free) / max(1, int(need.sum())))).long()
+        start = torch.cat([torch.zeros(1, dtype=torch.long, device=DEV), need.cumsum(0)])
+        table = torch.full((n, W), -9, dtype=I32, device=DEV)
+        kv = torch.zeros(n, dtype=I32, device=DEV)
+        copies = torch.full((n, 2), -5, dtype=I32, device=DEV)
+        counts = torch.full((2,), -5, dtype=I32, device=DEV)
+        want_refs, total = refs.clone(), int(start[-1])
+        want_refs[free[:total]] = 1
+        own = torch.arange(W, device=DEV) < need[:, None]
+        want = table.clone()
+        want[own] = free[:total].to(I32)
+        S.pages_reserve(refs, kv, table, 16, (16 * start).to(I32), copies, counts)
+        assert counts.tolist() == [0, len(free) - total], turn
+        assert torch.equal(kv, (16 * need).to(I32)) and bool((copies == -5).all())
+        assert torch.equal(table, want), turn
+        assert torch.equal(refs, want_refs), turn
+    assert S.device_status() == 0
+
+
 def caches(layers, P, Hkv, page, D, joined, seed=0):
     g = torch.Generator(device=DEV)
     g.manual_seed(seed)
