@@ -17,6 +17,8 @@
 // of no rows 4.2); chunks of 200 prompts in a pool of 430,000 pages 10.2 us in
 // two calls; a pool of 1,100 pages compacted 7.3 us, one of 336,000 with 32,500
 // moves 15.3 us.
+#include <limits.h>
+
 #include <atomic>
 
 #include "cluster.cuh"
@@ -578,7 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kBatch = 4;  // loads of a thread that are in flight together
 constexpr int kColumns = 128;
 
-__device__ __forceinline__ int went_to(int page) { return -1 - page; }
+// (of a page that is free: no count is below -2^30, so that none is taken for this)
+__device__ __forceinline__ int went_to(int page) { return INT_MIN + page; }
+__device__ __forceinline__ bool is_told(int mark, int n) { return mark < INT_MIN + n; }
+__device__ __forceinline__ int told(int mark) { return mark - INT_MIN; }
 
 // What stays where it is, into other refs: a thread of `step` has number `first`.
 __device__ __forceinline__ void stay_pass(const smoe_page_pool &p, int32_t *refs_out, int n, int64_t first, int64_t step)
@@ -638,8 +643,8 @@ __device__ __forceinline__ void table_pass(const smoe_page_pool &p, const int32_
 #pragma unroll
     for (int i = 0; i < kColumns / 32; ++i) {
         const bool above = page[i] >= n && page[i] < p.num_pages;
-        bad = bad || static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.num_pages) || (above && to[i] >= 0);
-        out[min(j0 + 32 * i, pages - 1)] = above && to[i] < 0 ? went_to(to[i]) : page[i];
+        bad = bad || static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.num_pages) || (above && !is_told(to[i], n));
+        out[min(j0 + 32 * i, pages - 1)] = above && is_told(to[i], n) ? told(to[i]) : page[i];
     }
     if (bad)
         set_status(status, kStatusBadArg);

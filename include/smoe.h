@@ -775,9 +775,9 @@ smoe_status smoe_beam_select(const smoe_beam_args *args, void *workspace, size_t
  * ceil(kv_len[s] / page_size) entries of its table row name; refs[p] counts
  * the sequences whose row names page p there, and whatever else of the
  * program holds it (a prefix kept for later requests adds 1 itself).  A page
- * is free where that is not above 0.  All arrays are DEVICE int32 and belong to
- * one stream at a time.  Entries of a row past a sequence's pages are neither
- * read nor changed. */
+ * is free where that is not above 0 (nor is it ever below -2^30).  All arrays
+ * are DEVICE int32 and belong to one stream at a time.  Entries of a row past a
+ * sequence's pages are neither read nor changed. */
 typedef struct {
     int32_t *refs;             /* [num_pages], 16-byte aligned                */
     int32_t *kv_len;           /* [num_seqs]                                  */

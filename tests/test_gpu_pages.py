@@ -252,6 +252,29 @@ def test_compact_records_bad_rows(S):
     assert d.refs.tolist() == [1] * 8 + [0] * 42
 
 
+@pytest.mark.parametrize("P", [40, 140_003])   # by one launch, by four
+@pytest.mark.parametrize("count", [0, -1, -3, -(2 ** 30)])
+@pytest.mark.parametrize("apart", [False, True])
+def test_compact_of_free_pages_below_zero(S, P, count, apart):
+    """An entry that names a page which nobody holds stays and is recorded, whatever is in its count."""
+    p = Pool(P, 16, 2, 4)
+    p.kv, p.table = [48, 30], [[1, 7, 9, -9], [3, 12, -9, -9]]     # page 9 has no holder
+    p.refs = [count] * P
+    for q in (1, 3, 7, 12):
+        p.refs[q] = 1
+    d = OnDevice(p)
+    out = dict(refs_out=torch.full((P,), 99, dtype=I32, device=DEV),
+               page_table_out=torch.full((2, 4), -9, dtype=I32, device=DEV)) if apart else {}
+    copies = torch.full((P // 2, 2), -5, dtype=I32, device=DEV)
+    counts = torch.zeros(2, dtype=I32, device=DEV)
+    S.pages_compact(*d.pool, copies, counts, **out)
+    assert counts.tolist() == [2, 4] and copies[:3].tolist() == [[7, 0], [12, 2], [-5, -5]]
+    refs, table = out.get("refs_out", d.refs).tolist(), out.get("page_table_out", d.table).tolist()
+    assert refs[:4] == [1] * 4 and all(r <= 0 for r in refs[4:])
+    assert table == [[1, 0, 9, -9], [3, 2, -9, -9]]
+    assert S.device_status() == -5
+
+
 def test_no_sequences_and_full_pools(S):
     p = Pool(400, 16, 1, 400)
     p.reserve([400 * 16])
