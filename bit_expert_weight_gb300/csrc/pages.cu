@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t held_before = before;
     for (int64_t at = run.first; at < run.last && at < n; at += chunk(L)) {
         const uint32_t in = nibbles_below<L>(at, min(run.last, (int64_t)n), lane);
-        const uint32_t held = held_nibbles<L>(p.refs, at, run.last, lane) & in;
+        const uint32_t held = (at == run.first ? first_held : held_nibbles<L>(p.refs, at, run.last, lane)) & in;
         const Ranks<L> ranks(~held & in, lane);
         const int64_t to = at - held_before;  // free pages before the chunk
 #pragma unroll
@@ -718,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t at = run.first; at < run.last; at += chunk(L)) {
         if (at + chunk(L) <= n)
             continue;
-        const uint32_t held = held_nibbles<L>(p.refs, at, run.last, lane) & ~nibbles_below<L>(at, n, lane);
+        const uint32_t held = (at == run.first ? first_held : held_nibbles<L>(p.refs, at, run.last, lane)) &
+                              ~nibbles_below<L>(at, n, lane);
         const Ranks<L> ranks(held, lane);
 #pragma unroll
         for (int i = 0; i < L; ++i) {
