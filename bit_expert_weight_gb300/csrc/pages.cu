@@ -13,10 +13,12 @@
 // of the cluster with what was written before it about as much), and issue
 // slots where one cluster goes over a whole table.  Measured on the device:
 // 4 sequences reordered 2.5 us, 512 of up to 16,001 keys 5.7 us; a step of 240
-// beams cut back, reordered and extended 10.6 us in two calls (fork 3.8, reserve
-// of no rows 4.2); chunks of 200 prompts in a pool of 430,000 pages 10.2 us in
-// two calls; a pool of 1,100 pages compacted 7.3 us, one of 336,000 with 32,500
-// moves 15.3 us.
+// beams cut back, reordered and extended 10.5 us in two calls (fork 3.9, reserve
+// of no rows 4.1); chunks of 200 prompts in a pool of 430,000 pages 10.1 us in
+// two calls; a pool of 1,100 pages compacted 7.4 us, one of 336,000 with 32,500
+// moves 14.3 us.  A call's instructions are read from L2 once each, a latency at
+// a time, so loops over chunks and passes are not unrolled (the smaller
+// compaction 7.9 us unrolled, with 40 KB of them; 7.4).
 #include <limits.h>
 
 #include <atomic>
@@ -304,17 +306,21 @@ struct Ranks {
 template <int L>
 __device__ __forceinline__ int count_held(const int32_t *refs, Run r, int lane, uint32_t &first_held)
 {
-    first_held = r.first < r.last ? held_nibbles<L>(refs, r.first, r.last, lane) : 0;
-    int n = __popc(first_held);
-    for (int64_t at = r.first + chunk(L); at < r.last; at += chunk(L))
-        n += __popc(held_nibbles<L>(refs, at, r.last, lane));
+    int n = 0;
+    first_held = 0;
+#pragma unroll 1
+    for (int64_t at = r.first; at < r.last; at += chunk(L)) {
+        const uint32_t w = held_nibbles<L>(refs, at, r.last, lane);
+        first_held = at == r.first ? w : first_held;
+        n += __popc(w);
+    }
     return warp_sum(n);
 }
 
 // Counts of every run.
 struct RunCounts {
     int own[kWarps];
-    int run[kMaxCluster * kWarps];
+    alignas(16) int run[kMaxCluster * kWarps];
 };
 
 // `mine`: the count of the warp's run, the same in all its lanes.  The kernel
@@ -331,18 +337,21 @@ __device__ __forceinline__ void share_counts(RunCounts &rc, int mine, int tid)
     cluster_sync();
 }
 
-// What the runs before r counted, by a warp.
-__device__ __forceinline__ int counted_before(const RunCounts &rc, int r, int lane)
+// What the runs before r counted, and all of them, by a warp.
+struct Counted {
+    int before, all;
+};
+__device__ __forceinline__ Counted counted(const RunCounts &rc, int r, int lane)
 {
-    int n = 0;
-    for (int i = lane; i < r; i += 32)
-        n += rc.run[i];
-    return warp_sum(n);
-}
-
-__device__ __forceinline__ int counted(const RunCounts &rc, int lane)
-{
-    return counted_before(rc, static_cast<int>(cluster_size()) * kWarps, lane);
+    Counted c = {0, 0};
+#pragma unroll
+    for (int i = 4 * lane; i < kMaxCluster * kWarps; i += 128) {
+        const int4 v = i < static_cast<int>(cluster_size()) * kWarps ? *reinterpret_cast<const int4 *>(rc.run + i)
+                                                                       : make_int4(0, 0, 0, 0);
+        c.all += v.x + v.y + v.z + v.w;
+        c.before += (i < r ? v.x : 0) + (i + 1 < r ? v.y : 0) + (i + 2 < r ? v.z : 0) + (i + 3 < r ? v.w : 0);
+    }
+    return {warp_sum(c.before), warp_sum(c.all)};
 }
 
 // ---------------------------------------------------------------- reserve
@@ -490,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    const int num_free = counted(sh.runs, lane);
+    const Counted free_pages = counted(sh.runs, run_of_warp(warp), lane);
+    const int num_free = free_pages.all;
     const bool lead = cluster_rank() == 0;
     if (bad || needed > num_free) {
         if (lead && tid == 0) {
@@ -548,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunk is given away: what is given is held from then on.  With L > 1 the
     // chunks of the CTA's runs are then dealt out by slices, so that no lane has
     // more than 4 pages to give.
-    int rank = counted_before(sh.runs, run_of_warp(warp), lane);
+    int rank = free_pages.before;
     for (int64_t at = run.first;; at += chunk(L)) {
         const bool more = at < run.last && rank < needed;
         if (L > 1 ? !__syncthreads_or(more) : !more)
@@ -576,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // then the moves are gone through as a list, and the tables.  Meanwhile the
 // entry of a moved page in refs_out (which will be 0) says where it went.  A
 // small pool's are done with by the same cluster; a large one's by launches of
-// the whole device (336,000 pages, 480 sequences: 15.2 us; by the cluster 20.3).
+// the whole device (336,000 pages, 480 sequences: 14.3 us; by the cluster 20.3).
 constexpr int kBatch = 4;  // loads of a thread that are in flight together
 constexpr int kColumns = 128;
 
@@ -589,6 +599,7 @@ __device__ __forceinline__ int told(int mark) { return mark - INT_MIN; }
 __device__ __forceinline__ void stay_pass(const smoe_page_pool &p, int32_t *refs_out, int n, int64_t first, int64_t step)
 {
     const bool whole = (reinterpret_cast<uintptr_t>(refs_out) & 15) == 0;
+#pragma unroll 1
     for (int64_t q = 4 * first; q < p.num_pages; q += 4 * step) {
         const int4 v = refs_at(p.refs, q, p.num_pages);
         if (whole && q >= n && q + 4 <= p.num_pages && v.x <= 0 && v.y <= 0 && v.z <= 0 && v.w <= 0) {
@@ -606,6 +617,7 @@ __device__ __forceinline__ void stay_pass(const smoe_page_pool &p, int32_t *refs
 __device__ __forceinline__ void move_pass(const smoe_page_pool &p, int32_t *refs_out, const int32_t *copies, int moves,
                                           int first, int step)
 {
+#pragma unroll 1
     for (int i0 = first; i0 < moves; i0 += kBatch * step) {
         int2 m[kBatch];
         int c[kBatch];
@@ -652,6 +664,7 @@ __device__ __forceinline__ void table_pass(const smoe_page_pool &p, const int32_
 
 __device__ __forceinline__ void clear_pass(int32_t *refs_out, const int32_t *copies, int moves, int first, int step)
 {
+#pragma unroll 1
     for (int i0 = first; i0 < moves; i0 += kBatch * step) {
         int from[kBatch];
 #pragma unroll
@@ -683,9 +696,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t first_held;
     const int mine = count_held<L>(p.refs, run, lane, first_held);
     share_counts(sh.runs, mine, tid);
-    const int n = counted(sh.runs, lane), before = counted_before(sh.runs, run_of_warp(warp), lane);
+    const Counted held_pages = counted(sh.runs, run_of_warp(warp), lane);
+    const int n = held_pages.all, before = held_pages.before;
     // The free pages below n, by their rank among the free.
     int64_t held_before = before;
+#pragma unroll 1
     for (int64_t at = run.first; at < run.last && at < n; at += chunk(L)) {
         const uint32_t in = nibbles_below<L>(at, min(run.last, (int64_t)n), lane);
         const uint32_t held = (at == run.first ? first_held : held_nibbles<L>(p.refs, at, run.last, lane)) & in;
@@ -715,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // The held pages from n on, by their rank.
     int64_t rank = max(before - sh.under, 0);
+#pragma unroll 1
     for (int64_t at = run.first; at < run.last; at += chunk(L)) {
         if (at + chunk(L) <= n)
             continue;
@@ -743,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     const int shift = log2_of(p.page_size), warps = cluster_size() * kWarps;
     const int wide = (p.table_stride + kColumns - 1) / kColumns;
+#pragma unroll 1
     for (int u = cluster_rank() * kWarps + warp; u < wide * p.num_seqs; u += warps) {
         const int s = u / wide, j0 = u % wide * kColumns, len = p.kv_len[s];
         if (!valid_len(p, len))
