@@ -17,8 +17,10 @@
 // Bound: HBM while the rows are read (12 logits of bf16 per cycle and SM, all
 // that comes), then a chain of latencies: words read again, the arrival, the
 // join.  Measured: 512 rows of 151,936 bf16 logits, 16 of each group of 8, 433 of
-// them read: 30.7 us, 4.3 TB/s; 60 fp32 rows of 100,003 11.5 us; 320 rows of 65,536
-// of which 0.3 % are allowed 18.1 us; 4 rows of 32,000 6.6 us.
+// them read: 30.6 us, 4.3 TB/s; 60 fp32 rows of 100,003 11.1 us; 320 rows of 65,536
+// of which 0.3 % are allowed 18.2 us; 4 rows of 32,000 6.5 us.  (Small calls wait
+// for instructions too, each read once: loops that a call goes round in once or
+// twice are not unrolled; with 92 KB of them, not 72, the fp32 rows took 11.5 us.)
 #include <float.h>
 #include <math.h>
 
@@ -112,22 +114,20 @@ __device__ __forceinline__ float logit_at(const uint4 &v, int e)
     return F32 ? __uint_as_float(u[e]) : e & 1 ? bf16hi_to_f32(u[e / 2]) : bf16lo_to_f32(u[e / 2]);
 }
 
-// Word w of a row (from the aligned word that the row begins in), -inf in the
-// places that are not the row's.
+// A word that is not all the row's, its logits one by one; -inf in the other
+// places.
 template <bool F32>
-__device__ __forceinline__ uint4 load_word(const uint8_t *base, int first, int vocab, int w, int end)
+__device__ __noinline__ uint4 edge_word(const uint8_t *base, int first, int vocab, int w)
 {
     constexpr int kP = kPer<F32>;
     const int at = w * kP - first;  // index of the word's first logit
-    if (w < end && at >= 0 && at + kP <= vocab)
-        return __ldcg(reinterpret_cast<const uint4 *>(base) + w);
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         u[i] = F32 ? 0xff800000u : 0xff80ff80u;
 #pragma unroll
         for (int e = i * kP / 4; e < (i + 1) * kP / 4; ++e)
-            if (w < end && at + e >= 0 && at + e < vocab) {
+            if (at + e >= 0 && at + e < vocab) {
                 if (F32) {
                     u[i] = reinterpret_cast<const uint32_t *>(base)[w * kP + e];
                 } else {
@@ -137,6 +137,19 @@ __device__ __forceinline__ uint4 load_word(const uint8_t *base, int first, int v
             }
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Word w of a row (from the aligned word that the row begins in), -inf in the
+// places that are not the row's.
+template <bool F32>
+__device__ __forceinline__ uint4 load_word(const uint8_t *base, int first, int vocab, int w, int end)
+{
+    constexpr int kP = kPer<F32>;
+    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;
+    const int at = w * kP - first;
+    if (w < end && at >= 0 && at + kP <= vocab)
+        return __ldcg(reinterpret_cast<const uint4 *>(base) + w);
+    return w < end ? edge_word<F32>(base, first, vocab, w) : make_uint4(kNone, kNone, kNone, kNone);
 }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
@@ -326,6 +339,7 @@ __device__ __forceinline__ bool collect(PartShared &sh, const Part &p, float bar
     const int hits = sh.hits;
     if (hits > kHits)
         return false;
+#pragma unroll 1
     for (int u = tid; u < hits * kWords; u += kThreads) {
         const int g = sh.hit[u / kWords];
         const int w = p.w0 + g / kThreads * kStepWords + u % kWords * kThreads + g % kThreads;
@@ -358,9 +372,11 @@ __device__ __noinline__ void collect_crowd(PartShared &sh, const Part &p, float 
 {
     constexpr int kP = kPer<F32>;
     const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll 1
     for (int turn = 0; turn < 2; ++turn) {
         if (turn == 1) {
             uint32_t o = 0;
+#pragma unroll 1
             for (int bit = 31; bit >= 0; --bit) {
                 const uint32_t t = o | 1u << bit;
                 int n = 0;
@@ -379,10 +395,12 @@ __device__ __noinline__ void collect_crowd(PartShared &sh, const Part &p, float 
             break;
     }
     int need = num_out - sh.queued, found = sh.queued;
+#pragma unroll 1
     for (int i = 0; i < p.steps && need > 0; ++i) {
         const bool maybe = sh.most[i][tid] >= bar;  // (if its largest is above, it may hold some too)
         if (!__syncthreads_or(maybe))
             continue;
+#pragma unroll 1
         for (int j = 0; j < kWords && need > 0; ++j) {
             const int w = p.w0 + i * kStepWords + j * kThreads + tid;
             uint4 v = make_uint4(0, 0, 0, 0);
@@ -430,6 +448,7 @@ __device__ __noinline__ void collect_crowd(PartShared &sh, const Part &p, float 
 // key's place is the number of larger ones, for all keys differ.
 __device__ __forceinline__ void rank_keys(const Key *keys, int n, int num_out, Key *out, int tid)
 {
+#pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
         const Key k = keys[i];
         int above = 0;
@@ -472,6 +491,7 @@ __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int pa
         return;
     float top = -INFINITY;
     Sum s = {-kMaxRef, 0.0f};
+#pragma unroll 1
     for (int step = 0; step < p.steps; ++step, w += kStepWords) {
         uint4 v[kWords];
 #pragma unroll
@@ -487,6 +507,7 @@ __device__ __forceinline__ void scan_part(const BeamArgs &b, int64_t row, int pa
     }
     const int busy = max(1, min(kWarps, (p.w1 - p.w0 + 31) / 32));  // warps with words
     uint32_t o = ordered(top), r = 0;
+#pragma unroll 1
     for (int i = 0; i < N; i += busy) {
         r = __reduce_max_sync(0xffffffffu, o);
         o = lane == __ffs(__ballot_sync(0xffffffffu, o == r)) - 1 ? 0 : o;
@@ -595,7 +616,7 @@ __device__ __forceinline__ Value ordered_value(Two t)
 
 constexpr int kCands = 512;
 constexpr int kSamples = 1024;
-constexpr int kFirst = 4;  // candidates of a thread that are loaded early
+constexpr int kFirst = 4;  // candidates of a thread that are loaded ahead
 
 // A candidate of a group, or none (0, 0): of equal values the one with the
 // larger `tie` comes first: the lower beam, the larger logit, the lower token.
@@ -717,8 +738,10 @@ __device__ __noinline__ void select_crowd(const BeamArgs &b, int group, JoinShar
     const int tid = threadIdx.x, lane = tid & 31, per = b.parts * a.num_out, all = a.beams * per;
     const Key *keys = b.keys + (int64_t)group * all;
     Candidate last = {~0ull, ~0ull};
+#pragma unroll 1
     for (int place = 0; place < a.num_out; ++place) {
         Candidate best = {0, 0};
+#pragma unroll 1
         for (int i = tid; i < all; i += kThreads) {
             const int beam = i / per;
             const Candidate c = candidate(a, sh, beam, i - beam * per, __ldcg(keys + i));
@@ -769,6 +792,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
     for (int j = 0; j < kFirst; ++j)
         first[j] = __ldcg(group_keys + min(tid + j * kThreads, all - 1));
     bool again = false;
+#pragma unroll 1
     for (int k = warp; k < a.beams; k += kWarps) {
         const float2 *stats = b.stats + (row0 + k) * P;
         const Key *keys = group_keys + k * per;
@@ -779,6 +803,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         Key top = 0;
         Two sum = {0.0f, 0.0f};
         float ref = -kMaxRef;
+#pragma unroll 1
         for (int p = lane; p < P; p += 32) {
             const Key t = __ldcg(keys + p * N);
             const float2 s = __ldcg(stats + p);
@@ -795,6 +820,7 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
             sh.score[k] = 0.25f * score;
         }
         if (state != kLive) {
+#pragma unroll 1
             for (int i = lane; i < each && k * each + i < kSamples; i += 32)
                 sh.sample[k * each + i] = 0;
             continue;
@@ -818,12 +844,14 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
         again = again || wrong;
         __syncwarp();
         if (!wrong)
+#pragma unroll 1
             for (int i = lane; i < each && k * each + i < kSamples; i += 32) {
                 const Key t = i < 32 ? sample : __ldcg(keys + i / depth * N + i % depth);
                 sh.sample[k * each + i] = t ? static_cast<uint32_t>(value_of(sh, k, t) >> 32) : 0;
             }
     }
     if (__syncthreads_or(again))
+#pragma unroll 1
         for (int k = 0; k < a.beams; ++k) {
             const float most = sh.again[k];
             if (sh.state[k] != kLive || isnan(most))
@@ -834,15 +862,17 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
                 sh.base[k] = 0.25f * most;
                 sh.off[k] = {0.25f * log.hi, 0.25f * log.lo};
             }
+#pragma unroll 1
             for (int i = tid; i < each && k * each + i < kSamples; i += kThreads)
                 sh.sample[k * each + i] = 0;
             __syncthreads();
         }
+#pragma unroll 1
     for (int i = tid; i < samples; i += kThreads) {
         // (of equal ones the earlier comes first; what is behind the samples is 0)
         const uint32_t v = sh.sample[i];
         int place = 0;
-#pragma unroll 8
+#pragma unroll 4
         for (int j = 0; j < samples; j += 4) {
             const uint4 x = *reinterpret_cast<const uint4 *>(sh.sample + j);
             place += ((x.x > v) | ((x.x == v) & (j < i))) + ((x.y > v) | ((x.y == v) & (j + 1 < i))) +
@@ -862,18 +892,22 @@ __device__ __forceinline__ void join_group(const BeamArgs &b, int group, JoinSha
                 sh.queue[at] = c;
         }
     };
+#pragma unroll 1
+    for (int i = tid; i < all; i += kThreads) {
+        offer(i, first[0]);
 #pragma unroll
-    for (int j = 0; j < kFirst; ++j)
-        if (tid + j * kThreads < all)
-            offer(tid + j * kThreads, first[j]);
-    for (int i = tid + kFirst * kThreads; i < all; i += kThreads)
-        offer(i, __ldcg(group_keys + i));
+        for (int j = 0; j + 1 < kFirst; ++j)
+            first[j] = first[j + 1];
+        const int ahead = i + kFirst * kThreads;
+        first[kFirst - 1] = ahead < all ? __ldcg(group_keys + ahead) : 0;
+    }
     __syncthreads();
     const int n = sh.queued;
     if (n > kCands) {
         select_crowd(b, group, sh);
         return;
     }
+#pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
         const Candidate c = sh.queue[i];
         int place = 0;
