@@ -17,8 +17,8 @@
 // Bound: HBM while the rows are read (12 logits of bf16 per cycle and SM, all
 // that comes), then a chain of latencies: words read again, the arrival, the
 // join.  Measured: 512 rows of 151,936 bf16 logits, 16 of each group of 8, 433 of
-// them read: 30.6 us, 4.3 TB/s; 60 fp32 rows of 100,003 11.1 us; 320 rows of 65,536
-// of which 0.3 % are allowed 18.2 us; 4 rows of 32,000 6.5 us.  (Small calls wait
+// them read: 30.4 us, 4.3 TB/s; 60 fp32 rows of 100,003 11.1 us; 320 rows of 65,536
+// of which 0.3 % are allowed 18.3 us; 4 rows of 32,000 6.5 us.  (Small calls wait
 // for instructions too, each read once: loops that a call goes round in once or
 // twice are not unrolled; with 92 KB of them, not 72, the fp32 rows took 11.5 us.)
 #include <float.h>

@@ -5,9 +5,9 @@
 // The first three change a few arrays of a pool, at most of some MB, in steps
 // that need one another's results.  Each runs as one thread-block cluster: its
 // barrier is the hardware's and its words pass through shared memory, so a call
-// is one launch, needs no workspace, and nothing of one launch is left for the
-// next to find.  Clusters have up to 16 CTAs (8: 13.3 us instead of 10.3 for the
-// chunks below, 18.2 instead of 15.2 for the larger compaction).
+// is one launch (a large pool's compaction: four), needs no workspace, and nothing
+// of one launch is left for the next to find.  Clusters have up to 16 CTAs (8 took 13.3 us instead of 10.3 for
+// the chunks below, 18.2 instead of 15.2 for the larger compaction).
 //
 // Bound: chains of loads and barriers (an L2 load 700 to 1,000 cycles, a barrier
 // of the cluster with what was written before it about as much), and issue
@@ -15,10 +15,10 @@
 // 4 sequences reordered 2.5 us, 512 of up to 16,001 keys 5.7 us; a step of 240
 // beams cut back, reordered and extended 10.5 us in two calls (fork 3.9, reserve
 // of no rows 4.1); chunks of 200 prompts in a pool of 430,000 pages 10.1 us in
-// two calls; a pool of 1,100 pages compacted 7.4 us, one of 336,000 with 32,500
-// moves 14.3 us.  A call's instructions are read from L2 once each, a latency at
+// two calls; a pool of 1,100 pages compacted 6.6 us, one of 336,000 with 32,500
+// moves 14.2 us.  A call's instructions are read from L2 once each, a latency at
 // a time, so loops over chunks and passes are not unrolled (the smaller
-// compaction 7.9 us unrolled, with 40 KB of them; 7.4).
+// compaction 7.9 us unrolled, with 40 KB of them).
 #include <limits.h>
 
 #include <atomic>
