@@ -366,7 +366,8 @@ __device__ __forceinline__ bool collect(PartShared &sh, const Part &p, float bar
 // Where many are at the bar itself (masked ones), those above it are few.  Else
 // the bar becomes the num_out-th largest group's (bit by bit): then fewer than
 // num_out groups are above it.  Of the logits that are equal to the bar the
-// first ones are taken in order, where they are needed.
+// first ones are taken in order, where they are needed (equal as they count: +inf
+// is the largest number, a NaN none).
 template <bool F32>
 __device__ __noinline__ void collect_crowd(PartShared &sh, const Part &p, float bar, int num_out, int tid)
 {
@@ -409,7 +410,7 @@ __device__ __noinline__ void collect_crowd(PartShared &sh, const Part &p, float 
                 v = load_word<F32>(p, w);
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
-                    mine += fminf(logit_at<F32>(v, e), FLT_MAX) == bar;
+                    mine += counted_logit(logit_at<F32>(v, e)) == bar;
             }
             int at = mine;
 #pragma unroll
@@ -431,7 +432,7 @@ __device__ __noinline__ void collect_crowd(PartShared &sh, const Part &p, float 
             if (mine) {
 #pragma unroll
                 for (int e = 0; e < kP; ++e)
-                    if (fminf(logit_at<F32>(v, e), FLT_MAX) == bar && at++ < need)
+                    if (counted_logit(logit_at<F32>(v, e)) == bar && at++ < need)
                         sh.queue[found + at - 1] = key_of(bar, w * kP - p.first + e);
             }
             found += min(all, need);
