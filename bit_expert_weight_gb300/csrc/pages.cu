@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     move_pass(p, refs_out, copies, moves, first, step);
     cluster_sync();
     const int shift = log2_of(p.page_size), warps = cluster_size() * kWarps;
-    const int wide = (p.table_stride + kColumns - 1) / kColumns;
+    const int wide = max((p.table_stride + kColumns - 1) / kColumns, 1);  // (lengths are looked at without columns too)
 #pragma unroll 1
     for (int u = cluster_rank() * kWarps + warp; u < wide * p.num_seqs; u += warps) {
         const int s = u / wide, j0 = u % wide * kColumns, len = p.kv_len[s];
@@ -957,9 +957,9 @@ cudaError_t launch_pages_compact(const smoe_page_pool &p, int32_t *refs_out, int
             e = launch_ahead(kernel, grid, kPassThreads, 0, 0, stream, args...);
     };
     pass(dim3(dev.sms * 2), move_kernel, p, refs_out, copies, counts);
-    if (p.num_seqs > 0 && p.table_stride > 0) {
+    if (p.num_seqs > 0) {
         const int columns = kPassThreads / 32 * kColumns, wide = (p.table_stride + columns - 1) / columns;
-        pass(dim3(wide < 64 ? wide : 64, p.num_seqs), table_kernel, p, refs_out, table_out, counts, dev.status);
+        pass(dim3(wide < 1 ? 1 : wide < 64 ? wide : 64, p.num_seqs), table_kernel, p, refs_out, table_out, counts, dev.status);
     }
     pass(dim3(dev.sms), clear_kernel, refs_out, copies, counts);
     return e;
