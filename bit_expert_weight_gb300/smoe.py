@@ -918,6 +918,9 @@ def pages_fork(refs: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tenso
     [sequences]."""
     dev = _device("refs", refs)
     S = kv_len.numel()
+    # (the parents of a selection of more outputs than beams are not one per sequence)
+    if (parent is not None and parent.numel() != S) or (keep is not None and keep.numel() != S):
+        raise ValueError("parent and keep must have one number per sequence")
     _check(load().smoe_pages_fork(_pool(refs, kv_len, page_table, page_size, dev),
                                   _device_array("parent", parent, torch.int32, S, dev),
                                   _device_array("keep", keep, torch.int32, S, dev),
