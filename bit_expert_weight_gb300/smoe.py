@@ -691,6 +691,12 @@ def _device_array(name, t, dtype, numel, dev):
     return t.data_ptr()
 
 
+def _check_rows(name, t, rows, width):
+    """t (or None) holds [rows, width] numbers, alone or with more rows behind them."""
+    if t is not None and t.numel() != rows * width and t.dim() > 1 and t.shape[-1] != width:
+        raise ValueError(f"{name} must be [{rows}, {width}]")
+
+
 def _cache(k_pages, v_pages, dev):
     """The members of smoe_kv_cache."""
     P, Hkv, page, D = shape = k_pages.shape
@@ -884,6 +890,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, ws: to
                torch.empty((G, num_out), dtype=i32, device=logits.device),
                torch.empty((G, num_out), dtype=i32, device=logits.device))
     to_scores, parents, tokens = out
+    _check_rows("last", last, G, K)
+    for t in out:
+        _check_rows("out", t, G, num_out)
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the device of the call's other tensors")
     a = _pack_beam(logits.data_ptr(), st[0] if G * K > 1 else 0,

@@ -25,3 +25,25 @@ def test_fork_takes_any_shape_of_them(S, calls, shape):  # noqa: F811
                                       keep=torch.zeros(shape, dtype=I32)))
     call(S, "pages_fork", change=dict(keep=None))
     assert calls.got["smoe_pages_fork"][2] == 0
+
+
+@pytest.mark.parametrize("name", ["last", "out/0", "out/1", "out/2"])
+def test_select_takes_rows_of_its_own_width(S, calls, name):  # noqa: F811
+    """Two groups of three beams, four outputs: rows of another width would be read or written
+    across one another; more rows than there are groups, or one long row, are not."""
+    def with_shape(shape, dtype=I32):
+        t = torch.zeros(shape, dtype=torch.float32 if name == "out/0" else dtype)
+        if name == "last":
+            return dict(last=t)
+        out = [torch.zeros(2, 4), torch.zeros(2, 4, dtype=I32), torch.zeros(2, 4, dtype=I32)]
+        out[int(name[-1])] = t
+        return dict(out=out)
+
+    wide = 3 if name == "last" else 4
+    for shape in ((2, wide), (5, wide), (2 * wide,), (9 * wide,), (2, wide, 1)):
+        call(S, "beam_select", change=with_shape(shape))
+    calls.got.clear()
+    for shape in ((2, wide + 1), (2, 2 * wide), (3, 2 * wide), (5, wide, 2)):
+        with pytest.raises(ValueError):
+            call(S, "beam_select", change=with_shape(shape))
+    assert not calls.got
