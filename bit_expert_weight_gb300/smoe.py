@@ -993,6 +993,7 @@ def pages_compact(refs: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Te
     i32 = torch.int32
     refs_out = refs if refs_out is None else refs_out
     page_table_out = page_table if page_table_out is None else page_table_out
+    _check_rows("page_table_out", page_table_out, *page_table.shape)
     if copies.dim() != 2 or copies.shape[1] != 2:
         raise ValueError("copies must be [at most, 2]")
     _check(load().smoe_pages_compact(

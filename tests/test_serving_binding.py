@@ -47,3 +47,15 @@ def test_select_takes_rows_of_its_own_width(S, calls, name):  # noqa: F811
         with pytest.raises(ValueError):
             call(S, "beam_select", change=with_shape(shape))
     assert not calls.got
+
+
+def test_compact_takes_a_table_of_its_own_width(S, calls):  # noqa: F811
+    """Three sequences of seven entries: a table to write of other columns would get each row in
+    another place; more rows, or one long row, are not."""
+    for shape in ((3, 7), (5, 7), (21,), (40,)):
+        call(S, "pages_compact", change=dict(page_table_out=torch.zeros(shape, dtype=I32)))
+    calls.got.clear()
+    for shape in ((3, 8), (3, 14), (4, 6), (2, 20)):
+        with pytest.raises(ValueError):
+            call(S, "pages_compact", change=dict(page_table_out=torch.zeros(shape, dtype=I32)))
+    assert not calls.got
