@@ -993,11 +993,12 @@ def pages_compact(refs: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Te
     i32 = torch.int32
     refs_out = refs if refs_out is None else refs_out
     page_table_out = page_table if page_table_out is None else page_table_out
-    _check_rows("page_table_out", page_table_out, *page_table.shape)
     if copies.dim() != 2 or copies.shape[1] != 2:
         raise ValueError("copies must be [at most, 2]")
+    pool = _pool(refs, kv_len, page_table, page_size, dev)
+    _check_rows("page_table_out", page_table_out, *page_table.shape)
     _check(load().smoe_pages_compact(
-        _pool(refs, kv_len, page_table, page_size, dev),
+        pool,
         _device_array("refs_out", refs_out, i32, refs.numel(), dev),
         _device_array("page_table_out", page_table_out, i32, page_table.numel(), dev),
         _device_array("copies", copies, i32, 0, dev), copies.shape[0],

@@ -59,3 +59,10 @@ def test_compact_takes_a_table_of_its_own_width(S, calls):  # noqa: F811
         with pytest.raises(ValueError):
             call(S, "pages_compact", change=dict(page_table_out=torch.zeros(shape, dtype=I32)))
     assert not calls.got
+
+
+@pytest.mark.parametrize("name", ["pages_fork", "pages_reserve", "pages_compact"])
+def test_tables_of_one_dimension_are_refused(S, calls, name):  # noqa: F811
+    with pytest.raises(ValueError):
+        call(S, name, change=dict(page_table=torch.zeros(21, dtype=I32)))
+    assert not calls.got
