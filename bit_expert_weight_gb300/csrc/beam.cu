@@ -18,9 +18,15 @@
 // that comes), then a chain of latencies: words read again, the arrival, the
 // join.  Measured: 512 rows of 151,936 bf16 logits, 16 of each group of 8, 433 of
 // them read: 30.4 us, 4.3 TB/s; 60 fp32 rows of 100,003 11.1 us; 320 rows of 65,536
-// of which 0.3 % are allowed 18.3 us; 4 rows of 32,000 6.5 us.  (Small calls wait
+// of which 0.3 % are allowed 18.3 us; 4 rows of 32,000 6.4 us.  (Small calls wait
 // for instructions too, each read once: loops that a call goes round in once or
 // twice are not unrolled; with 92 KB of them, not 72, the fp32 rows took 11.5 us.)
+// Rows with a NaN or +inf, and those whose logits above -inf are all the lowest
+// value, are summed again by the CTA that joins their group, one after the other:
+// a group of 32 such rows of 151,936 takes 1.01 ms instead of 25 us, one of 4 of
+// 32,000 25 instead of 6.4.  Rows of few allowed tokens among the type's lowest
+// value rank those too: 320 rows of 2,000, 32 of 16 beams, 1 % allowed 15.1 us (the
+// rest -inf: 10.6), one token allowed 43.9 (10.1); of 1,000 84 and 121 us.
 #include <float.h>
 #include <math.h>
 
@@ -34,10 +40,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// (512 rows of 151,936: 33.6 us with three, 47.9 with two, 36.1 with four, whose
-// threads have 64 registers and whose CTAs lie less evenly)
+// (512 rows of 151,936: 30.4 us with three, 30.9 with four, whose threads have 64
+// registers, not 74; two allow 80, of which three are resident all the same: 30.4)
 constexpr int kCtasPerSm = 3;
-constexpr int kWords = 4;                         // of 16 bytes, of a thread and step (3: 41.8 us, 8: 36.1)
+constexpr int kWords = 4;                         // of 16 bytes, of a thread and step (4: 30.4 us, 3: 38.4, 8: 31.5)
 constexpr int kStepWords = kThreads * kWords;     // of a CTA and step
 constexpr size_t kStatsAt = SMOE_MAX_SEQS * sizeof(unsigned);  // after the groups' counters
 constexpr int kMaxSteps = 24;                     // of a part
@@ -48,8 +54,8 @@ static_assert(kStatsAt + (size_t)(SMOE_MAX_SEQS * ((SMOE_MAX_VOCAB / 4 + 1) / (k
               "parts in the workspace");
 // Logits of more bytes than this are read as passing by (first to leave L2):
 // those of less may lie there, from the product that made them, and the few
-// words read again do (60 fp32 rows of 100,003: 12.5 us, 14.0 as passing by; 512
-// rows of 151,936: 36.9 us, 33.6 as passing by).
+// words read again do (60 fp32 rows of 100,003: 11.1 us, 11.9 as passing by; 512
+// rows of 151,936: 34.7 us, 30.4 as passing by).
 constexpr int64_t kPassing = 32 << 20;
 constexpr float kLog2e = 1.4426950408889634f;
 // A sum's reference stays within this: sums of rows whose largest logit is
@@ -961,8 +967,8 @@ cudaError_t launch_beam_select(const smoe_beam_args &a, void *workspace, const D
     const int per = f32 ? 4 : 8;
     const int words = (a.vocab + 2 * per - 2) / per;
     const int steps = (words + kStepWords - 1) / kStepWords;
-    // parts: up to two CTAs per SM, of a step at least (60 fp32 rows of 100,003: 13.4 us with
-    // two, 14.0 with three, 16.2 with four: each part costs its end again)
+    // parts: up to two CTAs per SM, of a step at least (60 fp32 rows of 100,003: 11.1 us with
+    // two and with three, 14.0 with four: each part costs its end again)
     const int64_t wave = dev.sms * 2 < kMaxWave ? dev.sms * 2 : kMaxWave;
     int64_t parts = wave / rows;
     const int least = (steps + kMaxSteps - 1) / kMaxSteps;

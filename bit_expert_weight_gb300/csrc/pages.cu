@@ -6,19 +6,20 @@
 // that need one another's results.  Each runs as one thread-block cluster: its
 // barrier is the hardware's and its words pass through shared memory, so a call
 // is one launch (a large pool's compaction: four), needs no workspace, and nothing
-// of one launch is left for the next to find.  Clusters have up to 16 CTAs (8 took 13.3 us instead of 10.3 for
-// the chunks below, 18.2 instead of 15.2 for the larger compaction).
+// of one launch is left for the next to find.  Clusters have up to 16 CTAs (8 take
+// 13.1 us instead of 10.0 for the chunks below, 17.4 instead of 14.1 for the larger
+// compaction).
 //
 // Bound: chains of loads and barriers (an L2 load 700 to 1,000 cycles, a barrier
 // of the cluster with what was written before it about as much), and issue
 // slots where one cluster goes over a whole table.  Measured on the device:
 // 4 sequences reordered 2.5 us, 512 of up to 16,001 keys 5.7 us; a step of 240
-// beams cut back, reordered and extended 10.5 us in two calls (fork 3.9, reserve
-// of no rows 4.1); chunks of 200 prompts in a pool of 430,000 pages 10.1 us in
-// two calls; a pool of 1,100 pages compacted 6.6 us, one of 336,000 with 32,500
-// moves 14.2 us.  A call's instructions are read from L2 once each, a latency at
+// beams cut back, reordered and extended 10.4 us in two calls (fork 3.9, reserve
+// of no rows 4.0); chunks of 200 prompts in a pool of 430,000 pages 10.0 us in
+// two calls; a pool of 1,100 pages compacted 7.1 us, one of 336,000 with 32,500
+// moves 14.1 us.  A call's instructions are read from L2 once each, a latency at
 // a time, so loops over chunks and passes are not unrolled (the smaller
-// compaction 7.9 us unrolled, with 40 KB of them).
+// compaction 7.5 us unrolled).
 #include <limits.h>
 
 #include <atomic>
@@ -181,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // warp of the cluster, dealt to its CTAs in turn (what is asked of pages is often
 // asked of the lowest), and in each run in chunks of 128 pages (L = 1) or of 1024
 // (L = 8 loads in flight), by the size of the pool: of up to two chunks of 128 for
-// each warp, or more (a step of 240 beams in a pool of 100,000 pages: 10.6 us
-// with 128, 11.3 with 1024; chunks of 200 prompts in one of 430,000: 17.2 and 10.2).
+// each warp, or more (a step of 240 beams in a pool of 100,000 pages: 10.4 us
+// with 128, 11.2 with 1024; chunks of 200 prompts in one of 430,000: 17.5 and 10.0).
 constexpr int chunk(int L) { return 128 * L; }
 
 struct Run {
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // then the moves are gone through as a list, and the tables.  Meanwhile the
 // entry of a moved page in refs_out (which will be 0) says where it went.  A
 // small pool's are done with by the same cluster; a large one's by launches of
-// the whole device (336,000 pages, 480 sequences: 14.3 us; by the cluster 20.3).
+// the whole device (336,000 pages, 480 sequences: 14.1 us; by the cluster 24.9).
 constexpr int kBatch = 4;  // loads of a thread that are in flight together
 constexpr int kColumns = 128;
 
@@ -814,8 +815,8 @@ __global__ void __launch_bounds__(kPassThreads)
 // Bound: HBM, each page is read and written once.  A unit is 16 KB of one
 // page's keys or values in one cache.  Many CTAs of one to a few units each keep
 // the most loads in flight: 601 pages in two layers (630 MB read and written) take
-// 93.9 us, 6.7 TB/s, with 32 CTAs per SM, 102 us with 8 that go on and on; more than
-// 32 would cost calls of few pages.  12 pages in four layers: 2.1 us.
+// 93.9 us, 6.7 TB/s, with 32 CTAs per SM, 103.8 us with 8 that go on and on, 93.2
+// with 64.  12 pages in four layers: 2.2 us.
 constexpr int kCopyThreads = 256;
 constexpr int kUnitWords = 1024;  // of 16 bytes
 
@@ -903,8 +904,8 @@ int cluster_for(int64_t n)
 constexpr int kRound = kMaxCluster * kWarps * chunk(1);
 bool small_chunks(const smoe_page_pool &p) { return p.num_pages <= 2 * kRound; }
 // A pool of one round, with tables of few entries, is also compacted by the one
-// launch: 1,100 pages take 8.4 us a call, and 12.6 by four launches, which the
-// host takes longer for (8.3 us on the device).
+// launch: 1,100 pages take 7.3 us a call, and 13.4 by four launches, which the
+// host takes longer for (7.5 us on the device).
 bool compact_alone(const smoe_page_pool &p)
 {
     return p.num_pages <= kRound && (int64_t)p.num_seqs * p.table_stride <= 1 << 16;

@@ -96,7 +96,8 @@ class BeamSearch:
 
     def step(self):
         """One more token of every beam.  (A beam that leads nowhere has token -1; any other
-        may stand for it, its score stays -inf.)"""
+        may stand for it, its score stays -inf.  A finished one gets a row as well, which
+        nothing reads: steps are alike then, and its pages go on growing with the others'.)"""
         a = self.attend(self.tokens.view(-1).clamp_min(0), self.single, 1)
         self.choose(self.model.logits(a))
 

@@ -747,8 +747,9 @@ typedef struct {
 /* The num_out best continuations of each group's beams, best first:
  *   value(k, v) = scores[k] + x_kv - log(sum_u exp(x_ku))
  * over the group's beams k and all tokens v; of equal values the lower k comes
- * first, and within a beam the larger logit, then the lower v.  parents gets the beam's row in logits (group *
- * beams + k), tokens v, scores_out the value rounded to fp32.
+ * first, and within a beam the larger logit, then the lower v.  parents gets the
+ * beam's row in logits (group * beams + k), tokens v, scores_out the value
+ * rounded to fp32.
  * A beam whose last token is end_token is finished: its logits do not matter,
  * and it has one continuation, end_token at its own score.  A logit of -inf or
  * NaN is never chosen and has no part in the sum; +inf counts as the largest
